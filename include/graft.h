@@ -58,7 +58,10 @@ typedef struct CUstream_st* graft_stream_t;
 #define GRAFT_STATUS_LENGTH 4         /* L[b] < 0 or L[b] > Lcap; that request was skipped */
 #define GRAFT_STATUS_TREE 8           /* a kept draft node's parent was not kept (cannot happen for finite logits) */
 #define GRAFT_STATUS_TIMEOUT 16       /* a bounded wait inside a kernel expired; that CTA's output is incomplete */
-#define GRAFT_STATUS_WORKSPACE 32     /* a workspace's arrival counter was found not zeroed (graft_build_tree, graft_tree_attention) */
+#define GRAFT_STATUS_WORKSPACE 32     /* a workspace's arrival counter was found not zeroed (graft_build_tree, graft_tree_attention, graft_paged_attention) */
+#define GRAFT_STATUS_PAGE 64          /* a page number outside the pool, or a page that no sequence holds, was read; it was skipped (read as zeros) */
+#define GRAFT_STATUS_PLAN 128         /* a plan that was not made for the call's arguments; nothing was computed */
+#define GRAFT_STATUS_SEQUENCE 256     /* a sequence index out of range, named twice, or not empty where it has to be; it was skipped */
 
 /* Limits. */
 #define GRAFT_MAX_KMAX 64        /* tree nodes per request (one uint64 ancestor mask) */
@@ -465,6 +468,194 @@ int graft_update_M_emitted(int32_t* M_succ, int32_t* M_cnt, int V, int W, int B,
 #define GRAFT_NOALLOC_MAX_PAIRS 16384
 int graft_update_M_noalloc(int32_t* M_succ, int32_t* M_cnt, int V, int W, const int32_t* src,
                            const int32_t* dst, int64_t n, int32_t* status, graft_stream_t stream);
+
+/*
+ * ------------------------------------------------------------------ paged cache
+ *
+ * A KV cache kept in pages, for serving: one pool of pages a layer, shared
+ * by all sequences, and one row of page numbers a sequence.  The verify
+ * step's rows (Graft article, architecture paragraph: one target forward
+ * over the merged tree) go straight to their pages: graft_rope_append
+ * rotates and writes them at rows lengths[b] .., graft_paged_attention
+ * attends over them under the tree mask (or causally: prompt chunks, single
+ * tokens), graft_pages_compact keeps the accepted ones.
+ */
+#define GRAFT_BF16 0
+#define GRAFT_FP16 1
+#define GRAFT_MAX_SEQS 4096      /* sequences (rows of the block table) */
+#define GRAFT_MAX_PAGE_ROWS 256  /* page rows: 16, 32, 64, 128 or 256 */
+
+/*
+ * GraftPagedCache — where a paged cache lies (host struct, passed by
+ * pointer; its tensors are the caller's device memory).
+ *
+ *   dtype        GRAFT_BF16 or GRAFT_FP16: pools and every Q, K, V, O of the calls
+ *   Hkv          KV heads; head_dim must be 128
+ *   page_rows    rows of a page: a power of two, 16 .. 256
+ *   num_pages    pages of a pool; num_pages * page_rows < 2^31
+ *   n_seqs       sequences, 1 .. GRAFT_MAX_SEQS
+ *   max_pages    page numbers of a block-table row; max_pages * page_rows and
+ *                n_seqs * max_pages < 2^31
+ *   n_layers     entries of K_layers / V_layers
+ *   block_table  [n_seqs][max_pages] i32: row r of sequence b lies in page
+ *                block_table[b][r / page_rows], slot r % page_rows
+ *   lengths      [n_seqs] i32: rows that the sequence's context holds
+ *   held         [n_seqs] i32: page numbers in use of each row (reserve, fork, free)
+ *   page_refs    [num_pages] i32: sequences that hold each page, 0 = free
+ *                (reserve, fork, free)
+ *   K_layers, V_layers  device arrays of n_layers device pointers to pools
+ *                [num_pages][page_rows][Hkv][128] (reserve, compact)
+ *   status       device word for GRAFT_STATUS_* bits, or NULL
+ * Pools are 16-byte aligned.  A sequence's rows past its length, and the
+ * pages that no sequence holds, may hold anything, NaN included.
+ */
+typedef struct GraftPagedCache {
+    int32_t dtype, Hkv, head_dim, page_rows, num_pages, n_seqs, max_pages, n_layers;
+    int32_t* block_table;
+    int32_t* lengths;
+    int32_t* held;
+    int32_t* page_refs;
+    void* const* K_layers;
+    void* const* V_layers;
+    int32_t* status;
+} GraftPagedCache;
+
+/*
+ * graft_rope_inv_freq — angular frequencies of rotary positions, in 64 bits
+ * (host only): out[i] = base^(-2i / rot_dim), i < rot_dim / 2, scaled for
+ * contexts longer than the `original` one.
+ *   scaling 0  none
+ *           1  all divided by `stretch`
+ *           2  by wavelength: waves longer than original / low divided by
+ *              `stretch`, waves shorter than original / high kept, a linear
+ *              blend between (low = 1, high = 4 usually)
+ *           3  YaRN: pairs turning fewer than `low` times in the original
+ *              context divided by `stretch`, those turning more than `high`
+ *              times kept, a ramp over the pair index between (low = 1,
+ *              high = 32 usually); *factor = 0.1 ln(stretch) + 1
+ *   *factor  multiplies the rotated part of Q and K (1 except for scaling 3); may be NULL
+ */
+int graft_rope_inv_freq(int rot_dim, double base, int scaling, double stretch, double low, double high,
+                        double original, double* out /* host */, float* factor /* host */);
+
+/*
+ * graft_rope_append — rotary positions, and new K and V rows into their pages.
+ *
+ * Rows 0 .. N-1 are the new rows of all sequences, ragged: sequence b's are
+ * q_start[b] .. q_start[b+1] - 1 (q_start [n_seqs + 1] i32, rising from >= 0,
+ * at most N; rows outside every sequence are neither read for their value nor
+ * written).  The i-th new row of sequence b is its cache row lengths[b] + i;
+ * its position is pos[row] ([N] i32), or lengths[b] + i where pos is NULL.
+ *   Q, Q_out [N][Hq][128], K, V [N][Hkv][128], heads contiguous, rows
+ *   q_stride, k_stride, v_stride, qo_stride elements apart (multiples of 8).
+ * Pair p of the first rot_dim dims of every Q and K head turns by the angle
+ * a = position * inv_freq[p] ([rot_dim / 2] f64, device):
+ *   (x, y) -> factor * (x cos a - y sin a, x sin a + y cos a)
+ * with (x, y) dims (p, p + rot_dim / 2), or (2p, 2p + 1) if interleaved; the
+ * other dims are copied.  Angles are reduced exactly (64-bit fractions of a
+ * turn), so far positions lose nothing; the rotation runs in 32 bits and is
+ * rounded once.  rot_dim is a multiple of 16, 0 .. 128 (0: no rotation,
+ * inv_freq may be NULL).  Hq = 0 (Q NULL) appends alone; Q_out may be Q.
+ * lengths are not advanced.  A row whose cache row lies outside the block
+ * table sets GRAFT_STATUS_LENGTH, outside the pool GRAFT_STATUS_PAGE; its K
+ * and V are not written.
+ */
+int graft_rope_append(const GraftPagedCache* cache, void* K_pool, void* V_pool, int N, int Hq,
+                      const int32_t* q_start, const int32_t* pos, const double* inv_freq, int rot_dim,
+                      int interleaved, float factor, const void* Q, int64_t q_stride, const void* K,
+                      int64_t k_stride, const void* V, int64_t v_stride, void* Q_out, int64_t qo_stride,
+                      graft_stream_t stream);
+
+/*
+ * graft_paged_plan — splits a step's attention over the GPU, on the device,
+ * from lengths and q_start as they are when it runs.  One plan serves every
+ * layer's graft_paged_attention of the step.
+ *   max_new  no sequence has more new rows than this (checked)
+ *   tree     the attention calls will pass a tree mask (max_new <= 64)
+ * A sequence with lengths[b] < 0, more rows than its block-table row can
+ * hold, or new rows outside 0 .. max_new sets GRAFT_STATUS_LENGTH and is left
+ * out: its rows of O are not written.  plan: graft_paged_plan_size bytes,
+ * 256-byte aligned.
+ */
+int graft_paged_plan_size(const GraftPagedCache* cache, int N, int Hq, int max_new, size_t* bytes);
+int graft_paged_plan(const GraftPagedCache* cache, int N, int Hq, const int32_t* q_start, int max_new, int tree,
+                     void* plan, size_t plan_bytes, graft_stream_t stream);
+
+/*
+ * graft_paged_attention — attention of the new rows of every sequence over
+ * its pages, for one layer; the new rows' own K and V are in the pages
+ * already (graft_rope_append).
+ *   Q [N][Hq][128] rows q_stride elements apart (a multiple of 8), O
+ *   [N][Hq][128] dense; 16-byte aligned
+ *   mask  NULL: causal, the i-th new row sees cache rows 0 .. lengths[b] + i;
+ *         else [N] u64: it sees cache rows 0 .. lengths[b] - 1 and new row j
+ *         where bit j of mask[row] is set (graft_build_tree's tree_mask for
+ *         equal chunks of Kmax nodes)
+ * O = softmax over the visible rows of scale * q.k, applied to V; query head
+ * h reads KV head h / (Hq / Hkv), Hq / Hkv <= 64.  Scores and sums in 32 bits.  A row
+ * that sees nothing gives zeros.  What a row does not see has no effect on
+ * it, whatever it holds (NaN and infinities included).  Rows of O outside
+ * every sequence are left as they were.
+ * plan: of the same cache sizes, N, Hq, max_new and tree (else
+ * GRAFT_STATUS_PLAN); the lengths are the plan's.  ws:
+ * graft_paged_attention_workspace_size bytes, ZERO-FILLED once by its owner
+ * (arrival counters; every call leaves them at zero; after
+ * GRAFT_STATUS_TIMEOUT zero it again).  A workspace or a plan buffer of more
+ * bytes serves smaller calls too.  Calls sharing a workspace must not run at
+ * the same time.
+ */
+int graft_paged_attention_workspace_size(const GraftPagedCache* cache, int N, int Hq, int max_new, size_t* bytes);
+int graft_paged_attention(const GraftPagedCache* cache, const void* K_pool, const void* V_pool, int N, int Hq,
+                          int max_new, const void* plan, size_t plan_bytes, const void* Q, int64_t q_stride,
+                          const uint64_t* mask, float scale, void* O, void* ws, size_t ws_bytes,
+                          graft_stream_t stream);
+
+/*
+ * graft_pages_compact — after a verify step: in every layer, cache row
+ * lengths[b] + t receives row lengths[b] + path[b][t], t < acc_len[b]
+ * (graft_accept_compact's path and acc_len; path rises strictly, so the moves
+ * are made in place), and lengths_out[b] = lengths[b] + acc_len[b].
+ * lengths_out may be lengths.  A path that does not rise within [0, Kmax)
+ * sets GRAFT_STATUS_TREE, rows outside the block table GRAFT_STATUS_LENGTH or
+ * the pool GRAFT_STATUS_PAGE; that sequence keeps its rows and its length.
+ */
+int graft_pages_compact(const GraftPagedCache* cache, int Kmax, const int32_t* path, const int32_t* acc_len,
+                        int32_t* lengths_out, graft_stream_t stream);
+
+/*
+ * graft_pages_reserve — pages for new_rows[b] more rows of every sequence
+ * (new_rows [n_seqs] i32; 0 leaves a sequence alone).  Page numbers that the
+ * rows lengths[b] .. lengths[b] + new_rows[b] - 1 need and the sequence lacks
+ * are taken from the free pages (page_refs 0), the lowest first, in the order
+ * of the sequences; a page there that is shared (page_refs > 1 when the call
+ * starts) is replaced by a new one, and its rows below lengths[b] are copied
+ * in every layer (copy on write).  If the free pages run out, that
+ * sequence and those after it that need pages set
+ * GRAFT_STATUS_CACHE_OVERFLOW and are left as they were; so is, with
+ * GRAFT_STATUS_LENGTH, one that would outgrow its block-table row or holds
+ * fewer pages than its length fills, and, with GRAFT_STATUS_PAGE, one whose
+ * page there has no reference.  Workspace: graft_pages_reserve_workspace_size.
+ */
+int graft_pages_reserve_workspace_size(const GraftPagedCache* cache, size_t* bytes);
+int graft_pages_reserve(const GraftPagedCache* cache, const int32_t* new_rows, void* ws, size_t ws_bytes,
+                        graft_stream_t stream);
+
+/*
+ * graft_pages_fork — sequence dst[i] becomes a copy of src[i] by sharing the
+ * pages of its lengths[src[i]] rows (page_refs rise; graft_pages_reserve
+ * copies a shared page before it is written).  src, dst [n] i32, n <=
+ * GRAFT_MAX_SEQS; every dst is empty (held 0) and named once, and no src is
+ * another fork's dst (else GRAFT_STATUS_SEQUENCE, and that fork is skipped).
+ */
+int graft_pages_fork(const GraftPagedCache* cache, int n, const int32_t* src, const int32_t* dst,
+                     graft_stream_t stream);
+
+/*
+ * graft_pages_free — gives back the pages of sequences seqs[0 .. n-1]:
+ * page_refs fall, held and lengths become 0, the block-table rows -1.  A
+ * sequence named twice is freed once (GRAFT_STATUS_SEQUENCE).
+ */
+int graft_pages_free(const GraftPagedCache* cache, int n, const int32_t* seqs, graft_stream_t stream);
 
 /* Human-readable text for a return code (static string). */
 const char* graft_status_string(int code);

@@ -29,6 +29,7 @@ Modules:
 * ``attention``  tree-masked GQA attention (softmax definition, fp64)
 * ``accept``     greedy longest-accepted-path and KV compaction
 * ``update_m``   online update of the adjacency table M
+* ``paged``      the paged cache: rotary positions, attention over pages, compaction, page lifecycle
 * ``step``       one whole verify step composed from the above
 * ``tiny_lm``    a tiny random-init transformer used for the losslessness pin
 

@@ -25,10 +25,14 @@ STATUS_LENGTH = 4
 STATUS_TREE = 8
 STATUS_TIMEOUT = 16
 STATUS_WORKSPACE = 32
+STATUS_PAGE = 64
+STATUS_PLAN = 128
+STATUS_SEQUENCE = 256
 EMPTY_TOKEN = -1
 
 MAX_KMAX = 64
 MAX_CHECKPOINTS = 4
+MAX_SEQS = 4096
 HEAD_DIM = 128
 
 
@@ -60,6 +64,14 @@ class GraftAttnTuning(ctypes.Structure):
     attention (0 in a field keeps the default plan)."""
     _fields_ = [("tiles", ctypes.c_int32), ("min_chunk", ctypes.c_int32), ("persist_ctas", ctypes.c_int32),
                 ("split", ctypes.c_int32), ("wait_ns", ctypes.c_int32), ("reserved", ctypes.c_int32 * 3)]
+
+
+class GraftPagedCache(ctypes.Structure):
+    """Mirror of the C struct GraftPagedCache (graft.h); ``paged.PagedCache`` fills and keeps one."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "Hkv", "head_dim", "page_rows", "num_pages", "n_seqs",
+                                              "max_pages", "n_layers")] + \
+               [(n, ctypes.c_void_p) for n in ("block_table", "lengths", "held", "page_refs", "K_layers", "V_layers",
+                                               "status")]
 
 
 class GraftError(RuntimeError):
@@ -101,6 +113,19 @@ _SIGNATURES = {
     "graft_update_M_noalloc": [_P, _P, _I, _I, _P, _P, _I64, _P, _P],
     "graft_update_M_emitted_workspace_size": [_I, _I, ctypes.POINTER(_SZ)],
     "graft_update_M_emitted": [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P],
+    "graft_rope_inv_freq": [_I, ctypes.c_double, _I, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                            ctypes.c_double, _P, _P],
+    "graft_rope_append": [_P, _P, _P, _I, _I, _P, _P, _P, _I, _I, ctypes.c_float, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                          _P],
+    "graft_paged_plan_size": [_P, _I, _I, _I, ctypes.POINTER(_SZ)],
+    "graft_paged_plan": [_P, _I, _I, _P, _I, _I, _P, _SZ, _P],
+    "graft_paged_attention_workspace_size": [_P, _I, _I, _I, ctypes.POINTER(_SZ)],
+    "graft_paged_attention": [_P, _P, _P, _I, _I, _I, _P, _SZ, _P, _I64, _P, ctypes.c_float, _P, _P, _SZ, _P],
+    "graft_pages_compact": [_P, _I, _P, _P, _P, _P],
+    "graft_pages_reserve_workspace_size": [_P, ctypes.POINTER(_SZ)],
+    "graft_pages_reserve": [_P, _P, _P, _SZ, _P],
+    "graft_pages_fork": [_P, _I, _P, _P, _P],
+    "graft_pages_free": [_P, _I, _P, _P],
     "graft_status_string": [_I],
     "graft_version": [],
     "graft_launch_count": [],
@@ -476,3 +501,18 @@ def graft_seed_M_from_tokens(M_succ, M_cnt, tokens, status=None, ws=None, stream
         return
     t = tokens.reshape(-1)
     graft_update_M(M_succ, M_cnt, t[:-1], t[1:], status=status, ws=ws, stream=stream)
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "wavelength": 2, "yarn": 3}
+
+
+def graft_rope_inv_freq(rot_dim: int, base: float, scaling: str = "none", stretch: float = 1.0, low: float = 1.0,
+                        high: float = 4.0, original: float = 8192.0, device=None):
+    """Angular frequencies of rotary positions (float64 [rot_dim / 2], on ``device``) and the factor on Q and K."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    out = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float64)
+    factor = ctypes.c_float()
+    _check(lib().graft_rope_inv_freq(rot_dim, base, ROPE_SCALINGS[scaling], stretch, low, high, original,
+                                     out.data_ptr(), ctypes.addressof(factor)), "graft_rope_inv_freq")
+    return (out if device is None else out.to(device)), factor.value

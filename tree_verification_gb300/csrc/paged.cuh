@@ -1,0 +1,142 @@
+// Shared by the paged-cache kernels: argument checks, page lookup, the attention plan's layout.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace graft {
+namespace paged {
+
+constexpr int HD = GRAFT_HEAD_DIM;
+
+// Host checks of a cache's sizes; `tables` adds the arrays that reserve, fork and free need.
+int check_cache(const GraftPagedCache* c);
+int check_tables(const GraftPagedCache* c);
+
+inline int log2_exact(int x) {
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// ---------------------------------------------------------------- the attention plan
+// A work item of the attention is one entry (a block of query rows of one sequence) and one KV head,
+// against a range of keys.  The plan is one buffer:
+//   PlanHead | few entries | their unit prefix sums | the CTAs' first units
+// "Few" entries go to the kernel of paged_few.cu: at most `few_rows` query rows (new rows x group).
+struct PlanHead {
+    int32_t magic, N, Hq, Hkv, n_seqs, max_new, tree, page_rows, max_pages, num_pages, few_rows, ctas;
+    int32_t n_few;       // few entries
+    int32_t few_ctas;    // CTAs that share them
+    int64_t few_units;   // 16-key units over entries and heads
+    int32_t reserved[16];
+};
+constexpr int32_t kPlanMagic = 0x47503033;
+
+struct Entry {
+    int32_t b;       // sequence
+    int32_t q0;      // its first new row
+    int32_t n, L;    // new rows, rows before them
+    int32_t row0;    // first query row of the block (row = new row x group + head of the group)
+    int32_t rows;    // query rows of the block
+    int32_t keys;    // keys that any of them may see
+    int32_t units;   // of 16 keys
+};
+
+struct Start {
+    int32_t entry, head, unit, pad;
+};
+
+struct PlanShape {
+    int max_few;   // bound on the few entries
+    int ctas;      // CTAs of the few kernel at most
+    int few_rows;  // query rows of a few entry at most (16 or 32)
+    size_t off_few, off_prefix, off_start, bytes;
+};
+
+// CTA k of `ctas` takes units [first_unit(k), first_unit(k + 1)).
+__host__ __device__ __forceinline__ int64_t first_unit(int64_t units, int ctas, int k) {
+    const int64_t each = units / ctas, left = units % ctas;
+    return each * k + (k < left ? k : left);
+}
+// The CTA that takes unit u.
+__host__ __device__ __forceinline__ int unit_cta(int64_t units, int ctas, int64_t u) {
+    const int64_t each = units / ctas, left = units % ctas, big = left * (each + 1);
+    return (int)(u < big ? u / (each + 1) : left + (u - big) / each);
+}
+
+PlanShape plan_shape(const GraftPagedCache* c, int N, int Hq, int max_new);
+
+// Partial results of cut items: every CTA has at most two (its first item's end, its last item's start).
+// The partial rows come first in the workspace, in a size of the device's alone, the counters last: calls of
+// other shapes that share a workspace (one after another) never write over the counters.
+constexpr int kFewRows = 32;
+struct FewWs {
+    float* o;        // [ctas][2][kFewRows][128]
+    float2* ml;      // [ctas][2][kFewRows]: maximum (log2 units), sum
+    int32_t* count;  // [entries][Hkv] arrivals, zero between calls
+};
+
+struct AttnArgs {
+    GraftPagedCache c;
+    const void* K;
+    const void* V;
+    const char* plan;
+    const void* Q;
+    int64_t q_stride;
+    const uint64_t* mask;
+    void* O;
+    float scale;
+    int N, Hq, G, max_new, page_shift;
+    PlanShape shape;
+    FewWs few;
+};
+
+int few_launch(const AttnArgs& a, cudaStream_t st);
+
+// Is the plan one for these arguments?  (The lengths and row counts in it were checked when it was made.)
+__device__ __forceinline__ bool plan_fits(const AttnArgs& a, const PlanHead& h) {
+    return h.magic == kPlanMagic && h.N == a.N && h.Hq == a.Hq && h.Hkv == a.c.Hkv && h.n_seqs == a.c.n_seqs &&
+           h.max_new == a.max_new && h.tree == (a.mask != nullptr) && h.page_rows == a.c.page_rows &&
+           h.max_pages == a.c.max_pages && h.num_pages == a.c.num_pages && h.few_rows == a.shape.few_rows &&
+           h.ctas == a.shape.ctas;
+}
+
+// ---------------------------------------------------------------- element types
+template <int DT>
+struct Elem;
+template <>
+struct Elem<GRAFT_BF16> {
+    using T = __nv_bfloat16;
+    using T2 = __nv_bfloat162;
+    static __device__ __forceinline__ float2 up(uint32_t w) {
+        return __bfloat1622float2(*reinterpret_cast<const T2*>(&w));
+    }
+    static __device__ __forceinline__ uint32_t down(float x, float y) {
+        const T2 v = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    // either half of the pair is infinite or NaN: its exponent bits are all set
+    static __device__ __forceinline__ bool odd(uint32_t w) {
+        return ((w & 0x7f80u) == 0x7f80u) || ((w & 0x7f800000u) == 0x7f800000u);
+    }
+};
+template <>
+struct Elem<GRAFT_FP16> {
+    using T = __half;
+    using T2 = __half2;
+    static __device__ __forceinline__ float2 up(uint32_t w) { return __half22float2(*reinterpret_cast<const T2*>(&w)); }
+    static __device__ __forceinline__ uint32_t down(float x, float y) {
+        const T2 v = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    static __device__ __forceinline__ bool odd(uint32_t w) {
+        return ((w & 0x7c00u) == 0x7c00u) || ((w & 0x7c000000u) == 0x7c000000u);
+    }
+};
+
+}  // namespace paged
+}  // namespace graft

@@ -1,0 +1,507 @@
+// Attention of a few query rows a KV head over a paged cache: single tokens,
+// short chunks and small trees (new rows x group up to 16 or 32 at a time).
+//
+//   o = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),  s_j = scale log2(e) q.k_j
+//
+// with a running maximum m and sum (one pass over the keys).  Such calls read
+// 512 bytes of K and V a key and head for at most 32 rows' products, so HBM
+// bounds them; the work is split by keys, evenly over the CTAs, whatever the
+// sequences' lengths: the plan lays the 16-key units of all (entry, KV head)
+// items side by side and gives every CTA an equal run of them.  Within a run
+// each warp takes every kWarps-th unit, streams it through its own ring of
+// kStages units in shared memory with cp.async (no CTA barrier inside a run:
+// a warp waits for its own copies alone), and keeps its rows' O in registers
+// (mma.sync m16n8k16, 32-bit accumulators: 16 rows are too few to fill a
+// tcgen05 tile, and the products take a quarter of the time the bytes do).
+// A page row index costs a lookup per unit; a lane holds one, 32 units ahead.
+//
+// Items that a run's edges cut are joined by the CTA that arrives last (a
+// counter an item): it reads the pieces' 32-bit partial rows in their order,
+// so the result does not depend on which CTA that is.
+#include <cmath>
+
+#include "paged.cuh"
+
+namespace graft {
+namespace paged {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 3;
+constexpr int kUnit = 16;                          // keys of a unit
+constexpr int kUnitBytes = kUnit * HD * 2;         // of K, or of V
+constexpr int kRowPad = 132;                       // floats of a staged partial row: 4 banks apart
+constexpr int kRing = kWarps * kStages * 2 * kUnitBytes;
+
+constexpr int smem_bytes(int RT) {
+    const int merge = kWarps * RT * 16 * kRowPad * 4;
+    return (kRing > merge ? kRing : merge) + kWarps * RT * 16 * 8 + 16;
+}
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// byte offset of 16-byte chunk ch (0..15) of row r in a [rows][128] 16-bit tile
+__device__ __forceinline__ uint32_t swz(int r, int ch) { return (uint32_t)(r * (HD * 2) + ((ch ^ (r & 7)) << 4)); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+    const int n = valid ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr)
+                 : "memory");
+}
+template <int DT>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    if (DT == GRAFT_BF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};\n"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};\n"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float safe(float m) { return m == -INFINITY ? 0.f : m; }
+// Weights are 2^(s - m + lift).  fp16 reaches down to 2^-24 only: lifted by 2^7 the small weights of a long
+// context keep their bits (and the largest, 2^(8 + 7), still fits); sums and O carry the same factor.
+template <int DT>
+constexpr float kLift = DT == GRAFT_FP16 ? 7.f : 0.f;
+
+// RT: 16-row tiles a warp holds.
+template <int DT, int RT>
+__global__ void __launch_bounds__(kThreads, 2)
+few_kernel(const __grid_constant__ AttnArgs a) {
+    using E = Elem<DT>;
+    using T = typename E::T;
+    extern __shared__ __align__(128) unsigned char smem[];
+    griddep_enter();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const PlanHead& head = *reinterpret_cast<const PlanHead*>(a.plan);
+    if (!plan_fits(a, head)) {
+        if (blockIdx.x == 0 && tid == 0) flag_status(a.c.status, GRAFT_STATUS_PLAN);
+        return;
+    }
+    const int ctas = head.few_ctas, cta = blockIdx.x;
+    if (cta >= ctas) return;
+    const int64_t total = head.few_units;
+    const Entry* entries = reinterpret_cast<const Entry*>(a.plan + a.shape.off_few);
+    const int64_t* prefix = reinterpret_cast<const int64_t*>(a.plan + a.shape.off_prefix);
+    const Start* starts = reinterpret_cast<const Start*>(a.plan + a.shape.off_start);
+    int64_t left = first_unit(total, ctas, cta + 1) - first_unit(total, ctas, cta);
+    Start at = starts[cta];
+
+    constexpr int kMergeBytes = kWarps * RT * 16 * kRowPad * 4;
+    float* s_part = reinterpret_cast<float*>(smem);
+    float2* s_ml = reinterpret_cast<float2*>(smem + (kRing > kMergeBytes ? kRing : kMergeBytes));
+    int* s_last = reinterpret_cast<int*>(s_ml + kWarps * RT * 16);
+    const uint32_t ring = smem_u32(smem) + warp * (kStages * 2 * kUnitBytes);
+    unsigned char* ring_p = smem + warp * (kStages * 2 * kUnitBytes);
+    const T* Kp = static_cast<const T*>(a.K);
+    const T* Vp = static_cast<const T*>(a.V);
+    const T* Qp = static_cast<const T*>(a.Q);
+    const float sl2 = a.scale * 1.4426950408889634f;
+    const int64_t key_stride = (int64_t)a.c.Hkv * HD;
+
+    while (left > 0) {
+        const Entry e = entries[at.entry];
+        const int u0 = at.unit;
+        const int u1 = (int)min((int64_t)e.units, u0 + left);
+        const int kvh = at.head;
+        const int32_t* table = a.c.block_table + (int64_t)e.b * a.c.max_pages;
+
+        // pages of this warp's next 32 units, one a lane
+        auto fetch_pages = [&](int i0) {
+            const int u = u0 + warp + (i0 + lane) * kWarps;
+            int p = -1;
+            if (u < u1) {
+                p = table[(u * kUnit) >> a.page_shift];
+                if (p < 0 || p >= a.c.num_pages) {
+                    p = -1;
+                    flag_status(a.c.status, GRAFT_STATUS_PAGE);
+                }
+            }
+            return p;
+        };
+        const int mine = (u1 - u0 - warp + kWarps - 1) / kWarps;  // this warp's units (may be <= 0)
+        int pages = fetch_pages(0), pages_at = 0;
+        auto load = [&](int i) {
+            if (i < mine) {
+                if (i - pages_at >= 32) {
+                    pages_at = i;
+                    pages = fetch_pages(i);
+                }
+                const int key0 = (u0 + warp + i * kWarps) * kUnit;
+                const int page = __shfl_sync(0xffffffffu, pages, i - pages_at);
+                const int64_t row = ((int64_t)max(page, 0) << a.page_shift) + (key0 & (a.c.page_rows - 1));
+                const int64_t off = (row * a.c.Hkv + kvh) * HD;
+                const uint32_t k = ring + (i % kStages) * 2 * kUnitBytes, v = k + kUnitBytes;
+#pragma unroll
+                for (int x = 0; x < kUnit * 16 / 32; ++x) {
+                    const int r = x * 2 + (lane >> 4), ch = lane & 15;
+                    const bool ok = page >= 0 && key0 + r < e.keys;
+                    const int64_t o = off + (ok ? r * key_stride : 0) + ch * 8;
+                    cp_async16(k + swz(r, ch), Kp + o, ok);
+                    cp_async16(v + swz(r, ch), Vp + o, ok);
+                }
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) load(i);
+
+        // Q fragments straight from memory; rows past the block read as zeros
+        uint32_t qf[RT][8][4];
+        int limit[RT][2];        // keys below it are seen
+        uint64_t anc[RT][2];     // new rows seen (tree)
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = t * 16 + (lane >> 2) + h * 8;
+                const bool ok = r < e.rows;
+                const int row = e.row0 + r, tok = row / a.G;
+                const int g = row - tok * a.G;
+                const T* q = Qp + (ok ? (int64_t)(e.q0 + tok) * a.q_stride + (kvh * a.G + g) * HD : 0);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const int col = kk * 16 + (lane & 3) * 2;
+                    qf[t][kk][h] = ok ? *reinterpret_cast<const uint32_t*>(q + col) : 0u;
+                    qf[t][kk][h + 2] = ok ? *reinterpret_cast<const uint32_t*>(q + col + 8) : 0u;
+                }
+                anc[t][h] = 0;
+                if (!ok) {
+                    limit[t][h] = 0;
+                } else if (a.mask != nullptr) {
+                    limit[t][h] = e.L;
+                    anc[t][h] = a.mask[e.q0 + tok];
+                } else {
+                    limit[t][h] = e.L + tok + 1;
+                }
+            }
+        float m_run[RT][2], l_run[RT][2], o[RT][16][4];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            m_run[t][0] = m_run[t][1] = -INFINITY;
+            l_run[t][0] = l_run[t][1] = 0.f;
+#pragma unroll
+            for (int d = 0; d < 16; ++d) o[t][d][0] = o[t][d][1] = o[t][d][2] = o[t][d][3] = 0.f;
+        }
+
+        for (int i = 0; i < mine; ++i) {
+            load(i + kStages - 1);
+            cp_wait<kStages - 1>();
+            __syncwarp();
+            const uint32_t tK = ring + (i % kStages) * 2 * kUnitBytes, tV = tK + kUnitBytes;
+            const int key0 = (u0 + warp + i * kWarps) * kUnit;
+            float s[RT][2][4];
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+                uint32_t b0, b1, b2, b3;
+                const int m = lane >> 3;
+                ldsm_x4(tK + swz((m >> 1) * 8 + (lane & 7), kk * 2 + (m & 1)), b0, b1, b2, b3);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    mma16816<DT>(s[t][0], qf[t][kk], b0, b1);
+                    mma16816<DT>(s[t][1], qf[t][kk], b2, b3);
+                }
+            }
+            const bool edge = key0 + kUnit > e.L;  // the unit holds new rows, or ends the keys
+            auto sees = [&](int t, int h, int key) -> bool {
+                if (key < limit[t][h]) return true;
+                const int j = key - e.L;
+                return a.mask != nullptr && j >= 0 && j < e.n && ((anc[t][h] >> j) & 1ull);
+            };
+            bool up = false;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int h = x >> 1;
+                        float v = s[t][n][x] * sl2;
+                        if (edge) v = sees(t, h, key0 + n * 8 + (lane & 3) * 2 + (x & 1)) ? v : -INFINITY;
+                        s[t][n][x] = v;
+                        up |= v > m_run[t][h] + 8.f;
+                    }
+            // the maximum moves only when a score passes it by 8 (weights stay below 2^8: 16-bit P and the
+            // 32-bit sums carry them), so most units need no row maximum and leave O alone
+            if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float mx = fmaxf(fmaxf(s[t][0][2 * h], s[t][0][2 * h + 1]),
+                                         fmaxf(s[t][1][2 * h], s[t][1][2 * h + 1]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        const float m = fmaxf(m_run[t][h], mx);
+                        const float alpha = ex2(m_run[t][h] - safe(m));
+                        m_run[t][h] = m;
+                        l_run[t][h] *= alpha;
+#pragma unroll
+                        for (int d = 0; d < 16; ++d) {
+                            o[t][d][2 * h] *= alpha;
+                            o[t][d][2 * h + 1] *= alpha;
+                        }
+                    }
+            }
+            uint32_t p[RT][4];
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float m = safe(m_run[t][h]) - kLift<DT>;
+                        const uint32_t w = E::down(ex2(s[t][n][2 * h] - m), ex2(s[t][n][2 * h + 1] - m));
+                        // the sum adds the rounded weights that the product uses: they add up to one
+                        const float2 f = E::up(w);
+                        l_run[t][h] += f.x + f.y;
+                        p[t][n * 2 + h] = w;
+                    }
+            if (edge) {
+                // A new row of V may hold infinities or NaN that some rows do not see, and 0 * NaN is NaN:
+                // such elements are added to the rows that see them and taken out of the product.
+                bool odd = false;
+#pragma unroll
+                for (int x = 0; x < kUnitBytes / 512; ++x) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(ring_p + (tV - ring) + x * 512 + lane * 16);
+                    odd |= E::odd(v.x) || E::odd(v.y) || E::odd(v.z) || E::odd(v.w);
+                }
+                if (__any_sync(0xffffffffu, odd)) {
+                    for (int key = 0; key < kUnit; ++key)
+                        for (int d = 0; d < 16; ++d) {
+                            const uint32_t w = *reinterpret_cast<const uint32_t*>(ring_p + (tV - ring) + swz(key, d) +
+                                                                                  (lane & 3) * 4);
+                            if (!E::odd(w)) continue;
+                            float2 f = E::up(w);
+                            if (isfinite(f.x)) f.x = 0.f;
+                            if (isfinite(f.y)) f.y = 0.f;
+                            for (int t = 0; t < RT; ++t)
+                                for (int h = 0; h < 2; ++h)
+                                    if (sees(t, h, key0 + key)) {
+#pragma unroll
+                                        for (int dd = 0; dd < 16; ++dd)
+                                            if (dd == d) {
+                                                o[t][dd][2 * h] += f.x;
+                                                o[t][dd][2 * h + 1] += f.y;
+                                            }
+                                    }
+                        }
+                    __syncwarp();
+                    for (int x = lane; x < kUnitBytes / 4; x += 32) {
+                        uint32_t* w = reinterpret_cast<uint32_t*>(ring_p + (tV - ring)) + x;
+                        const float2 f = E::up(*w);
+                        *w = (isfinite(f.x) ? (*w & 0xffffu) : 0u) | (isfinite(f.y) ? (*w & 0xffff0000u) : 0u);
+                    }
+                    __syncwarp();
+                }
+            }
+#pragma unroll
+            for (int dp = 0; dp < 8; ++dp) {
+                uint32_t b0, b1, b2, b3;
+                const int m = lane >> 3;
+                ldsm_x4_t(tV + swz((m & 1) * 8 + (lane & 7), dp * 2 + (m >> 1)), b0, b1, b2, b3);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    mma16816<DT>(o[t][2 * dp], p[t], b0, b1);
+                    mma16816<DT>(o[t][2 * dp + 1], p[t], b2, b3);
+                }
+            }
+            __syncwarp();
+        }
+        cp_wait<0>();
+        __syncthreads();  // every ring is free: the partial rows take its place
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                l_run[t][h] += __shfl_xor_sync(0xffffffffu, l_run[t][h], 1);
+                l_run[t][h] += __shfl_xor_sync(0xffffffffu, l_run[t][h], 2);
+                const int r = t * 16 + (lane >> 2) + h * 8;
+                if (r < e.rows) {
+                    float* dst = s_part + (warp * RT * 16 + r) * kRowPad + (lane & 3) * 2;
+#pragma unroll
+                    for (int d = 0; d < 16; ++d)
+                        *reinterpret_cast<float2*>(dst + d * 8) = make_float2(o[t][d][2 * h], o[t][d][2 * h + 1]);
+                    if ((lane & 3) == 0) s_ml[warp * RT * 16 + r] = make_float2(m_run[t][h], l_run[t][h]);
+                }
+            }
+        __syncthreads();
+
+        // joins the warps' rows; a lane takes four dims
+        auto join = [&](int r, float4& acc, float& m, float& l) {
+            m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w * RT * 16 + r].x);
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 ml = s_ml[w * RT * 16 + r];
+                if (ml.x == -INFINITY && ml.y == 0.f) continue;  // saw no key
+                const float x = ex2(ml.x - safe(m));
+                const float4 v = *reinterpret_cast<const float4*>(s_part + (w * RT * 16 + r) * kRowPad + lane * 4);
+                acc.x += x * v.x;
+                acc.y += x * v.y;
+                acc.z += x * v.z;
+                acc.w += x * v.w;
+                l += x * ml.y;
+            }
+        };
+        auto put = [&](int r, const float4& acc, float l) {
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            const int row = e.row0 + r, tok = row / a.G, g = row - tok * a.G;
+            T* dst = static_cast<T*>(a.O) + ((int64_t)(e.q0 + tok) * a.Hq + kvh * a.G + g) * HD + lane * 4;
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(E::down(acc.x * inv, acc.y * inv), E::down(acc.z * inv, acc.w * inv));
+        };
+        const int64_t g0 = prefix[at.entry] + (int64_t)kvh * e.units;
+        const int c0 = unit_cta(total, ctas, g0), c1 = unit_cta(total, ctas, g0 + e.units - 1);
+        if (c0 == c1) {
+            for (int r = warp; r < e.rows; r += kWarps) {
+                float4 acc;
+                float m, l;
+                join(r, acc, m, l);
+                put(r, acc, l);
+            }
+        } else {
+            constexpr int rows = kFewRows;
+            const int slot = cta * 2 + (cta == c0 ? 1 : 0);
+            for (int r = warp; r < e.rows; r += kWarps) {
+                float4 acc;
+                float m, l;
+                join(r, acc, m, l);
+                *reinterpret_cast<float4*>(a.few.o + ((int64_t)slot * rows + r) * HD + lane * 4) = acc;
+                if (lane == 0) a.few.ml[(int64_t)slot * rows + r] = make_float2(m, l);
+            }
+            __threadfence();
+            __syncthreads();
+            int32_t* count = a.few.count + (int64_t)at.entry * a.c.Hkv + kvh;
+            if (tid == 0) {
+                const int pieces = c1 - c0 + 1;
+                const int before = atomicAdd(count, 1);
+                if (before >= pieces) flag_status(a.c.status, GRAFT_STATUS_WORKSPACE);
+                *s_last = before == pieces - 1;
+                if (before == pieces - 1) *count = 0;
+            }
+            __syncthreads();
+            if (*s_last) {
+                __threadfence();
+                // each warp joins every kWarps-th piece, then the warps are joined as above
+                for (int r = 0; r < e.rows; ++r) {
+                    float m = -INFINITY, l = 0.f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    constexpr int kB = 8;
+                    for (int p0 = c0 + warp; p0 <= c1; p0 += kB * kWarps) {
+                        float2 ml[kB];
+                        float4 v[kB];
+#pragma unroll
+                        for (int x = 0; x < kB; ++x) {
+                            const int p = p0 + x * kWarps;
+                            ml[x] = make_float2(-INFINITY, 0.f);
+                            v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (p <= c1) {
+                                const int64_t sl = ((int64_t)p * 2 + (p == c0 ? 1 : 0)) * rows + r;
+                                ml[x] = __ldcg(a.few.ml + sl);
+                                v[x] = __ldcg(reinterpret_cast<const float4*>(a.few.o + sl * HD) + lane);
+                            }
+                        }
+                        float mx = m;
+#pragma unroll
+                        for (int x = 0; x < kB; ++x) mx = fmaxf(mx, ml[x].x);
+                        const float keep = ex2(m - safe(mx));
+                        acc.x *= keep;
+                        acc.y *= keep;
+                        acc.z *= keep;
+                        acc.w *= keep;
+                        l *= keep;
+                        m = mx;
+#pragma unroll
+                        for (int x = 0; x < kB; ++x) {
+                            if (ml[x].x == -INFINITY && ml[x].y == 0.f) continue;
+                            const float f = ex2(ml[x].x - safe(m));
+                            acc.x += f * v[x].x;
+                            acc.y += f * v[x].y;
+                            acc.z += f * v[x].z;
+                            acc.w += f * v[x].w;
+                            l += f * ml[x].y;
+                        }
+                    }
+                    *reinterpret_cast<float4*>(s_part + (warp * RT * 16 + r) * kRowPad + lane * 4) = acc;
+                    if (lane == 0) s_ml[warp * RT * 16 + r] = make_float2(m, l);
+                }
+                __syncthreads();
+                for (int r = warp; r < e.rows; r += kWarps) {
+                    float4 acc;
+                    float m, l;
+                    join(r, acc, m, l);
+                    put(r, acc, l);
+                }
+            }
+        }
+        __syncthreads();  // the staged rows are read: the next run's copies may overwrite them
+        left -= u1 - u0;
+        at.unit = 0;
+        if (u1 == e.units && ++at.head == a.c.Hkv) {
+            at.head = 0;
+            ++at.entry;
+        }
+    }
+}
+
+template <int DT, int RT>
+int launch(const AttnArgs& a, cudaStream_t st) {
+    static bool attr_set[64] = {};
+    int dev = 0;
+    if (!cuda_ok(cudaGetDevice(&dev))) return GRAFT_ERR_CUDA;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        if (!cuda_ok(cudaFuncSetAttribute(few_kernel<DT, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          smem_bytes(RT))))
+            return GRAFT_ERR_CUDA;
+        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    launch_pdl(few_kernel<DT, RT>, dim3(a.shape.ctas), dim3(kThreads), smem_bytes(RT), st, a);
+    count_launches(1);
+    return launch_status();
+}
+
+}  // namespace
+
+int few_launch(const AttnArgs& a, cudaStream_t st) {
+    const bool one = a.shape.few_rows == 16;
+    if (a.c.dtype == GRAFT_BF16) return one ? launch<GRAFT_BF16, 1>(a, st) : launch<GRAFT_BF16, 2>(a, st);
+    return one ? launch<GRAFT_FP16, 1>(a, st) : launch<GRAFT_FP16, 2>(a, st);
+}
+
+}  // namespace paged
+}  // namespace graft

@@ -1,0 +1,331 @@
+// Rotary positions of Q and K, and the new K and V rows into their pages.
+//
+// Pair (x, y) of a head turns by a = position * w:
+//   x' = f (x cos a - y sin a),  y' = f (x sin a + y cos a).
+// Far positions: a's whole turns are dropped exactly.  w / 2 pi is held as a
+// 64-bit fraction of a turn, W = round(w / 2 pi * 2^64); position * W modulo
+// 2^64 is then the fraction of the turn itself (whole turns overflow away),
+// off by at most |position| / 2^65 turns plus w's own 64-bit rounding, and
+// its upper 32 bits go to sincospi.  No 64-bit floating product a position.
+//
+// Memory bound: every element is read and written once.  A CTA takes
+// kTokens rows with all their heads, so a row's cosines are computed once
+// and serve Hq + Hkv heads; each thread's loads (32 bytes a unit: the two
+// 16-byte chunks whose dims pair up) are issued before the CTA looks up the
+// sequences and pages, so the look-up's three dependent reads run behind them.
+#include <cmath>
+
+#include "paged.cuh"
+
+namespace graft {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTokens = 2;
+constexpr int kAhead = 3;  // units a thread loads before the look-up
+
+struct RopeArgs {
+    GraftPagedCache c;
+    uint4* K_pool;
+    uint4* V_pool;
+    const int32_t* q_start;
+    const int32_t* pos;
+    const double* inv_freq;
+    const uint4* Q;
+    const uint4* K;
+    const uint4* V;
+    uint4* Q_out;
+    int64_t qs, ks, vs, qos;  // row strides in 16-byte chunks
+    int N, Hq, rot, page_shift;
+    bool inter;
+    float factor;
+};
+
+// Last b with q_start[b] <= row, by a warp: 32 probes at a time.
+__device__ __forceinline__ int find_seq(const int32_t* q_start, int n, int row) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = n + 1;  // answer in [lo, lo + len), or -1
+    while (len > 1) {
+        const int step = (len + 31) / 32;
+        const int at = lo + lane * step;
+        const bool le = lane * step < len && q_start[at] <= row;
+        const unsigned m = __ballot_sync(0xffffffffu, le);
+        if (m == 0) return -1;
+        const int hit = 31 - __clz(m);
+        len = min(step, len - hit * step);
+        lo += hit * step;
+        if (step == 1) break;
+    }
+    return lo;
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t turn2(uint32_t a, uint32_t& b, float2 cs0, float2 cs1) {
+    using E = Elem<DT>;
+    const float2 x = E::up(a), y = E::up(b);
+    b = E::down(x.x * cs0.y + y.x * cs0.x, x.y * cs1.y + y.y * cs1.x);
+    return E::down(x.x * cs0.x - y.x * cs0.y, x.y * cs1.x - y.y * cs1.y);
+}
+template <int DT>
+__device__ __forceinline__ uint32_t turn1(uint32_t a, float2 cs) {
+    using E = Elem<DT>;
+    const float2 x = E::up(a);
+    return E::down(x.x * cs.x - x.y * cs.y, x.x * cs.y + x.y * cs.x);
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads)
+rope_append_kernel(const __grid_constant__ RopeArgs a) {
+    __shared__ float2 s_cs[kTokens][HD / 2];
+    __shared__ int64_t s_dst[kTokens];  // cache row in the pool, -1: not written
+    __shared__ int s_live[kTokens], s_pos[kTokens];
+    griddep_enter();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int t0 = blockIdx.x * kTokens;
+    const int nt = min(kTokens, a.N - t0);
+    const int heads = a.Hq + 2 * a.c.Hkv;
+    const int units = nt * heads * 8;  // a head is 8 units of two 16-byte chunks
+    const int rot_units = a.rot / 16;
+
+    // unit -> its token, head, source and two chunks
+    struct Unit {
+        int t, h, c0, c1;
+        const uint4* src;
+    };
+    auto unit_of = [&](int u) {
+        Unit x;
+        const int i = u & 7;
+        const int th = u >> 3;
+        x.t = th / heads;
+        x.h = th - x.t * heads;
+        // rotated units of the half layout pair chunk i with chunk i + rot / 16
+        const bool half = !a.inter && i < rot_units && x.h < a.Hq + a.c.Hkv;
+        x.c0 = half ? i : 2 * i;
+        x.c1 = half ? i + rot_units : 2 * i + 1;
+        const int64_t row = t0 + x.t;
+        if (x.h < a.Hq)
+            x.src = a.Q + row * a.qs + x.h * 16;
+        else if (x.h < a.Hq + a.c.Hkv)
+            x.src = a.K + row * a.ks + (x.h - a.Hq) * 16;
+        else
+            x.src = a.V + row * a.vs + (x.h - a.Hq - a.c.Hkv) * 16;
+        return x;
+    };
+    uint4 buf[kAhead][2];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const int u = tid + k * kThreads;
+        if (u < units) {
+            const Unit x = unit_of(u);
+            buf[k][0] = x.src[x.c0];
+            buf[k][1] = x.src[x.c1];
+        }
+    }
+    if (warp < nt) {
+        const int row = t0 + warp;
+        const int b = find_seq(a.q_start, a.c.n_seqs, row);
+        const bool live = b >= 0 && b < a.c.n_seqs && row < a.q_start[b + 1];
+        if (lane == 0) {
+            int64_t dst = -1;
+            int pos = 0;
+            if (live) {
+                const int L = a.c.lengths[b];
+                const int64_t r = (int64_t)L + (row - a.q_start[b]);
+                pos = a.pos != nullptr ? a.pos[row] : (int)r;
+                if (L < 0 || (r >> a.page_shift) >= a.c.max_pages) {
+                    flag_status(a.c.status, GRAFT_STATUS_LENGTH);
+                } else {
+                    const int page = a.c.block_table[(int64_t)b * a.c.max_pages + (r >> a.page_shift)];
+                    if (page < 0 || page >= a.c.num_pages)
+                        flag_status(a.c.status, GRAFT_STATUS_PAGE);
+                    else
+                        dst = ((int64_t)page << a.page_shift) + (r & (a.c.page_rows - 1));
+                }
+            }
+            s_live[warp] = live;
+            s_pos[warp] = pos;
+            s_dst[warp] = dst;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < nt * (a.rot / 2); i += kThreads) {
+        const int t = i / (a.rot / 2), p = i - t * (a.rot / 2);
+        // 2^64 / 2 pi; a frequency of a turn or more per position keeps only its fraction
+        const double turns = a.inv_freq[p] * 0.15915494309189533577;
+        const uint64_t w = (uint64_t)__double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+        const uint64_t f = w * (uint64_t)(int64_t)s_pos[t];
+        float s, c;
+        sincospif((float)(int32_t)(f >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+        s_cs[t][p] = make_float2(c * a.factor, s * a.factor);
+    }
+    __syncthreads();
+    auto finish = [&](int u, uint4 x0, uint4 x1) {
+        const Unit x = unit_of(u);
+        if (!s_live[x.t]) return;
+        const int i = u & 7;
+        if (i < rot_units && x.h < a.Hq + a.c.Hkv) {
+            if (a.inter) {
+                const float4* cs = reinterpret_cast<const float4*>(&s_cs[x.t][i * 8]);
+                uint32_t* w0 = &x0.x;
+                uint32_t* w1 = &x1.x;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float4 p = cs[k], q = cs[k + 2];
+                    w0[2 * k] = turn1<DT>(w0[2 * k], make_float2(p.x, p.y));
+                    w0[2 * k + 1] = turn1<DT>(w0[2 * k + 1], make_float2(p.z, p.w));
+                    w1[2 * k] = turn1<DT>(w1[2 * k], make_float2(q.x, q.y));
+                    w1[2 * k + 1] = turn1<DT>(w1[2 * k + 1], make_float2(q.z, q.w));
+                }
+            } else {
+                const float4* cs = reinterpret_cast<const float4*>(&s_cs[x.t][i * 8]);
+                uint32_t* w0 = &x0.x;
+                uint32_t* w1 = &x1.x;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float4 p = cs[k];
+                    w0[k] = turn2<DT>(w0[k], w1[k], make_float2(p.x, p.y), make_float2(p.z, p.w));
+                }
+            }
+        }
+        uint4* dst;
+        if (x.h < a.Hq) {
+            dst = a.Q_out + (int64_t)(t0 + x.t) * a.qos + x.h * 16;
+        } else {
+            if (s_dst[x.t] < 0) return;
+            const bool k = x.h < a.Hq + a.c.Hkv;
+            dst = (k ? a.K_pool : a.V_pool) +
+                  (s_dst[x.t] * a.c.Hkv + (x.h - a.Hq - (k ? 0 : a.c.Hkv))) * 16;
+        }
+        dst[x.c0] = x0;
+        dst[x.c1] = x1;
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const int u = tid + k * kThreads;
+        if (u < units) finish(u, buf[k][0], buf[k][1]);
+    }
+    for (int u = tid + kAhead * kThreads; u < units; u += kThreads) {
+        const Unit x = unit_of(u);
+        finish(u, x.src[x.c0], x.src[x.c1]);
+    }
+}
+
+}  // namespace
+
+int check_cache(const GraftPagedCache* c) {
+    if (c == nullptr) return GRAFT_ERR_INVALID_ARG;
+    if (c->dtype != GRAFT_BF16 && c->dtype != GRAFT_FP16) return GRAFT_ERR_INVALID_ARG;
+    if (c->Hkv < 1 || c->num_pages < 1 || c->n_seqs < 1 || c->max_pages < 1 || c->n_layers < 0)
+        return GRAFT_ERR_INVALID_ARG;
+    if (c->head_dim != HD || c->Hkv > 1024) return GRAFT_ERR_UNSUPPORTED_SHAPE;
+    const int p = c->page_rows;
+    if (p < 16 || p > GRAFT_MAX_PAGE_ROWS || (p & (p - 1)) != 0) return GRAFT_ERR_UNSUPPORTED_SHAPE;
+    if (c->n_seqs > GRAFT_MAX_SEQS || c->n_layers > 16384) return GRAFT_ERR_UNSUPPORTED_SHAPE;
+    if ((int64_t)c->num_pages * p >= (1LL << 31) || (int64_t)c->max_pages * p >= (1LL << 31) ||
+        (int64_t)c->n_seqs * c->max_pages >= (1LL << 31))
+        return GRAFT_ERR_UNSUPPORTED_SHAPE;
+    if (c->block_table == nullptr || c->lengths == nullptr) return GRAFT_ERR_INVALID_ARG;
+    return GRAFT_OK;
+}
+
+int check_tables(const GraftPagedCache* c) {
+    const int rc = check_cache(c);
+    if (rc != GRAFT_OK) return rc;
+    if (c->held == nullptr || c->page_refs == nullptr) return GRAFT_ERR_INVALID_ARG;
+    return GRAFT_OK;
+}
+
+}  // namespace paged
+}  // namespace graft
+
+using namespace graft;
+using namespace graft::paged;
+
+extern "C" int graft_rope_inv_freq(int rot_dim, double base, int scaling, double stretch, double low, double high,
+                                   double original, double* out, float* factor) {
+    if (out == nullptr || rot_dim < 2 || rot_dim % 2 != 0 || !(base > 0.0) || !std::isfinite(base) || scaling < 0 ||
+        scaling > 3)
+        return GRAFT_ERR_INVALID_ARG;
+    if (rot_dim > HD) return GRAFT_ERR_UNSUPPORTED_SHAPE;
+    if (scaling != 0 && (!(stretch > 0.0) || !std::isfinite(stretch))) return GRAFT_ERR_INVALID_ARG;
+    if (scaling >= 2 && (!(low > 0.0) || !(high > low) || !(original > 0.0) || !std::isfinite(high) ||
+                         !std::isfinite(original)))
+        return GRAFT_ERR_INVALID_ARG;
+    if (scaling == 3 && base == 1.0) return GRAFT_ERR_INVALID_ARG;  // every pair turns alike: no ramp
+    const double two_pi = 6.283185307179586477;
+    double ramp_low = 0, ramp_high = 1;
+    if (scaling == 3) {
+        // the pair index at which a pair turns r times in the original context
+        auto at = [&](double r) { return rot_dim * std::log(original / (two_pi * r)) / (2 * std::log(base)); };
+        ramp_low = std::fmax(std::floor(at(high)), 0.0);
+        ramp_high = std::fmin(std::ceil(at(low)), (double)(rot_dim - 1));
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double w = std::pow(base, -2.0 * i / rot_dim);
+        if (scaling == 1) {
+            w /= stretch;
+        } else if (scaling == 2) {
+            const double wave = two_pi / w;
+            const double keep = std::fmin(std::fmax((original / wave - low) / (high - low), 0.0), 1.0);
+            w = (1 - keep) * w / stretch + keep * w;
+        } else if (scaling == 3) {
+            const double ramp =
+                std::fmin(std::fmax((i - ramp_low) / std::fmax(ramp_high - ramp_low, 1e-3), 0.0), 1.0);
+            w = w * (1 - ramp) + w / stretch * ramp;
+        }
+        out[i] = w;
+    }
+    if (factor != nullptr) *factor = scaling == 3 ? (float)(0.1 * std::log(stretch) + 1.0) : 1.f;
+    return GRAFT_OK;
+}
+
+extern "C" int graft_rope_append(const GraftPagedCache* cache, void* K_pool, void* V_pool, int N, int Hq,
+                                 const int32_t* q_start, const int32_t* pos, const double* inv_freq, int rot_dim,
+                                 int interleaved, float factor, const void* Q, int64_t q_stride, const void* K,
+                                 int64_t k_stride, const void* V, int64_t v_stride, void* Q_out, int64_t qo_stride,
+                                 graft_stream_t stream) {
+    const int rc = check_cache(cache);
+    if (rc != GRAFT_OK) return rc;
+    if (N < 0 || Hq < 0) return GRAFT_ERR_INVALID_ARG;
+    if (Hq > 8192) return GRAFT_ERR_UNSUPPORTED_SHAPE;
+    if (rot_dim < 0 || rot_dim > HD || rot_dim % 16 != 0) return GRAFT_ERR_UNSUPPORTED_SHAPE;
+    if (N == 0) return GRAFT_OK;
+    if (q_start == nullptr || K == nullptr || V == nullptr || K_pool == nullptr || V_pool == nullptr)
+        return GRAFT_ERR_INVALID_ARG;
+    if (Hq > 0 && (Q == nullptr || Q_out == nullptr)) return GRAFT_ERR_INVALID_ARG;
+    if (rot_dim > 0 && inv_freq == nullptr) return GRAFT_ERR_INVALID_ARG;
+    if (!(aligned16(Q) && aligned16(K) && aligned16(V) && aligned16(Q_out) && aligned16(K_pool) && aligned16(V_pool)))
+        return GRAFT_ERR_INVALID_ARG;
+    if (k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride < (int64_t)cache->Hkv * HD ||
+        v_stride < (int64_t)cache->Hkv * HD)
+        return GRAFT_ERR_INVALID_ARG;
+    if (Hq > 0 && (q_stride % 8 != 0 || qo_stride % 8 != 0 || q_stride < (int64_t)Hq * HD || qo_stride < (int64_t)Hq * HD))
+        return GRAFT_ERR_INVALID_ARG;
+    RopeArgs a{};
+    a.c = *cache;
+    a.K_pool = static_cast<uint4*>(K_pool);
+    a.V_pool = static_cast<uint4*>(V_pool);
+    a.q_start = q_start;
+    a.pos = pos;
+    a.inv_freq = inv_freq;
+    a.Q = static_cast<const uint4*>(Q);
+    a.K = static_cast<const uint4*>(K);
+    a.V = static_cast<const uint4*>(V);
+    a.Q_out = static_cast<uint4*>(Q_out);
+    a.qs = q_stride / 8;
+    a.ks = k_stride / 8;
+    a.vs = v_stride / 8;
+    a.qos = qo_stride / 8;
+    a.N = N;
+    a.Hq = Hq;
+    a.rot = rot_dim;
+    a.page_shift = log2_exact(cache->page_rows);
+    a.inter = interleaved != 0;
+    a.factor = factor;
+    const dim3 grid((unsigned)((N + kTokens - 1) / kTokens));
+    const auto kernel = cache->dtype == GRAFT_BF16 ? rope_append_kernel<GRAFT_BF16> : rope_append_kernel<GRAFT_FP16>;
+    launch_pdl(kernel, grid, dim3(kThreads), 0, (cudaStream_t)stream, a);
+    count_launches(1);
+    return launch_status();
+}
