@@ -586,7 +586,7 @@ int graft_paged_plan(const GraftPagedCache* cache, int N, int Hq, const int32_t*
  * its pages, for one layer; the new rows' own K and V are in the pages
  * already (graft_rope_append).
  *   Q [N][Hq][128] rows q_stride elements apart (a multiple of 8), O
- *   [N][Hq][128] dense; 16-byte aligned
+ *   [N][Hq][128] dense; 16-byte aligned (O: 32)
  *   mask  NULL: causal, the i-th new row sees cache rows 0 .. lengths[b] + i;
  *         else [N] u64: it sees cache rows 0 .. lengths[b] - 1 and new row j
  *         where bit j of mask[row] is set (graft_build_tree's tree_mask for

@@ -366,11 +366,16 @@ def test_host_refusals_of_the_handle():
     c.held = None
     with pytest.raises(ValueError):
         c.free(s.lengths)
-    # a buffer that would have to grow while a graph is being captured
+    # a buffer that would have to grow while a graph is being captured (two sequences of at most two rows never
+    # need one, whatever N: the premise is checked first)
+    import ctypes
+    n = ctypes.c_size_t()
+    assert gb().lib().graft_paged_plan_size(c._c, 100000, 8, 100000, ctypes.byref(n)) == 0
+    assert n.value > c._buffers["plan"].numel()
     g = torch.cuda.CUDAGraph()
     with pytest.raises(ValueError):
         with torch.cuda.graph(g):
-            c.plan(s.q_start, 100000, 8, 2)
+            c.plan(s.q_start, 100000, 8, 100000)
     torch.cuda.synchronize()
 
 

@@ -25,14 +25,18 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // ---------------------------------------------------------------- the attention plan
 // A work item of the attention is one entry (a block of query rows of one sequence) and one KV head,
 // against a range of keys.  The plan is one buffer:
-//   PlanHead | few entries | their unit prefix sums | the CTAs' first units
-// "Few" entries go to the kernel of paged_few.cu: at most `few_rows` query rows (new rows x group).
+//   PlanHead | few entries | their unit prefix sums | the CTAs' first units | wide entries, unsorted | wide
+//   entries | split row blocks
+// "Few" entries (paged_few.cu): sequences of at most few_rows query rows (new rows x group).  "Wide" ones
+// (paged_wide.cu): all others, in blocks of two tiles of tile_tokens new rows.
 struct PlanHead {
     int32_t magic, N, Hq, Hkv, n_seqs, max_new, tree, page_rows, max_pages, num_pages, few_rows, ctas;
     int32_t n_few;       // few entries
     int32_t few_ctas;    // CTAs that share them
     int64_t few_units;   // 16-key units over entries and heads
-    int32_t reserved[16];
+    int32_t n_wide;      // wide entries
+    int32_t n_groups;    // row blocks split by keys
+    int32_t reserved[14];
 };
 constexpr int32_t kPlanMagic = 0x47503033;
 
@@ -46,6 +50,22 @@ struct Entry {
     int32_t units;   // of 16 keys
 };
 
+constexpr int kBlockKeys = 128;
+
+struct Wide {
+    int32_t b, q0, n, L;  // sequence, its first new row, new rows, rows before them
+    int32_t tok0;         // first new row of the block
+    int32_t two;          // the block has a second tile
+    int32_t blk0, nblk;   // range of 128-key blocks
+    int32_t keys;         // keys that any row of the block may see
+    int32_t part;         // partial rows of the range (x Hkv, + KV head), -1: the rows are written to O
+    int32_t pad[2];
+};
+
+struct Group {
+    int32_t q0, n, tok0, ranges, part0, pad[3];
+};
+
 struct Start {
     int32_t entry, head, unit, pad;
 };
@@ -54,7 +74,13 @@ struct PlanShape {
     int max_few;   // bound on the few entries
     int ctas;      // CTAs of the few kernel at most
     int few_rows;  // query rows of a few entry at most (16 or 32)
-    size_t off_few, off_prefix, off_start, bytes;
+    int few, wide; // whether the calls launch either kernel
+    int sms;
+    int tile_tokens;  // new rows of a 128-row tile
+    int max_pairs;    // bound on the wide row blocks
+    int max_wide;     // bound on the wide entries
+    int max_groups;   // bound on the split row blocks, 0: nothing is split
+    size_t off_few, off_prefix, off_start, off_pairs, off_wide, off_group, bytes;
 };
 
 // CTA k of `ctas` takes units [first_unit(k), first_unit(k + 1)).
@@ -93,8 +119,11 @@ struct AttnArgs {
     int N, Hq, G, max_new, page_shift;
     PlanShape shape;
     FewWs few;
+    float* wide_o;    // [partial row blocks][2][128][128] normalised
+    float* wide_lse;  // [partial row blocks][2][128] log2-sum-exp
 };
 
+int wide_launch(const AttnArgs& a, cudaStream_t st);
 int few_launch(const AttnArgs& a, cudaStream_t st);
 
 // Is the plan one for these arguments?  (The lengths and row counts in it were checked when it was made.)

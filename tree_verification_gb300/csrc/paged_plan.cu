@@ -11,6 +11,7 @@ namespace paged {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = 1024;  // of wide entries by their blocks
 
 template <class T>
 __device__ __forceinline__ T scan_block(T v, T* s_warp, T* total) {
@@ -43,15 +44,23 @@ __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int32_t* __restrict__ q_start, int max_new,
             int tree, char* plan, PlanShape shape) {
     __shared__ int64_t s_warp[32];
+    __shared__ int s_hist[kBuckets];
+    __shared__ int s_max;
     griddep_enter();
     const int tid = threadIdx.x, G = Hq / c.Hkv;
     Entry* few = reinterpret_cast<Entry*>(plan + shape.off_few);
     int64_t* prefix = reinterpret_cast<int64_t*>(plan + shape.off_prefix);
     Start* start = reinterpret_cast<Start*>(plan + shape.off_start);
-    int n_few = 0;
+    Wide* pairs = reinterpret_cast<Wide*>(plan + shape.off_pairs);
+    Wide* wide = reinterpret_cast<Wide*>(plan + shape.off_wide);
+    Group* groups = reinterpret_cast<Group*>(plan + shape.off_group);
+    const int pair = 2 * shape.tile_tokens;
+    int n_few = 0, n_pairs = 0;
+    if (tid == 0) s_max = 1;
+    s_hist[tid] = 0;
     for (int b0 = 0; b0 < c.n_seqs; b0 += kPlanThreads) {
         const int b = b0 + tid;
-        int q0 = 0, n = 0, L = 0, count = 0;
+        int q0 = 0, n = 0, L = 0, count = 0, wcount = 0;
         if (b < c.n_seqs) {
             q0 = q_start[b];
             const int64_t q1 = q_start[b + 1];
@@ -62,32 +71,111 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
                 flag_status(c.status, GRAFT_STATUS_LENGTH);
             } else {
                 n = (int)rows;
-                count = (n * G + shape.few_rows - 1) / shape.few_rows;
+                if (n > 0 && shape.few && (n * G <= shape.few_rows || !shape.wide))
+                    count = 1;
+                else
+                    wcount = (n + pair - 1) / pair;
             }
         }
+        // (sequences that do not overlap have at most max_few and max_pairs blocks; starts that do not rise
+        // could claim more, and those are left out)
         int64_t total;
         int64_t at = n_few + scan_block<int64_t>(count, s_warp, &total);
-        // (sequences that do not overlap have at most shape.max_few blocks; starts that do not rise could
-        // claim more, and those are left out)
-        for (int j = 0; j < count; ++j, ++at) {
+        if (count > 0) {
             if (at >= shape.max_few) {
+                flag_status(c.status, GRAFT_STATUS_LENGTH);
+            } else {
+                Entry e;
+                e.b = b;
+                e.q0 = q0;
+                e.n = n;
+                e.L = L;
+                e.row0 = 0;
+                e.rows = n * G;
+                e.keys = L + n;
+                e.units = (e.keys + 15) / 16;
+                few[at] = e;
+            }
+        }
+        n_few = (int)min((int64_t)shape.max_few, n_few + total);
+        if (!shape.wide) continue;
+        at = n_pairs + scan_block<int64_t>(wcount, s_warp, &total);
+        int most = 1;
+        for (int j = 0; j < wcount; ++j, ++at) {
+            if (at >= shape.max_pairs) {
                 flag_status(c.status, GRAFT_STATUS_LENGTH);
                 break;
             }
-            Entry e;
-            e.b = b;
-            e.q0 = q0;
-            e.n = n;
-            e.L = L;
-            e.row0 = j * shape.few_rows;
-            e.rows = min(n * G - e.row0, shape.few_rows);
-            e.keys = tree ? L + n : L + (e.row0 + e.rows - 1) / G + 1;
-            e.units = (e.keys + 15) / 16;
-            few[at] = e;
+            Wide w{};
+            w.b = b;
+            w.q0 = q0;
+            w.n = n;
+            w.L = L;
+            w.tok0 = j * pair;
+            w.two = n - w.tok0 > shape.tile_tokens;
+            w.keys = tree ? L + n : L + min(w.tok0 + pair, n);
+            w.nblk = (w.keys + kBlockKeys - 1) / kBlockKeys;
+            w.part = -1;
+            pairs[at] = w;
+            most = max(most, w.nblk);
         }
-        n_few = (int)min((int64_t)shape.max_few, n_few + total);
+        if (wcount > 0) atomicMax(&s_max, most);
+        n_pairs = (int)min((int64_t)shape.max_pairs, n_pairs + total);
     }
     __syncthreads();
+    // ---- wide entries: split by keys where they would leave SMs without work, else sorted, longest first
+    int n_wide = n_pairs, n_groups = 0;
+    if (n_pairs > 0 && shape.max_groups > 0 && n_pairs * c.Hkv < shape.sms) {
+        int64_t blocks;
+        const int mine = tid < n_pairs ? pairs[tid].nblk : 0;
+        scan_block<int64_t>(mine, s_warp, &blocks);
+        // the shortest range (two blocks at least) at which the items fit one wave: the even share, unless
+        // rounding up makes too many; then by halving between it and one range a row block
+        const int slots = shape.sms / c.Hkv;
+        int len = (int)max((int64_t)2, (blocks + slots - 1) / slots), most = max(s_max, len);
+        int64_t items, first;
+        for (int lo = len;;) {
+            first = scan_block<int64_t>((mine + len - 1) / len, s_warp, &items);
+            if (items > slots) {
+                lo = len + 1;
+            } else {
+                if (len == lo) break;
+                most = len;
+            }
+            len = (lo + most) / 2;
+        }
+        int64_t splits, split_parts;
+        const int ranges = (mine + len - 1) / len;
+        const int64_t group = scan_block<int64_t>(ranges > 1, s_warp, &splits);
+        const int64_t part = scan_block<int64_t>(ranges > 1 ? ranges : 0, s_warp, &split_parts);
+        if (ranges > 0) {
+            Wide w = pairs[tid];
+            const int nblk = w.nblk, each = nblk / ranges, left = nblk % ranges;
+            if (ranges > 1)
+                groups[group] = Group{w.q0, w.n, w.tok0, ranges, (int)part * c.Hkv, {0, 0, 0}};
+            for (int j = 0; j < ranges; ++j) {
+                w.blk0 = each * j + min(j, left);
+                w.nblk = each + (j < left);
+                w.part = ranges > 1 ? (int)(part + j) * c.Hkv : -1;
+                wide[first + j] = w;
+            }
+        }
+        n_wide = (int)items;
+        n_groups = (int)splits;
+    } else if (n_pairs > 0) {
+        const int64_t most = s_max;
+        auto bucket = [&](int nblk) { return (int)(((most - nblk) * (kBuckets - 1)) / most); };
+        for (int e = tid; e < n_pairs; e += kPlanThreads) atomicAdd(&s_hist[bucket(pairs[e].nblk)], 1);
+        __syncthreads();
+        int64_t total;
+        const int before = (int)scan_block<int64_t>(s_hist[tid], s_warp, &total);
+        s_hist[tid] = before;
+        __syncthreads();
+        for (int e = tid; e < n_pairs; e += kPlanThreads) {
+            const Wide w = pairs[e];
+            wide[atomicAdd(&s_hist[bucket(w.nblk)], 1)] = w;
+        }
+    }
     int64_t units = 0;
     for (int e0 = 0; e0 < n_few; e0 += kPlanThreads) {
         const int e = e0 + tid;
@@ -135,6 +223,8 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
         h.n_few = n_few;
         h.few_ctas = ctas;
         h.few_units = units;
+        h.n_wide = n_wide;
+        h.n_groups = n_groups;
         *reinterpret_cast<PlanHead*>(plan) = h;
     }
 }
@@ -148,12 +238,21 @@ int check_attention(const GraftPagedCache* c, int N, int Hq, int max_new) {
     return GRAFT_OK;
 }
 
-FewWs carve_few(WsCarver& w, const GraftPagedCache* c, const PlanShape& s) {
+// Partial rows first, in sizes of the device's alone, then the counters (see FewWs).  Split row blocks have at
+// most one range a slot of the wave, and one more a block.
+void carve(WsCarver& w, const GraftPagedCache* c, const PlanShape& s, AttnArgs* a) {
     FewWs f;
     f.o = w.take<float>((size_t)s.ctas * 2 * kFewRows * HD);
     f.ml = w.take<float2>((size_t)s.ctas * 2 * kFewRows);
+    const size_t parts = (size_t)s.sms * 2;
+    float* wo = w.take<float>(parts * 2 * 128 * HD);
+    float* wl = w.take<float>(parts * 2 * 128);
     f.count = w.take<int32_t>((size_t)s.max_few * c->Hkv);
-    return f;
+    if (a != nullptr) {
+        a->few = f;
+        a->wide_o = wo;
+        a->wide_lse = wl;
+    }
 }
 
 }  // namespace
@@ -164,14 +263,29 @@ PlanShape plan_shape(const GraftPagedCache* c, int N, int Hq, int max_new) {
     int sms = device_sm_count();
     if (sms <= 0) sms = 148;
     s.ctas = 2 * sms;
+    s.sms = sms;
     s.few_rows = (int64_t)max_new * G <= 16 ? 16 : 32;
+    // Up to 32 query rows the few kernel reads K and V at HBM speed; past that its products take longer than
+    // the bytes.  A step whose rows are all taken by full sequences (N = n_seqs x max_new) has no short ones.
+    s.wide = (int64_t)max_new * G > kFewRows;
+    s.few = !s.wide || (int64_t)N < (int64_t)c->n_seqs * max_new;
+    s.tile_tokens = 128 / G;
     // sequences with rows: at most n_seqs and at most N; each ends in at most one block that is not full
     const int64_t seqs = c->n_seqs < N ? c->n_seqs : N;
-    s.max_few = (int)(((int64_t)N * G) / s.few_rows + seqs);
+    s.max_few = s.few ? (int)seqs : 0;
+    const int full_pairs = N / (2 * s.tile_tokens);
+    s.max_pairs = s.wide ? (int)(full_pairs + seqs) : 0;
+    // where even the full row blocks fill the SMs nothing is split
+    const bool split = s.wide && (int64_t)full_pairs * c->Hkv < sms;
+    s.max_wide = s.max_pairs + (split ? sms / c->Hkv : 0);
+    s.max_groups = split ? (s.max_pairs < sms / c->Hkv ? s.max_pairs : sms / c->Hkv) : 0;
     s.off_few = align_up(sizeof(PlanHead), kWsAlign);
     s.off_prefix = align_up(s.off_few + sizeof(Entry) * (size_t)s.max_few, kWsAlign);
     s.off_start = align_up(s.off_prefix + sizeof(int64_t) * (size_t)s.max_few, kWsAlign);
-    s.bytes = align_up(s.off_start + sizeof(Start) * (size_t)(s.ctas + 1), kWsAlign);
+    s.off_pairs = align_up(s.off_start + sizeof(Start) * (size_t)(s.ctas + 1), kWsAlign);
+    s.off_wide = align_up(s.off_pairs + sizeof(Wide) * (size_t)s.max_pairs, kWsAlign);
+    s.off_group = align_up(s.off_wide + sizeof(Wide) * (size_t)s.max_wide, kWsAlign);
+    s.bytes = align_up(s.off_group + sizeof(Group) * (size_t)s.max_groups, kWsAlign);
     return s;
 }
 
@@ -209,7 +323,7 @@ extern "C" int graft_paged_attention_workspace_size(const GraftPagedCache* cache
     const int rc = check_attention(cache, N, Hq, max_new);
     if (rc != GRAFT_OK) return rc;
     WsCarver w(nullptr);
-    carve_few(w, cache, plan_shape(cache, N, Hq, max_new));
+    carve(w, cache, plan_shape(cache, N, Hq, max_new), nullptr);
     *bytes = w.bytes();
     return GRAFT_OK;
 }
@@ -225,15 +339,16 @@ extern "C" int graft_paged_attention(const GraftPagedCache* cache, const void* K
     if (K_pool == nullptr || V_pool == nullptr || Q == nullptr || O == nullptr) return GRAFT_ERR_INVALID_ARG;
     if (!(aligned16(K_pool) && aligned16(V_pool) && aligned16(Q) && aligned16(O))) return GRAFT_ERR_INVALID_ARG;
     if (q_stride % 8 != 0 || q_stride < (int64_t)Hq * HD) return GRAFT_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(O) & 31) != 0) return GRAFT_ERR_INVALID_ARG;  // rows leave in 32-byte pieces
     if (!(scale > 0.f)) return GRAFT_ERR_INVALID_ARG;
     AttnArgs a{};
     a.shape = plan_shape(cache, N, Hq, max_new);
     if (!ws_ok(plan, plan_bytes, a.shape.bytes)) return GRAFT_ERR_WORKSPACE;
     WsCarver sizer(nullptr);
-    carve_few(sizer, cache, a.shape);
+    carve(sizer, cache, a.shape, nullptr);
     if (!ws_ok(ws, ws_bytes, sizer.bytes())) return GRAFT_ERR_WORKSPACE;
     WsCarver w(ws);
-    a.few = carve_few(w, cache, a.shape);
+    carve(w, cache, a.shape, &a);
     a.c = *cache;
     a.K = K_pool;
     a.V = V_pool;
@@ -248,5 +363,9 @@ extern "C" int graft_paged_attention(const GraftPagedCache* cache, const void* K
     a.G = Hq / cache->Hkv;
     a.max_new = max_new;
     a.page_shift = log2_exact(cache->page_rows);
-    return few_launch(a, (cudaStream_t)stream);
+    if (a.shape.few) {
+        const int rc2 = few_launch(a, (cudaStream_t)stream);
+        if (rc2 != GRAFT_OK) return rc2;
+    }
+    return a.shape.wide ? wide_launch(a, (cudaStream_t)stream) : GRAFT_OK;
 }
