@@ -66,13 +66,18 @@ struct Group {
     int32_t q0, n, tok0, ranges, part0, pad[3];
 };
 
+// Where a CTA of the few kernel starts: everything its first item needs, in one read.
 struct Start {
-    int32_t entry, head, unit, pad;
+    Entry e;
+    int32_t entry, head, unit, ctas;
+    int64_t item_first;  // the item's first unit among all
+    int64_t count;       // units of the CTA's run
 };
 
 struct PlanShape {
     int max_few;   // bound on the few entries
     int ctas;      // CTAs of the few kernel at most
+    int few_warps; // warps of such a CTA
     int few_rows;  // query rows of a few entry at most (16 or 32)
     int few, wide; // whether the calls launch either kernel
     int sms;

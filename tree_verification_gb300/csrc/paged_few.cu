@@ -26,18 +26,19 @@ namespace graft {
 namespace paged {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
 constexpr int kUnit = 16;                          // keys of a unit
 constexpr int kUnitBytes = kUnit * HD * 2;         // of K, or of V
 constexpr int kRowPad = 132;                       // floats of a staged partial row: 4 banks apart
-constexpr int kRing = kWarps * kStages * 2 * kUnitBytes;
 
-constexpr int smem_bytes(int RT) {
-    const int merge = kWarps * RT * 16 * kRowPad * 4;
-    return (kRing > merge ? kRing : merge) + kWarps * RT * 16 * 8 + 16;
+// W: warps of a CTA, RT: 16-row tiles of a warp
+constexpr int ring_bytes(int W, int RT) {
+    const int ring = W * kStages * 2 * kUnitBytes, merge = W * RT * 16 * kRowPad * 4;
+    return ring > merge ? ring : merge;
 }
+// ring (or staged rows) | Q of two row tiles | maxima and sums | flag
+constexpr int q_bytes(int RT) { return RT > 1 ? RT * 16 * HD * 2 : 0; }
+constexpr int smem_bytes(int W, int RT) { return ring_bytes(W, RT) + q_bytes(RT) + W * RT * 16 * 8 + 16; }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -91,34 +92,40 @@ __device__ __forceinline__ float safe(float m) { return m == -INFINITY ? 0.f : m
 template <int DT>
 constexpr float kLift = DT == GRAFT_FP16 ? 7.f : 0.f;
 
-// RT: 16-row tiles a warp holds.
-template <int DT, int RT>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int DT, int RT, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, 8 / kWarps)
 few_kernel(const __grid_constant__ AttnArgs a) {
     using E = Elem<DT>;
     using T = typename E::T;
     extern __shared__ __align__(128) unsigned char smem[];
     griddep_enter();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const PlanHead& head = *reinterpret_cast<const PlanHead*>(a.plan);
-    if (!plan_fits(a, head)) {
-        if (blockIdx.x == 0 && tid == 0) flag_status(a.c.status, GRAFT_STATUS_PLAN);
-        return;
-    }
-    const int ctas = head.few_ctas, cta = blockIdx.x;
-    if (cta >= ctas) return;
-    const int64_t total = head.few_units;
+    const int cta = blockIdx.x;
     const Entry* entries = reinterpret_cast<const Entry*>(a.plan + a.shape.off_few);
-    const int64_t* prefix = reinterpret_cast<const int64_t*>(a.plan + a.shape.off_prefix);
-    const Start* starts = reinterpret_cast<const Start*>(a.plan + a.shape.off_start);
-    int64_t left = first_unit(total, ctas, cta + 1) - first_unit(total, ctas, cta);
-    Start at = starts[cta];
+    // The run's state is the CTA's, not a thread's: shared memory holds it, the registers are for O and Q.
+    __shared__ Start s_at;
+    __shared__ int64_t s_total;
+    {
+        const PlanHead head = *reinterpret_cast<const PlanHead*>(a.plan);
+        const Start first = reinterpret_cast<const Start*>(a.plan + a.shape.off_start)[cta];
+        if (!plan_fits(a, head)) {
+            if (cta == 0 && tid == 0) flag_status(a.c.status, GRAFT_STATUS_PLAN);
+            return;
+        }
+        if (cta >= head.few_ctas) return;
+        if (tid == 0) {
+            s_at = first;
+            s_at.ctas = head.few_ctas;
+            s_total = head.few_units;
+        }
+    }
+    __syncthreads();
 
-    constexpr int kMergeBytes = kWarps * RT * 16 * kRowPad * 4;
     float* s_part = reinterpret_cast<float*>(smem);
-    float2* s_ml = reinterpret_cast<float2*>(smem + (kRing > kMergeBytes ? kRing : kMergeBytes));
+    float2* s_ml = reinterpret_cast<float2*>(smem + ring_bytes(kWarps, RT) + q_bytes(RT));
     int* s_last = reinterpret_cast<int*>(s_ml + kWarps * RT * 16);
     const uint32_t ring = smem_u32(smem) + warp * (kStages * 2 * kUnitBytes);
+    const uint32_t s_q = smem_u32(smem + ring_bytes(kWarps, RT));
     unsigned char* ring_p = smem + warp * (kStages * 2 * kUnitBytes);
     const T* Kp = static_cast<const T*>(a.K);
     const T* Vp = static_cast<const T*>(a.V);
@@ -126,11 +133,12 @@ few_kernel(const __grid_constant__ AttnArgs a) {
     const float sl2 = a.scale * 1.4426950408889634f;
     const int64_t key_stride = (int64_t)a.c.Hkv * HD;
 
-    while (left > 0) {
-        const Entry e = entries[at.entry];
-        const int u0 = at.unit;
-        const int u1 = (int)min((int64_t)e.units, u0 + left);
-        const int kvh = at.head;
+    while (true) {
+        const Entry& e = s_at.e;
+        const int keys = e.keys, L = e.L, n_new = e.n;
+        const int u0 = s_at.unit;
+        const int u1 = (int)min((int64_t)e.units, u0 + s_at.count);
+        const int kvh = s_at.head;
         const int32_t* table = a.c.block_table + (int64_t)e.b * a.c.max_pages;
 
         // pages of this warp's next 32 units, one a lane
@@ -162,7 +170,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
                 for (int x = 0; x < kUnit * 16 / 32; ++x) {
                     const int r = x * 2 + (lane >> 4), ch = lane & 15;
-                    const bool ok = page >= 0 && key0 + r < e.keys;
+                    const bool ok = page >= 0 && key0 + r < keys;
                     const int64_t o = off + (ok ? r * key_stride : 0) + ch * 8;
                     cp_async16(k + swz(r, ch), Kp + o, ok);
                     cp_async16(v + swz(r, ch), Vp + o, ok);
@@ -173,8 +181,18 @@ few_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) load(i);
 
-        // Q fragments straight from memory; rows past the block read as zeros
-        uint32_t qf[RT][8][4];
+        // Q: rows past the block read as zeros.  One row tile's fragments stay in registers, straight from
+        // memory; two tiles' would not fit beside O, so they go through shared memory, read again every unit.
+        uint32_t qf[RT > 1 ? 1 : 8][4];
+        if (RT > 1) {
+            for (int x = tid; x < RT * 16 * 16; x += kWarps * 32) {
+                const int r = x >> 4, ch = x & 15;
+                const int row = e.row0 + r, tok = row / a.G, g = row - tok * a.G;
+                const bool ok = r < e.rows;
+                cp_async16(s_q + swz(r, ch),
+                           Qp + (ok ? (int64_t)(e.q0 + tok) * a.q_stride + (kvh * a.G + g) * HD + ch * 8 : 0), ok);
+            }
+        }
         int limit[RT][2];        // keys below it are seen
         uint64_t anc[RT][2];     // new rows seen (tree)
 #pragma unroll
@@ -185,12 +203,14 @@ few_kernel(const __grid_constant__ AttnArgs a) {
                 const bool ok = r < e.rows;
                 const int row = e.row0 + r, tok = row / a.G;
                 const int g = row - tok * a.G;
-                const T* q = Qp + (ok ? (int64_t)(e.q0 + tok) * a.q_stride + (kvh * a.G + g) * HD : 0);
+                if (RT == 1) {
+                    const T* q = Qp + (ok ? (int64_t)(e.q0 + tok) * a.q_stride + (kvh * a.G + g) * HD : 0);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const int col = kk * 16 + (lane & 3) * 2;
-                    qf[t][kk][h] = ok ? *reinterpret_cast<const uint32_t*>(q + col) : 0u;
-                    qf[t][kk][h + 2] = ok ? *reinterpret_cast<const uint32_t*>(q + col + 8) : 0u;
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const int col = kk * 16 + (lane & 3) * 2;
+                        qf[kk][h] = ok ? *reinterpret_cast<const uint32_t*>(q + col) : 0u;
+                        qf[kk][h + 2] = ok ? *reinterpret_cast<const uint32_t*>(q + col + 8) : 0u;
+                    }
                 }
                 anc[t][h] = 0;
                 if (!ok) {
@@ -211,6 +231,10 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             for (int d = 0; d < 16; ++d) o[t][d][0] = o[t][d][1] = o[t][d][2] = o[t][d][3] = 0.f;
         }
 
+        if (RT > 1) {
+            cp_wait<0>();  // Q, and the first units with it
+            __syncthreads();
+        }
         for (int i = 0; i < mine; ++i) {
             load(i + kStages - 1);
             cp_wait<kStages - 1>();
@@ -229,15 +253,17 @@ few_kernel(const __grid_constant__ AttnArgs a) {
                 ldsm_x4(tK + swz((m >> 1) * 8 + (lane & 7), kk * 2 + (m & 1)), b0, b1, b2, b3);
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    mma16816<DT>(s[t][0], qf[t][kk], b0, b1);
-                    mma16816<DT>(s[t][1], qf[t][kk], b2, b3);
+                    uint32_t* q = qf[RT > 1 ? 0 : kk];
+                    if (RT > 1) ldsm_x4(s_q + swz(t * 16 + (lane & 15), kk * 2 + (lane >> 4)), q[0], q[1], q[2], q[3]);
+                    mma16816<DT>(s[t][0], q, b0, b1);
+                    mma16816<DT>(s[t][1], q, b2, b3);
                 }
             }
-            const bool edge = key0 + kUnit > e.L;  // the unit holds new rows, or ends the keys
+            const bool edge = key0 + kUnit > L;  // the unit holds new rows, or ends the keys
             auto sees = [&](int t, int h, int key) -> bool {
                 if (key < limit[t][h]) return true;
-                const int j = key - e.L;
-                return a.mask != nullptr && j >= 0 && j < e.n && ((anc[t][h] >> j) & 1ull);
+                const int j = key - L;
+                return a.mask != nullptr && j >= 0 && j < n_new && ((anc[t][h] >> j) & 1ull);
             };
             bool up = false;
 #pragma unroll
@@ -385,7 +411,8 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             *reinterpret_cast<uint2*>(dst) =
                 make_uint2(E::down(acc.x * inv, acc.y * inv), E::down(acc.z * inv, acc.w * inv));
         };
-        const int64_t g0 = prefix[at.entry] + (int64_t)kvh * e.units;
+        const int64_t total = s_total, g0 = s_at.item_first;
+        const int ctas = s_at.ctas;
         const int c0 = unit_cta(total, ctas, g0), c1 = unit_cta(total, ctas, g0 + e.units - 1);
         if (c0 == c1) {
             for (int r = warp; r < e.rows; r += kWarps) {
@@ -406,7 +433,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             }
             __threadfence();
             __syncthreads();
-            int32_t* count = a.few.count + (int64_t)at.entry * a.c.Hkv + kvh;
+            int32_t* count = a.few.count + (int64_t)s_at.entry * a.c.Hkv + kvh;
             if (tid == 0) {
                 const int pieces = c1 - c0 + 1;
                 const int before = atomicAdd(count, 1);
@@ -417,48 +444,55 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             __syncthreads();
             if (*s_last) {
                 __threadfence();
-                // each warp joins every kWarps-th piece, then the warps are joined as above
-                for (int r = 0; r < e.rows; ++r) {
-                    float m = -INFINITY, l = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    constexpr int kB = 8;
-                    for (int p0 = c0 + warp; p0 <= c1; p0 += kB * kWarps) {
-                        float2 ml[kB];
-                        float4 v[kB];
+                // Each warp joins every kWarps-th piece of every row, then the warps are joined as above.  A warp's
+                // reads (rows x its pieces) are issued kB at a time, whatever rows they belong to.
+                const int per = (c1 - c0 + 1 - warp + kWarps - 1) / kWarps;  // its pieces (may be <= 0)
+                if (per <= 0) {
+                    for (int r = lane; r < e.rows; r += 32)
+                        s_ml[warp * RT * 16 + r] = make_float2(-INFINITY, 0.f);
+                }
+                constexpr int kB = 16;
+                int rl = 0, pl = 0, rp = 0, pp = 0;  // row and piece of the next read, of the next sum
+                float m = -INFINITY, l = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int done = 0; done < e.rows * per; done += kB) {
+                    float2 ml[kB];
+                    float4 v[kB];
 #pragma unroll
-                        for (int x = 0; x < kB; ++x) {
-                            const int p = p0 + x * kWarps;
-                            ml[x] = make_float2(-INFINITY, 0.f);
-                            v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (p <= c1) {
-                                const int64_t sl = ((int64_t)p * 2 + (p == c0 ? 1 : 0)) * rows + r;
-                                ml[x] = __ldcg(a.few.ml + sl);
-                                v[x] = __ldcg(reinterpret_cast<const float4*>(a.few.o + sl * HD) + lane);
+                    for (int x = 0; x < kB; ++x) {
+                        if (rl < e.rows) {
+                            const int p = c0 + warp + pl * kWarps;
+                            const int64_t sl = ((int64_t)p * 2 + (p == c0 ? 1 : 0)) * rows + rl;
+                            ml[x] = __ldcg(a.few.ml + sl);
+                            v[x] = __ldcg(reinterpret_cast<const float4*>(a.few.o + sl * HD) + lane);
+                            if (++pl == per) {
+                                pl = 0;
+                                ++rl;
                             }
                         }
-                        float mx = m;
+                    }
 #pragma unroll
-                        for (int x = 0; x < kB; ++x) mx = fmaxf(mx, ml[x].x);
-                        const float keep = ex2(m - safe(mx));
-                        acc.x *= keep;
-                        acc.y *= keep;
-                        acc.z *= keep;
-                        acc.w *= keep;
-                        l *= keep;
-                        m = mx;
-#pragma unroll
-                        for (int x = 0; x < kB; ++x) {
-                            if (ml[x].x == -INFINITY && ml[x].y == 0.f) continue;
-                            const float f = ex2(ml[x].x - safe(m));
-                            acc.x += f * v[x].x;
-                            acc.y += f * v[x].y;
-                            acc.z += f * v[x].z;
-                            acc.w += f * v[x].w;
-                            l += f * ml[x].y;
+                    for (int x = 0; x < kB; ++x) {
+                        if (rp < e.rows) {
+                            const float mx = fmaxf(m, ml[x].x);
+                            const float keep = ex2(m - safe(mx)), f = ex2(ml[x].x - safe(mx));
+                            acc.x = acc.x * keep + f * v[x].x;
+                            acc.y = acc.y * keep + f * v[x].y;
+                            acc.z = acc.z * keep + f * v[x].z;
+                            acc.w = acc.w * keep + f * v[x].w;
+                            l = l * keep + f * ml[x].y;
+                            m = mx;
+                            if (++pp == per) {
+                                *reinterpret_cast<float4*>(s_part + (warp * RT * 16 + rp) * kRowPad + lane * 4) = acc;
+                                if (lane == 0) s_ml[warp * RT * 16 + rp] = make_float2(m, l);
+                                m = -INFINITY;
+                                l = 0.f;
+                                acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                                pp = 0;
+                                ++rp;
+                            }
                         }
                     }
-                    *reinterpret_cast<float4*>(s_part + (warp * RT * 16 + r) * kRowPad + lane * 4) = acc;
-                    if (lane == 0) s_ml[warp * RT * 16 + r] = make_float2(m, l);
                 }
                 __syncthreads();
                 for (int r = warp; r < e.rows; r += kWarps) {
@@ -469,38 +503,51 @@ few_kernel(const __grid_constant__ AttnArgs a) {
                 }
             }
         }
-        __syncthreads();  // the staged rows are read: the next run's copies may overwrite them
-        left -= u1 - u0;
-        at.unit = 0;
-        if (u1 == e.units && ++at.head == a.c.Hkv) {
-            at.head = 0;
-            ++at.entry;
+        __syncthreads();  // the staged rows are read: the next item's copies may overwrite them
+        const int64_t left = s_at.count - (u1 - u0);
+        if (left <= 0) break;
+        // the run goes on with the next head, or the next entry's first
+        __syncthreads();
+        if (tid == 0) {
+            s_at.count = left;
+            s_at.unit = 0;
+            s_at.item_first += s_at.e.units;
+            if (++s_at.head == a.c.Hkv) {
+                s_at.head = 0;
+                s_at.e = entries[++s_at.entry];
+            }
         }
+        __syncthreads();
     }
 }
 
-template <int DT, int RT>
+template <int DT, int RT, int W>
 int launch(const AttnArgs& a, cudaStream_t st) {
     static bool attr_set[64] = {};
     int dev = 0;
     if (!cuda_ok(cudaGetDevice(&dev))) return GRAFT_ERR_CUDA;
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        if (!cuda_ok(cudaFuncSetAttribute(few_kernel<DT, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          smem_bytes(RT))))
+        if (!cuda_ok(cudaFuncSetAttribute(few_kernel<DT, RT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          smem_bytes(W, RT))))
             return GRAFT_ERR_CUDA;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    launch_pdl(few_kernel<DT, RT>, dim3(a.shape.ctas), dim3(kThreads), smem_bytes(RT), st, a);
+    launch_pdl(few_kernel<DT, RT, W>, dim3(a.shape.ctas), dim3(W * 32), smem_bytes(W, RT), st, a);
     count_launches(1);
     return launch_status();
+}
+
+template <int DT>
+int launch_type(const AttnArgs& a, cudaStream_t st) {
+    if (a.shape.few_warps == 4)
+        return a.shape.few_rows == 16 ? launch<DT, 1, 4>(a, st) : launch<DT, 2, 4>(a, st);
+    return a.shape.few_rows == 16 ? launch<DT, 1, 8>(a, st) : launch<DT, 2, 8>(a, st);
 }
 
 }  // namespace
 
 int few_launch(const AttnArgs& a, cudaStream_t st) {
-    const bool one = a.shape.few_rows == 16;
-    if (a.c.dtype == GRAFT_BF16) return one ? launch<GRAFT_BF16, 1>(a, st) : launch<GRAFT_BF16, 2>(a, st);
-    return one ? launch<GRAFT_FP16, 1>(a, st) : launch<GRAFT_FP16, 2>(a, st);
+    return a.c.dtype == GRAFT_BF16 ? launch_type<GRAFT_BF16>(a, st) : launch_type<GRAFT_FP16>(a, st);
 }
 
 }  // namespace paged

@@ -185,12 +185,11 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
         units += total;
     }
     __syncthreads();
-    // at least kMinUnits units a CTA: a CTA's own start and end cost more than the keys it would save another
-    constexpr int64_t kMinUnits = 8;
-    const int64_t want = (units + kMinUnits - 1) / kMinUnits;
+    // a unit for every warp at least: a CTA's own start and end cost more than the keys it would take over
+    const int64_t want = (units + shape.few_warps - 1) / shape.few_warps;
     const int ctas = (int)(want < shape.ctas ? want : shape.ctas);
-    for (int k = tid; k <= shape.ctas; k += kPlanThreads) {
-        Start s{n_few, 0, 0, 0};
+    for (int k = tid; k < shape.ctas; k += kPlanThreads) {
+        Start s{};
         if (k < ctas) {
             const int64_t u = first_unit(units, ctas, k);
             int lo = 0, hi = n_few;  // the entry with prefix[lo] <= u < prefix[lo + 1]
@@ -200,9 +199,12 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
                 else hi = mid;
             }
             const int64_t in = u - prefix[lo];
+            s.e = few[lo];
             s.entry = lo;
-            s.head = (int)(in / few[lo].units);
-            s.unit = (int)(in % few[lo].units);
+            s.head = (int)(in / s.e.units);
+            s.unit = (int)(in % s.e.units);
+            s.item_first = prefix[lo] + (int64_t)s.head * s.e.units;
+            s.count = first_unit(units, ctas, k + 1) - u;
         }
         start[k] = s;
     }
@@ -242,8 +244,9 @@ int check_attention(const GraftPagedCache* c, int N, int Hq, int max_new) {
 // most one range a slot of the wave, and one more a block.
 void carve(WsCarver& w, const GraftPagedCache* c, const PlanShape& s, AttnArgs* a) {
     FewWs f;
-    f.o = w.take<float>((size_t)s.ctas * 2 * kFewRows * HD);
-    f.ml = w.take<float2>((size_t)s.ctas * 2 * kFewRows);
+    const size_t slots = (size_t)s.sms * 2 * 2;  // two a CTA, at most two CTAs an SM
+    f.o = w.take<float>(slots * kFewRows * HD);
+    f.ml = w.take<float2>(slots * kFewRows);
     const size_t parts = (size_t)s.sms * 2;
     float* wo = w.take<float>(parts * 2 * 128 * HD);
     float* wl = w.take<float>(parts * 2 * 128);
@@ -262,7 +265,6 @@ PlanShape plan_shape(const GraftPagedCache* c, int N, int Hq, int max_new) {
     const int G = Hq / c->Hkv;
     int sms = device_sm_count();
     if (sms <= 0) sms = 148;
-    s.ctas = 2 * sms;
     s.sms = sms;
     s.few_rows = (int64_t)max_new * G <= 16 ? 16 : 32;
     // Up to 32 query rows the few kernel reads K and V at HBM speed; past that its products take longer than
@@ -273,6 +275,10 @@ PlanShape plan_shape(const GraftPagedCache* c, int N, int Hq, int max_new) {
     // sequences with rows: at most n_seqs and at most N; each ends in at most one block that is not full
     const int64_t seqs = c->n_seqs < N ? c->n_seqs : N;
     s.max_few = s.few ? (int)seqs : 0;
+    // Many items: two CTAs of four warps an SM, so that one streams while the other joins its warps and starts
+    // anew.  Few: one of eight, whose runs are twice as long and cut an item into half as many pieces.
+    s.few_warps = seqs * c->Hkv >= 2 * sms ? 4 : 8;
+    s.ctas = sms * 8 / s.few_warps;
     const int full_pairs = N / (2 * s.tile_tokens);
     s.max_pairs = s.wide ? (int)(full_pairs + seqs) : 0;
     // where even the full row blocks fill the SMs nothing is split
@@ -282,7 +288,7 @@ PlanShape plan_shape(const GraftPagedCache* c, int N, int Hq, int max_new) {
     s.off_few = align_up(sizeof(PlanHead), kWsAlign);
     s.off_prefix = align_up(s.off_few + sizeof(Entry) * (size_t)s.max_few, kWsAlign);
     s.off_start = align_up(s.off_prefix + sizeof(int64_t) * (size_t)s.max_few, kWsAlign);
-    s.off_pairs = align_up(s.off_start + sizeof(Start) * (size_t)(s.ctas + 1), kWsAlign);
+    s.off_pairs = align_up(s.off_start + sizeof(Start) * (size_t)s.ctas, kWsAlign);
     s.off_wide = align_up(s.off_pairs + sizeof(Wide) * (size_t)s.max_pairs, kWsAlign);
     s.off_group = align_up(s.off_wide + sizeof(Wide) * (size_t)s.max_wide, kWsAlign);
     s.bytes = align_up(s.off_group + sizeof(Group) * (size_t)s.max_groups, kWsAlign);

@@ -27,6 +27,10 @@ import torch
 
 from . import binding as gb
 
+# the calls behind torch.cuda.current_device and current_stream, without the objects those build (3 us a call)
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
@@ -105,12 +109,12 @@ class PagedCache:
         return t
 
     def _call(self, name: str, *args) -> None:
-        fn = getattr(self._lib, name)
-        if torch.cuda.current_device() == self._index:
-            rc = fn(self._c, *args, torch.cuda.current_stream().cuda_stream)
+        stream = _raw_stream(self._index)
+        if _current_device() == self._index:
+            rc = getattr(self._lib, name)(self._c, *args, stream)
         else:
             with torch.cuda.device(self._index):
-                rc = fn(self._c, *args, torch.cuda.current_stream().cuda_stream)
+                rc = getattr(self._lib, name)(self._c, *args, stream)
         if rc:
             gb._check(rc, name)
 
