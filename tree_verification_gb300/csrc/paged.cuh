@@ -33,7 +33,7 @@ struct PlanHead {
     int32_t magic, N, Hq, Hkv, n_seqs, max_new, tree, page_rows, max_pages, num_pages, few_rows, ctas;
     int32_t n_few;       // few entries
     int32_t few_ctas;    // CTAs that share them
-    int64_t few_units;   // 16-key units over entries and heads
+    int32_t pad;
     int32_t n_wide;      // wide entries
     int32_t n_groups;    // row blocks split by keys
     int32_t reserved[14];
@@ -66,12 +66,15 @@ struct Group {
     int32_t q0, n, tok0, ranges, part0, pad[3];
 };
 
-// Where a CTA of the few kernel starts: everything its first item needs, in one read.
+// Where a CTA of the few kernel starts: everything its first item needs, in one read.  Either a CTA takes an even
+// run of all units, over whatever items they belong to (step 0), or a share of one item alone.
 struct Start {
     Entry e;
-    int32_t entry, head, unit, ctas;
-    int64_t item_first;  // the item's first unit among all
-    int64_t count;       // units of the CTA's run
+    int32_t entry, head, unit, count;  // units of the CTA
+    int32_t ctas;                      // step 0: CTAs that share all units
+    int32_t step, cta0, pieces;        // the item's pieces: CTAs cta0, cta0 + step, ...
+    int64_t item_first;                // step 0: the item's first unit among all
+    int64_t total;                     // step 0: all units
 };
 
 struct PlanShape {

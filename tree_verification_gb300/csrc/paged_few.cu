@@ -36,9 +36,9 @@ constexpr int ring_bytes(int W, int RT) {
     const int ring = W * kStages * 2 * kUnitBytes, merge = W * RT * 16 * kRowPad * 4;
     return ring > merge ? ring : merge;
 }
-// ring (or staged rows) | Q of two row tiles | maxima and sums | flag
+// ring (or staged rows) | Q of two row tiles | maxima and sums
 constexpr int q_bytes(int RT) { return RT > 1 ? RT * 16 * HD * 2 : 0; }
-constexpr int smem_bytes(int W, int RT) { return ring_bytes(W, RT) + q_bytes(RT) + W * RT * 16 * 8 + 16; }
+constexpr int smem_bytes(int W, int RT) { return ring_bytes(W, RT) + q_bytes(RT) + W * RT * 16 * 8; }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -92,6 +92,98 @@ __device__ __forceinline__ float safe(float m) { return m == -INFINITY ? 0.f : m
 template <int DT>
 constexpr float kLift = DT == GRAFT_FP16 ? 7.f : 0.f;
 
+// Joins the warps' staged rows r (the sum of the weights in l); a lane takes four dims.
+template <int W, int RT>
+__device__ __forceinline__ void join_warps(const float* s_part, const float2* s_ml, int r, float4& acc, float& m,
+                                           float& l) {
+    const int lane = threadIdx.x & 31;
+    m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) m = fmaxf(m, s_ml[w * RT * 16 + r].x);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const float2 ml = s_ml[w * RT * 16 + r];
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;  // saw no key
+        const float x = ex2(ml.x - safe(m));
+        const float4 v = *reinterpret_cast<const float4*>(s_part + (w * RT * 16 + r) * kRowPad + lane * 4);
+        acc.x += x * v.x;
+        acc.y += x * v.y;
+        acc.z += x * v.z;
+        acc.w += x * v.w;
+        l += x * ml.y;
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void put_row(const AttnArgs& a, const Entry& e, int kvh, int r, const float4& acc, float l) {
+    using E = Elem<DT>;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int row = e.row0 + r, tok = row / a.G, g = row - tok * a.G;
+    typename E::T* dst = static_cast<typename E::T*>(a.O) + ((int64_t)(e.q0 + tok) * a.Hq + kvh * a.G + g) * HD +
+                         (threadIdx.x & 31) * 4;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(E::down(acc.x * inv, acc.y * inv), E::down(acc.z * inv, acc.w * inv));
+}
+
+// Joins an item's pieces, by the CTA that arrived last.  The pieces' rows come to shared memory with cp.async, as
+// many as the ring holds at a time (all reads in flight at once, little code: this part runs cold), then a thread
+// sums four dims of a row over them.  More pieces than fit: the sums so far take the first place of the next lot.
+template <int DT, int RT, int W>
+__device__ __forceinline__ void join_pieces(const AttnArgs& a, const Start& at, unsigned char* smem) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n_rows = at.e.rows, step = at.step, kvh = at.head, c0 = at.cta0, pieces = at.pieces;
+    const int row_floats = n_rows * HD;
+    const int cap = ring_bytes(W, RT) / (n_rows * (HD * 4 + 8));
+    float* s_o = reinterpret_cast<float*>(smem);                            // [cap][n_rows][128]
+    float2* s_ml = reinterpret_cast<float2*>(s_o + (size_t)cap * row_floats);  // [cap][n_rows]
+    int have = 0;
+    for (int p0 = 0; p0 < pieces;) {
+        const int n = min(cap - have, pieces - p0);
+        for (int p = warp; p < n; p += W) {
+            // a run's last item (the one that it starts) has the CTA's second slot
+            const int q = p0 + p;
+            const int64_t slot = step > 0 ? (c0 + q * step) * 2 : (c0 + q) * 2 + (q == 0 ? 1 : 0);
+            const float* src = a.few.o + slot * kFewRows * HD;
+            const uint32_t dst = smem_u32(s_o + (size_t)(have + p) * row_floats);
+#pragma unroll 4
+            for (int i = lane; i < n_rows * 32; i += 32) cp_async16(dst + i * 16, src + i * 4, true);
+            if (lane < n_rows) s_ml[(have + p) * n_rows + lane] = __ldcg(a.few.ml + slot * kFewRows + lane);
+        }
+        cp_commit();
+        cp_wait<0>();
+        __syncthreads();
+        p0 += n;
+        const int all = have + n;
+        for (int x = tid; x < n_rows * 32; x += W * 32) {
+            const int r = x >> 5;
+            float m = -INFINITY, l = 0.f;
+            for (int p = 0; p < all; ++p) m = fmaxf(m, s_ml[p * n_rows + r].x);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int p = 0; p < all; ++p) {
+                const float2 ml = s_ml[p * n_rows + r];
+                const float f = ex2(ml.x - safe(m));
+                const float4 v = *reinterpret_cast<const float4*>(s_o + (size_t)p * row_floats + x * 4);
+                acc.x += f * v.x;
+                acc.y += f * v.y;
+                acc.z += f * v.z;
+                acc.w += f * v.w;
+                l += f * ml.y;
+            }
+            if (p0 == pieces) {
+                put_row<DT>(a, at.e, kvh, r, acc, l);
+            } else {
+                *reinterpret_cast<float4*>(s_o + x * 4) = acc;
+                __syncwarp();  // (a row's maxima are read by the warp that sums the row alone)
+                if (lane == 0) s_ml[r] = make_float2(m, l);
+            }
+        }
+        have = 1;
+        __syncthreads();
+    }
+}
+
 template <int DT, int RT, int kWarps>
 __global__ void __launch_bounds__(kWarps * 32, 8 / kWarps)
 few_kernel(const __grid_constant__ AttnArgs a) {
@@ -103,8 +195,8 @@ few_kernel(const __grid_constant__ AttnArgs a) {
     const int cta = blockIdx.x;
     const Entry* entries = reinterpret_cast<const Entry*>(a.plan + a.shape.off_few);
     // The run's state is the CTA's, not a thread's: shared memory holds it, the registers are for O and Q.
-    __shared__ Start s_at;
-    __shared__ int64_t s_total;
+    __shared__ Start s_at, s_pending[2];
+    __shared__ int s_n_pending;
     {
         const PlanHead head = *reinterpret_cast<const PlanHead*>(a.plan);
         const Start first = reinterpret_cast<const Start*>(a.plan + a.shape.off_start)[cta];
@@ -115,15 +207,13 @@ few_kernel(const __grid_constant__ AttnArgs a) {
         if (cta >= head.few_ctas) return;
         if (tid == 0) {
             s_at = first;
-            s_at.ctas = head.few_ctas;
-            s_total = head.few_units;
+            s_n_pending = 0;
         }
     }
     __syncthreads();
 
     float* s_part = reinterpret_cast<float*>(smem);
     float2* s_ml = reinterpret_cast<float2*>(smem + ring_bytes(kWarps, RT) + q_bytes(RT));
-    int* s_last = reinterpret_cast<int*>(s_ml + kWarps * RT * 16);
     const uint32_t ring = smem_u32(smem) + warp * (kStages * 2 * kUnitBytes);
     const uint32_t s_q = smem_u32(smem + ring_bytes(kWarps, RT));
     unsigned char* ring_p = smem + warp * (kStages * 2 * kUnitBytes);
@@ -137,7 +227,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
         const Entry& e = s_at.e;
         const int keys = e.keys, L = e.L, n_new = e.n;
         const int u0 = s_at.unit;
-        const int u1 = (int)min((int64_t)e.units, u0 + s_at.count);
+        const int u1 = min(e.units, u0 + s_at.count);
         const int kvh = s_at.head;
         const int32_t* table = a.c.block_table + (int64_t)e.b * a.c.max_pages;
 
@@ -192,6 +282,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
                 cp_async16(s_q + swz(r, ch),
                            Qp + (ok ? (int64_t)(e.q0 + tok) * a.q_stride + (kvh * a.G + g) * HD + ch * 8 : 0), ok);
             }
+            cp_commit();
         }
         int limit[RT][2];        // keys below it are seen
         uint64_t anc[RT][2];     // new rows seen (tree)
@@ -235,6 +326,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             cp_wait<0>();  // Q, and the first units with it
             __syncthreads();
         }
+#pragma unroll 1
         for (int i = 0; i < mine; ++i) {
             load(i + kStages - 1);
             cp_wait<kStages - 1>();
@@ -324,7 +416,9 @@ few_kernel(const __grid_constant__ AttnArgs a) {
                     odd |= E::odd(v.x) || E::odd(v.y) || E::odd(v.z) || E::odd(v.w);
                 }
                 if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
                     for (int key = 0; key < kUnit; ++key)
+#pragma unroll 1
                         for (int d = 0; d < 16; ++d) {
                             const uint32_t w = *reinterpret_cast<const uint32_t*>(ring_p + (tV - ring) + swz(key, d) +
                                                                                   (lane & 3) * 4);
@@ -344,6 +438,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
                                     }
                         }
                     __syncwarp();
+#pragma unroll 1
                     for (int x = lane; x < kUnitBytes / 4; x += 32) {
                         uint32_t* w = reinterpret_cast<uint32_t*>(ring_p + (tV - ring)) + x;
                         const float2 f = E::up(*w);
@@ -384,50 +479,26 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             }
         __syncthreads();
 
-        // joins the warps' rows; a lane takes four dims
-        auto join = [&](int r, float4& acc, float& m, float& l) {
-            m = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w * RT * 16 + r].x);
-            acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            l = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float2 ml = s_ml[w * RT * 16 + r];
-                if (ml.x == -INFINITY && ml.y == 0.f) continue;  // saw no key
-                const float x = ex2(ml.x - safe(m));
-                const float4 v = *reinterpret_cast<const float4*>(s_part + (w * RT * 16 + r) * kRowPad + lane * 4);
-                acc.x += x * v.x;
-                acc.y += x * v.y;
-                acc.z += x * v.z;
-                acc.w += x * v.w;
-                l += x * ml.y;
-            }
-        };
-        auto put = [&](int r, const float4& acc, float l) {
-            const float inv = l != 0.f ? 1.f / l : 0.f;
-            const int row = e.row0 + r, tok = row / a.G, g = row - tok * a.G;
-            T* dst = static_cast<T*>(a.O) + ((int64_t)(e.q0 + tok) * a.Hq + kvh * a.G + g) * HD + lane * 4;
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(E::down(acc.x * inv, acc.y * inv), E::down(acc.z * inv, acc.w * inv));
-        };
-        const int64_t total = s_total, g0 = s_at.item_first;
-        const int ctas = s_at.ctas;
-        const int c0 = unit_cta(total, ctas, g0), c1 = unit_cta(total, ctas, g0 + e.units - 1);
-        if (c0 == c1) {
+        const int step = s_at.step;
+        int c0 = s_at.cta0, pieces = s_at.pieces;
+        if (step == 0) {
+            c0 = unit_cta(s_at.total, s_at.ctas, s_at.item_first);
+            pieces = unit_cta(s_at.total, s_at.ctas, s_at.item_first + e.units - 1) - c0 + 1;
+        }
+        if (pieces == 1) {
             for (int r = warp; r < e.rows; r += kWarps) {
                 float4 acc;
                 float m, l;
-                join(r, acc, m, l);
-                put(r, acc, l);
+                join_warps<kWarps, RT>(s_part, s_ml, r, acc, m, l);
+                put_row<DT>(a, e, kvh, r, acc, l);
             }
         } else {
             constexpr int rows = kFewRows;
-            const int slot = cta * 2 + (cta == c0 ? 1 : 0);
+            const int slot = step > 0 ? cta * 2 : cta * 2 + (cta == c0 ? 1 : 0);
             for (int r = warp; r < e.rows; r += kWarps) {
                 float4 acc;
                 float m, l;
-                join(r, acc, m, l);
+                join_warps<kWarps, RT>(s_part, s_ml, r, acc, m, l);
                 *reinterpret_cast<float4*>(a.few.o + ((int64_t)slot * rows + r) * HD + lane * 4) = acc;
                 if (lane == 0) a.few.ml[(int64_t)slot * rows + r] = make_float2(m, l);
             }
@@ -435,76 +506,21 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             __syncthreads();
             int32_t* count = a.few.count + (int64_t)s_at.entry * a.c.Hkv + kvh;
             if (tid == 0) {
-                const int pieces = c1 - c0 + 1;
                 const int before = atomicAdd(count, 1);
                 if (before >= pieces) flag_status(a.c.status, GRAFT_STATUS_WORKSPACE);
-                *s_last = before == pieces - 1;
-                if (before == pieces - 1) *count = 0;
-            }
-            __syncthreads();
-            if (*s_last) {
-                __threadfence();
-                // Each warp joins every kWarps-th piece of every row, then the warps are joined as above.  A warp's
-                // reads (rows x its pieces) are issued kB at a time, whatever rows they belong to.
-                const int per = (c1 - c0 + 1 - warp + kWarps - 1) / kWarps;  // its pieces (may be <= 0)
-                if (per <= 0) {
-                    for (int r = lane; r < e.rows; r += 32)
-                        s_ml[warp * RT * 16 + r] = make_float2(-INFINITY, 0.f);
-                }
-                constexpr int kB = 16;
-                int rl = 0, pl = 0, rp = 0, pp = 0;  // row and piece of the next read, of the next sum
-                float m = -INFINITY, l = 0.f;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int done = 0; done < e.rows * per; done += kB) {
-                    float2 ml[kB];
-                    float4 v[kB];
-#pragma unroll
-                    for (int x = 0; x < kB; ++x) {
-                        if (rl < e.rows) {
-                            const int p = c0 + warp + pl * kWarps;
-                            const int64_t sl = ((int64_t)p * 2 + (p == c0 ? 1 : 0)) * rows + rl;
-                            ml[x] = __ldcg(a.few.ml + sl);
-                            v[x] = __ldcg(reinterpret_cast<const float4*>(a.few.o + sl * HD) + lane);
-                            if (++pl == per) {
-                                pl = 0;
-                                ++rl;
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int x = 0; x < kB; ++x) {
-                        if (rp < e.rows) {
-                            const float mx = fmaxf(m, ml[x].x);
-                            const float keep = ex2(m - safe(mx)), f = ex2(ml[x].x - safe(mx));
-                            acc.x = acc.x * keep + f * v[x].x;
-                            acc.y = acc.y * keep + f * v[x].y;
-                            acc.z = acc.z * keep + f * v[x].z;
-                            acc.w = acc.w * keep + f * v[x].w;
-                            l = l * keep + f * ml[x].y;
-                            m = mx;
-                            if (++pp == per) {
-                                *reinterpret_cast<float4*>(s_part + (warp * RT * 16 + rp) * kRowPad + lane * 4) = acc;
-                                if (lane == 0) s_ml[warp * RT * 16 + rp] = make_float2(m, l);
-                                m = -INFINITY;
-                                l = 0.f;
-                                acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                                pp = 0;
-                                ++rp;
-                            }
-                        }
-                    }
-                }
-                __syncthreads();
-                for (int r = warp; r < e.rows; r += kWarps) {
-                    float4 acc;
-                    float m, l;
-                    join(r, acc, m, l);
-                    put(r, acc, l);
+                if (before == pieces - 1) {
+                    // the last to arrive: it joins the pieces, after its run (a run cuts at most two items), when
+                    // O's registers are free for the reads
+                    *count = 0;
+                    Start& p = s_pending[s_n_pending++];
+                    p = s_at;
+                    p.cta0 = c0;
+                    p.pieces = pieces;
                 }
             }
         }
         __syncthreads();  // the staged rows are read: the next item's copies may overwrite them
-        const int64_t left = s_at.count - (u1 - u0);
+        const int left = s_at.count - (u1 - u0);
         if (left <= 0) break;
         // the run goes on with the next head, or the next entry's first
         __syncthreads();
@@ -518,6 +534,10 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             }
         }
         __syncthreads();
+    }
+    __threadfence();
+    for (int k = 0; k < s_n_pending; ++k) {
+        join_pieces<DT, RT, kWarps>(a, s_pending[k], smem);
     }
 }
 

@@ -40,12 +40,36 @@ __device__ __forceinline__ T scan_block(T v, T* s_warp, T* total) {
     return before + x - v;
 }
 
+// The shortest piece length >= least at which the n items of s_units units, cut into such pieces, make at most
+// `slots` pieces in all (at length `most`, the longest item's, they do): each warp tries one of 32 lengths.
+__device__ __forceinline__ int piece_length(const int* s_units, int n, int slots, int least, int most, int* s_fits) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int lo = least, hi = max(most, least);
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32;
+        const int len = min(lo + warp * step, hi);
+        int64_t items = 0;
+        for (int i = lane; i < n; i += 32) items += (s_units[i] + len - 1) / len;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) items += __shfl_xor_sync(0xffffffffu, items, d);
+        if (lane == 0) s_fits[warp] = items <= slots;
+        __syncthreads();
+        const unsigned m = __ballot_sync(0xffffffffu, s_fits[lane] != 0);
+        __syncthreads();
+        const int hit = m != 0 ? __ffs(m) - 1 : 32;  // the first length tried that fits
+        hi = min(lo + hit * step, hi);
+        lo = hit > 0 ? min(lo + (hit - 1) * step + 1, hi) : hi;
+    }
+    return lo;
+}
+
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int32_t* __restrict__ q_start, int max_new,
             int tree, char* plan, PlanShape shape) {
     __shared__ int64_t s_warp[32];
     __shared__ int s_hist[kBuckets];
-    __shared__ int s_max;
+    __shared__ int s_first[kPlanThreads];  // units of the items, then their first pieces
+    __shared__ int s_max, s_few_max, s_fits[32];
     griddep_enter();
     const int tid = threadIdx.x, G = Hq / c.Hkv;
     Entry* few = reinterpret_cast<Entry*>(plan + shape.off_few);
@@ -129,21 +153,13 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
         int64_t blocks;
         const int mine = tid < n_pairs ? pairs[tid].nblk : 0;
         scan_block<int64_t>(mine, s_warp, &blocks);
-        // the shortest range (two blocks at least) at which the items fit one wave: the even share, unless
-        // rounding up makes too many; then by halving between it and one range a row block
         const int slots = shape.sms / c.Hkv;
-        int len = (int)max((int64_t)2, (blocks + slots - 1) / slots), most = max(s_max, len);
-        int64_t items, first;
-        for (int lo = len;;) {
-            first = scan_block<int64_t>((mine + len - 1) / len, s_warp, &items);
-            if (items > slots) {
-                lo = len + 1;
-            } else {
-                if (len == lo) break;
-                most = len;
-            }
-            len = (lo + most) / 2;
-        }
+        s_first[tid] = mine;
+        __syncthreads();
+        const int len =
+            piece_length(s_first, n_pairs, slots, (int)max((int64_t)2, (blocks + slots - 1) / slots), s_max, s_fits);
+        int64_t items;
+        const int64_t first = scan_block<int64_t>((mine + len - 1) / len, s_warp, &items);
         int64_t splits, split_parts;
         const int ranges = (mine + len - 1) / len;
         const int64_t group = scan_block<int64_t>(ranges > 1, s_warp, &splits);
@@ -177,20 +193,64 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
         }
     }
     int64_t units = 0;
+    if (tid == 0) s_few_max = 1;
+    __syncthreads();
     for (int e0 = 0; e0 < n_few; e0 += kPlanThreads) {
         const int e = e0 + tid;
         int64_t total;
         const int64_t before = scan_block<int64_t>(e < n_few ? (int64_t)few[e].units * c.Hkv : 0, s_warp, &total);
         if (e < n_few) prefix[e] = units + before;
+        if (e < n_few) atomicMax(&s_few_max, few[e].units);
         units += total;
     }
     __syncthreads();
-    // a unit for every warp at least: a CTA's own start and end cost more than the keys it would take over
-    const int64_t want = (units + shape.few_warps - 1) / shape.few_warps;
-    const int ctas = (int)(want < shape.ctas ? want : shape.ctas);
-    for (int k = tid; k < shape.ctas; k += kPlanThreads) {
-        Start s{};
-        if (k < ctas) {
+    // Where every item can have CTAs of its own (items no more than CTAs), pieces of one length: a CTA that ends
+    // one item and starts the next pays the latencies of both, about as long as kSwitch units take.  A unit a
+    // warp at least.
+    const int kSwitch = 5 * shape.few_warps / 2;
+    int ctas = 0;
+    bool own_ctas = false;
+    if (units > 0 && (int64_t)n_few * c.Hkv <= shape.ctas) {
+        const int mine = tid < n_few ? few[tid].units : 0;
+        const int slots = shape.ctas / c.Hkv;
+        const int64_t even = (units + shape.ctas - 1) / shape.ctas;
+        s_first[tid] = mine;
+        __syncthreads();
+        const int len = piece_length(s_first, n_few, slots, (int)max((int64_t)shape.few_warps, even), s_few_max, s_fits);
+        int64_t items;
+        const int64_t first = scan_block<int64_t>((mine + len - 1) / len, s_warp, &items);
+        if (len <= even + kSwitch || len == shape.few_warps) {
+            own_ctas = true;
+            ctas = (int)items * c.Hkv;
+            if (tid < n_few) s_first[tid] = (int)first;
+            __syncthreads();
+            for (int k = tid; k < ctas; k += kPlanThreads) {
+                const int piece = k / c.Hkv;
+                int lo = 0, hi = n_few;  // the entry with s_first[lo] <= piece < s_first[lo + 1]
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (s_first[mid] <= piece) lo = mid;
+                    else hi = mid;
+                }
+                Start s{};
+                s.e = few[lo];
+                s.entry = lo;
+                s.head = k - piece * c.Hkv;
+                s.pieces = (s.e.units + len - 1) / len;
+                const int j = piece - s_first[lo], each = s.e.units / s.pieces, left = s.e.units % s.pieces;
+                s.unit = each * j + min(j, left);
+                s.count = each + (j < left);
+                s.ctas = ctas;
+                s.step = c.Hkv;
+                s.cta0 = s_first[lo] * c.Hkv + s.head;
+                start[k] = s;
+            }
+        }
+    }
+    if (!own_ctas) {
+        const int64_t want = (units + shape.few_warps - 1) / shape.few_warps;
+        ctas = (int)(want < shape.ctas ? want : shape.ctas);
+        for (int k = tid; k < ctas; k += kPlanThreads) {
             const int64_t u = first_unit(units, ctas, k);
             int lo = 0, hi = n_few;  // the entry with prefix[lo] <= u < prefix[lo + 1]
             while (hi - lo > 1) {
@@ -199,14 +259,17 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
                 else hi = mid;
             }
             const int64_t in = u - prefix[lo];
+            Start s{};
             s.e = few[lo];
             s.entry = lo;
             s.head = (int)(in / s.e.units);
             s.unit = (int)(in % s.e.units);
             s.item_first = prefix[lo] + (int64_t)s.head * s.e.units;
-            s.count = first_unit(units, ctas, k + 1) - u;
+            s.count = (int)(first_unit(units, ctas, k + 1) - u);
+            s.ctas = ctas;
+            s.total = units;
+            start[k] = s;
         }
-        start[k] = s;
     }
     if (tid == 0) {
         PlanHead h{};
@@ -224,7 +287,6 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
         h.ctas = shape.ctas;
         h.n_few = n_few;
         h.few_ctas = ctas;
-        h.few_units = units;
         h.n_wide = n_wide;
         h.n_groups = n_groups;
         *reinterpret_cast<PlanHead*>(plan) = h;
