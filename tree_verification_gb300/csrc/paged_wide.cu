@@ -15,8 +15,8 @@
 // pairs and feeds the PV product from there.  The pipeline (rings, barriers,
 // the order of the products) is that of the dense persistent kernel
 // (attention_tcp.cu).  What pages and ragged chunks change:
-//   * a block of K or V comes in pieces, one TMA box per page (a page of 128
-//     rows or more is one box); the producer's lanes each hold a page number,
+//   * a block of K or V comes in pieces, one TMA box per page (a block inside
+//     a page of 128 rows or more is one box); the producer's lanes each hold a page number,
 //     fetched one block ahead, and issue their own box.  A page that the
 //     item's keys do not reach, or outside the pool, is a box out of bounds:
 //     zeros.
@@ -35,6 +35,7 @@
 #include <cudaTypedefs.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "paged.cuh"
 #include "tc_ptx.cuh"
@@ -49,8 +50,11 @@ constexpr int BN = kBlockKeys;
 constexpr int SK = 2;  // K ring depth
 constexpr int SV = 3;  // V ring depth
 constexpr int NTHREADS = 320;
-constexpr uint32_t BOX_BYTES = BN * 64 * 2;          // 128 keys (or rows) x 64 dims
-constexpr uint32_t BLK_BYTES = 2 * BOX_BYTES;        // one K or V block
+// A K or V block lies as 16 groups of 8 keys, a group as its two halves of 64 dims (8 rows of 128 bytes each,
+// 128-byte swizzle): groups 2 KB apart, halves 1 KB.  So one box brings a page's rows with all their dims, and
+// both products still find their operand at one stride.
+constexpr uint32_t HALF_BYTES = 1024, GROUP_BYTES = 2048;
+constexpr uint32_t BLK_BYTES = (BN / 8) * GROUP_BYTES;
 constexpr uint32_t Q_TILE_BYTES = 2 * 128 * 64 * 2;  // 128 rows x 128 dims
 constexpr uint32_t OFF_Q = 0;
 constexpr uint32_t OFF_K = OFF_Q + 2 * Q_TILE_BYTES;
@@ -99,6 +103,14 @@ template <int DT>
 __host__ __device__ constexpr uint32_t idesc(int N, bool b_mn) {
     return (1u << 4) | (DT == GRAFT_BF16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? (1u << 16) : 0u) |
            ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
+        "%6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
 }
 // a pair of weights rounded, and their sum in 32 bits
 template <int DT>
@@ -229,23 +241,22 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
         // ------------------------------------------------------------ producer: every lane issues its own boxes
         const int page_box = min(a.c.page_rows, BN);  // rows of a box
         const int pieces = BN / page_box;
-        const int piece = lane >> 1, half = lane & 1;
-        const bool issues = piece < pieces;
+        const bool issues = lane < pieces;
         struct Cur {
             int k, j;      // place in the deal (-1: past the end), block
             int kvh;
             int blk0, nblk, keys, tok, two, b;  // of the item
-            int row;       // first pool row of this lane's box of block j (out of bounds: zeros)
+            int row;       // first pool row / 8 of this lane's box of block j (out of bounds: zeros)
         };
         auto lookup = [&](Cur& c) {
             if (c.k < 0 || !issues) return;
-            const int key = (c.blk0 + c.j) * BN + piece * page_box;
-            int row = 0x7fffffff - 256;
+            const int key = (c.blk0 + c.j) * BN + lane * page_box;
+            int row = 0x7fffffff >> 3;
             if (key < c.keys) {
                 const int page = a.c.block_table[(int64_t)c.b * a.c.max_pages + (key >> a.page_shift)];
                 if (page >= 0 && page < a.c.num_pages)
-                    row = (page << a.page_shift) + (key & (a.c.page_rows - 1));
-                else if (half == 0)
+                    row = ((page << a.page_shift) + (key & (a.c.page_rows - 1))) >> 3;
+                else
                     flag_status(a.c.status, GRAFT_STATUS_PAGE);
             }
             c.row = row;
@@ -276,7 +287,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
             if (lane == 0) mbar_expect_tx(full, BLK_BYTES);
             __syncwarp();
             if (issues)
-                tma_load_3d(dst + half * BOX_BYTES + piece * page_box * 128, map, full, half * 64, c.kvh, c.row);
+                tma_load_5d(dst + lane * (page_box / 8) * GROUP_BYTES, map, full, 0, 0, 0, c.row, c.kvh);
             advance(c);
             lookup(c);
         };
@@ -335,8 +346,8 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
             const uint32_t idS = idesc<DT>(BN, false);
             const uint32_t idO = idesc<DT>(HD, true);
             const uint64_t q_desc = sdesc_sw128(base + OFF_Q, 16, 1024);
-            const uint64_t k_desc = sdesc_sw128(base + OFF_K, 16, 1024);
-            const uint64_t v_desc = sdesc_sw128(base + OFF_V, BOX_BYTES, 1024);
+            const uint64_t k_desc = sdesc_sw128(base + OFF_K, 16, GROUP_BYTES);
+            const uint64_t v_desc = sdesc_sw128(base + OFF_V, HALF_BYTES, GROUP_BYTES);
             int kst = 0, kph = 0;
             int vst = 0, vph = 0;
             uint32_t pph0 = 0, pph1 = 0;  // phases of the tiles' P barriers
@@ -357,7 +368,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
                     if (kk == HD / 16 - 2) ready = test_pre(nxt);
-                    const uint32_t off = (kk >> 2) * BOX_BYTES + (kk & 3) * 32;
+                    const uint32_t off = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
                     const uint32_t qoff = t * Q_TILE_BYTES + (kk >> 2) * (Q_TILE_BYTES / 2) + (kk & 3) * 32;
                     mma_bf16_ss(tmem + TM_S + t * 128, q_desc + (qoff >> 4), kd + (off >> 4), idS, kk > 0);
                 }
@@ -375,22 +386,19 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk) {
                     if (kk == BN / 16 - 2) ready = test_pre(nxt);
-                    mma_bf16_ts(tmem + TM_O + t * 128, p + kk * 8, vd + ((kk * 2048) >> 4), idO, !first || kk > 0);
+                    mma_bf16_ts(tmem + TM_O + t * 128, p + kk * 8, vd + ((kk * 2 * GROUP_BYTES) >> 4), idO, !first || kk > 0);
                 }
                 if (last) mma_commit(bar(BAR_VE + vst));
                 return ready;
             };
             bool ok = true;
             int q = 0, q1 = 0;  // items issued; those of two tiles
-            for (int k = 0; ok; ++k) {
-                const int i = item_index(k, n_items);
-                if (i < 0) break;
-                const Wide* w = wide + i / a.c.Hkv;
-                const int nblk = w->nblk;
-                const bool two = w->two != 0;
+            // one item's products; a copy each for one and two tiles, so that the loop decides nothing
+            auto run_item = [&](auto two_tiles, int nblk) {
+                constexpr bool two = decltype(two_tiles)::value;
                 ok = mbar_wait(bar(BAR_Q), q & 1, kWaitNs) && !aborted(abort_flag) &&
                      mbar_wait(bar(BAR_KF + kst), kph, kWaitNs);
-                if (!ok) break;
+                if (!ok) return;
                 tc_fence_after();
                 Pre vf{BAR_VF + vst, (uint32_t)vph};
                 bool vf_ready = group_S(0, !two, two ? none : vf);
@@ -436,6 +444,15 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                 ++ndone;
                 ++q;
                 q1 += two;
+            };
+            for (int k = 0; ok; ++k) {
+                const int i = item_index(k, n_items);
+                if (i < 0) break;
+                const Wide& w = wide[i / a.c.Hkv];
+                if (w.two != 0)
+                    run_item(std::true_type{}, w.nblk);
+                else
+                    run_item(std::false_type{}, w.nblk);
             }
             if (!ok && !aborted(abort_flag)) raise_abort(abort_flag, a.c.status);
         }
@@ -455,34 +472,35 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
         for (int k = 0; ok; ++k) {
             const int i = item_index(k, n_items);
             if (i < 0) break;
-            const int kvh = i % a.c.Hkv;
-            int nblk, blk0, edge, keys, limit, L;
-            uint64_t anc = 0;
+            // The block loop holds only counts; an edge block reads the item and the row's mask again, and so
+            // does the epilogue.
+            int nblk, edge;
             bool two;
             {
-                const Wide w = wide[i / a.c.Hkv];
+                const Wide& w = wide[i / a.c.Hkv];
                 nblk = w.nblk;
-                blk0 = w.blk0;
-                keys = w.keys;
-                L = w.L;
                 two = w.two != 0;
-                const int tok = w.tok0 + t * T + rtok;
+                // first block that some row of the tile does not see whole
+                edge = (a.mask != nullptr ? w.L : min(w.L + w.tok0 + t * T + 1, w.keys)) / BN - w.blk0;
+            }
+            auto row_of = [&](const Wide& w, int& tok, int& limit, uint64_t& anc) -> bool {
+                tok = w.tok0 + t * T + rtok;
                 const bool row_ok = rtok < T && tok < w.n;
                 limit = 0;
+                anc = 0;
                 if (row_ok) {
-                    limit = a.mask != nullptr ? L : L + tok + 1;
+                    limit = a.mask != nullptr ? w.L : w.L + tok + 1;
                     if (a.mask != nullptr)
                         anc = a.mask[w.q0 + tok] & (w.n >= 64 ? ~0ull : ((1ull << w.n) - 1ull));
                 }
-                // first block that some row of the tile does not see whole
-                edge = (a.mask != nullptr ? L : min(L + w.tok0 + t * T + 1, keys)) / BN - blk0;
-            }
+                return row_ok;
+            };
             if (t == 1 && !two) {
                 gv += nblk;
                 ++q;
                 continue;
             }
-            volatile uint32_t* odd_word = odd_item + (two ? (n_two & 1) : 2 + ((q - n_two) & 1));
+            auto odd_word = [&]() { return odd_item + (two ? (n_two & 1) : 2 + ((q - n_two) & 1)); };
             // (a row that sees none of the range's first block sees none of the range: new rows see a run of keys
             // from the front, and a tree's 64 keys lie in one block unless prefix keys come first; so the maximum
             // of a row that is still -inf after the first block stays so, and its weights are 0)
@@ -494,7 +512,26 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                     if (!ok) break;
                     ++g;
                     tc_fence_after();
-                    const int kb = (blk0 + j) * BN;
+                    if (j >= edge) {
+                        // Masked scores are written back as -inf, in a pass of their own over S in tensor memory:
+                        // the block loop proper carries no masking code (inlined it cost all blocks 4%).
+                        const Wide& w = wide[i / a.c.Hkv];
+                        int tok, limit;
+                        uint64_t anc;
+                        row_of(w, tok, limit, anc);
+                        uint32_t keep[4];
+                        keep_bits(keep, (w.blk0 + j) * BN, limit, w.L, anc);
+#pragma unroll
+                        for (int x = 0; x < BN / 32; ++x) {
+                            float s[32];
+                            tmem_ld32(sbuf + x * 32, s);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) s[y] = ((keep[x] >> y) & 1u) ? s[y] : -INFINITY;
+                            tmem_st32(sbuf + x * 32, s);
+                        }
+                        tmem_wait_st();
+                    }
                     if (t == 0 && j >= edge) {
                         // Tile 0 cleans the V block before either tile's PV reads it: rows past the last key
                         // (their pages may hold anything) and infinite or NaN elements that masked rows would
@@ -504,27 +541,30 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                         if (!ok) break;
                         uint8_t* v0 = gbase + OFF_V + (vb % SV) * BLK_BYTES;
                         bool odd = false;
-                        const int lo = max(L - kb, 0), n = BN - lo;
+                        const Wide& w = wide[i / a.c.Hkv];
+                        const int kb = (w.blk0 + j) * BN, keys = w.keys;
+                        const int lo = max(w.L - kb, 0), n = BN - lo;
                         for (int x = r; x < n * 16; x += 128) {
                             const int rr = lo + x / 16, c16 = x % 16;
-                            uint4* p = reinterpret_cast<uint4*>(v0 + (c16 >= 8 ? BOX_BYTES : 0) + rr * 128 +
+                            uint4* p = reinterpret_cast<uint4*>(v0 + (rr >> 3) * GROUP_BYTES +
+                                                                (c16 >> 3) * HALF_BYTES + (rr & 7) * 128 +
                                                                 (c16 & 7) * 16);
                             uint4 v = *p;
                             if (kb + rr >= keys) {
                                 *p = make_uint4(0, 0, 0, 0);
                             } else if (E::odd(v.x) || E::odd(v.y) || E::odd(v.z) || E::odd(v.w)) {
                                 odd = true;
-                                uint32_t* w = &v.x;
+                                uint32_t* e = &v.x;
 #pragma unroll
                                 for (int y = 0; y < 4; ++y) {
-                                    const float2 f = E::up(w[y]);
-                                    w[y] = (isfinite(f.x) ? (w[y] & 0xffffu) : 0u) |
-                                           (isfinite(f.y) ? (w[y] & 0xffff0000u) : 0u);
+                                    const float2 f = E::up(e[y]);
+                                    e[y] = (isfinite(f.x) ? (e[y] & 0xffffu) : 0u) |
+                                           (isfinite(f.y) ? (e[y] & 0xffff0000u) : 0u);
                                 }
                                 *p = v;
                             }
                         }
-                        if (odd) *odd_word = (uint32_t)k + 1;
+                        if (odd) *odd_word() = (uint32_t)k + 1;
                         fence_proxy_async_smem();
                     }
                     float alpha = 1.f;
@@ -539,13 +579,6 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
 #pragma unroll
                         for (int x = 0; x < BN / 32; ++x) tmem_ld32(sbuf + x * 32, s + x * 32);
                         tmem_wait_ld();
-                        if (j >= edge) {
-                            uint32_t w[4];
-                            keep_bits(w, kb, limit, L, anc);
-#pragma unroll
-                            for (int x = 0; x < BN; ++x)
-                                s[x] = ((w[x >> 5] >> (x & 31)) & 1u) ? s[x] : -INFINITY;
-                        }
                         const bool full = j == 0 || pass == 1;
                         if (full) {
                             float m8[8];
@@ -604,8 +637,10 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
             tc_fence_after();
             {
                 const Wide w = wide[i / a.c.Hkv];
-                const int tok = w.tok0 + t * T + rtok;
-                const bool row_ok = rtok < T && tok < w.n;
+                const int kvh = i % a.c.Hkv;
+                int tok, limit;
+                uint64_t anc;
+                const bool row_ok = row_of(w, tok, limit, anc);
                 const float inv = l_sum != 0.f ? 1.f / l_sum : 0.f;
                 const bool direct = w.part < 0;
                 typename E::T* orow =
@@ -641,9 +676,9 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                 }
                 if (row_ok && !direct)
                     a.wide_lse[prow] = l_sum == 0.f ? -INFINITY : m_used + log2f(l_sum) - kLift;
-                if (*odd_word == (uint32_t)k + 1 && row_ok)
+                if (*odd_word() == (uint32_t)k + 1 && row_ok)
                     add_odd<DT>(a.c, a.V, a.c.block_table + (int64_t)w.b * a.c.max_pages, a.page_shift, kvh,
-                                max(w.blk0 * BN, L), min((w.blk0 + w.nblk) * BN, keys), limit, L, anc,
+                                max(w.blk0 * BN, w.L), min((w.blk0 + w.nblk) * BN, w.keys), limit, w.L, anc,
                                 direct ? orow : nullptr, direct ? nullptr : part);
             }
             gv += nblk;
@@ -749,12 +784,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-bool encode(CUtensorMap* m, int dtype, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
+bool encode(CUtensorMap* m, int dtype, int rank, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
             const cuuint32_t* box) {
     auto enc = encoder();
     if (enc == nullptr) return false;
-    cuuint32_t es[3] = {1, 1, 1};
-    return enc(m, dtype == GRAFT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+    cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return enc(m, dtype == GRAFT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
                const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -790,15 +825,16 @@ int wide_launch(const AttnArgs& a, cudaStream_t st) {
         const cuuint64_t dims[3] = {HD, (cuuint64_t)a.Hq, (cuuint64_t)a.N};
         const cuuint64_t strides[2] = {HD * es, (cuuint64_t)a.q_stride * es};
         const cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)a.shape.tile_tokens};
-        if (!encode(&m.q, a.c.dtype, a.Q, dims, strides, box)) return GRAFT_ERR_CUDA;
+        if (!encode(&m.q, a.c.dtype, 3, a.Q, dims, strides, box)) return GRAFT_ERR_CUDA;
     }
     {
-        // pools: (dim, KV head, row)
-        const cuuint64_t dims[3] = {HD, (cuuint64_t)a.c.Hkv, (cuuint64_t)a.c.num_pages * a.c.page_rows};
-        const cuuint64_t strides[2] = {HD * es, (cuuint64_t)a.c.Hkv * HD * es};
-        const cuuint32_t box[3] = {64, 1, (cuuint32_t)(a.c.page_rows < BN ? a.c.page_rows : BN)};
-        if (!encode(&m.k, a.c.dtype, a.K, dims, strides, box)) return GRAFT_ERR_CUDA;
-        if (!encode(&m.v, a.c.dtype, a.V, dims, strides, box)) return GRAFT_ERR_CUDA;
+        // pools: (dim of a half, row of a group, half, group, KV head)
+        const cuuint64_t row = (cuuint64_t)a.c.Hkv * HD * es;
+        const cuuint64_t dims[5] = {64, 8, 2, (cuuint64_t)a.c.num_pages * a.c.page_rows / 8, (cuuint64_t)a.c.Hkv};
+        const cuuint64_t strides[4] = {row, 64 * es, 8 * row, HD * es};
+        const cuuint32_t box[5] = {64, 8, 2, (cuuint32_t)(a.c.page_rows < BN ? a.c.page_rows : BN) / 8, 1};
+        if (!encode(&m.k, a.c.dtype, 5, a.K, dims, strides, box)) return GRAFT_ERR_CUDA;
+        if (!encode(&m.v, a.c.dtype, 5, a.V, dims, strides, box)) return GRAFT_ERR_CUDA;
     }
     return a.c.dtype == GRAFT_BF16 ? launch<GRAFT_BF16>(a, m, st) : launch<GRAFT_FP16>(a, m, st);
 }
