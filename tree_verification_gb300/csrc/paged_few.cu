@@ -27,6 +27,7 @@ namespace paged {
 namespace {
 
 constexpr int kStages = 3;
+constexpr int kAhead = 4;                          // units a warp brings into L2 ahead of the grid wait
 constexpr int kUnit = 16;                          // keys of a unit
 constexpr int kUnitBytes = kUnit * HD * 2;         // of K, or of V
 constexpr int kRowPad = 132;                       // floats of a staged partial row: 4 banks apart
@@ -140,41 +141,55 @@ __device__ __forceinline__ void join_pieces(const AttnArgs& a, const Start& at, 
     int have = 0;
     for (int p0 = 0; p0 < pieces;) {
         const int n = min(cap - have, pieces - p0);
+        // a run's last item (the one that it starts) has the CTA's second slot
+        auto slot_of = [&](int q) -> int64_t { return step > 0 ? (c0 + q * step) * 2 : (c0 + q) * 2 + (q == 0 ? 1 : 0); };
         for (int p = warp; p < n; p += W) {
-            // a run's last item (the one that it starts) has the CTA's second slot
-            const int q = p0 + p;
-            const int64_t slot = step > 0 ? (c0 + q * step) * 2 : (c0 + q) * 2 + (q == 0 ? 1 : 0);
-            const float* src = a.few.o + slot * kFewRows * HD;
+            const float* src = a.few.o + slot_of(p0 + p) * kFewRows * HD;
             const uint32_t dst = smem_u32(s_o + (size_t)(have + p) * row_floats);
 #pragma unroll 4
             for (int i = lane; i < n_rows * 32; i += 32) cp_async16(dst + i * 16, src + i * 4, true);
-            if (lane < n_rows) s_ml[(have + p) * n_rows + lane] = __ldcg(a.few.ml + slot * kFewRows + lane);
+        }
+        for (int x = tid; x < n * n_rows; x += W * 32) {
+            const int p = x / n_rows, r = x - p * n_rows;
+            s_ml[have * n_rows + x] = __ldcg(a.few.ml + slot_of(p0 + p) * kFewRows + r);
         }
         cp_commit();
         cp_wait<0>();
         __syncthreads();
         p0 += n;
         const int all = have + n;
-        for (int x = tid; x < n_rows * 32; x += W * 32) {
-            const int r = x >> 5;
+        for (int r = warp; r < n_rows; r += W) {
+            // a lane weighs one piece, and sums four dims over all
             float m = -INFINITY, l = 0.f;
-            for (int p = 0; p < all; ++p) m = fmaxf(m, s_ml[p * n_rows + r].x);
+            for (int p = lane; p < all; p += 32) m = fmaxf(m, s_ml[p * n_rows + r].x);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int p = 0; p < all; ++p) {
-                const float2 ml = s_ml[p * n_rows + r];
-                const float f = ex2(ml.x - safe(m));
-                const float4 v = *reinterpret_cast<const float4*>(s_o + (size_t)p * row_floats + x * 4);
-                acc.x += f * v.x;
-                acc.y += f * v.y;
-                acc.z += f * v.z;
-                acc.w += f * v.w;
-                l += f * ml.y;
+            for (int q0 = 0; q0 < all; q0 += 32) {
+                float f = 0.f;
+                if (q0 + lane < all) {
+                    const float2 ml = s_ml[(q0 + lane) * n_rows + r];
+                    f = ex2(ml.x - safe(m));
+                    l += f * ml.y;
+                }
+                const int n = min(all - q0, 32);
+#pragma unroll 8
+                for (int p = 0; p < n; ++p) {
+                    const float g = __shfl_sync(0xffffffffu, f, p);
+                    const float4 v =
+                        *reinterpret_cast<const float4*>(s_o + (size_t)(q0 + p) * row_floats + r * HD + lane * 4);
+                    acc.x += g * v.x;
+                    acc.y += g * v.y;
+                    acc.z += g * v.z;
+                    acc.w += g * v.w;
+                }
             }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
             if (p0 == pieces) {
                 put_row<DT>(a, at.e, kvh, r, acc, l);
             } else {
-                *reinterpret_cast<float4*>(s_o + x * 4) = acc;
+                *reinterpret_cast<float4*>(s_o + r * HD + lane * 4) = acc;
                 __syncwarp();  // (a row's maxima are read by the warp that sums the row alone)
                 if (lane == 0) s_ml[r] = make_float2(m, l);
             }
@@ -190,28 +205,13 @@ few_kernel(const __grid_constant__ AttnArgs a) {
     using E = Elem<DT>;
     using T = typename E::T;
     extern __shared__ __align__(128) unsigned char smem[];
-    griddep_enter();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cta = blockIdx.x;
     const Entry* entries = reinterpret_cast<const Entry*>(a.plan + a.shape.off_few);
     // The run's state is the CTA's, not a thread's: shared memory holds it, the registers are for O and Q.
     __shared__ Start s_at, s_pending[2];
+    __shared__ PlanHead s_head;
     __shared__ int s_n_pending;
-    {
-        const PlanHead head = *reinterpret_cast<const PlanHead*>(a.plan);
-        const Start first = reinterpret_cast<const Start*>(a.plan + a.shape.off_start)[cta];
-        if (!plan_fits(a, head)) {
-            if (cta == 0 && tid == 0) flag_status(a.c.status, GRAFT_STATUS_PLAN);
-            return;
-        }
-        if (cta >= head.few_ctas) return;
-        if (tid == 0) {
-            s_at = first;
-            s_n_pending = 0;
-        }
-    }
-    __syncthreads();
-
     float* s_part = reinterpret_cast<float*>(smem);
     float2* s_ml = reinterpret_cast<float2*>(smem + ring_bytes(kWarps, RT) + q_bytes(RT));
     const uint32_t ring = smem_u32(smem) + warp * (kStages * 2 * kUnitBytes);
@@ -223,54 +223,116 @@ few_kernel(const __grid_constant__ AttnArgs a) {
     const float sl2 = a.scale * 1.4426950408889634f;
     const int64_t key_stride = (int64_t)a.c.Hkv * HD;
 
+    // ---- the item at hand
+    int u0 = 0, u1 = 0, kvh = 0, keys = 0, L = 0, n_new = 0;
+    int mine = 0;                 // this warp's units (may be <= 0)
+    int pages = -1, pages_at = 0; // pages of this warp's units pages_at .. pages_at + 31, one a lane
+    const int32_t* table = a.c.block_table;
+    const Entry& e = s_at.e;
+    auto begin = [&]() {
+        keys = e.keys;
+        L = e.L;
+        n_new = e.n;
+        u0 = s_at.unit;
+        u1 = min(e.units, u0 + s_at.count);
+        kvh = s_at.head;
+        table = a.c.block_table + (int64_t)e.b * a.c.max_pages;
+        mine = (u1 - u0 - warp + kWarps - 1) / kWarps;
+    };
+    auto fetch_pages = [&](int i0, bool flag) {
+        const int u = u0 + warp + (i0 + lane) * kWarps;
+        int p = -1;
+        if (u < u1) {
+            p = __ldcg(table + ((u * kUnit) >> a.page_shift));
+            if (p < 0 || p >= a.c.num_pages) {
+                p = -1;
+                if (flag) flag_status(a.c.status, GRAFT_STATUS_PAGE);
+            }
+        }
+        return p;
+    };
+    auto load = [&](int i) {
+        if (i < mine) {
+            if (i - pages_at >= 32) {
+                pages_at = i;
+                pages = fetch_pages(i, true);
+            }
+            const int key0 = (u0 + warp + i * kWarps) * kUnit;
+            const int page = __shfl_sync(0xffffffffu, pages, i - pages_at);
+            const int64_t row = ((int64_t)max(page, 0) << a.page_shift) + (key0 & (a.c.page_rows - 1));
+            const int64_t off = (row * a.c.Hkv + kvh) * HD;
+            const uint32_t k = ring + (i % kStages) * 2 * kUnitBytes, v = k + kUnitBytes;
+#pragma unroll
+            for (int x = 0; x < kUnit * 16 / 32; ++x) {
+                const int r = x * 2 + (lane >> 4), ch = lane & 15;
+                const bool ok = page >= 0 && key0 + r < keys;
+                const int64_t o = off + (ok ? r * key_stride : 0) + ch * 8;
+                cp_async16(k + swz(r, ch), Kp + o, ok);
+                cp_async16(v + swz(r, ch), Vp + o, ok);
+            }
+        }
+        cp_commit();
+    };
+
+    // ---- before the previous kernel has finished
+    // The plan and the pages are read ahead of the grid wait and the first units brought into L2: a guess, since
+    // whatever runs before may still write them.  Every index is checked, the reads are read again after the wait,
+    // and a guess that does not hold is dropped; nothing but L2's contents depends on it (L2 is where all writes
+    // meet, so a line brought in early is not stale).
+    constexpr int kHeadWords = sizeof(PlanHead) / 4, kStartWords = sizeof(Start) / 4;
+    static_assert(kHeadWords + kStartWords <= kWarps * 32, "one word a thread");
+    const int32_t* word = tid < kHeadWords
+                              ? reinterpret_cast<const int32_t*>(a.plan) + tid
+                              : reinterpret_cast<const int32_t*>(a.plan + a.shape.off_start) + cta * kStartWords +
+                                    (tid - kHeadWords);
+    int32_t* s_word = tid < kHeadWords ? reinterpret_cast<int32_t*>(&s_head) + tid
+                                       : reinterpret_cast<int32_t*>(&s_at) + (tid - kHeadWords);
+    const bool has_word = tid < kHeadWords + kStartWords;
+    int32_t guess = 0;
+    if (has_word) *s_word = guess = __ldcg(word);
+    if (tid == 0) s_n_pending = 0;
+    __syncthreads();
+    const bool sound = plan_fits(a, s_head) && cta < s_head.few_ctas && e.b >= 0 && e.b < a.c.n_seqs && e.keys > 0 &&
+                 e.L >= 0 && e.keys <= (int64_t)a.c.max_pages * a.c.page_rows &&
+                 e.units == (e.keys - 1) / kUnit + 1 && s_at.unit >= 0 && s_at.unit < e.units && s_at.count > 0 &&
+                 s_at.head >= 0 && s_at.head < a.c.Hkv && e.row0 == 0 && e.rows > 0 && e.rows <= RT * 16 && e.q0 >= 0 &&
+                 e.q0 < a.N && (e.rows - 1) / a.G < a.N - e.q0;
+    if (sound) {
+        begin();
+        pages = fetch_pages(0, false);
+        for (int i = 0; i < min(mine, kAhead); ++i) {
+            const int key0 = (u0 + warp + i * kWarps) * kUnit;
+            const int page = __shfl_sync(0xffffffffu, pages, i);
+            if (page < 0) continue;
+            const int64_t row = ((int64_t)page << a.page_shift) + (key0 & (a.c.page_rows - 1));
+            const T* at = Kp + ((row + (lane >> 1)) * a.c.Hkv + kvh) * HD + (lane & 1) * 64;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(Vp + (at - Kp)));
+        }
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    // reads the plan anew; false: nothing to do
+    auto reread = [&]() -> bool {
+        cp_wait<0>();
+        __syncthreads();
+        if (has_word) *s_word = __ldcg(word);
+        __syncthreads();
+        if (!plan_fits(a, s_head)) {
+            if (cta == 0 && tid == 0) flag_status(a.c.status, GRAFT_STATUS_PLAN);
+            return false;
+        }
+        if (cta >= s_head.few_ctas) return false;
+        begin();
+        pages = fetch_pages(0, true);
+        return true;
+    };
+    if (!sound && !reread()) return;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) load(i);
+    bool guessed = sound;  // the first item is as yet a guess
+
     while (true) {
-        const Entry& e = s_at.e;
-        const int keys = e.keys, L = e.L, n_new = e.n;
-        const int u0 = s_at.unit;
-        const int u1 = min(e.units, u0 + s_at.count);
-        const int kvh = s_at.head;
-        const int32_t* table = a.c.block_table + (int64_t)e.b * a.c.max_pages;
-
-        // pages of this warp's next 32 units, one a lane
-        auto fetch_pages = [&](int i0) {
-            const int u = u0 + warp + (i0 + lane) * kWarps;
-            int p = -1;
-            if (u < u1) {
-                p = table[(u * kUnit) >> a.page_shift];
-                if (p < 0 || p >= a.c.num_pages) {
-                    p = -1;
-                    flag_status(a.c.status, GRAFT_STATUS_PAGE);
-                }
-            }
-            return p;
-        };
-        const int mine = (u1 - u0 - warp + kWarps - 1) / kWarps;  // this warp's units (may be <= 0)
-        int pages = fetch_pages(0), pages_at = 0;
-        auto load = [&](int i) {
-            if (i < mine) {
-                if (i - pages_at >= 32) {
-                    pages_at = i;
-                    pages = fetch_pages(i);
-                }
-                const int key0 = (u0 + warp + i * kWarps) * kUnit;
-                const int page = __shfl_sync(0xffffffffu, pages, i - pages_at);
-                const int64_t row = ((int64_t)max(page, 0) << a.page_shift) + (key0 & (a.c.page_rows - 1));
-                const int64_t off = (row * a.c.Hkv + kvh) * HD;
-                const uint32_t k = ring + (i % kStages) * 2 * kUnitBytes, v = k + kUnitBytes;
-#pragma unroll
-                for (int x = 0; x < kUnit * 16 / 32; ++x) {
-                    const int r = x * 2 + (lane >> 4), ch = lane & 15;
-                    const bool ok = page >= 0 && key0 + r < keys;
-                    const int64_t o = off + (ok ? r * key_stride : 0) + ch * 8;
-                    cp_async16(k + swz(r, ch), Kp + o, ok);
-                    cp_async16(v + swz(r, ch), Vp + o, ok);
-                }
-            }
-            cp_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) load(i);
-
         // Q: rows past the block read as zeros.  One row tile's fragments stay in registers, straight from
         // memory; two tiles' would not fit beside O, so they go through shared memory, read again every unit.
         uint32_t qf[RT > 1 ? 1 : 8][4];
@@ -291,9 +353,9 @@ few_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = t * 16 + (lane >> 2) + h * 8;
-                const bool ok = r < e.rows;
                 const int row = e.row0 + r, tok = row / a.G;
                 const int g = row - tok * a.G;
+                const bool ok = r < e.rows;
                 if (RT == 1) {
                     const T* q = Qp + (ok ? (int64_t)(e.q0 + tok) * a.q_stride + (kvh * a.G + g) * HD : 0);
 #pragma unroll
@@ -322,6 +384,24 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             for (int d = 0; d < 16; ++d) o[t][d][0] = o[t][d][1] = o[t][d][2] = o[t][d][3] = 0.f;
         }
 
+        if (guessed) {
+            // every read of the guess again, behind the reads that it issued
+            guessed = false;
+            const int now = fetch_pages(0, true);
+            if (__syncthreads_or(has_word && __ldcg(word) != guess)) {
+                if (!reread()) return;
+#pragma unroll 1
+                for (int i = 0; i < kStages - 1; ++i) load(i);
+                continue;
+            }
+            if (__any_sync(0xffffffffu, now != pages)) {
+                cp_wait<0>();
+                __syncwarp();
+                pages = now;
+#pragma unroll 1
+                for (int i = 0; i < kStages - 1; ++i) load(i);
+            }
+        }
         if (RT > 1) {
             cp_wait<0>();  // Q, and the first units with it
             __syncthreads();
@@ -534,8 +614,13 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             }
         }
         __syncthreads();
+        begin();
+        pages = fetch_pages(0, true);
+        pages_at = 0;
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) load(i);
     }
-    __threadfence();
+    // (the pieces are read from L2, after the barrier behind the counter's atomic; their writers fenced before it)
     for (int k = 0; k < s_n_pending; ++k) {
         join_pieces<DT, RT, kWarps>(a, s_pending[k], smem);
     }
