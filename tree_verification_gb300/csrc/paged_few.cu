@@ -300,6 +300,12 @@ few_kernel(const __grid_constant__ AttnArgs a) {
     if (sound) {
         begin();
         pages = fetch_pages(0, false);
+        if (warp == 0 && lane < e.rows) {
+            const int tok = lane / a.G;
+            const T* q = Qp + (int64_t)(e.q0 + tok) * a.q_stride + (kvh * a.G + lane - tok * a.G) * HD;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
+        }
         for (int i = 0; i < min(mine, kAhead); ++i) {
             const int key0 = (u0 + warp + i * kWarps) * kUnit;
             const int page = __shfl_sync(0xffffffffu, pages, i);
@@ -328,8 +334,6 @@ few_kernel(const __grid_constant__ AttnArgs a) {
         return true;
     };
     if (!sound && !reread()) return;
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) load(i);
     bool guessed = sound;  // the first item is as yet a guess
 
     while (true) {
@@ -384,14 +388,16 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             for (int d = 0; d < 16; ++d) o[t][d][0] = o[t][d][1] = o[t][d][2] = o[t][d][3] = 0.f;
         }
 
+        // (Q's reads, and those that check the guess, go ahead of the units': a unit's bytes take the SM's read
+        // port for longer than any of them)
+        const int now = guessed ? fetch_pages(0, true) : pages;
+        const int32_t again = guessed && has_word ? __ldcg(word) : guess;
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) load(i);
         if (guessed) {
-            // every read of the guess again, behind the reads that it issued
             guessed = false;
-            const int now = fetch_pages(0, true);
-            if (__syncthreads_or(has_word && __ldcg(word) != guess)) {
+            if (__syncthreads_or(again != guess)) {
                 if (!reread()) return;
-#pragma unroll 1
-                for (int i = 0; i < kStages - 1; ++i) load(i);
                 continue;
             }
             if (__any_sync(0xffffffffu, now != pages)) {
@@ -617,8 +623,6 @@ few_kernel(const __grid_constant__ AttnArgs a) {
         begin();
         pages = fetch_pages(0, true);
         pages_at = 0;
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) load(i);
     }
     // (the pieces are read from L2, after the barrier behind the counter's atomic; their writers fenced before it)
     for (int k = 0; k < s_n_pending; ++k) {
