@@ -63,7 +63,7 @@ struct Wide {
 };
 
 struct Group {
-    int32_t q0, n, tok0, ranges, part0, pad[3];
+    int32_t q0, n, tok0, tiles, ranges, part0, pad[2];
 };
 
 // Where a CTA of the few kernel starts: everything its first item needs, in one read.  Either a CTA takes an even
@@ -127,7 +127,7 @@ struct AttnArgs {
     int N, Hq, G, max_new, page_shift;
     PlanShape shape;
     FewWs few;
-    float* wide_o;    // [partial row blocks][2][128][128] normalised
+    float* wide_o;    // [partial row blocks][2][32][128][4] normalised: four dims of the 128 rows side by side
     float* wide_lse;  // [partial row blocks][2][128] log2-sum-exp
 };
 

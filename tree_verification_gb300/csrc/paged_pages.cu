@@ -12,18 +12,18 @@ namespace paged {
 namespace {
 
 // ---------------------------------------------------------------- compaction
-// One CTA per (layer, sequence).  A thread owns 16-byte columns of a row; it
-// moves rows in rising order, kBatch loads before their stores: the path
-// rises strictly, so path[t] >= t, and a row is overwritten only after every
-// move that reads it has read it (moves never read below their own t).
+// A CTA takes one sequence in every G-th layer, two layers at a time, so that
+// the look-up (two dependent reads) is paid once for both.  A thread owns 16-byte
+// columns of a row; it moves rows in rising order, kBatch loads (in two
+// layers) before their stores: the path rises strictly, so path[t] >= t, and
+// a row is overwritten only after every move that reads it has read it (moves
+// never read below their own t).
 constexpr int kMoveThreads = 256;
-constexpr int kBatch = 8;
+constexpr int kBatch = 3;
 
 // Where move t of sequence b reads and writes (rows of the pool), or the status bits that forbid it.
-__device__ __forceinline__ int find_move(const GraftPagedCache& c, int Kmax, const int32_t* path, int L, int b, int t,
+__device__ __forceinline__ int find_move(const GraftPagedCache& c, int Kmax, int p, int before, int L, int b, int t,
                                          int page_shift, int64_t* src, int64_t* dst) {
-    const int p = path[(int64_t)b * Kmax + t];
-    const int before = t > 0 ? path[(int64_t)b * Kmax + t - 1] : -1;
     if (p <= before || p >= Kmax) return GRAFT_STATUS_TREE;
     const int64_t from = (int64_t)L + p, to = (int64_t)L + t;
     if ((from >> page_shift) >= c.max_pages) return GRAFT_STATUS_LENGTH;
@@ -40,28 +40,53 @@ compact_rows_kernel(const __grid_constant__ GraftPagedCache c, int Kmax, const i
                     const int32_t* __restrict__ acc_len, int32_t* lengths_out, int page_shift) {
     __shared__ int64_t s_src[GRAFT_MAX_KMAX], s_dst[GRAFT_MAX_KMAX];
     griddep_enter();
-    const int l = blockIdx.x, b = blockIdx.y, t = threadIdx.x;
-    const int n = acc_len[b], L = c.lengths[b];
-    int bad = (n < 0 || n > Kmax) ? GRAFT_STATUS_TREE : L < 0 ? GRAFT_STATUS_LENGTH : 0;
-    if (!bad && t < n) bad = find_move(c, Kmax, path, L, b, t, page_shift, &s_src[t], &s_dst[t]);
-    if (bad && l == 0) flag_status(c.status, bad);
-    const int stop = __syncthreads_or(bad);
-    if (l == 0 && t == 0 && lengths_out != nullptr) lengths_out[b] = stop ? L : L + n;
-    if (stop || c.n_layers == 0) return;
+    const int b = blockIdx.y, t = threadIdx.x;
     const int per = c.Hkv * (HD / 8);  // 16-byte columns of a row
-    uint4* K = static_cast<uint4*>(c.K_layers[l]);
-    uint4* V = static_cast<uint4*>(c.V_layers[l]);
+    // everything that depends on nothing is read at once: the path, the lengths, the first pools
+    int p = 0, before = -1;
+    if (t < Kmax) {
+        p = path[(int64_t)b * Kmax + t];
+        if (t > 0) before = path[(int64_t)b * Kmax + t - 1];
+    }
+    const int n = acc_len[b], L = c.lengths[b];
+    auto pool_of = [&](int l, int x) -> uint4* {
+        return l < c.n_layers && x < 2 * per ? static_cast<uint4*>((x < per ? c.K_layers : c.V_layers)[l]) : nullptr;
+    };
+    const int G = gridDim.x;
+    uint4* pool0 = pool_of(blockIdx.x, t);
+    uint4* pool1 = pool_of(blockIdx.x + G, t);
+    int bad = (n < 0 || n > Kmax) ? GRAFT_STATUS_TREE : L < 0 ? GRAFT_STATUS_LENGTH : 0;
+    if (!bad && t < n) bad = find_move(c, Kmax, p, before, L, b, t, page_shift, &s_src[t], &s_dst[t]);
+    if (bad && blockIdx.x == 0) flag_status(c.status, bad);
+    const int stop = __syncthreads_or(bad);
+    if (blockIdx.x == 0 && t == 0 && lengths_out != nullptr) lengths_out[b] = stop ? L : L + n;
+    if (stop) return;
+    // moves that stay where they are (the root's, and those of a path that starts 0, 1, ...) come first
+    int first = 0;
+    while (first < n && s_src[first] == s_dst[first]) ++first;
+    // a thread's column in two layers at a time
     for (int x = t; x < 2 * per; x += kMoveThreads) {
-        uint4* pool = x < per ? K : V;
         const int col = x < per ? x : x - per;
-        for (int t0 = 0; t0 < n; t0 += kBatch) {
-            uint4 v[kBatch];
+        for (int l = blockIdx.x; l < c.n_layers; l += 2 * G) {
+            for (int t0 = first; t0 < n; t0 += kBatch) {
+                uint4 v[2][kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (t0 + k < n && s_src[t0 + k] != s_dst[t0 + k]) v[k] = pool[s_src[t0 + k] * per + col];
+                for (int k = 0; k < kBatch; ++k)
+                    if (t0 + k < n) {
+                        v[0][k] = pool0[s_src[t0 + k] * per + col];
+                        if (pool1 != nullptr) v[1][k] = pool1[s_src[t0 + k] * per + col];
+                    }
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (t0 + k < n && s_src[t0 + k] != s_dst[t0 + k]) pool[s_dst[t0 + k] * per + col] = v[k];
+                for (int k = 0; k < kBatch; ++k)
+                    if (t0 + k < n) {
+                        pool0[s_dst[t0 + k] * per + col] = v[0][k];
+                        if (pool1 != nullptr) pool1[s_dst[t0 + k] * per + col] = v[1][k];
+                    }
+            }
+            const int next_l = l + 2 * G < c.n_layers ? l + 2 * G : (int)blockIdx.x;
+            const int next_x = l + 2 * G < c.n_layers ? x : x + kMoveThreads;
+            pool0 = pool_of(next_l, next_x);
+            pool1 = pool_of(next_l + G, next_x);
         }
     }
 }
@@ -75,7 +100,10 @@ compact_lengths_kernel(const __grid_constant__ GraftPagedCache c, int Kmax, cons
     const int n = acc_len[b], L = c.lengths[b];
     int64_t src, dst;
     bool bad = n < 0 || n > Kmax || L < 0;
-    if (!bad && t < n) bad = find_move(c, Kmax, path, L, b, t, page_shift, &src, &dst) != 0;
+    if (!bad && t < n) {
+        const int before = t > 0 ? path[(int64_t)b * Kmax + t - 1] : -1;
+        bad = find_move(c, Kmax, path[(int64_t)b * Kmax + t], before, L, b, t, page_shift, &src, &dst) != 0;
+    }
     if (!__syncthreads_or(bad) && t == 0) c.lengths[b] = L + n;
 }
 
@@ -289,30 +317,33 @@ reserve_kernel(const __grid_constant__ GraftPagedCache c, const int32_t* __restr
         if (w.old[i] >= 0) atomicSub(c.page_refs + w.old[i], 1);
 }
 
-// Rows of the replaced last pages, every layer: a CTA copies up to 16 rows of K or V of one sequence.
+// Rows of the replaced last pages, every layer: a CTA copies up to kCopyRows rows of K or V of one sequence.  (CTAs
+// that took several layers each, the next one's rows read before this one's were written, were slower: 30 against
+// 26 us for a turnover of 48 samples in 36 layers.)
 constexpr int kCopyRows = 16;
-__global__ void __launch_bounds__(256)
+constexpr int kCopyThreads = 256;
+constexpr int kCopyBatch = 8;
+__global__ void __launch_bounds__(kCopyThreads)
 copy_tails_kernel(const __grid_constant__ GraftPagedCache c, const Tail* __restrict__ tails, int pieces,
                   int page_shift) {
     griddep_enter();
     const int b = blockIdx.x / pieces, r0 = (blockIdx.x - b * pieces) * kCopyRows;
+    uint4* pool = static_cast<uint4*>(((blockIdx.y & 1) ? c.V_layers : c.K_layers)[blockIdx.y >> 1]);
     const Tail tail = tails[b];
     const int rows = min(tail.rows - r0, kCopyRows);
     if (rows <= 0) return;
-    const int l = blockIdx.y >> 1;
-    uint4* pool = static_cast<uint4*>((blockIdx.y & 1) ? c.V_layers[l] : c.K_layers[l]);
     const int per = c.Hkv * (HD / 8);
     const uint4* from = pool + (((int64_t)tail.src << page_shift) + r0) * per;
     uint4* to = pool + (((int64_t)tail.dst << page_shift) + r0) * per;
     const int n = rows * per;  // rows of a page lie side by side
-    for (int x = threadIdx.x; x < n; x += 256 * 8) {
-        uint4 v[8];
+    for (int x = threadIdx.x; x < n; x += kCopyThreads * kCopyBatch) {
+        uint4 v[kCopyBatch];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (x + k * 256 < n) v[k] = from[x + k * 256];
+        for (int k = 0; k < kCopyBatch; ++k)
+            if (x + k * kCopyThreads < n) v[k] = from[x + k * kCopyThreads];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (x + k * 256 < n) to[x + k * 256] = v[k];
+        for (int k = 0; k < kCopyBatch; ++k)
+            if (x + k * kCopyThreads < n) to[x + k * kCopyThreads] = v[k];
     }
 }
 
@@ -341,8 +372,12 @@ extern "C" int graft_pages_compact(const GraftPagedCache* cache, int Kmax, const
     const int shift = log2_exact(cache->page_rows);
     const bool in_place = lengths_out == cache->lengths;
     cudaStream_t st = (cudaStream_t)stream;
-    launch_pdl(compact_rows_kernel, dim3(cache->n_layers > 0 ? cache->n_layers : 1, cache->n_seqs), dim3(kMoveThreads),
-               0, st, *cache, Kmax, path, acc_len, in_place ? nullptr : lengths_out, shift);
+    // CTAs a sequence: one a layer where they all fit the GPU at once, else one for two layers (64 sequences in 36
+    // layers: 11.4 us; one a layer 15.5, one for six layers 12.6)
+    const int n_layers = cache->n_layers > 0 ? cache->n_layers : 1;
+    const int G = (int64_t)n_layers * cache->n_seqs <= 4LL * device_sm_count() ? n_layers : (n_layers + 1) / 2;
+    launch_pdl(compact_rows_kernel, dim3(G, cache->n_seqs), dim3(kMoveThreads), 0, st, *cache, Kmax, path, acc_len,
+               in_place ? nullptr : lengths_out, shift);
     count_launches(1);
     if (in_place) {
         launch_pdl(compact_lengths_kernel, dim3(cache->n_seqs), dim3(GRAFT_MAX_KMAX), 0, st, *cache, Kmax, path,
@@ -379,8 +414,8 @@ extern "C" int graft_pages_reserve(const GraftPagedCache* cache, const int32_t* 
     count_launches(1);
     if (cache->n_layers > 0) {
         const int pieces = (cache->page_rows + kCopyRows - 1) / kCopyRows;
-        launch_pdl(copy_tails_kernel, dim3(cache->n_seqs * pieces, cache->n_layers * 2), dim3(256), 0, st, *cache,
-                   static_cast<const Tail*>(w.tail), pieces, shift);
+        launch_pdl(copy_tails_kernel, dim3(cache->n_seqs * pieces, cache->n_layers * 2), dim3(kCopyThreads), 0, st,
+                   *cache, static_cast<const Tail*>(w.tail), pieces, shift);
         count_launches(1);
     }
     return launch_status();

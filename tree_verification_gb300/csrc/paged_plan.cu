@@ -150,14 +150,35 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
     // ---- wide entries: split by keys where they would leave SMs without work, else sorted, longest first
     int n_wide = n_pairs, n_groups = 0;
     if (n_pairs > 0 && shape.max_groups > 0 && n_pairs * c.Hkv < shape.sms) {
-        int64_t blocks;
-        const int mine = tid < n_pairs ? pairs[tid].nblk : 0;
-        scan_block<int64_t>(mine, s_warp, &blocks);
+        // Where single tiles would still fit one wave the items are single tiles: twice the key ranges' length, half
+        // the partial rows (64-node tree at group 4 over 4096 keys: see the table of measurements).
+        int64_t tiles;
+        scan_block<int64_t>(tid < n_pairs ? 1 + pairs[tid].two : 0, s_warp, &tiles);
         const int slots = shape.sms / c.Hkv;
+        const bool single = tiles <= slots;
+        Wide w{};
+        int mine = 0;
+        const int e = single ? tid >> 1 : tid;
+        if (e < n_pairs) {
+            w = pairs[e];
+            const int t = single ? tid & 1 : 0;
+            if (t == 0 || w.two) {
+                if (single) {
+                    w.tok0 += t * shape.tile_tokens;
+                    w.keys = tree ? w.L + w.n : w.L + min(w.tok0 + shape.tile_tokens, w.n);
+                    w.nblk = (w.keys + kBlockKeys - 1) / kBlockKeys;
+                    w.two = 0;
+                }
+                mine = w.nblk;
+            }
+        }
+        int64_t blocks;
+        scan_block<int64_t>(mine, s_warp, &blocks);
+        // the shortest range (two blocks at least) at which the items fit one wave
         s_first[tid] = mine;
         __syncthreads();
-        const int len =
-            piece_length(s_first, n_pairs, slots, (int)max((int64_t)2, (blocks + slots - 1) / slots), s_max, s_fits);
+        const int len = piece_length(s_first, single ? 2 * n_pairs : n_pairs, slots,
+                                     (int)max((int64_t)2, (blocks + slots - 1) / slots), s_max, s_fits);
         int64_t items;
         const int64_t first = scan_block<int64_t>((mine + len - 1) / len, s_warp, &items);
         int64_t splits, split_parts;
@@ -165,10 +186,9 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
         const int64_t group = scan_block<int64_t>(ranges > 1, s_warp, &splits);
         const int64_t part = scan_block<int64_t>(ranges > 1 ? ranges : 0, s_warp, &split_parts);
         if (ranges > 0) {
-            Wide w = pairs[tid];
             const int nblk = w.nblk, each = nblk / ranges, left = nblk % ranges;
             if (ranges > 1)
-                groups[group] = Group{w.q0, w.n, w.tok0, ranges, (int)part * c.Hkv, {0, 0, 0}};
+                groups[group] = Group{w.q0, w.n, w.tok0, 1 + w.two, ranges, (int)part * c.Hkv, {0, 0}};
             for (int j = 0; j < ranges; ++j) {
                 w.blk0 = each * j + min(j, left);
                 w.nblk = each + (j < left);
@@ -353,7 +373,7 @@ PlanShape plan_shape(const GraftPagedCache* c, int N, int Hq, int max_new) {
     // where even the full row blocks fill the SMs nothing is split
     const bool split = s.wide && (int64_t)full_pairs * c->Hkv < sms;
     s.max_wide = s.max_pairs + (split ? sms / c->Hkv : 0);
-    s.max_groups = split ? (s.max_pairs < sms / c->Hkv ? s.max_pairs : sms / c->Hkv) : 0;
+    s.max_groups = split ? (2 * s.max_pairs < sms / c->Hkv ? 2 * s.max_pairs : sms / c->Hkv) : 0;
     s.off_few = align_up(sizeof(PlanHead), kWsAlign);
     s.off_prefix = align_up(s.off_few + sizeof(Entry) * (size_t)s.max_few, kWsAlign);
     s.off_start = align_up(s.off_prefix + sizeof(int64_t) * (size_t)s.max_few, kWsAlign);

@@ -8,11 +8,12 @@
 // off by at most |position| / 2^65 turns plus w's own 64-bit rounding, and
 // its upper 32 bits go to sincospi.  No 64-bit floating product a position.
 //
-// Memory bound: every element is read and written once.  A CTA takes
-// kTokens rows with all their heads, so a row's cosines are computed once
+// Memory bound: every element is read and written once.  A CTA takes one or
+// two rows with all their heads, so a row's cosines are computed once
 // and serve Hq + Hkv heads; each thread's loads (32 bytes a unit: the two
 // 16-byte chunks whose dims pair up) are issued before the CTA looks up the
-// sequences and pages, so the look-up's three dependent reads run behind them.
+// sequences and pages, so the look-up's dependent reads run behind them; the
+// page's number is read while the cosines are computed.
 #include <cmath>
 
 #include "paged.cuh"
@@ -21,9 +22,9 @@ namespace graft {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kTokens = 2;
-constexpr int kAhead = 3;  // units a thread loads before the look-up
+constexpr int kAhead = 5;  // units a thread loads before the look-up
 
 struct RopeArgs {
     GraftPagedCache c;
@@ -38,26 +39,44 @@ struct RopeArgs {
     uint4* Q_out;
     int64_t qs, ks, vs, qos;  // row strides in 16-byte chunks
     int N, Hq, rot, page_shift;
+    int tokens;  // rows of a CTA
     bool inter;
     float factor;
 };
 
-// Last b with q_start[b] <= row, by a warp: 32 probes at a time.
-__device__ __forceinline__ int find_seq(const int32_t* q_start, int n, int row) {
+struct Place {
+    int b;      // sequence, -1: the row is no sequence's
+    int first;  // its first new row
+    int L;      // rows before them
+};
+
+// The sequence of a row, by a warp: 32 probes at a time until 32 sequences are left, whose starts, ends and
+// lengths are read at once (up to 32 sequences: one read's latency).
+__device__ __forceinline__ Place find_seq(const RopeArgs& a, int row) {
     const int lane = threadIdx.x & 31;
-    int lo = 0, len = n + 1;  // answer in [lo, lo + len), or -1
-    while (len > 1) {
+    int lo = 0, len = a.c.n_seqs;  // the last b with q_start[b] <= row lies in [lo, lo + len), or there is none
+    while (len > 32) {
         const int step = (len + 31) / 32;
-        const int at = lo + lane * step;
-        const bool le = lane * step < len && q_start[at] <= row;
-        const unsigned m = __ballot_sync(0xffffffffu, le);
-        if (m == 0) return -1;
-        const int hit = 31 - __clz(m);
-        len = min(step, len - hit * step);
+        const int at = lane * step;
+        const unsigned m = __ballot_sync(0xffffffffu, at < len && a.q_start[lo + at] <= row);
+        const int hit = m == 0 ? 0 : 31 - __clz(m);
         lo += hit * step;
-        if (step == 1) break;
+        len = min(step, len - hit * step);
     }
-    return lo;
+    int first = 0, end = 0, L = 0;
+    const bool have = lane < len;
+    if (have) {
+        first = a.q_start[lo + lane];
+        end = a.q_start[lo + lane + 1];
+        L = a.c.lengths[lo + lane];
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, have && first <= row);
+    const int hit = m == 0 ? 0 : 31 - __clz(m);
+    Place p;
+    p.first = __shfl_sync(0xffffffffu, first, hit);
+    p.L = __shfl_sync(0xffffffffu, L, hit);
+    p.b = m != 0 && row < __shfl_sync(0xffffffffu, end, hit) ? lo + hit : -1;
+    return p;
 }
 
 template <int DT>
@@ -82,8 +101,8 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
     __shared__ int s_live[kTokens], s_pos[kTokens];
     griddep_enter();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int t0 = blockIdx.x * kTokens;
-    const int nt = min(kTokens, a.N - t0);
+    const int t0 = blockIdx.x * a.tokens;
+    const int nt = min(a.tokens, a.N - t0);
     const int heads = a.Hq + 2 * a.c.Hkv;
     const int units = nt * heads * 8;  // a head is 8 units of two 16-byte chunks
     const int rot_units = a.rot / 16;
@@ -122,33 +141,27 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
             buf[k][1] = x.src[x.c1];
         }
     }
+    // one warp a row; what the cosines need first, the page behind them
+    int page_at = -1;  // entry of the block table
+    int64_t r = 0;
     if (warp < nt) {
         const int row = t0 + warp;
-        const int b = find_seq(a.q_start, a.c.n_seqs, row);
-        const bool live = b >= 0 && b < a.c.n_seqs && row < a.q_start[b + 1];
+        const int given = a.pos != nullptr ? a.pos[row] : 0;
+        const Place p = find_seq(a, row);
+        r = (int64_t)p.L + (row - p.first);
         if (lane == 0) {
-            int64_t dst = -1;
-            int pos = 0;
-            if (live) {
-                const int L = a.c.lengths[b];
-                const int64_t r = (int64_t)L + (row - a.q_start[b]);
-                pos = a.pos != nullptr ? a.pos[row] : (int)r;
-                if (L < 0 || (r >> a.page_shift) >= a.c.max_pages) {
+            s_live[warp] = p.b >= 0;
+            s_pos[warp] = a.pos != nullptr ? given : (int)r;
+            if (p.b >= 0) {
+                if (p.L < 0 || (r >> a.page_shift) >= a.c.max_pages)
                     flag_status(a.c.status, GRAFT_STATUS_LENGTH);
-                } else {
-                    const int page = a.c.block_table[(int64_t)b * a.c.max_pages + (r >> a.page_shift)];
-                    if (page < 0 || page >= a.c.num_pages)
-                        flag_status(a.c.status, GRAFT_STATUS_PAGE);
-                    else
-                        dst = ((int64_t)page << a.page_shift) + (r & (a.c.page_rows - 1));
-                }
+                else
+                    page_at = p.b * a.c.max_pages + (int)(r >> a.page_shift);
             }
-            s_live[warp] = live;
-            s_pos[warp] = pos;
-            s_dst[warp] = dst;
         }
     }
     __syncthreads();
+    const int page = page_at >= 0 ? a.c.block_table[page_at] : 0;
     for (int i = tid; i < nt * (a.rot / 2); i += kThreads) {
         const int t = i / (a.rot / 2), p = i - t * (a.rot / 2);
         // 2^64 / 2 pi; a frequency of a turn or more per position keeps only its fraction
@@ -158,6 +171,11 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
         float s, c;
         sincospif((float)(int32_t)(f >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
         s_cs[t][p] = make_float2(c * a.factor, s * a.factor);
+    }
+    if (warp < nt && lane == 0) {
+        const bool in_pool = page >= 0 && page < a.c.num_pages;
+        if (page_at >= 0 && !in_pool) flag_status(a.c.status, GRAFT_STATUS_PAGE);
+        s_dst[warp] = page_at >= 0 && in_pool ? ((int64_t)page << a.page_shift) + (r & (a.c.page_rows - 1)) : -1;
     }
     __syncthreads();
     auto finish = [&](int u, uint4 x0, uint4 x1) {
@@ -323,7 +341,10 @@ extern "C" int graft_rope_append(const GraftPagedCache* cache, void* K_pool, voi
     a.page_shift = log2_exact(cache->page_rows);
     a.inter = interleaved != 0;
     a.factor = factor;
-    const dim3 grid((unsigned)((N + kTokens - 1) / kTokens));
+    // two rows a CTA share a look-up; few rows go one to a CTA, over more SMs (64 rows: 6.2 against 8.2 us)
+    const int sms = device_sm_count();
+    a.tokens = N <= 4 * sms ? 1 : kTokens;
+    const dim3 grid((unsigned)((N + a.tokens - 1) / a.tokens));
     const auto kernel = cache->dtype == GRAFT_BF16 ? rope_append_kernel<GRAFT_BF16> : rope_append_kernel<GRAFT_FP16>;
     launch_pdl(kernel, grid, dim3(kThreads), 0, (cudaStream_t)stream, a);
     count_launches(1);

@@ -146,7 +146,7 @@ __device__ __forceinline__ void keep_bits(uint32_t* w, int kb, int limit, int L,
 }
 
 // Infinite and NaN elements of V that row r sees among keys [k0, k1): added to the row's 128 dims where they
-// were written (16-bit rows of O, or 32-bit partial rows).  Rare, so out of line and straight from memory.
+// were written (16-bit rows of O, or 32-bit partial rows, four dims every 512 floats).  Rare, so out of line and straight from memory.
 template <int DT>
 __device__ __noinline__ void add_odd(const GraftPagedCache& c, const void* V, const int32_t* table, int page_shift,
                                      int kvh, int k0, int k1, int limit, int L, uint64_t anc, void* row16,
@@ -165,8 +165,9 @@ __device__ __noinline__ void add_odd(const GraftPagedCache& c, const void* V, co
             if (isfinite(f.x)) f.x = 0.f;
             if (isfinite(f.y)) f.y = 0.f;
             if (row32 != nullptr) {
-                row32[2 * x] += f.x;
-                row32[2 * x + 1] += f.y;
+                float* o = row32 + (x >> 1) * 512 + (x & 1) * 2;
+                o[0] += f.x;
+                o[1] += f.y;
             } else {
                 uint32_t* o = static_cast<uint32_t*>(row16) + x;
                 const float2 g = E::up(*o);
@@ -227,10 +228,12 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
     griddep_wait();
     griddep_launch_dependents();
     const PlanHead& head = *reinterpret_cast<const PlanHead*>(a.plan);
+    const Wide* wide = reinterpret_cast<const Wide*>(a.plan + a.shape.off_wide);
+    // (the first item's line is on its way while the head is read)
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(wide + min((int)(blockIdx.x / a.c.Hkv), a.shape.max_wide - 1)));
     const bool fits = plan_fits(a, head);
     if (!fits && blockIdx.x == 0 && tid == 0) flag_status(a.c.status, GRAFT_STATUS_PLAN);
     const int n_items = fits ? head.n_wide * a.c.Hkv : 0;
-    const Wide* wide = reinterpret_cast<const Wide*>(a.plan + a.shape.off_wide);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
@@ -645,8 +648,9 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                 const bool direct = w.part < 0;
                 typename E::T* orow =
                     static_cast<typename E::T*>(a.O) + ((int64_t)(w.q0 + tok) * a.Hq + kvh * G + rg) * HD;
-                const int64_t prow = ((int64_t)(w.part + kvh) * 2 + t) * 128 + r;
-                float* part = a.wide_o + (direct ? 0 : prow) * HD;
+                // partial rows lie four dims at a time, the tile's 128 rows side by side: a warp's store is one run
+                const int64_t pblk = (int64_t)(w.part + kvh) * 2 + t;
+                float* part = a.wide_o + (direct ? 0 : pblk * 128 * HD + r * 4);
                 for (int c0 = 0; c0 < HD; c0 += 32) {
                     float o[32];
                     tmem_ld32(tmem + lane_base + TM_O + t * 128 + c0, o);
@@ -666,16 +670,13 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                         }
                     } else {
 #pragma unroll
-                        for (int x = 0; x < 32; x += 8) {
-                            uint32_t v[8];
-#pragma unroll
-                            for (int y = 0; y < 8; ++y) v[y] = __float_as_uint(o[x + y] * inv);
-                            st_global_v8(part + c0 + x, v);
-                        }
+                        for (int x = 0; x < 32; x += 4)
+                            *reinterpret_cast<float4*>(part + ((c0 + x) / 4) * 512) =
+                                make_float4(o[x] * inv, o[x + 1] * inv, o[x + 2] * inv, o[x + 3] * inv);
                     }
                 }
                 if (row_ok && !direct)
-                    a.wide_lse[prow] = l_sum == 0.f ? -INFINITY : m_used + log2f(l_sum) - kLift;
+                    a.wide_lse[pblk * 128 + r] = l_sum == 0.f ? -INFINITY : m_used + log2f(l_sum) - kLift;
                 if (*odd_word() == (uint32_t)k + 1 && row_ok)
                     add_odd<DT>(a.c, a.V, a.c.block_table + (int64_t)w.b * a.c.max_pages, a.page_shift, kvh,
                                 max(w.blk0 * BN, w.L), min((w.blk0 + w.nblk) * BN, w.keys), limit, w.L, anc,
@@ -712,63 +713,71 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Joins the key ranges of split row blocks: O = sum_c 2^(lse_c - lse) O_c.  One warp a row, four dims a lane; a
-// batch of ranges' loads is issued together.
-constexpr int kBatch = 20;
+// Joins the key ranges of split row blocks: O = sum_c 2^(lse_c - lse) O_c.  A thread takes eight dims of a row, a
+// warp 32 rows side by side (its reads are runs of 512 bytes, and each lane weighs its own row); a batch of
+// ranges' reads is issued together.
+constexpr int kBatch = 10;
 template <int DT>
 __global__ void __launch_bounds__(256, 2)
 join_kernel(const __grid_constant__ AttnArgs a) {
     using E = Elem<DT>;
-    griddep_enter();
+    // The plan is read ahead of the grid wait: the kernel before this one is the attention, which let this one
+    // start after its own wait, and so after the plan was written.
     const PlanHead& head = *reinterpret_cast<const PlanHead*>(a.plan);
-    if (!plan_fits(a, head) || (int)blockIdx.y >= head.n_groups * a.c.Hkv) return;
-    const Group gr = reinterpret_cast<const Group*>(a.plan + a.shape.off_group)[blockIdx.y / a.c.Hkv];
-    const int kvh = blockIdx.y % a.c.Hkv;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.x * 8 + warp, t = row >> 7, r = row & 127;
+    const int item = blockIdx.y;
+    const Group gr = reinterpret_cast<const Group*>(a.plan + a.shape.off_group)[item / a.c.Hkv];
+    const bool live = plan_fits(a, head) && item < head.n_groups * a.c.Hkv;
+    griddep_enter();
+    if (!live) return;
+    const int kvh = item % a.c.Hkv;
+    // 16 CTAs an item: 8 a tile, two groups of eight dims each
+    const int t = blockIdx.x >> 3, r = threadIdx.x & 127, c = (blockIdx.x & 7) * 2 + (threadIdx.x >> 7);
     const int T = a.shape.tile_tokens;
     const int tok = gr.tok0 + t * T + r / a.G;
-    if (r / a.G >= T || tok >= gr.n) return;
-    const float* lse = a.wide_lse + ((int64_t)(gr.part0 + kvh) * 2 + t) * 128 + r;
-    const float* po = a.wide_o + (((int64_t)(gr.part0 + kvh) * 2 + t) * 128 + r) * HD + lane * 4;
+    if (r / a.G >= T || tok >= gr.n || t >= gr.tiles) return;
+    const int64_t blk = (int64_t)(gr.part0 + kvh) * 2 + t;
+    const float* lse = a.wide_lse + blk * 128 + r;
+    const float* po = a.wide_o + blk * 128 * HD + c * 1024 + r * 4;
     const int64_t step = (int64_t)a.c.Hkv * 2 * 128;
     float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int c0 = 0; c0 < gr.ranges; c0 += kBatch) {
         float lc[kBatch];
-        float4 v[kBatch];
+        float4 v[kBatch][2];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int c = c0 + u;
-            lc[u] = c < gr.ranges ? lse[c * step] : -INFINITY;
-            v[u] = c < gr.ranges ? *reinterpret_cast<const float4*>(po + c * step * HD) : make_float4(0, 0, 0, 0);
+            const int x = c0 + u;
+            lc[u] = -INFINITY;
+            v[u][0] = v[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x < gr.ranges) {
+                lc[u] = lse[x * step];
+                v[u][0] = *reinterpret_cast<const float4*>(po + x * step * HD);
+                v[u][1] = *reinterpret_cast<const float4*>(po + x * step * HD + 512);
+            }
         }
         float mb = m;
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) mb = fmaxf(mb, lc[u]);
         const float base = mb == -INFINITY ? 0.f : mb;
         const float s = ex2(m - base);
-        acc.x *= s;
-        acc.y *= s;
-        acc.z *= s;
-        acc.w *= s;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) acc[x] *= s;
         l *= s;
         m = mb;
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            if (lc[u] == -INFINITY) continue;  // saw no key of the range
-            const float w = ex2(lc[u] - base);
-            acc.x += w * v[u].x;
-            acc.y += w * v[u].y;
-            acc.z += w * v[u].z;
-            acc.w += w * v[u].w;
+            const float w = ex2(lc[u] - base);  // 0 for a range of which the row saw no key: its partial row is 0
+            const float* f = &v[u][0].x;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) acc[x] += w * f[x];
             l += w;
         }
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
     typename E::T* dst =
-        static_cast<typename E::T*>(a.O) + ((int64_t)(gr.q0 + tok) * a.Hq + kvh * a.G + r % a.G) * HD + lane * 4;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(E::down(acc.x * inv, acc.y * inv), E::down(acc.z * inv, acc.w * inv));
+        static_cast<typename E::T*>(a.O) + ((int64_t)(gr.q0 + tok) * a.Hq + kvh * a.G + r % a.G) * HD + c * 8;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(E::down(acc[0] * inv, acc[1] * inv), E::down(acc[2] * inv, acc[3] * inv),
+                                                E::down(acc[4] * inv, acc[5] * inv), E::down(acc[6] * inv, acc[7] * inv));
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -809,7 +818,7 @@ int launch(const AttnArgs& a, const Maps& m, cudaStream_t st) {
     launch_pdl(wide_kernel<DT>, dim3(a.shape.sms), dim3(NTHREADS), SMEM_BYTES, st, m, a);
     count_launches(1);
     if (a.shape.max_groups > 0) {
-        launch_pdl(join_kernel<DT>, dim3(32, a.shape.max_groups * a.c.Hkv), dim3(256), 0, st, a);
+        launch_pdl(join_kernel<DT>, dim3(16, a.shape.max_groups * a.c.Hkv), dim3(256), 0, st, a);
         count_launches(1);
     }
     return launch_status();
