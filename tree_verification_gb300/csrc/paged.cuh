@@ -25,18 +25,17 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // ---------------------------------------------------------------- the attention plan
 // A work item of the attention is one entry (a block of query rows of one sequence) and one KV head,
 // against a range of keys.  The plan is one buffer:
-//   PlanHead | few entries | their unit prefix sums | the CTAs' first units | wide entries, unsorted | wide
-//   entries | split row blocks
+//   PlanHead | few entries | their unit prefix sums | the CTAs' first units |
+//   wide row blocks, unsorted | wide items of whole rounds | the CTAs' last items | where each CTA's lie |
+//   row blocks split by keys
 // "Few" entries (paged_few.cu): sequences of at most few_rows query rows (new rows x group).  "Wide" ones
 // (paged_wide.cu): all others, in blocks of two tiles of tile_tokens new rows.
 struct PlanHead {
     int32_t magic, N, Hq, Hkv, n_seqs, max_new, tree, page_rows, max_pages, num_pages, few_rows, ctas;
-    int32_t n_few;       // few entries
-    int32_t few_ctas;    // CTAs that share them
-    int32_t pad;
-    int32_t n_wide;      // wide entries
+    int32_t few_ctas;    // CTAs of the few kernel that have work
+    int32_t rounds;      // whole rounds of wide items: every CTA takes one of each
     int32_t n_groups;    // row blocks split by keys
-    int32_t reserved[14];
+    int32_t reserved[16];
 };
 constexpr int32_t kPlanMagic = 0x47503033;
 
@@ -58,12 +57,14 @@ struct Wide {
     int32_t two;          // the block has a second tile
     int32_t blk0, nblk;   // range of 128-key blocks
     int32_t keys;         // keys that any row of the block may see
-    int32_t part;         // partial rows of the range (x Hkv, + KV head), -1: the rows are written to O
-    int32_t pad[2];
+    int32_t kvh;          // KV head
+    int32_t part;         // partial rows of the range, -1: the rows are written to O
+    int32_t pad;
 };
 
+// A row block of one KV head whose key ranges are joined: partial rows part0, part0 + step, ...
 struct Group {
-    int32_t q0, n, tok0, tiles, ranges, part0, pad[2];
+    int32_t q0, n, tok0, tiles, kvh, ranges, part0, step;
 };
 
 // Where a CTA of the few kernel starts: everything its first item needs, in one read.  Either a CTA takes an even
@@ -86,9 +87,8 @@ struct PlanShape {
     int sms;
     int tile_tokens;  // new rows of a 128-row tile
     int max_pairs;    // bound on the wide row blocks
-    int max_wide;     // bound on the wide entries
-    int max_groups;   // bound on the split row blocks, 0: nothing is split
-    size_t off_few, off_prefix, off_start, off_pairs, off_wide, off_group, bytes;
+    int max_groups;   // bound on the row blocks split by keys, 0: nothing is split
+    size_t off_few, off_prefix, off_start, off_pairs, off_wide, off_last, off_where, off_group, bytes;
 };
 
 // CTA k of `ctas` takes units [first_unit(k), first_unit(k + 1)).
@@ -105,13 +105,11 @@ __host__ __device__ __forceinline__ int unit_cta(int64_t units, int ctas, int64_
 PlanShape plan_shape(const GraftPagedCache* c, int N, int Hq, int max_new);
 
 // Partial results of cut items: every CTA has at most two (its first item's end, its last item's start).
-// The partial rows come first in the workspace, in a size of the device's alone, the counters last: calls of
-// other shapes that share a workspace (one after another) never write over the counters.
 constexpr int kFewRows = 32;
 struct FewWs {
+    int32_t* count;  // [entries][Hkv] arrivals, zero between calls
     float* o;        // [ctas][2][kFewRows][128]
     float2* ml;      // [ctas][2][kFewRows]: maximum (log2 units), sum
-    int32_t* count;  // [entries][Hkv] arrivals, zero between calls
 };
 
 struct AttnArgs {
@@ -125,6 +123,7 @@ struct AttnArgs {
     void* O;
     float scale;
     int N, Hq, G, max_new, page_shift;
+    int after_wide;  // the few kernel runs beside the wide one
     PlanShape shape;
     FewWs few;
     float* wide_o;    // [partial row blocks][2][32][128][4] normalised: four dims of the 128 rows side by side
@@ -132,6 +131,7 @@ struct AttnArgs {
 };
 
 int wide_launch(const AttnArgs& a, cudaStream_t st);
+int join_launch(const AttnArgs& a, cudaStream_t st);
 int few_launch(const AttnArgs& a, cudaStream_t st);
 
 // Is the plan one for these arguments?  (The lengths and row counts in it were checked when it was made.)

@@ -316,8 +316,12 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             asm volatile("prefetch.global.L2 [%0];" ::"l"(Vp + (at - Kp)));
         }
     }
-    griddep_wait();
+    if (!a.after_wide) griddep_wait();
     griddep_launch_dependents();
+    // Beside the wide kernel the wait comes last, so that this kernel's end is that of both.
+    auto leave = [&]() {
+        if (a.after_wide) griddep_wait();
+    };
     // reads the plan anew; false: nothing to do
     auto reread = [&]() -> bool {
         cp_wait<0>();
@@ -333,7 +337,10 @@ few_kernel(const __grid_constant__ AttnArgs a) {
         pages = fetch_pages(0, true);
         return true;
     };
-    if (!sound && !reread()) return;
+    if (!sound && !reread()) {
+        leave();
+        return;
+    }
     bool guessed = sound;  // the first item is as yet a guess
 
     while (true) {
@@ -397,7 +404,10 @@ few_kernel(const __grid_constant__ AttnArgs a) {
         if (guessed) {
             guessed = false;
             if (__syncthreads_or(again != guess)) {
-                if (!reread()) return;
+                if (!reread()) {
+                    leave();
+                    return;
+                }
                 continue;
             }
             if (__any_sync(0xffffffffu, now != pages)) {
@@ -628,6 +638,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
     for (int k = 0; k < s_n_pending; ++k) {
         join_pieces<DT, RT, kWarps>(a, s_pending[k], smem);
     }
+    leave();
 }
 
 template <int DT, int RT, int W>

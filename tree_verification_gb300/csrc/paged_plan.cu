@@ -11,7 +11,13 @@ namespace paged {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = 1024;  // of wide entries by their blocks
+constexpr int kBuckets = 1024;  // of wide row blocks by their length
+// (in blocks of a two-tile item's time, about 1.7 us)
+constexpr int kItemCost = 2;           // an item's start and end
+constexpr int kMinGain = 16;           // what splitting the last items costs: second pieces, partial rows, their join
+constexpr int kSnap = 3;               // blocks of a piece at least
+constexpr float kTileTime = 0.85f;     // a block of a single tile
+constexpr float kPairCost = 2.f;       // twice the partial rows
 
 template <class T>
 __device__ __forceinline__ T scan_block(T v, T* s_warp, T* total) {
@@ -63,209 +69,105 @@ __device__ __forceinline__ int piece_length(const int* s_units, int n, int slots
     return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads)
-plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int32_t* __restrict__ q_start, int max_new,
-            int tree, char* plan, PlanShape shape) {
+// A length at which n items of `units` units in all make at most `slots` pieces: rounding up adds less than one a
+// piece to units / length.
+__device__ __forceinline__ int longest_piece(int64_t units, int n, int slots, int most) {
+    if (slots <= n) return most;
+    return (int)min((int64_t)most, (units + slots - n - 1) / (slots - n));
+}
+
+// Is a sequence's block of rows for the few kernel?
+__device__ __forceinline__ bool is_few(const PlanShape& shape, int rows) {
+    return rows > 0 && shape.few && (rows <= shape.few_rows || !shape.wide);
+}
+
+constexpr int kFewInSmem = 512;
+
+template <class ReadSeq>
+__device__ __forceinline__ void plan_few(const GraftPagedCache& c, int Hq, char* plan, const PlanShape& shape,
+                                         ReadSeq read_seq) {
     __shared__ int64_t s_warp[32];
-    __shared__ int s_hist[kBuckets];
-    __shared__ int s_first[kPlanThreads];  // units of the items, then their first pieces
-    __shared__ int s_max, s_few_max, s_fits[32];
-    griddep_wait();
+    __shared__ Entry s_few[kFewInSmem];
+    __shared__ int64_t s_prefix[kFewInSmem];
+    __shared__ int s_units[kPlanThreads], s_most, s_fits[32];
     const int tid = threadIdx.x, G = Hq / c.Hkv;
     Entry* few = reinterpret_cast<Entry*>(plan + shape.off_few);
     int64_t* prefix = reinterpret_cast<int64_t*>(plan + shape.off_prefix);
     Start* start = reinterpret_cast<Start*>(plan + shape.off_start);
-    Wide* pairs = reinterpret_cast<Wide*>(plan + shape.off_pairs);
-    Wide* wide = reinterpret_cast<Wide*>(plan + shape.off_wide);
-    Group* groups = reinterpret_cast<Group*>(plan + shape.off_group);
-    const int pair = 2 * shape.tile_tokens;
-    int n_few = 0, n_pairs = 0;
-    if (tid == 0) s_max = 1;
-    s_hist[tid] = 0;
+    int n_few = 0;
+    int64_t units = 0;  // over entries and heads
+    if (tid == 0) s_most = 1;
     for (int b0 = 0; b0 < c.n_seqs; b0 += kPlanThreads) {
-        const int b = b0 + tid;
-        int q0 = 0, n = 0, L = 0, count = 0, wcount = 0;
-        if (b < c.n_seqs) {
-            q0 = q_start[b];
-            const int64_t q1 = q_start[b + 1];
-            L = c.lengths[b];
-            const int64_t rows = q1 - q0;
-            if (q0 < 0 || rows < 0 || q1 > N || rows > max_new || L < 0 ||
-                (int64_t)L + rows > (int64_t)c.max_pages * c.page_rows) {
-                flag_status(c.status, GRAFT_STATUS_LENGTH);
-            } else {
-                n = (int)rows;
-                if (n > 0 && shape.few && (n * G <= shape.few_rows || !shape.wide))
-                    count = 1;
-                else
-                    wcount = (n + pair - 1) / pair;
+        int q0, n, L;
+        read_seq(b0 + tid, q0, n, L);
+        const bool mine = is_few(shape, n * G);
+        const Entry e{b0 + tid, q0, n, L, 0, n * G, L + n, (L + n + 15) / 16};
+        int64_t total, all;
+        const int at = n_few + (int)scan_block<int64_t>(mine, s_warp, &total);
+        const int64_t before = units + scan_block<int64_t>(mine ? (int64_t)e.units * c.Hkv : 0, s_warp, &all);
+        // (sequences that do not overlap number max_few at most; starts that do not rise could claim more)
+        if (mine && at < shape.max_few) {
+            few[at] = e;
+            prefix[at] = before;
+            if (at < kFewInSmem) {
+                s_few[at] = e;
+                s_prefix[at] = before;
             }
-        }
-        // (sequences that do not overlap have at most max_few and max_pairs blocks; starts that do not rise
-        // could claim more, and those are left out)
-        int64_t total;
-        int64_t at = n_few + scan_block<int64_t>(count, s_warp, &total);
-        if (count > 0) {
-            if (at >= shape.max_few) {
-                flag_status(c.status, GRAFT_STATUS_LENGTH);
-            } else {
-                Entry e;
-                e.b = b;
-                e.q0 = q0;
-                e.n = n;
-                e.L = L;
-                e.row0 = 0;
-                e.rows = n * G;
-                e.keys = L + n;
-                e.units = (e.keys + 15) / 16;
-                few[at] = e;
-            }
+            atomicMax(&s_most, e.units);
+        } else if (mine) {
+            flag_status(c.status, GRAFT_STATUS_LENGTH);
         }
         n_few = (int)min((int64_t)shape.max_few, n_few + total);
-        if (!shape.wide) continue;
-        at = n_pairs + scan_block<int64_t>(wcount, s_warp, &total);
-        int most = 1;
-        for (int j = 0; j < wcount; ++j, ++at) {
-            if (at >= shape.max_pairs) {
-                flag_status(c.status, GRAFT_STATUS_LENGTH);
-                break;
-            }
-            Wide w{};
-            w.b = b;
-            w.q0 = q0;
-            w.n = n;
-            w.L = L;
-            w.tok0 = j * pair;
-            w.two = n - w.tok0 > shape.tile_tokens;
-            w.keys = tree ? L + n : L + min(w.tok0 + pair, n);
-            w.nblk = (w.keys + kBlockKeys - 1) / kBlockKeys;
-            w.part = -1;
-            pairs[at] = w;
-            most = max(most, w.nblk);
-        }
-        if (wcount > 0) atomicMax(&s_max, most);
-        n_pairs = (int)min((int64_t)shape.max_pairs, n_pairs + total);
+        units += all;
     }
     __syncthreads();
-    // ---- wide entries: split by keys where they would leave SMs without work, else sorted, longest first
-    int n_wide = n_pairs, n_groups = 0;
-    if (n_pairs > 0 && shape.max_groups > 0 && n_pairs * c.Hkv < shape.sms) {
-        // Where single tiles would still fit one wave the items are single tiles: twice the key ranges' length, half
-        // the partial rows (64-node tree at group 4 over 4096 keys: see the table of measurements).
-        int64_t tiles;
-        scan_block<int64_t>(tid < n_pairs ? 1 + pairs[tid].two : 0, s_warp, &tiles);
-        const int slots = shape.sms / c.Hkv;
-        const bool single = tiles <= slots;
-        Wide w{};
-        int mine = 0;
-        const int e = single ? tid >> 1 : tid;
-        if (e < n_pairs) {
-            w = pairs[e];
-            const int t = single ? tid & 1 : 0;
-            if (t == 0 || w.two) {
-                if (single) {
-                    w.tok0 += t * shape.tile_tokens;
-                    w.keys = tree ? w.L + w.n : w.L + min(w.tok0 + shape.tile_tokens, w.n);
-                    w.nblk = (w.keys + kBlockKeys - 1) / kBlockKeys;
-                    w.two = 0;
-                }
-                mine = w.nblk;
-            }
-        }
-        int64_t blocks;
-        scan_block<int64_t>(mine, s_warp, &blocks);
-        // the shortest range (two blocks at least) at which the items fit one wave
-        s_first[tid] = mine;
-        __syncthreads();
-        const int len = piece_length(s_first, single ? 2 * n_pairs : n_pairs, slots,
-                                     (int)max((int64_t)2, (blocks + slots - 1) / slots), s_max, s_fits);
-        int64_t items;
-        const int64_t first = scan_block<int64_t>((mine + len - 1) / len, s_warp, &items);
-        int64_t splits, split_parts;
-        const int ranges = (mine + len - 1) / len;
-        const int64_t group = scan_block<int64_t>(ranges > 1, s_warp, &splits);
-        const int64_t part = scan_block<int64_t>(ranges > 1 ? ranges : 0, s_warp, &split_parts);
-        if (ranges > 0) {
-            const int nblk = w.nblk, each = nblk / ranges, left = nblk % ranges;
-            if (ranges > 1)
-                groups[group] = Group{w.q0, w.n, w.tok0, 1 + w.two, ranges, (int)part * c.Hkv, {0, 0}};
-            for (int j = 0; j < ranges; ++j) {
-                w.blk0 = each * j + min(j, left);
-                w.nblk = each + (j < left);
-                w.part = ranges > 1 ? (int)(part + j) * c.Hkv : -1;
-                wide[first + j] = w;
-            }
-        }
-        n_wide = (int)items;
-        n_groups = (int)splits;
-    } else if (n_pairs > 0) {
-        const int64_t most = s_max;
-        auto bucket = [&](int nblk) { return (int)(((most - nblk) * (kBuckets - 1)) / most); };
-        for (int e = tid; e < n_pairs; e += kPlanThreads) atomicAdd(&s_hist[bucket(pairs[e].nblk)], 1);
-        __syncthreads();
-        int64_t total;
-        const int before = (int)scan_block<int64_t>(s_hist[tid], s_warp, &total);
-        s_hist[tid] = before;
-        __syncthreads();
-        for (int e = tid; e < n_pairs; e += kPlanThreads) {
-            const Wide w = pairs[e];
-            wide[atomicAdd(&s_hist[bucket(w.nblk)], 1)] = w;
-        }
-    }
-    int64_t units = 0;
-    if (tid == 0) s_few_max = 1;
-    __syncthreads();
-    for (int e0 = 0; e0 < n_few; e0 += kPlanThreads) {
-        const int e = e0 + tid;
-        int64_t total;
-        const int64_t before = scan_block<int64_t>(e < n_few ? (int64_t)few[e].units * c.Hkv : 0, s_warp, &total);
-        if (e < n_few) prefix[e] = units + before;
-        if (e < n_few) atomicMax(&s_few_max, few[e].units);
-        units += total;
-    }
-    __syncthreads();
+    auto entry_at = [&](int i) { return i < kFewInSmem ? s_few[i] : few[i]; };
+    auto prefix_at = [&](int i) { return i < kFewInSmem ? s_prefix[i] : prefix[i]; };
+    // (without those left out, if any were)
+    if (n_few > 0) units = prefix_at(n_few - 1) + (int64_t)entry_at(n_few - 1).units * c.Hkv;
     // Where every item can have CTAs of its own (items no more than CTAs), pieces of one length: a CTA that ends
     // one item and starts the next pays the latencies of both, about as long as kSwitch units take.  A unit a
     // warp at least.
     const int kSwitch = 5 * shape.few_warps / 2;
     int ctas = 0;
     bool own_ctas = false;
-    if (units > 0 && (int64_t)n_few * c.Hkv <= shape.ctas) {
-        const int mine = tid < n_few ? few[tid].units : 0;
+    if (units > 0 && n_few <= kFewInSmem && (int64_t)n_few * c.Hkv <= shape.ctas) {
+        const int mine = tid < n_few ? s_few[tid].units : 0;
         // an SM's share left free for every item: the CTAs that join pieces hold theirs longest, and the next
         // call's CTAs find room elsewhere (decode of one sequence: 10.4 -> 9.0 us a call)
         int slots = shape.ctas / c.Hkv;
         if (n_few * 8 <= slots) slots -= n_few;
         const int64_t even = (units + shape.ctas - 1) / shape.ctas;
-        s_first[tid] = mine;
+        s_units[tid] = mine;
         __syncthreads();
-        const int len = piece_length(s_first, n_few, slots, (int)max((int64_t)shape.few_warps, even), s_few_max, s_fits);
+        const int len = piece_length(s_units, n_few, slots, (int)max((int64_t)shape.few_warps, even),
+                                     longest_piece(units / c.Hkv, n_few, slots, s_most), s_fits);
         int64_t items;
-        const int64_t first = scan_block<int64_t>((mine + len - 1) / len, s_warp, &items);
+        const int first = (int)scan_block<int64_t>((mine + len - 1) / len, s_warp, &items);
         if (len <= even + kSwitch || len == shape.few_warps) {
             own_ctas = true;
             ctas = (int)items * c.Hkv;
-            if (tid < n_few) s_first[tid] = (int)first;
+            s_units[tid] = first;
             __syncthreads();
             for (int k = tid; k < ctas; k += kPlanThreads) {
                 const int piece = k / c.Hkv;
-                int lo = 0, hi = n_few;  // the entry with s_first[lo] <= piece < s_first[lo + 1]
+                int lo = 0, hi = n_few;  // the entry with s_units[lo] <= piece < s_units[lo + 1]
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) / 2;
-                    if (s_first[mid] <= piece) lo = mid;
+                    if (s_units[mid] <= piece) lo = mid;
                     else hi = mid;
                 }
                 Start s{};
-                s.e = few[lo];
+                s.e = s_few[lo];
                 s.entry = lo;
                 s.head = k - piece * c.Hkv;
                 s.pieces = (s.e.units + len - 1) / len;
-                const int j = piece - s_first[lo], each = s.e.units / s.pieces, left = s.e.units % s.pieces;
+                const int j = piece - s_units[lo], each = s.e.units / s.pieces, left = s.e.units % s.pieces;
                 s.unit = each * j + min(j, left);
                 s.count = each + (j < left);
                 s.ctas = ctas;
                 s.step = c.Hkv;
-                s.cta0 = s_first[lo] * c.Hkv + s.head;
+                s.cta0 = s_units[lo] * c.Hkv + s.head;
                 start[k] = s;
             }
         }
@@ -278,24 +180,303 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
             int lo = 0, hi = n_few;  // the entry with prefix[lo] <= u < prefix[lo + 1]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
-                if (prefix[mid] <= u) lo = mid;
+                if (prefix_at(mid) <= u) lo = mid;
                 else hi = mid;
             }
-            const int64_t in = u - prefix[lo];
+            const int64_t in = u - prefix_at(lo);
             Start s{};
-            s.e = few[lo];
+            s.e = entry_at(lo);
             s.entry = lo;
             s.head = (int)(in / s.e.units);
             s.unit = (int)(in % s.e.units);
-            s.item_first = prefix[lo] + (int64_t)s.head * s.e.units;
+            s.item_first = prefix_at(lo) + (int64_t)s.head * s.e.units;
             s.count = (int)(first_unit(units, ctas, k + 1) - u);
             s.ctas = ctas;
             s.total = units;
             start[k] = s;
         }
     }
+    if (tid == 0) reinterpret_cast<PlanHead*>(plan)->few_ctas = ctas;
+}
+
+template <class ReadSeq>
+__device__ __forceinline__ void plan_wide(const GraftPagedCache& c, int N, int Hq, int tree, char* plan,
+                                          const PlanShape& shape, ReadSeq read_seq) {
+    __shared__ int64_t s_warp[32];
+    __shared__ int s_hist[kBuckets], s_first[kPlanThreads], s_max, s_fits[32];
+    const int tid = threadIdx.x, G = Hq / c.Hkv;
+    Wide* pairs = reinterpret_cast<Wide*>(plan + shape.off_pairs);
+    Wide* wide = reinterpret_cast<Wide*>(plan + shape.off_wide);
+    Wide* last = reinterpret_cast<Wide*>(plan + shape.off_last);
+    int32_t* where = reinterpret_cast<int32_t*>(plan + shape.off_where);
+    Group* groups = reinterpret_cast<Group*>(plan + shape.off_group);
+    const int pair = 2 * shape.tile_tokens;
+    int n_pairs = 0;
+    if (tid == 0) s_max = 1;
+    for (int b0 = 0; b0 < c.n_seqs; b0 += kPlanThreads) {
+        int q0, n, L;
+        read_seq(b0 + tid, q0, n, L);
+        const int count = is_few(shape, n * G) ? 0 : (n + pair - 1) / pair;
+        int64_t total;
+        int64_t at = n_pairs + scan_block<int64_t>(count, s_warp, &total);
+        int most = 1;
+        for (int j = 0; j < count; ++j, ++at) {
+            if (at >= shape.max_pairs) {  // (as in plan_few)
+                flag_status(c.status, GRAFT_STATUS_LENGTH);
+                break;
+            }
+            Wide w{};
+            w.b = b0 + tid;
+            w.q0 = q0;
+            w.n = n;
+            w.L = L;
+            w.tok0 = j * pair;
+            w.two = n - w.tok0 > shape.tile_tokens;
+            w.keys = tree ? L + n : L + min(w.tok0 + pair, n);
+            w.nblk = (w.keys + kBlockKeys - 1) / kBlockKeys;
+            w.part = -1;
+            pairs[at] = w;
+            most = max(most, w.nblk);
+        }
+        if (count > 0) atomicMax(&s_max, most);
+        n_pairs = (int)min((int64_t)shape.max_pairs, n_pairs + total);
+    }
+    __syncthreads();
+    const int P = shape.sms;
+    int rounds = 0, n_groups = 0;
+    if (n_pairs == 0) {
+        for (int k = tid; k <= P; k += kPlanThreads) where[k] = 0;
+    } else if (shape.max_groups > 0 && n_pairs * c.Hkv * 3 <= P) {
+        // ---- Three SMs an item or more: all are split by keys into ranges of about one length, one a CTA, so short that
+        // they just fit (two blocks at least).  The row blocks may be cut into their single tiles for that: half the
+        // partial rows, but a tile alone takes kTileTime of two tiles' time a block; the estimate decides (one
+        // request's 64-node tree at group 4 over 4096 keys: 16.3 us in single tiles, 17.7 in pairs; 300 rows of a
+        // prompt over 6000: 77 and 44).
+        const int slots = P / c.Hkv;
+        auto block_of = [&](bool single, int e) {
+            Wide w = pairs[single ? e >> 1 : e];
+            const int t = single ? e & 1 : 0;
+            if (t == 1 && !w.two) {
+                w.nblk = 0;
+            } else if (single) {
+                w.tok0 += t * shape.tile_tokens;
+                w.keys = tree ? w.L + w.n : w.L + min(w.tok0 + shape.tile_tokens, w.n);
+                w.nblk = (w.keys + kBlockKeys - 1) / kBlockKeys;
+                w.two = 0;
+            }
+            return w;
+        };
+        auto length_of = [&](bool single, int count, int64_t tiles) {
+            s_first[tid] = tid < count ? block_of(single, tid).nblk : 0;
+            int64_t blocks;
+            scan_block<int64_t>(s_first[tid], s_warp, &blocks);
+            return piece_length(s_first, count, slots, (int)max((int64_t)2, (blocks + slots - 1) / slots),
+                                longest_piece(blocks, (int)tiles, slots, s_max), s_fits);
+        };
+        int64_t tiles;
+        scan_block<int64_t>(tid < n_pairs ? 1 + pairs[tid].two : 0, s_warp, &tiles);
+        int len = length_of(false, n_pairs, n_pairs);
+        bool single = false;
+        if (tiles <= slots) {
+            const int alone = length_of(true, 2 * n_pairs, tiles);
+            single = alone * kTileTime <= len + kPairCost;
+            if (single) len = alone;
+        }
+        const int n = single ? 2 * n_pairs : n_pairs;
+        Wide w{};
+        if (tid < n) w = block_of(single, tid);
+        const int ranges = (w.nblk + len - 1) / len;
+        // three sums in one: ranges, split blocks, their ranges
+        int64_t sums;
+        const int64_t mine3 =
+            (int64_t)ranges | (int64_t)(ranges > 1) << 20 | (int64_t)(ranges > 1 ? ranges : 0) << 40;
+        const int64_t before3 = scan_block<int64_t>(mine3, s_warp, &sums);
+        const int first = (int)(before3 & 0xfffff), group = (int)(before3 >> 20 & 0xfffff), part = (int)(before3 >> 40);
+        const int items = (int)(sums & 0xfffff) * c.Hkv;
+        n_groups = (int)(sums >> 20 & 0xfffff) * c.Hkv;
+        s_first[tid] = first;
+        s_hist[tid] = part;
+        if (ranges > 1)
+            for (int h = 0; h < c.Hkv; ++h)
+                groups[group * c.Hkv + h] =
+                    Group{w.q0, w.n, w.tok0, 1 + w.two, h, ranges, part * c.Hkv + h, c.Hkv};
+        __syncthreads();
+        for (int k = tid; k < items; k += kPlanThreads) {
+            const int r = k / c.Hkv;
+            int lo = 0, hi = n;  // the block with s_first[lo] <= r < s_first[lo + 1]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (s_first[mid] <= r) lo = mid;
+                else hi = mid;
+            }
+            Wide x = block_of(single, lo);
+            const int count = (x.nblk + len - 1) / len, j = r - s_first[lo];
+            const int each = x.nblk / count, left = x.nblk % count;
+            x.blk0 = each * j + min(j, left);
+            x.nblk = each + (j < left);
+            x.kvh = k - r * c.Hkv;
+            x.part = count > 1 ? (s_hist[lo] + j) * c.Hkv + x.kvh : -1;
+            last[k] = x;
+        }
+        for (int k = tid; k <= P; k += kPlanThreads) where[k] = min(k, items);
+    } else {
+        // ---- Items in the order of their blocks, the longest first, the heads of a row block side by side (their K
+        // and V lie in the same pages).  The order decides what is split, so it is the same every time (equal
+        // blocks by their place); past what one pass ranks nothing is split, and equal blocks may change places.
+        const bool ranked = n_pairs <= kPlanThreads;
+        auto put = [&](int at, Wide w) {
+            for (int h = 0; h < c.Hkv; ++h) {
+                w.kvh = h;
+                wide[(int64_t)at * c.Hkv + h] = w;
+            }
+        };
+        if (ranked) {
+            s_first[tid] = tid < n_pairs ? pairs[tid].nblk : 0;
+            __syncthreads();
+            if (tid < n_pairs) {
+                const int mine = s_first[tid];
+                int rank = 0;
+                for (int j = 0; j < n_pairs; ++j) rank += s_first[j] > mine || (s_first[j] == mine && j < tid);
+                s_hist[rank] = mine;
+                put(rank, pairs[tid]);
+            }
+        } else {
+            const int64_t most = s_max;
+            auto bucket = [&](int nblk) { return (int)(((most - nblk) * (kBuckets - 1)) / most); };
+            s_hist[tid] = 0;
+            __syncthreads();
+            for (int e = tid; e < n_pairs; e += kPlanThreads) atomicAdd(&s_hist[bucket(pairs[e].nblk)], 1);
+            __syncthreads();
+            int64_t total;
+            const int before = (int)scan_block<int64_t>(s_hist[tid], s_warp, &total);
+            s_hist[tid] = before;
+            __syncthreads();
+            for (int e = tid; e < n_pairs; e += kPlanThreads) {
+                const Wide w = pairs[e];
+                put(atomicAdd(&s_hist[bucket(w.nblk)], 1), w);
+            }
+        }
+        __syncthreads();
+        const int n_items = n_pairs * c.Hkv;
+        rounds = n_items / P;
+        const int rem = n_items - rounds * P;  // < P
+        const Wide* rest = wide + (int64_t)rounds * P;
+        // ---- The items past the whole rounds: split over all CTAs where their even share is kMinGain blocks below
+        // the longest (group 16 over 8192 keys: 10 trees, eight items past one round, 204 -> 122 us; 5 trees, 80
+        // items, 103 -> 77; 8 trees, 128 items, 104 whole and 120 split).
+        auto blocks_of = [&](int i) { return s_hist[i / c.Hkv]; };  // of item i (ranked)
+        const int mine = ranked && tid < rem ? blocks_of(rounds * P + tid) : 0;
+        int64_t blocks;
+        const int before = (int)scan_block<int64_t>(mine, s_warp, &blocks);
+        if (shape.max_groups > 0 && ranked && rem > 0 && blocks_of(rounds * P) >= blocks / P + kMinGain) {
+            s_first[tid] = tid < rem ? before : (int)blocks;  // an item's place on the line of their blocks
+            // what a CTA has done when the rounds end, an item's own cost included
+            int load = 0;
+            for (int k = 0; k < rounds && tid < P; ++k) load += blocks_of(k * P + ((k & 1) ? P - 1 - tid : tid)) + kItemCost;
+            // the level that the rest fills every CTA up to (those above it take nothing)
+            bool takes = tid < P;
+            int64_t level = 0, sum;
+            for (int it = 0; it < 2; ++it) {
+                scan_block<int64_t>(takes ? (int64_t)load << 11 | 1 : 0, s_warp, &sum);
+                level = ((sum >> 11) + blocks) / (sum & 2047);
+                takes = takes && load <= level;
+            }
+            // (the shares' sum is off by rounding and by what dropped out last: the cuts are scaled to the blocks)
+            const int64_t share = takes ? level - load : 0;
+            const int64_t ahead = scan_block<int64_t>(share, s_warp, &sum);
+            const int64_t from = ahead * blocks / sum, to = (ahead + share) * blocks / sum;
+            auto item_of = [&](int x) {  // the item whose blocks hold x
+                int lo = 0, hi = rem;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (s_first[mid] <= x) lo = mid;
+                    else hi = mid;
+                }
+                return lo;
+            };
+            auto end_of = [&](int i) { return i + 1 < rem ? s_first[i + 1] : (int)blocks; };
+            auto snap = [&](int64_t x) {  // a cut keeps kSnap blocks on both sides, or moves to the item's edge
+                if (x >= blocks) return (int)blocks;
+                const int i = item_of((int)x), s = s_first[i], e = end_of(i);
+                return x - s < kSnap ? s : e - x < kSnap ? e : (int)x;
+            };
+            const int lo = tid < P ? snap(from) : (int)blocks;
+            const int hi = tid == P - 1 ? (int)blocks : tid < P ? snap(to) : (int)blocks;
+            int i0 = 0, pieces = 0, cuts = 0;
+            bool head = false;  // the last piece starts an item that goes on in the next CTA
+            if (lo < hi) {
+                i0 = item_of(lo);
+                const int i1 = item_of(hi - 1);
+                pieces = i1 - i0 + 1;
+                head = hi < end_of(i1) && s_first[i1] >= lo;
+                cuts = (lo > s_first[i0] || hi < end_of(i0)) + (i1 > i0 && hi < end_of(i1));
+            }
+            __syncthreads();
+            s_hist[tid] = lo < hi ? lo : -1;  // where a CTA's share starts
+            int64_t total;
+            const int64_t before3 = scan_block<int64_t>((int64_t)pieces | (int64_t)cuts << 20 | (int64_t)head << 40,
+                                                        s_warp, &total);
+            const int at = (int)(before3 & 0xfffff), group = (int)(before3 >> 40);
+            int part = (int)(before3 >> 20 & 0xfffff);
+            n_groups = (int)(total >> 40);
+            if (tid < P) where[tid] = at;
+            if (tid == 0) where[P] = (int)(total & 0xfffff);
+            for (int j = 0; j < pieces; ++j) {
+                const int i = i0 + j, s = s_first[i], e = end_of(i);
+                const int p0 = max(lo, s), p1 = min(hi, e);
+                Wide x = rest[i];
+                x.blk0 = p0 - s;
+                x.nblk = p1 - p0;
+                const bool cut = p0 > s || p1 < e;
+                if (cut && p0 == s) {
+                    int ranges = 1;
+                    for (int k = tid + 1; k < P && s_hist[k] < e; ++k) ranges += s_hist[k] >= 0;
+                    groups[group] = Group{x.q0, x.n, x.tok0, 1 + x.two, x.kvh, ranges, part, 1};
+                }
+                x.part = cut ? part++ : -1;
+                last[at + j] = x;
+            }
+        } else {
+            // one of them a CTA, the longest to those that the snake served last
+            if (tid < rem) last[(rounds & 1) ? rem - 1 - tid : tid] = rest[tid];
+            for (int k = tid; k <= P; k += kPlanThreads)
+                where[k] = (rounds & 1) ? min(max(k - (P - rem), 0), rem) : min(k, rem);
+        }
+    }
     if (tid == 0) {
-        PlanHead h{};
+        PlanHead& h = *reinterpret_cast<PlanHead*>(plan);
+        h.rounds = rounds;
+        h.n_groups = n_groups;
+    }
+}
+
+// Block 0 plans the few entries, block 1 the wide items (a grid of one block has only the one kind).
+__global__ void __launch_bounds__(kPlanThreads)
+plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int32_t* __restrict__ q_start, int max_new,
+            int tree, char* plan, const __grid_constant__ PlanShape shape) {
+    griddep_wait();
+    const bool wide_block = blockIdx.x > 0 || !shape.few;
+    // Every block checks all sequences, the first one sets the status.
+    auto read_seq = [&](int b, int& q0, int& n, int& L) {
+        q0 = n = L = 0;
+        if (b >= c.n_seqs) return;
+        const int64_t from = q_start[b], to = q_start[b + 1], len = c.lengths[b];
+        const int64_t rows = to - from;
+        if (from < 0 || rows < 0 || to > N || rows > max_new || len < 0 ||
+            len + rows > (int64_t)c.max_pages * c.page_rows) {
+            if (blockIdx.x == 0) flag_status(c.status, GRAFT_STATUS_LENGTH);
+            return;
+        }
+        q0 = (int)from;
+        n = (int)rows;
+        L = (int)len;
+    };
+    if (wide_block)
+        plan_wide(c, N, Hq, tree, plan, shape, read_seq);
+    else
+        plan_few(c, Hq, plan, shape, read_seq);
+    if (threadIdx.x == 0 && blockIdx.x == 0) {
+        PlanHead& h = *reinterpret_cast<PlanHead*>(plan);
         h.magic = kPlanMagic;
         h.N = N;
         h.Hq = Hq;
@@ -308,11 +489,6 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
         h.num_pages = c.num_pages;
         h.few_rows = shape.few_rows;
         h.ctas = shape.ctas;
-        h.n_few = n_few;
-        h.few_ctas = ctas;
-        h.n_wide = n_wide;
-        h.n_groups = n_groups;
-        *reinterpret_cast<PlanHead*>(plan) = h;
     }
     // the attention reads the plan ahead of its grid wait, as a guess that is checked after it: it starts when the
     // plan is written, so that the guess holds
@@ -329,17 +505,17 @@ int check_attention(const GraftPagedCache* c, int N, int Hq, int max_new) {
     return GRAFT_OK;
 }
 
-// Partial rows first, in sizes of the device's alone, then the counters (see FewWs).  Split row blocks have at
-// most one range a slot of the wave, and one more a block.
+// Counters first (one a sequence and KV head: a place that depends on the cache alone, so that calls of other shapes
+// that share a workspace never write over them), then the partial rows.
 void carve(WsCarver& w, const GraftPagedCache* c, const PlanShape& s, AttnArgs* a) {
     FewWs f;
+    f.count = w.take<int32_t>((size_t)c->n_seqs * c->Hkv);
     const size_t slots = (size_t)s.sms * 2 * 2;  // two a CTA, at most two CTAs an SM
     f.o = w.take<float>(slots * kFewRows * HD);
     f.ml = w.take<float2>(slots * kFewRows);
-    const size_t parts = (size_t)s.sms * 2;
+    const size_t parts = s.max_groups > 0 ? (size_t)s.sms * 2 : 0;  // a wave's cuts leave at most two pieces each
     float* wo = w.take<float>(parts * 2 * 128 * HD);
     float* wl = w.take<float>(parts * 2 * 128);
-    f.count = w.take<int32_t>((size_t)s.max_few * c->Hkv);
     if (a != nullptr) {
         a->few = f;
         a->wide_o = wo;
@@ -370,16 +546,17 @@ PlanShape plan_shape(const GraftPagedCache* c, int N, int Hq, int max_new) {
     s.ctas = sms * 8 / s.few_warps;
     const int full_pairs = N / (2 * s.tile_tokens);
     s.max_pairs = s.wide ? (int)(full_pairs + seqs) : 0;
-    // where even the full row blocks fill the SMs nothing is split
-    const bool split = s.wide && (int64_t)full_pairs * c->Hkv < sms;
-    s.max_wide = s.max_pairs + (split ? sms / c->Hkv : 0);
-    s.max_groups = split ? (2 * s.max_pairs < sms / c->Hkv ? 2 * s.max_pairs : sms / c->Hkv) : 0;
+    // Many rounds even themselves out; up to eight, what is left over may be split by keys.
+    const int64_t full_items = (int64_t)full_pairs * c->Hkv, most_blocks = 2LL * s.max_pairs * c->Hkv;
+    s.max_groups = s.wide && full_items < 8LL * sms ? (int)(most_blocks < sms ? most_blocks : sms) : 0;
     s.off_few = align_up(sizeof(PlanHead), kWsAlign);
     s.off_prefix = align_up(s.off_few + sizeof(Entry) * (size_t)s.max_few, kWsAlign);
     s.off_start = align_up(s.off_prefix + sizeof(int64_t) * (size_t)s.max_few, kWsAlign);
     s.off_pairs = align_up(s.off_start + sizeof(Start) * (size_t)s.ctas, kWsAlign);
     s.off_wide = align_up(s.off_pairs + sizeof(Wide) * (size_t)s.max_pairs, kWsAlign);
-    s.off_group = align_up(s.off_wide + sizeof(Wide) * (size_t)s.max_wide, kWsAlign);
+    s.off_last = align_up(s.off_wide + sizeof(Wide) * (size_t)s.max_pairs * c->Hkv, kWsAlign);
+    s.off_where = align_up(s.off_last + (s.wide ? sizeof(Wide) * 2 * (size_t)sms : 0), kWsAlign);
+    s.off_group = align_up(s.off_where + (s.wide ? sizeof(int32_t) * (size_t)(sms + 1) : 0), kWsAlign);
     s.bytes = align_up(s.off_group + sizeof(Group) * (size_t)s.max_groups, kWsAlign);
     return s;
 }
@@ -406,7 +583,7 @@ extern "C" int graft_paged_plan(const GraftPagedCache* cache, int N, int Hq, con
     if (q_start == nullptr) return GRAFT_ERR_INVALID_ARG;
     const PlanShape s = plan_shape(cache, N, Hq, max_new);
     if (!ws_ok(plan, plan_bytes, s.bytes)) return GRAFT_ERR_WORKSPACE;
-    launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, (cudaStream_t)stream, *cache, N, Hq, q_start, max_new,
+    launch_pdl(plan_kernel, dim3(s.few && s.wide ? 2 : 1), dim3(kPlanThreads), 0, (cudaStream_t)stream, *cache, N, Hq, q_start, max_new,
                tree != 0 ? 1 : 0, static_cast<char*>(plan), s);
     count_launches(1);
     return launch_status();
@@ -458,9 +635,15 @@ extern "C" int graft_paged_attention(const GraftPagedCache* cache, const void* K
     a.G = Hq / cache->Hkv;
     a.max_new = max_new;
     a.page_shift = log2_exact(cache->page_rows);
-    if (a.shape.few) {
-        const int rc2 = few_launch(a, (cudaStream_t)stream);
-        if (rc2 != GRAFT_OK) return rc2;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (!a.shape.wide) return few_launch(a, st);
+    // Steps of both kinds: the few kernel comes second and does not wait for the first, which has waited for all
+    // that came before; its CTAs take the SMs that the wide items leave one by one.
+    int rc2 = wide_launch(a, st);
+    if (rc2 == GRAFT_OK && a.shape.few) {
+        a.after_wide = 1;
+        rc2 = few_launch(a, st);
     }
-    return a.shape.wide ? wide_launch(a, (cudaStream_t)stream) : GRAFT_OK;
+    if (rc2 == GRAFT_OK && a.shape.max_groups > 0) rc2 = join_launch(a, st);
+    return rc2;
 }

@@ -6,7 +6,8 @@
 // A work item is 256 query rows (two tiles of T = 128 / G new rows with their
 // G heads; one tile where the rest of the sequence fits it) of one sequence
 // and KV head against a range of 128-key blocks; the plan lists the items,
-// longest first, and they are dealt to one persistent CTA per SM in a snake.
+// longest first, deals whole rounds of them to one persistent CTA per SM in a
+// snake, and splits what is left over by keys, so that all end together.
 // Tensor-core bound: 4 x 128 x 128 products a row and key block; two tiles
 // share every K and V block, so a block's 64 KB serve 256 rows.
 //
@@ -123,13 +124,6 @@ __device__ __forceinline__ float2 add_pair(float2 acc, uint32_t w) {
     return make_float2(x, y);
 }
 
-// The snake deal: this CTA's k-th item, or -1 past the end.
-__device__ __forceinline__ int item_index(int k, int n_items) {
-    const int P = gridDim.x, p = blockIdx.x;
-    const int i = k * P + ((k & 1) ? (P - 1 - p) : p);
-    return i < n_items ? i : -1;
-}
-
 // What a row sees of the 128 keys from kb on: keys below `limit`, and new row j (key L + j) where bit j of anc is set.
 __device__ __forceinline__ void keep_bits(uint32_t* w, int kb, int limit, int L, uint64_t anc) {
 #pragma unroll
@@ -229,11 +223,19 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
     griddep_launch_dependents();
     const PlanHead& head = *reinterpret_cast<const PlanHead*>(a.plan);
     const Wide* wide = reinterpret_cast<const Wide*>(a.plan + a.shape.off_wide);
+    const Wide* last = reinterpret_cast<const Wide*>(a.plan + a.shape.off_last);
     // (the first item's line is on its way while the head is read)
-    asm volatile("prefetch.global.L1 [%0];" ::"l"(wide + min((int)(blockIdx.x / a.c.Hkv), a.shape.max_wide - 1)));
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(last + blockIdx.x));
+    const int* where = reinterpret_cast<const int*>(a.plan + a.shape.off_where) + blockIdx.x;
+    const int where0 = where[0], where1 = where[1];
     const bool fits = plan_fits(a, head);
     if (!fits && blockIdx.x == 0 && tid == 0) flag_status(a.c.status, GRAFT_STATUS_PLAN);
-    const int n_items = fits ? head.n_wide * a.c.Hkv : 0;
+    const int rounds = fits ? head.rounds : 0, n_mine = fits ? rounds + where1 - where0 : 0;
+    // this CTA's k-th item: one of every round, dealt in a snake, then its last ones
+    auto item_at = [&](int k) -> const Wide* {
+        if (k < rounds) return wide + (k * (int)gridDim.x + ((k & 1) ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x));
+        return last + (where0 + k - rounds);
+    };
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
@@ -265,13 +267,12 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
             c.row = row;
         };
         auto seek = [&](Cur& c) {
-            const int i = item_index(c.k, n_items);
-            if (i < 0) {
+            if (c.k >= n_mine) {
                 c.k = -1;
                 return;
             }
-            const Wide w = wide[i / a.c.Hkv];
-            c.kvh = i % a.c.Hkv;
+            const Wide w = *item_at(c.k);
+            c.kvh = w.kvh;
             c.j = 0;
             c.blk0 = w.blk0;
             c.nblk = w.nblk;
@@ -448,10 +449,8 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                 ++q;
                 q1 += two;
             };
-            for (int k = 0; ok; ++k) {
-                const int i = item_index(k, n_items);
-                if (i < 0) break;
-                const Wide& w = wide[i / a.c.Hkv];
+            for (int k = 0; ok && k < n_mine; ++k) {
+                const Wide& w = *item_at(k);
                 if (w.two != 0)
                     run_item(std::true_type{}, w.nblk);
                 else
@@ -472,15 +471,14 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
         bool ok = true;
         int q = 0, n_two = 0;  // items passed (phase of DONE); those of two tiles
         int g = 0, gv = 0;     // blocks of this tile, blocks of the CTA
-        for (int k = 0; ok; ++k) {
-            const int i = item_index(k, n_items);
-            if (i < 0) break;
+        for (int k = 0; ok && k < n_mine; ++k) {
+            const Wide* at = item_at(k);
             // The block loop holds only counts; an edge block reads the item and the row's mask again, and so
             // does the epilogue.
             int nblk, edge;
             bool two;
             {
-                const Wide& w = wide[i / a.c.Hkv];
+                const Wide& w = *at;
                 nblk = w.nblk;
                 two = w.two != 0;
                 // first block that some row of the tile does not see whole
@@ -518,7 +516,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                     if (j >= edge) {
                         // Masked scores are written back as -inf, in a pass of their own over S in tensor memory:
                         // the block loop proper carries no masking code (inlined it cost all blocks 4%).
-                        const Wide& w = wide[i / a.c.Hkv];
+                        const Wide& w = *at;
                         int tok, limit;
                         uint64_t anc;
                         row_of(w, tok, limit, anc);
@@ -544,7 +542,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                         if (!ok) break;
                         uint8_t* v0 = gbase + OFF_V + (vb % SV) * BLK_BYTES;
                         bool odd = false;
-                        const Wide& w = wide[i / a.c.Hkv];
+                        const Wide& w = *at;
                         const int kb = (w.blk0 + j) * BN, keys = w.keys;
                         const int lo = max(w.L - kb, 0), n = BN - lo;
                         for (int x = r; x < n * 16; x += 128) {
@@ -639,8 +637,8 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
             if (!ok) break;
             tc_fence_after();
             {
-                const Wide w = wide[i / a.c.Hkv];
-                const int kvh = i % a.c.Hkv;
+                const Wide w = *at;
+                const int kvh = w.kvh;
                 int tok, limit;
                 uint64_t anc;
                 const bool row_ok = row_of(w, tok, limit, anc);
@@ -649,7 +647,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                 typename E::T* orow =
                     static_cast<typename E::T*>(a.O) + ((int64_t)(w.q0 + tok) * a.Hq + kvh * G + rg) * HD;
                 // partial rows lie four dims at a time, the tile's 128 rows side by side: a warp's store is one run
-                const int64_t pblk = (int64_t)(w.part + kvh) * 2 + t;
+                const int64_t pblk = (int64_t)w.part * 2 + t;
                 float* part = a.wide_o + (direct ? 0 : pblk * 128 * HD + r * 4);
                 for (int c0 = 0; c0 < HD; c0 += 32) {
                     float o[32];
@@ -718,27 +716,17 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
 // ranges' reads is issued together.
 constexpr int kBatch = 10;
 template <int DT>
-__global__ void __launch_bounds__(256, 2)
-join_kernel(const __grid_constant__ AttnArgs a) {
+__device__ __forceinline__ void join_rows(const AttnArgs& a, const Group& gr, int part) {
     using E = Elem<DT>;
-    // The plan is read ahead of the grid wait: the kernel before this one is the attention, which let this one
-    // start after its own wait, and so after the plan was written.
-    const PlanHead& head = *reinterpret_cast<const PlanHead*>(a.plan);
-    const int item = blockIdx.y;
-    const Group gr = reinterpret_cast<const Group*>(a.plan + a.shape.off_group)[item / a.c.Hkv];
-    const bool live = plan_fits(a, head) && item < head.n_groups * a.c.Hkv;
-    griddep_enter();
-    if (!live) return;
-    const int kvh = item % a.c.Hkv;
-    // 16 CTAs an item: 8 a tile, two groups of eight dims each
-    const int t = blockIdx.x >> 3, r = threadIdx.x & 127, c = (blockIdx.x & 7) * 2 + (threadIdx.x >> 7);
+    // part 0 .. 15 of a group: 8 a tile, of two groups of eight dims each
+    const int t = part >> 3, r = threadIdx.x & 127, c = (part & 7) * 2 + (threadIdx.x >> 7);
     const int T = a.shape.tile_tokens;
     const int tok = gr.tok0 + t * T + r / a.G;
     if (r / a.G >= T || tok >= gr.n || t >= gr.tiles) return;
-    const int64_t blk = (int64_t)(gr.part0 + kvh) * 2 + t;
+    const int64_t blk = (int64_t)gr.part0 * 2 + t;
     const float* lse = a.wide_lse + blk * 128 + r;
     const float* po = a.wide_o + blk * 128 * HD + c * 1024 + r * 4;
-    const int64_t step = (int64_t)a.c.Hkv * 2 * 128;
+    const int64_t step = (int64_t)gr.step * 2 * 128;
     float m = -INFINITY, l = 0.f;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int c0 = 0; c0 < gr.ranges; c0 += kBatch) {
@@ -775,9 +763,21 @@ join_kernel(const __grid_constant__ AttnArgs a) {
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
     typename E::T* dst =
-        static_cast<typename E::T*>(a.O) + ((int64_t)(gr.q0 + tok) * a.Hq + kvh * a.G + r % a.G) * HD + c * 8;
+        static_cast<typename E::T*>(a.O) + ((int64_t)(gr.q0 + tok) * a.Hq + gr.kvh * a.G + r % a.G) * HD + c * 8;
     *reinterpret_cast<uint4*>(dst) = make_uint4(E::down(acc[0] * inv, acc[1] * inv), E::down(acc[2] * inv, acc[3] * inv),
                                                 E::down(acc[4] * inv, acc[5] * inv), E::down(acc[6] * inv, acc[7] * inv));
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256, 2)
+join_kernel(const __grid_constant__ AttnArgs a) {
+    // The plan is read ahead of the grid wait: the kernels before this one are the attention's, of which the first
+    // let the next start after its own wait, and so after the plan was written.
+    const PlanHead& head = *reinterpret_cast<const PlanHead*>(a.plan);
+    const Group* groups = reinterpret_cast<const Group*>(a.plan + a.shape.off_group);
+    const int tasks = plan_fits(a, head) ? head.n_groups * 16 : 0;
+    griddep_enter();
+    for (int task = blockIdx.x; task < tasks; task += gridDim.x) join_rows<DT>(a, groups[task >> 4], task & 15);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -817,10 +817,6 @@ int launch(const AttnArgs& a, const Maps& m, cudaStream_t st) {
     }
     launch_pdl(wide_kernel<DT>, dim3(a.shape.sms), dim3(NTHREADS), SMEM_BYTES, st, m, a);
     count_launches(1);
-    if (a.shape.max_groups > 0) {
-        launch_pdl(join_kernel<DT>, dim3(16, a.shape.max_groups * a.c.Hkv), dim3(256), 0, st, a);
-        count_launches(1);
-    }
     return launch_status();
 }
 
@@ -846,6 +842,15 @@ int wide_launch(const AttnArgs& a, cudaStream_t st) {
         if (!encode(&m.v, a.c.dtype, 5, a.V, dims, strides, box)) return GRAFT_ERR_CUDA;
     }
     return a.c.dtype == GRAFT_BF16 ? launch<GRAFT_BF16>(a, m, st) : launch<GRAFT_FP16>(a, m, st);
+}
+
+int join_launch(const AttnArgs& a, cudaStream_t st) {
+    const auto kernel = a.c.dtype == GRAFT_BF16 ? join_kernel<GRAFT_BF16> : join_kernel<GRAFT_FP16>;
+    // (four CTAs an SM at most: where nothing turns out to be split they only come and go)
+    const int tasks = 16 * a.shape.max_groups, most = 4 * a.shape.sms;
+    launch_pdl(kernel, dim3(tasks < most ? tasks : most), dim3(256), 0, st, a);
+    count_launches(1);
+    return launch_status();
 }
 
 }  // namespace paged
