@@ -649,3 +649,62 @@ def test_bad_page_calls_are_flagged_and_skipped():
     s.cache.free(s.i32([0]))
     assert s.status() == b.STATUS_PAGE
     assert min(s.cache.page_refs.tolist()) == 0
+
+
+# ------------------------------------------------------------------ schedules
+@pytest.mark.parametrize("Hkv,G,page,new,lens", [
+    (2, 8, 16, [200, 1, 1, 1], [5, 900, 300, 0]),            # both kinds: the few rows run beside the wide ones
+    (8, 16, 16, [64] * 5, [700, 650, 600, 64, 0]),           # two thirds of a wave of items: shared out by keys
+    (8, 16, 32, [64] * 6, [1500, 1400, 700, 600, 64, 0]),    # past one round: what is left over is split
+    (4, 16, 64, [300, 2, 64], [1000, 3000, 10]),
+    (1, 4, 16, [1] * 40, list(range(0, 4000, 100))),         # one item a sequence
+    (8, 4, 16, [2] * 45, list(range(0, 900, 20))),           # more items than CTAs: even runs over them
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_every_schedule_and_the_same_bits_every_time(dtype, Hkv, G, page, new, lens):
+    s = Setup(lens, new, Hkv, page, dtype, seed=len(new))
+    Q, O = run_attention(s, G)
+    check_attention(s, O, Q, 0.09)
+    Qd = Q.to(DEV)
+    for _ in range(5):
+        again = torch.full_like(O, 7.0)
+        s.cache.plan(s.q_start, O.shape[0], O.shape[1], max(new))
+        s.cache.attend(0, Qd, 0.09, out=again)
+        assert torch.equal(again, O)
+    assert s.status() == 0
+
+
+def test_more_sequences_than_a_block_has_threads():
+    rng = np.random.default_rng(8)
+    n = 1100
+    new = [int(x) for x in rng.integers(0, 3, n)]
+    new[700] = 20
+    s = Setup([int(x) for x in rng.integers(0, 30, n)], new, 1, 16, seed=8)
+    Q, O = run_attention(s, 2, pad=1)
+    check_attention(s, O, Q, 0.09)
+
+
+def test_two_graphs_of_one_handle_one_after_another():
+    s = Setup([300, 90], [64, 1], 2, 16, seed=14)
+    Q = s.randn(65, 8, 128)
+    Qd, outs, graphs = Q.to(DEV), [], []
+    for _ in range(2):
+        O = torch.zeros(65, 8, 128, dtype=s.dtype, device=DEV)
+
+        def step():
+            s.cache.plan(s.q_start, 65, 8, 64)
+            s.cache.attend(0, Qd, 0.1, out=O)
+
+        step()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        outs.append(O)
+        graphs.append(g)
+    # a larger plan in between replaces the handle's buffers; the graphs keep theirs
+    s.cache.plan(s.q_start, 5000, 8, 4000)
+    for g, O in zip(graphs, outs):
+        O.zero_()
+        g.replay()
+        assert s.status() == 0
+        check_attention(s, O, Q, 0.1)

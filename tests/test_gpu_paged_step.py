@@ -1,0 +1,185 @@
+"""The paged verify step, chained: every stage against the oracle, over several steps with forks between them."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import accept as oacc
+from oracle import paged as opg
+from oracle import update_m as oupd
+from tests.helpers import gb
+from tree_verification_gb300 import synth
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+B, KMAX, HQ, HKV, LAYERS, PAGE, V, W = 3, 16, 8, 2, 2, 16, 512, 4
+
+
+def i32(x):
+    return torch.from_numpy(np.ascontiguousarray(np.asarray(x, np.int32))).to(DEV)
+
+
+class World:
+    """A cache of three sequences (the last one empty), its pools, M, and a step."""
+
+    def __init__(self, world, dtype=torch.bfloat16, **kw):
+        from tree_verification_gb300.paged import PagedCache
+        from tree_verification_gb300.paged_step import PagedVerifyStep
+        self.rng = np.random.default_rng(world)
+        self.g = torch.Generator(device=DEV).manual_seed(world)
+        lens, P, M = [37, 48, 0], 40, 12
+        counts = [-(-n // PAGE) for n in lens]
+        ids = self.rng.permutation(P)
+        table = np.full((B, M), -1, np.int32)
+        refs = np.zeros(P, np.int32)
+        at = 0
+        for b, c in enumerate(counts):
+            table[b, :c] = ids[at:at + c]
+            at += c
+        refs[ids[:at]] = 1
+        self.pages = opg.Pages(table, counts, lens, refs, PAGE)
+        self.K = torch.randn(LAYERS, P, PAGE, HKV, 128, generator=self.g, device=DEV).to(dtype)
+        self.V = torch.randn(LAYERS, P, PAGE, HKV, 128, generator=self.g, device=DEV).to(dtype)
+        self.cache = PagedCache(list(self.K), list(self.V), i32(table), i32(lens), page_refs=i32(refs), held=i32(counts))
+        self.cfg = gb().graft_config_init(KMAX, 4, 3, V, W, [0, 1], 0.3)
+        self.w, self.factor = gb().graft_rope_inv_freq(128, 10000.0, "yarn", 4.0, 1.0, 32.0, 64.0, device=DEV)
+        self.step = PagedVerifyStep(self.cfg, self.cache, HQ, inv_freq=self.w, factor=self.factor, **kw)
+        s, c = synth.empty_M(V, W)
+        self.M = [torch.from_numpy(s).to(DEV), torch.from_numpy(c).to(DEV)]
+        self.dtype = dtype
+
+    def inputs(self):
+        n = lambda *s: torch.randn(*s, generator=self.g, device=DEV)  # noqa: E731
+        dl, roots = n(B, 4, 3, V), i32(self.rng.integers(0, V, B))
+        tree = gb().graft_build_tree(self.cfg, dl, roots, self.M[0], self.cache.lengths)
+        tl = n(B, KMAX, V)
+        synth.plant_paths(tl, tree["tok"].cpu().numpy(), tree["parent"].cpu().numpy(), tree["depth"].cpu().numpy(),
+                          self.rng.integers(1, 5, B))
+        qkv = [n(B * KMAX, HQ + 2 * HKV, 128).to(self.dtype) for _ in range(LAYERS)]
+        return dict(draft_logits=dl, root_tok=roots, Q=[x[:, :HQ] for x in qkv], K=[x[:, HQ:HQ + HKV] for x in qkv],
+                    V=[x[:, HQ + HKV:] for x in qkv], target_logits=tl)
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+@pytest.mark.parametrize("m_policy", ["tree", "both"])
+def test_chained_steps_match_the_oracle(m_policy):
+    w = World(1, m_policy=m_policy)
+    c, st, P = w.cache, w.step, w.pages
+    for k in range(4):
+        if k == 2:  # the empty sequence's rows so far go; it becomes a copy of the first one
+            c.free(i32([2]))
+            c.fork(i32([0]), i32([2]))
+            P.free([2])
+            P.fork([0], [2])
+        lens = list(P.lengths)
+        assert c.lengths.tolist() == lens
+        inp = w.inputs()
+        Kp, Vp = np64(w.K), np64(w.V)
+        seen = []
+        s0, c0 = w.M[0].cpu().numpy(), w.M[1].cpu().numpy()
+        st.run(M_succ=w.M[0], M_cnt=w.M[1], attended=lambda l, O: seen.append((st.Qr.clone(), O.clone(), w.K[l].clone(),
+                                                                                w.V[l].clone())), **inp)
+        torch.cuda.synchronize()
+        assert int(st.status.item()) == 0
+        # pages: reserved, the shared last page copied
+        copies, refused = P.reserve([KMAX] * B)
+        assert not refused and (k != 2 or len(copies) == 2)
+        for a, b, r in copies:
+            Kp[:, b, :r], Vp[:, b, :r] = Kp[:, a, :r], Vp[:, a, :r]
+        assert c.page_refs.tolist() == P.refs and c.held.tolist() == P.held
+        table = np.array(P.table)
+        pos = st.tree["pos"].cpu().numpy().reshape(-1)
+        mask = st.tree["mask"].cpu().numpy().view(np.uint64).reshape(-1)
+        starts = np.arange(B + 1) * KMAX
+        for l, (q, o, kl, vl) in enumerate(seen):
+            # rotated rows: half a step of bf16 and 32-bit products
+            for name, x in (("Q", inp["Q"][l]), ("K", inp["K"][l])):
+                ref = opg.rope(np64(x), pos, w.w.cpu().numpy(), False, w.factor)
+                tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * w.factor * np.abs(np64(x)).max()
+                if name == "Q":
+                    got = np64(q).reshape(ref.shape)
+                else:
+                    got = np.stack([np64(kl)[table[b, (lens[b] + i) // PAGE], (lens[b] + i) % PAGE]
+                                    for b in range(B) for i in range(KMAX)])
+                assert (np.abs(got - ref) <= tol).all()
+            for b in range(B):  # (the mirror takes the rows as the GPU rounded them)
+                for i in range(KMAX):
+                    p, r = table[b, (lens[b] + i) // PAGE], (lens[b] + i) % PAGE
+                    Kp[l, p, r] = np64(kl[p, r])
+                    Vp[l, p, r] = np64(vl[p, r])
+                    assert np.array_equal(Vp[l, p, r], np64(inp["V"][l][b * KMAX + i]))
+            ref, size = opg.attention(np64(q).reshape(-1, HQ, 128), Kp[l], Vp[l], table, lens, starts, st.scale, mask,
+                                      absolute=True)
+            err = np.abs(np64(o).reshape(ref.shape) - ref)
+            assert (err <= 2.0 ** -8 * (2 * np.abs(ref) + size) + 2.0 ** -12 * size + 1e-6).all()
+        # acceptance and compaction
+        acc, path = [], np.full((B, KMAX), -1)
+        for b in range(B):
+            t = {n: st.tree[n][b].tolist() for n in ("tok", "parent", "depth")}
+            _, n, p, out_tok, bonus = oacc.accept(inp["target_logits"][b].cpu().numpy(), t["tok"], t["parent"], t["depth"])
+            assert st.acc["acc_len"][b].item() == n and st.acc["path"][b, :n].tolist() == p
+            assert st.acc["out_tok"][b, :n].tolist() == out_tok and st.acc["bonus"][b].item() == bonus
+            acc.append(n)
+            path[b, :n] = p
+        Kp, Vp, new = opg.compact(Kp, Vp, table, lens, path, acc)
+        assert c.lengths.tolist() == list(new) and max(acc) > 1
+        P.lengths = [int(x) for x in new]
+        for b in range(B):
+            for r in range(P.lengths[b]):
+                p, x = table[b, r // PAGE], r % PAGE
+                assert np.array_equal(np64(w.K[:, p, x]), Kp[:, p, x]) and np.array_equal(np64(w.V[:, p, x]), Vp[:, p, x])
+        if m_policy == "tree":
+            g = st.acc["argmax"].cpu().numpy().reshape(-1)
+            s1, c1 = oupd.update_M(s0, c0, st.tree["tok"].cpu().numpy().reshape(-1), g)
+            assert np.array_equal(w.M[0].cpu().numpy(), s1) and np.array_equal(w.M[1].cpu().numpy(), c1)
+
+
+def test_a_captured_step_is_the_step():
+    a, b = World(5), World(5)
+    first, later = a.inputs(), a.inputs()
+    b.inputs(), b.inputs()
+    names = [n for n in first if n not in ("Q", "K", "V")]
+    held = {n: first[n].clone() for n in names}
+    rows = {n: [x.clone() for x in first[n]] for n in "QKV"}
+    for inp in (first, first, later):
+        a.step.run(M_succ=a.M[0], M_cnt=a.M[1], **inp)
+    torch.cuda.synchronize()
+    b.step.capture(M_succ=b.M[0], M_cnt=b.M[1], **held, **rows)  # runs the first step, then captures it
+    b.step.graph.replay()
+    for n in names:
+        held[n].copy_(later[n])
+    for n in "QKV":
+        for x, y in zip(rows[n], later[n]):
+            x.copy_(y)
+    b.step.graph.replay()
+    torch.cuda.synchronize()
+    assert int(a.step.status.item()) == int(b.step.status.item()) == 0
+    assert torch.equal(a.cache.lengths, b.cache.lengths) and torch.equal(a.step.acc["out_tok"], b.step.acc["out_tok"])
+    assert torch.equal(a.step.O, b.step.O) and torch.equal(a.K, b.K) and torch.equal(a.V, b.V)
+    assert torch.equal(a.cache.page_refs, b.cache.page_refs) and torch.equal(a.M[1], b.M[1])
+
+
+def test_sampling_and_fp16():
+    w = World(9, dtype=torch.float16, temperature=0.7, seed=3)
+    inp = w.inputs()
+    w.step.run(M_succ=w.M[0], M_cnt=w.M[1], **inp)
+    torch.cuda.synchronize()
+    assert int(w.step.status.item()) == 0
+    y = gb().graft_sample_tokens(inp["target_logits"], w.step.tree["pos"], 0.7, 3)
+    assert torch.equal(y, w.step.acc["argmax"])
+    assert w.cache.lengths.tolist() == [a + b for a, b in zip([37, 48, 0], w.step.acc["acc_len"].tolist())]
+
+
+def test_refusals():
+    from tree_verification_gb300.paged import PagedCache
+    from tree_verification_gb300.paged_step import PagedVerifyStep
+    w = World(2)
+    with pytest.raises(ValueError):
+        PagedVerifyStep(w.cfg, w.cache, 7)
+    with pytest.raises(ValueError):
+        PagedVerifyStep(w.cfg, w.cache, 8, m_policy="none")
+    bare = PagedCache(list(w.K), list(w.V), w.cache.block_table, w.cache.lengths)
+    with pytest.raises(ValueError):
+        PagedVerifyStep(w.cfg, bare, 8)

@@ -135,9 +135,10 @@ __device__ __forceinline__ void plan_few(const GraftPagedCache& c, int Hq, char*
         const int mine = tid < n_few ? s_few[tid].units : 0;
         // an SM's share left free for every item: the CTAs that join pieces hold theirs longest, and the next
         // call's CTAs find room elsewhere (decode of one sequence: 10.4 -> 9.0 us a call)
+        // (not where the runs are long and every SM counts: 65536 keys, 49 against 51 us)
         int slots = shape.ctas / c.Hkv;
-        if (n_few * 8 <= slots) slots -= n_few;
         const int64_t even = (units + shape.ctas - 1) / shape.ctas;
+        if (n_few * 8 <= slots && even <= 8 * shape.few_warps) slots -= n_few;
         s_units[tid] = mine;
         __syncthreads();
         const int len = piece_length(s_units, n_few, slots, (int)max((int64_t)shape.few_warps, even),
