@@ -222,23 +222,38 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
 // One CTA.  Demands are counted and summed in the order of the sequences,
 // the lowest free pages found (in tiles of the reference counts, until the
 // demand is met) and handed out; the replaced pages' references fall last,
-// so that "shared" means the same to every sequence of the call.
+// so that "shared" means the same to every sequence of the call.  Latency
+// bound: what depends on nothing is read at once (a thread's sequence and its
+// share of the first tile), and the pages found first stay in shared memory.
+constexpr int kTile = kPlanThreads * 4;
+constexpr int kFreshInSmem = 2048;
 __global__ void __launch_bounds__(kPlanThreads)
 reserve_kernel(const __grid_constant__ GraftPagedCache c, const int32_t* __restrict__ new_rows, ReserveWs w,
                int page_shift) {
     __shared__ int s_warp[32];
     __shared__ int s_first[GRAFT_MAX_SEQS], s_need[GRAFT_MAX_SEQS];  // rank of the first new page, their number
+    __shared__ int s_fresh[kFreshInSmem];
     griddep_enter();
     const int tid = threadIdx.x;
+    auto read_tile = [&](int p0) {  // which of this thread's four pages are free, as bits
+        int bits = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int p = p0 + tid * 4 + k;
+            bits |= (p < c.num_pages && c.page_refs[p] == 0) << k;
+        }
+        return bits;
+    };
+    int free = read_tile(0);
     int demand = 0;
     for (int b0 = 0; b0 < c.n_seqs; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int need = 0, bad = 0;
-        const int rows = b < c.n_seqs ? new_rows[b] : 0;
+        const bool mine = b < c.n_seqs;
+        const int rows = mine ? new_rows[b] : 0, held = mine ? c.held[b] : 0;
+        const int64_t L = mine ? c.lengths[b] : 0;
         if (rows != 0) {
-            const int64_t L = c.lengths[b];
             const int64_t pages = (L + rows + c.page_rows - 1) >> page_shift;
-            const int held = c.held[b];
             const int64_t first = L >> page_shift;
             if (L < 0 || rows < 0 || held < 0 || pages > c.max_pages || held > c.max_pages || held < first) {
                 bad = GRAFT_STATUS_LENGTH;
@@ -259,27 +274,24 @@ reserve_kernel(const __grid_constant__ GraftPagedCache c, const int32_t* __restr
         }
         int total;
         const int before = block_scan(need, s_warp, &total);
-        if (b < c.n_seqs) {
+        if (mine) {
             s_first[b] = demand + before;
             s_need[b] = bad ? -1 : need;
         }
         demand += total;
     }
     int found = 0;
-    for (int p0 = 0; p0 < c.num_pages && found < demand; p0 += kPlanThreads * 4) {
-        int free[4], n = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int p = p0 + tid * 4 + k;
-            free[k] = p < c.num_pages && c.page_refs[p] == 0;
-            n += free[k];
-        }
+    for (int p0 = 0; p0 < c.num_pages && found < demand; p0 += kTile) {
+        if (p0 > 0) free = read_tile(p0);
         int total;
-        int at = found + block_scan(n, s_warp, &total);
+        int at = found + block_scan(__popc(free), s_warp, &total);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (free[k]) {
-                w.fresh[at] = p0 + tid * 4 + k;
+            if (free >> k & 1) {
+                if (at < kFreshInSmem)
+                    s_fresh[at] = p0 + tid * 4 + k;
+                else
+                    w.fresh[at] = p0 + tid * 4 + k;
                 w.old[at] = -1;
                 ++at;
             }
@@ -301,13 +313,13 @@ reserve_kernel(const __grid_constant__ GraftPagedCache c, const int32_t* __restr
                 for (int k = first; k < pages; ++k) {
                     const int old = k < held ? row[k] : -1;
                     if (old >= 0 && c.page_refs[old] <= 1) continue;
-                    const int p = w.fresh[at];
+                    const int p = at < kFreshInSmem ? s_fresh[at] : w.fresh[at];
                     w.old[at++] = old;
                     c.page_refs[p] = 1;
                     row[k] = p;
                     if (old >= 0 && k == first) tail = Tail{old, p, (int)(L & (c.page_rows - 1)), 0};
                 }
-                c.held[b] = max(held, pages);
+                if (pages > held) c.held[b] = pages;
             }
         }
         w.tail[b] = tail;

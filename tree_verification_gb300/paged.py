@@ -118,30 +118,39 @@ class PagedCache:
         if rc:
             gb._check(rc, name)
 
+    # (the checks run once a tensor and call, a dozen times a step and layer: the usual case comes first, and only
+    # what it does not take is looked at again for a message)
     def _need(self, t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> int:
         """Checks a dense tensor on the cache's device; returns its address."""
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a tensor")
-        if t.dtype != dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
-            gb._need(t, name, dtype, shape)
-            raise ValueError(f"{name} must be on {self.device}")
-        return t.data_ptr()
+        try:
+            if t.dtype is dtype and t.get_device() == self._index and t.shape == shape and t.is_contiguous():
+                return t.data_ptr()
+        except AttributeError:
+            raise TypeError(f"{name} must be a tensor") from None
+        gb._need(t, name, dtype, shape)
+        raise ValueError(f"{name} must be on {self.device}")
 
     def _rows(self, t: torch.Tensor, name: str, N: int, H: int):
         """Checks [N][H][128] rows whose heads are contiguous; returns address and row stride."""
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a tensor")
-        if t.dtype != self.dtype or t.device != self.device:
+        width = H * 128
+        try:
+            if t.dtype is self.dtype and t.get_device() == self._index and t.shape == (N, H, 128):
+                s0, s1, s2 = t.stride()
+                if s2 == 1 and s1 == 128 and s0 >= width and not s0 & 7:
+                    return t.data_ptr(), s0
+        except AttributeError:
+            raise TypeError(f"{name} must be a tensor") from None
+        if t.dtype is not self.dtype or t.device != self.device:
             raise ValueError(f"{name} must be {self.dtype} on {self.device}")
         if t.shape != (N, H, gb.HEAD_DIM):
             raise ValueError(f"{name} must have shape {(N, H, gb.HEAD_DIM)}, got {tuple(t.shape)}")
         s0, s1, s2 = t.stride()
-        if N == 1 or H == 0:
-            s0 = max(s0, H * gb.HEAD_DIM)
+        if N <= 1 or H == 0:
+            s0 = width  # (the stride of a single row, or of no columns, means nothing)
         if H and (s2 != 1 or (H > 1 and s1 != gb.HEAD_DIM)):
             raise ValueError(f"{name} must have contiguous heads")
-        if s0 < H * gb.HEAD_DIM or s0 % 8:
-            raise ValueError(f"{name}'s rows must be at least {H * gb.HEAD_DIM} elements apart, by a multiple of 8")
+        if s0 < width or s0 % 8:
+            raise ValueError(f"{name}'s rows must be at least {width} elements apart, by a multiple of 8")
         return t.data_ptr(), s0
 
     def _layer(self, layer: int) -> int:
@@ -156,12 +165,16 @@ class PagedCache:
 
         Returns the rotated Q (``out``, which may be Q itself).  Q may be None.  Without inv_freq nothing is rotated."""
         layer = self._layer(layer)
+        if not isinstance(K, torch.Tensor) or K.dim() != 3:
+            raise ValueError("K must be [N][Hkv][128]")
         N = K.shape[0]
         kp, ks = self._rows(K, "K", N, self.Hkv)
         vp, vs = self._rows(V, "V", N, self.Hkv)
         qp = op = None
         qs = os = Hq = 0
         if Q is not None:
+            if not isinstance(Q, torch.Tensor) or Q.dim() != 3:
+                raise ValueError("Q must be [N][Hq][128]")
             Hq = Q.shape[1]
             qp, qs = self._rows(Q, "Q", N, Hq)
             if out is None:
