@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kTokens = 2;
-constexpr int kAhead = 5;  // units a thread loads before the look-up
+constexpr int kStep = kThreads / 8;  // heads that the CTA's threads hold at once
 
 struct RopeArgs {
     GraftPagedCache c;
@@ -93,8 +93,9 @@ __device__ __forceinline__ uint32_t turn1(uint32_t a, float2 cs) {
     return E::down(x.x * cs.x - x.y * cs.y, x.x * cs.y + x.y * cs.x);
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads)
+// kAhead: heads that a thread reads at a time, the first ones before the look-up
+template <int DT, int kAhead>
+__global__ void __launch_bounds__(kThreads, 5)
 rope_append_kernel(const __grid_constant__ RopeArgs a) {
     __shared__ float2 s_cs[kTokens][HD / 2];
     __shared__ int64_t s_dst[kTokens];  // cache row in the pool, -1: not written
@@ -103,44 +104,31 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int t0 = blockIdx.x * a.tokens;
     const int nt = min(a.tokens, a.N - t0);
-    const int heads = a.Hq + 2 * a.c.Hkv;
-    const int units = nt * heads * 8;  // a head is 8 units of two 16-byte chunks
+    const int heads = a.Hq + 2 * a.c.Hkv, turned = a.Hq + a.c.Hkv;
     const int rot_units = a.rot / 16;
-
-    // unit -> its token, head, source and two chunks
-    struct Unit {
-        int t, h, c0, c1;
-        const uint4* src;
-    };
-    auto unit_of = [&](int u) {
-        Unit x;
-        const int i = u & 7;
-        const int th = u >> 3;
-        x.t = th / heads;
-        x.h = th - x.t * heads;
-        // rotated units of the half layout pair chunk i with chunk i + rot / 16
-        const bool half = !a.inter && i < rot_units && x.h < a.Hq + a.c.Hkv;
-        x.c0 = half ? i : 2 * i;
-        x.c1 = half ? i + rot_units : 2 * i + 1;
-        const int64_t row = t0 + x.t;
-        if (x.h < a.Hq)
-            x.src = a.Q + row * a.qs + x.h * 16;
-        else if (x.h < a.Hq + a.c.Hkv)
-            x.src = a.K + row * a.ks + (x.h - a.Hq) * 16;
-        else
-            x.src = a.V + row * a.vs + (x.h - a.Hq - a.c.Hkv) * 16;
-        return x;
-    };
+    // A head is 8 units of two 16-byte chunks; a thread keeps its place i in the head and takes every kStep-th head,
+    // so that a row's cosines come to its registers once.  The rotated units of the half layout pair chunk i with
+    // chunk i + rot / 16.
+    const int i = tid & 7, h_first = tid >> 3;
+    const bool rotates = i < rot_units;
+    const int c0 = rotates && !a.inter ? i : 2 * i, c1 = rotates && !a.inter ? i + rot_units : 2 * i + 1;
     uint4 buf[kAhead][2];
+    auto fetch = [&](int t, int h0) {
+        const int64_t row = t0 + t;
+        const uint4* q = a.Q + row * a.qs;
+        const uint4* k = a.K + row * a.ks - a.Hq * 16;
+        const uint4* v = a.V + row * a.vs - turned * 16;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-        const int u = tid + k * kThreads;
-        if (u < units) {
-            const Unit x = unit_of(u);
-            buf[k][0] = x.src[x.c0];
-            buf[k][1] = x.src[x.c1];
+        for (int x = 0; x < kAhead; ++x) {
+            const int h = h0 + x * kStep;
+            if (h < heads) {
+                const uint4* src = (h < a.Hq ? q : h < turned ? k : v) + h * 16;
+                buf[x][0] = src[h < turned ? c0 : 2 * i];
+                buf[x][1] = src[h < turned ? c1 : 2 * i + 1];
+            }
         }
-    }
+    };
+    fetch(0, h_first);
     // one warp a row; what the cosines need first, the page behind them
     int page_at = -1;  // entry of the block table
     int64_t r = 0;
@@ -162,8 +150,8 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
     }
     __syncthreads();
     const int page = page_at >= 0 ? a.c.block_table[page_at] : 0;
-    for (int i = tid; i < nt * (a.rot / 2); i += kThreads) {
-        const int t = i / (a.rot / 2), p = i - t * (a.rot / 2);
+    for (int x = tid; x < nt * (a.rot / 2); x += kThreads) {
+        const int t = x >= a.rot / 2 ? 1 : 0, p = x - t * (a.rot / 2);
         // 2^64 / 2 pi; a frequency of a turn or more per position keeps only its fraction
         const double turns = a.inv_freq[p] * 0.15915494309189533577;
         const uint64_t w = (uint64_t)__double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
@@ -178,54 +166,52 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
         s_dst[warp] = page_at >= 0 && in_pool ? ((int64_t)page << a.page_shift) + (r & (a.c.page_rows - 1)) : -1;
     }
     __syncthreads();
-    auto finish = [&](int u, uint4 x0, uint4 x1) {
-        const Unit x = unit_of(u);
-        if (!s_live[x.t]) return;
-        const int i = u & 7;
-        if (i < rot_units && x.h < a.Hq + a.c.Hkv) {
-            if (a.inter) {
-                const float4* cs = reinterpret_cast<const float4*>(&s_cs[x.t][i * 8]);
-                uint32_t* w0 = &x0.x;
-                uint32_t* w1 = &x1.x;
+    for (int t = 0; t < nt; ++t) {
+        if (!s_live[t]) {
+            if (t + 1 < nt) fetch(t + 1, h_first);
+            continue;
+        }
+        float4 cs[4];
+        if (rotates) {
+            const float4* s = reinterpret_cast<const float4*>(&s_cs[t][i * 8]);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float4 p = cs[k], q = cs[k + 2];
-                    w0[2 * k] = turn1<DT>(w0[2 * k], make_float2(p.x, p.y));
-                    w0[2 * k + 1] = turn1<DT>(w0[2 * k + 1], make_float2(p.z, p.w));
-                    w1[2 * k] = turn1<DT>(w1[2 * k], make_float2(q.x, q.y));
-                    w1[2 * k + 1] = turn1<DT>(w1[2 * k + 1], make_float2(q.z, q.w));
-                }
-            } else {
-                const float4* cs = reinterpret_cast<const float4*>(&s_cs[x.t][i * 8]);
-                uint32_t* w0 = &x0.x;
-                uint32_t* w1 = &x1.x;
+            for (int k = 0; k < 4; ++k) cs[k] = s[k];
+        }
+        const int64_t dst = s_dst[t];
+        uint4* q = a.Q_out + (int64_t)(t0 + t) * a.qos;
+        uint4* k = a.K_pool + (dst * a.c.Hkv - a.Hq) * 16;
+        uint4* v = a.V_pool + (dst * a.c.Hkv - turned) * 16;
+        for (int h0 = h_first; h0 < heads; h0 += kAhead * kStep) {
+            if (h0 > h_first) fetch(t, h0);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 p = cs[k];
-                    w0[k] = turn2<DT>(w0[k], w1[k], make_float2(p.x, p.y), make_float2(p.z, p.w));
+            for (int x = 0; x < kAhead; ++x) {
+                const int h = h0 + x * kStep;
+                if (h >= heads) continue;
+                uint4 x0 = buf[x][0], x1 = buf[x][1];
+                if (rotates && h < turned) {
+                    uint32_t* w0 = &x0.x;
+                    uint32_t* w1 = &x1.x;
+                    if (a.inter) {
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            w0[2 * z] = turn1<DT>(w0[2 * z], make_float2(cs[z].x, cs[z].y));
+                            w0[2 * z + 1] = turn1<DT>(w0[2 * z + 1], make_float2(cs[z].z, cs[z].w));
+                            w1[2 * z] = turn1<DT>(w1[2 * z], make_float2(cs[z + 2].x, cs[z + 2].y));
+                            w1[2 * z + 1] = turn1<DT>(w1[2 * z + 1], make_float2(cs[z + 2].z, cs[z + 2].w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            w0[z] = turn2<DT>(w0[z], w1[z], make_float2(cs[z].x, cs[z].y), make_float2(cs[z].z, cs[z].w));
+                    }
                 }
+                if (h >= a.Hq && dst < 0) continue;
+                uint4* to = (h < a.Hq ? q : h < turned ? k : v) + h * 16;
+                to[h < turned ? c0 : 2 * i] = x0;
+                to[h < turned ? c1 : 2 * i + 1] = x1;
             }
         }
-        uint4* dst;
-        if (x.h < a.Hq) {
-            dst = a.Q_out + (int64_t)(t0 + x.t) * a.qos + x.h * 16;
-        } else {
-            if (s_dst[x.t] < 0) return;
-            const bool k = x.h < a.Hq + a.c.Hkv;
-            dst = (k ? a.K_pool : a.V_pool) +
-                  (s_dst[x.t] * a.c.Hkv + (x.h - a.Hq - (k ? 0 : a.c.Hkv))) * 16;
-        }
-        dst[x.c0] = x0;
-        dst[x.c1] = x1;
-    };
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-        const int u = tid + k * kThreads;
-        if (u < units) finish(u, buf[k][0], buf[k][1]);
-    }
-    for (int u = tid + kAhead * kThreads; u < units; u += kThreads) {
-        const Unit x = unit_of(u);
-        finish(u, x.src[x.c0], x.src[x.c1]);
+        if (t + 1 < nt) fetch(t + 1, h_first);
     }
 }
 
@@ -345,7 +331,11 @@ extern "C" int graft_rope_append(const GraftPagedCache* cache, void* K_pool, voi
     const int sms = device_sm_count();
     a.tokens = N <= 4 * sms ? 1 : kTokens;
     const dim3 grid((unsigned)((N + a.tokens - 1) / a.tokens));
-    const auto kernel = cache->dtype == GRAFT_BF16 ? rope_append_kernel<GRAFT_BF16> : rope_append_kernel<GRAFT_FP16>;
+    // (a row's heads in one go where three or five a thread do; 4096 rows of 48 heads: 21.4 us, 23.9 with five)
+    const bool three = Hq + 2 * cache->Hkv <= 3 * kStep;
+    const auto kernel = cache->dtype == GRAFT_BF16
+                            ? (three ? rope_append_kernel<GRAFT_BF16, 3> : rope_append_kernel<GRAFT_BF16, 5>)
+                            : (three ? rope_append_kernel<GRAFT_FP16, 3> : rope_append_kernel<GRAFT_FP16, 5>);
     launch_pdl(kernel, grid, dim3(kThreads), 0, (cudaStream_t)stream, a);
     count_launches(1);
     return launch_status();
