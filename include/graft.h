@@ -494,8 +494,8 @@ int graft_update_M_noalloc(int32_t* M_succ, int32_t* M_cnt, int V, int W, const 
  *   page_rows    rows of a page: a power of two, 16 .. 256
  *   num_pages    pages of a pool; num_pages * page_rows < 2^31
  *   n_seqs       sequences, 1 .. GRAFT_MAX_SEQS
- *   max_pages    page numbers of a block-table row; max_pages * page_rows and
- *                n_seqs * max_pages < 2^31
+ *   max_pages    page numbers of a block-table row; max_pages * page_rows <=
+ *                2^30, n_seqs * max_pages < 2^31
  *   n_layers     entries of K_layers / V_layers
  *   block_table  [n_seqs][max_pages] i32: row r of sequence b lies in page
  *                block_table[b][r / page_rows], slot r % page_rows

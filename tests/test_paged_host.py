@@ -32,7 +32,8 @@ BAD_CACHES = [(dict(dtype=2), -1), (dict(Hkv=0), -1), (dict(head_dim=64), -2), (
               (dict(page_rows=48), -2), (dict(page_rows=512), -2), (dict(num_pages=0), -1), (dict(n_seqs=0), -1),
               (dict(n_seqs=4097), -2), (dict(max_pages=0), -1), (dict(num_pages=1 << 27), -2),
               (dict(max_pages=1 << 27), -2), (dict(block_table=None), -1), (dict(lengths=None), -1),
-              (dict(n_layers=-1), -1), (dict(n_seqs=4096, max_pages=1 << 20, page_rows=16), -2)]
+              (dict(n_layers=-1), -1), (dict(n_seqs=4096, max_pages=1 << 20, page_rows=16), -2),
+              (dict(n_seqs=1, max_pages=(1 << 26) + 1, page_rows=16), -2)]
 
 
 @pytest.mark.parametrize("kw,rc", BAD_CACHES)
@@ -49,6 +50,13 @@ def test_bad_caches_are_refused_by_every_entry(kw, rc):
     assert lib.graft_pages_reserve(c, FAKE, FAKE, 1 << 30, None) == rc
     assert lib.graft_pages_fork(c, 1, FAKE, FAKE, None) == rc
     assert lib.graft_pages_free(c, 1, FAKE, None) == rc
+
+
+def test_the_longest_sequence_is_taken():
+    """2^30 rows, so that a row's number plus a call's new rows stays below 2^31."""
+    n = ctypes.c_size_t()
+    c, keep = cache(n_seqs=1, max_pages=1 << 26, page_rows=16)
+    assert gb().lib().graft_paged_plan_size(c, 4, 32, 1, ctypes.byref(n)) == 0 and n.value > 0
 
 
 def test_null_caches_are_refused():

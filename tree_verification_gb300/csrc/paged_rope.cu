@@ -226,7 +226,7 @@ int check_cache(const GraftPagedCache* c) {
     const int p = c->page_rows;
     if (p < 16 || p > GRAFT_MAX_PAGE_ROWS || (p & (p - 1)) != 0) return GRAFT_ERR_UNSUPPORTED_SHAPE;
     if (c->n_seqs > GRAFT_MAX_SEQS || c->n_layers > 16384) return GRAFT_ERR_UNSUPPORTED_SHAPE;
-    if ((int64_t)c->num_pages * p >= (1LL << 31) || (int64_t)c->max_pages * p >= (1LL << 31) ||
+    if ((int64_t)c->num_pages * p >= (1LL << 31) || (int64_t)c->max_pages * p > (1LL << 30) ||
         (int64_t)c->n_seqs * c->max_pages >= (1LL << 31))
         return GRAFT_ERR_UNSUPPORTED_SHAPE;
     if (c->block_table == nullptr || c->lengths == nullptr) return GRAFT_ERR_INVALID_ARG;
