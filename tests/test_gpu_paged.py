@@ -674,6 +674,35 @@ def test_every_schedule_and_the_same_bits_every_time(dtype, Hkv, G, page, new, l
     assert s.status() == 0
 
 
+# few items, single tiles among them, and several items a CTA
+ONE_TILE = [(32, 2, 64, [64], [n]) for n in (0, 64, 65, 128, 300, 4100)] + [
+    (8, 4, 16, [20] * 12, list(range(0, 1200, 100))),
+    (8, 4, 16, [9] * 45, [37 * x % 1100 for x in range(45)]),  # several a CTA, of one block and of more
+    (8, 4, 32, [20, 40, 20, 64, 9, 30], [700, 650, 130, 600, 64, 0]),  # single tiles and pairs
+    (2, 16, 128, [3, 8, 5], [2000, 100, 5000]),
+    (1, 5, 256, [25], [1500])]
+
+
+@pytest.mark.parametrize("Hkv,G,page,new,lens", ONE_TILE)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("tree,odd", [(False, False), (True, False), (False, True), (True, True)])
+def test_single_tiles(dtype, tree, odd, Hkv, G, page, new, lens):
+    s = Setup(lens, new, Hkv, page, dtype, seed=len(new) + lens[0])
+    mask = tree_masks(s.rng, new) if tree else None
+    if odd:
+        for b, n in enumerate(new):
+            for j, kind in ((0, float("inf")), (n // 2, float("nan")), (n - 1, float("-inf"))):
+                r = lens[b] + j
+                s.V0[0, int(s.table[b, r // page]), r % page, b % Hkv, 60 + 3 * j % 64:68 + 3 * j % 64] = kind
+        s.V.copy_(s.V0)
+    Q, O = run_attention(s, G, mask=mask, q_scale=4.0)
+    check_attention(s, O, Q, 0.09, mask)
+    again = torch.full_like(O, 7.0)
+    md = torch.from_numpy(mask.view(np.int64)).to(DEV) if tree else None
+    s.cache.attend(0, Q.to(DEV), 0.09, mask=md, out=again)
+    assert torch.equal(again.view(torch.int16), O.view(torch.int16)) and s.status() == 0
+
+
 def test_more_sequences_than_a_block_has_threads():
     rng = np.random.default_rng(8)
     n = 1100
