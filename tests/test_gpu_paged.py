@@ -703,6 +703,18 @@ def test_single_tiles(dtype, tree, odd, Hkv, G, page, new, lens):
     assert torch.equal(again.view(torch.int16), O.view(torch.int16)) and s.status() == 0
 
 
+@pytest.mark.parametrize("extra", [1, 3])
+def test_a_few_short_items_past_a_whole_round(extra):
+    """Every CTA is as busy as the next, and the blocks left over are fewer than the CTAs."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    s = Setup([2440] * (sms + extra), [17] * (sms + extra), 1, 128, seed=extra)
+    Q, O = run_attention(s, 8)
+    check_attention(s, O, Q, 0.09)
+    again = torch.full_like(O, 7.0)
+    s.cache.attend(0, Q.to(DEV), 0.09, out=again)
+    assert torch.equal(again, O) and s.status() == 0
+
+
 def test_more_sequences_than_a_block_has_threads():
     rng = np.random.default_rng(8)
     n = 1100

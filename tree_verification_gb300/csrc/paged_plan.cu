@@ -382,10 +382,19 @@ __device__ __forceinline__ void plan_wide(const GraftPagedCache& c, int N, int H
                 level = ((sum >> 11) + blocks) / (sum & 2047);
                 takes = takes && load <= level;
             }
-            // (the shares' sum is off by rounding and by what dropped out last: the cuts are scaled to the blocks)
-            const int64_t share = takes ? level - load : 0;
-            const int64_t ahead = scan_block<int64_t>(share, s_warp, &sum);
-            const int64_t from = ahead * blocks / sum, to = (ahead + share) * blocks / sum;
+            // (the shares' sum is off by rounding and by what dropped out last: the cuts are scaled to the blocks; the
+            // share of a few blocks over a level floor would be none at all, so then they go to the first CTAs alone)
+            int64_t share = takes ? level - load : 0;
+            const int64_t both = scan_block<int64_t>(share << 11 | takes, s_warp, &sum);
+            int64_t ahead = both >> 11, shares = sum >> 11;
+            const int64_t takers = sum & 2047, few_takers = (blocks + kSnap - 1) / kSnap;
+            if (few_takers < takers) {
+                const int64_t rank = both & 2047;
+                share = takes && rank < few_takers;
+                ahead = min(rank, few_takers);
+                shares = few_takers;
+            }
+            const int64_t from = ahead * blocks / shares, to = (ahead + share) * blocks / shares;
             auto item_of = [&](int x) {  // the item whose blocks hold x
                 int lo = 0, hi = rem;
                 while (hi - lo > 1) {
