@@ -35,7 +35,8 @@ struct PlanHead {
     int32_t few_ctas;    // CTAs of the few kernel that have work
     int32_t rounds;      // whole rounds of wide items: every CTA takes one of each
     int32_t n_groups;    // row blocks split by keys
-    int32_t reserved[16];
+    int32_t tiles;       // tiles of such a row block at most
+    int32_t reserved[15];
 };
 constexpr int32_t kPlanMagic = 0x47503033;
 

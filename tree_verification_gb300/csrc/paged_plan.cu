@@ -244,7 +244,7 @@ __device__ __forceinline__ void plan_wide(const GraftPagedCache& c, int N, int H
     }
     __syncthreads();
     const int P = shape.sms;
-    int rounds = 0, n_groups = 0;
+    int rounds = 0, n_groups = 0, most_tiles = 2;
     if (n_pairs == 0) {
         for (int k = tid; k <= P; k += kPlanThreads) where[k] = 0;
     } else if (shape.max_groups > 0 && n_pairs * c.Hkv * 3 <= P) {
@@ -281,7 +281,10 @@ __device__ __forceinline__ void plan_wide(const GraftPagedCache& c, int N, int H
         if (tiles <= slots) {
             const int alone = length_of(true, 2 * n_pairs, tiles);
             single = alone * kTileTime <= len + kPairCost;
-            if (single) len = alone;
+            if (single) {
+                len = alone;
+                most_tiles = 1;
+            }
         }
         const int n = single ? 2 * n_pairs : n_pairs;
         Wide w{};
@@ -457,15 +460,17 @@ __device__ __forceinline__ void plan_wide(const GraftPagedCache& c, int N, int H
         PlanHead& h = *reinterpret_cast<PlanHead*>(plan);
         h.rounds = rounds;
         h.n_groups = n_groups;
+        h.tiles = most_tiles;
     }
 }
 
 // Block 0 plans the few entries, block 1 the wide items (a grid of one block has only the one kind).
+template <bool kFew, bool kWide>
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int32_t* __restrict__ q_start, int max_new,
             int tree, char* plan, const __grid_constant__ PlanShape shape) {
     griddep_wait();
-    const bool wide_block = blockIdx.x > 0 || !shape.few;
+    const bool wide_block = kWide && (!kFew || blockIdx.x > 0);
     // Every block checks all sequences, the first one sets the status.
     auto read_seq = [&](int b, int& q0, int& n, int& L) {
         q0 = n = L = 0;
@@ -481,10 +486,10 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
         n = (int)rows;
         L = (int)len;
     };
-    if (wide_block)
-        plan_wide(c, N, Hq, tree, plan, shape, read_seq);
-    else
-        plan_few(c, Hq, plan, shape, read_seq);
+    if constexpr (kWide)
+        if (wide_block) plan_wide(c, N, Hq, tree, plan, shape, read_seq);
+    if constexpr (kFew)
+        if (!wide_block) plan_few(c, Hq, plan, shape, read_seq);
     if (threadIdx.x == 0 && blockIdx.x == 0) {
         PlanHead& h = *reinterpret_cast<PlanHead*>(plan);
         h.magic = kPlanMagic;
@@ -555,7 +560,8 @@ PlanShape plan_shape(const GraftPagedCache* c, int N, int Hq, int max_new) {
     s.few_warps = seqs * c->Hkv >= 2 * sms ? 4 : 8;
     s.ctas = sms * 8 / s.few_warps;
     const int full_pairs = N / (2 * s.tile_tokens);
-    s.max_pairs = s.wide ? (int)(full_pairs + seqs) : 0;
+    const int64_t most_pairs = seqs * ((max_new - 1) / (2 * s.tile_tokens) + 1);
+    s.max_pairs = s.wide ? (int)(full_pairs + seqs < most_pairs ? full_pairs + seqs : most_pairs) : 0;
     // Many rounds even themselves out; up to eight, what is left over may be split by keys.
     const int64_t full_items = (int64_t)full_pairs * c->Hkv, most_blocks = 2LL * s.max_pairs * c->Hkv;
     s.max_groups = s.wide && full_items < 8LL * sms ? (int)(most_blocks < sms ? most_blocks : sms) : 0;
@@ -593,8 +599,9 @@ extern "C" int graft_paged_plan(const GraftPagedCache* cache, int N, int Hq, con
     if (q_start == nullptr) return GRAFT_ERR_INVALID_ARG;
     const PlanShape s = plan_shape(cache, N, Hq, max_new);
     if (!ws_ok(plan, plan_bytes, s.bytes)) return GRAFT_ERR_WORKSPACE;
-    launch_pdl(plan_kernel, dim3(s.few && s.wide ? 2 : 1), dim3(kPlanThreads), 0, (cudaStream_t)stream, *cache, N, Hq, q_start, max_new,
-               tree != 0 ? 1 : 0, static_cast<char*>(plan), s);
+    const auto kernel = !s.wide ? plan_kernel<true, false> : s.few ? plan_kernel<true, true> : plan_kernel<false, true>;
+    launch_pdl(kernel, dim3(s.few && s.wide ? 2 : 1), dim3(kPlanThreads), 0, (cudaStream_t)stream, *cache, N, Hq,
+               q_start, max_new, tree != 0 ? 1 : 0, static_cast<char*>(plan), s);
     count_launches(1);
     return launch_status();
 }
