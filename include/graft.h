@@ -557,8 +557,8 @@ int graft_rope_inv_freq(int rot_dim, double base, int scaling, double stretch, d
  * rounded once.  rot_dim is a multiple of 16, 0 .. 128 (0: no rotation,
  * inv_freq may be NULL).  Hq = 0 (Q NULL) appends alone; Q_out may be Q.
  * lengths are not advanced.  A row whose cache row lies outside the block
- * table sets GRAFT_STATUS_LENGTH, outside the pool GRAFT_STATUS_PAGE; its K
- * and V are not written.
+ * table, or whose sequence starts before row 0, sets GRAFT_STATUS_LENGTH,
+ * one outside the pool GRAFT_STATUS_PAGE; its K and V are not written.
  */
 int graft_rope_append(const GraftPagedCache* cache, void* K_pool, void* V_pool, int N, int Hq,
                       const int32_t* q_start, const int32_t* pos, const double* inv_freq, int rot_dim,

@@ -460,6 +460,22 @@ def test_append_refuses_bad_rows_and_pages():
     assert torch.equal(torch.nan_to_num(s.K.float()), torch.nan_to_num(before.float()))
 
 
+@pytest.mark.parametrize("first", [-1, -2**31, -2**31 + 1, -2**31 + 5])
+def test_append_refuses_starts_before_the_rows(first):
+    s = Setup([3, 9], [4, 2], 2, 16, seed=9)
+    s.q_start[0] = first
+    K0, V0 = s.K.clone(), s.V.clone()
+    K, V = s.randn(6, 2, 128).to(DEV), s.randn(6, 2, 128).to(DEV)
+    s.cache.append(0, None, K, V, s.q_start)
+    assert s.status() == gb().STATUS_LENGTH
+    bits = lambda x: x.view(torch.int16)  # noqa: E731
+    rows = [int(s.table[1, r // 16]) * 16 + r % 16 for r in (9, 10)]
+    for pool, was, new in ((s.K[0], K0[0], K), (s.V[0], V0[0], V)):
+        flat, old = bits(pool).view(-1, 2, 128), bits(was).view(-1, 2, 128).clone()
+        old[rows] = bits(new)[4:]  # the other sequence's rows alone
+        assert torch.equal(flat, old)
+
+
 # ------------------------------------------------------------------ compaction
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("in_place", [False, True])

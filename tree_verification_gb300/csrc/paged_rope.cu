@@ -136,12 +136,12 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
         const int row = t0 + warp;
         const int given = a.pos != nullptr ? a.pos[row] : 0;
         const Place p = find_seq(a, row);
-        r = (int64_t)p.L + (row - p.first);
+        r = (int64_t)p.L + ((int64_t)row - p.first);
         if (lane == 0) {
             s_live[warp] = p.b >= 0;
             s_pos[warp] = a.pos != nullptr ? given : (int)r;
             if (p.b >= 0) {
-                if (p.L < 0 || (r >> a.page_shift) >= a.c.max_pages)
+                if (p.L < 0 || p.first < 0 || (r >> a.page_shift) >= a.c.max_pages)
                     flag_status(a.c.status, GRAFT_STATUS_LENGTH);
                 else
                     page_at = p.b * a.c.max_pages + (int)(r >> a.page_shift);
