@@ -601,7 +601,7 @@ int graft_paged_plan(const GraftPagedCache* cache, int N, int Hq, const int32_t*
  * graft_paged_attention_workspace_size bytes, ZERO-FILLED once by its owner
  * (arrival counters; every call leaves them at zero; after
  * GRAFT_STATUS_TIMEOUT zero it again).  A workspace or a plan buffer of more
- * bytes serves smaller calls too.  Calls sharing a workspace must not run at
+ * bytes serves smaller calls too, of other caches as well.  Calls sharing a workspace must not run at
  * the same time.
  */
 int graft_paged_attention_workspace_size(const GraftPagedCache* cache, int N, int Hq, int max_new, size_t* bytes);

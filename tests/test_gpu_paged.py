@@ -261,6 +261,23 @@ def test_calls_of_many_shapes_share_the_buffers():
         check_attention(s, O, Q, 0.09)
 
 
+def test_caches_of_other_sizes_share_a_workspace():
+    few = Setup([1500], [1], 2, 16, seed=40)
+    many = Setup([300 + 17 * x for x in range(90)], [1] * 90, 4, 16, seed=41)
+    mixed = Setup([700, 20, 900], [64, 1, 2], 2, 16, seed=42)
+    sizes = [(few, 1, 4), (many, 1, 8), (mixed, 64, 2)]
+    for s, max_new, G in sizes:
+        s.cache.plan(s.q_start, int(s.starts[-1]), s.Hkv * G, max_new)
+    ws = torch.zeros(max(s.cache._buffers["attention"].numel() for s, _, _ in sizes), dtype=torch.uint8, device=DEV)
+    for s, _, _ in sizes:
+        s.cache._buffers["attention"] = ws
+    for _ in range(2):
+        for s, max_new, G in sizes:
+            Q, O = run_attention(s, G)
+            assert s.cache._buffers["attention"] is ws
+            check_attention(s, O, Q, 0.09)
+
+
 def test_a_pool_past_32_bit_offsets():
     """Rows whose element offset in the pool passes 2^32."""
     from tree_verification_gb300.paged import PagedCache

@@ -108,7 +108,7 @@ PlanShape plan_shape(const GraftPagedCache* c, int N, int Hq, int max_new);
 // Partial results of cut items: every CTA has at most two (its first item's end, its last item's start).
 constexpr int kFewRows = 32;
 struct FewWs {
-    int32_t* count;  // [entries][Hkv] arrivals, zero between calls
+    int32_t* count;  // [2 x SMs] arrivals at the item that is cut and starts in a CTA, zero between calls
     float* o;        // [ctas][2][kFewRows][128]
     float2* ml;      // [ctas][2][kFewRows]: maximum (log2 units), sum
 };

@@ -600,7 +600,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             }
             __threadfence();
             __syncthreads();
-            int32_t* count = a.few.count + (int64_t)s_at.entry * a.c.Hkv + kvh;
+            int32_t* count = a.few.count + c0;  // (a CTA is the first of one cut item at most)
             if (tid == 0) {
                 const int before = atomicAdd(count, 1);
                 if (before >= pieces) flag_status(a.c.status, GRAFT_STATUS_WORKSPACE);

@@ -520,11 +520,11 @@ int check_attention(const GraftPagedCache* c, int N, int Hq, int max_new) {
     return GRAFT_OK;
 }
 
-// Counters first (one a sequence and KV head: a place that depends on the cache alone, so that calls of other shapes
-// that share a workspace never write over them), then the partial rows.
-void carve(WsCarver& w, const GraftPagedCache* c, const PlanShape& s, AttnArgs* a) {
+// Counters first, at a place and of a number that no argument changes: calls of other shapes and caches that share a
+// workspace never write over them.  Then the partial rows.
+void carve(WsCarver& w, const PlanShape& s, AttnArgs* a) {
     FewWs f;
-    f.count = w.take<int32_t>((size_t)c->n_seqs * c->Hkv);
+    f.count = w.take<int32_t>((size_t)s.sms * 2);
     const size_t slots = (size_t)s.sms * 2 * 2;  // two a CTA, at most two CTAs an SM
     f.o = w.take<float>(slots * kFewRows * HD);
     f.ml = w.take<float2>(slots * kFewRows);
@@ -612,7 +612,7 @@ extern "C" int graft_paged_attention_workspace_size(const GraftPagedCache* cache
     const int rc = check_attention(cache, N, Hq, max_new);
     if (rc != GRAFT_OK) return rc;
     WsCarver w(nullptr);
-    carve(w, cache, plan_shape(cache, N, Hq, max_new), nullptr);
+    carve(w, plan_shape(cache, N, Hq, max_new), nullptr);
     *bytes = w.bytes();
     return GRAFT_OK;
 }
@@ -634,10 +634,10 @@ extern "C" int graft_paged_attention(const GraftPagedCache* cache, const void* K
     a.shape = plan_shape(cache, N, Hq, max_new);
     if (!ws_ok(plan, plan_bytes, a.shape.bytes)) return GRAFT_ERR_WORKSPACE;
     WsCarver sizer(nullptr);
-    carve(sizer, cache, a.shape, nullptr);
+    carve(sizer, a.shape, nullptr);
     if (!ws_ok(ws, ws_bytes, sizer.bytes())) return GRAFT_ERR_WORKSPACE;
     WsCarver w(ws);
-    carve(w, cache, a.shape, &a);
+    carve(w, a.shape, &a);
     a.c = *cache;
     a.K = K_pool;
     a.V = V_pool;
