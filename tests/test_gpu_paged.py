@@ -396,6 +396,21 @@ def test_host_refusals_of_the_handle():
     torch.cuda.synchronize()
 
 
+def test_a_refused_plan_leaves_none():
+    s = Setup([70, 10], [2, 2], 2, 16, seed=25)
+    Q = s.randn(4, 8, 128).to(DEV)
+    s.cache.plan(s.q_start, 4, 8, 2)
+    with pytest.raises(ValueError):
+        s.cache.plan(s.q_start.long(), 4, 8, 3)
+    with pytest.raises(ValueError):
+        s.cache.attend(0, Q, 0.1)
+    s.cache.plan(s.q_start, 4, 8, 2)
+    with pytest.raises(gb().GraftError):
+        s.cache.plan(s.q_start, 4, 7, 2)
+    with pytest.raises(ValueError):
+        s.cache.attend(0, Q, 0.1)
+
+
 # ------------------------------------------------------------------ rotary and append
 def run_append(s, G, rot, interleaved, factor=1.0, pos=None, pad=0, far=1.0, strided=True):
     N, Hq, H = int(s.starts[-1]) + pad, s.Hkv * G, s.Hkv

@@ -99,7 +99,9 @@ class PagedCache:
     def _buffer(self, name: str, nbytes: int, zero: bool) -> torch.Tensor:
         t = self._buffers.get(name)
         if t is None or t.numel() < nbytes:
-            if torch.cuda.is_current_stream_capturing():
+            with torch.cuda.device(self._index):
+                capturing = torch.cuda.is_current_stream_capturing()
+            if capturing:
                 raise ValueError(f"the {name} buffer must grow: run the call once before capturing it")
             if t is not None:
                 self._kept.append(t)
@@ -192,6 +194,8 @@ class PagedCache:
 
     def plan(self, q_start, N: int, Hq: int, max_new: int, tree: bool = False) -> None:
         """graft_paged_plan for a step of N rows; serves every attend() until the next plan()."""
+        self._plan_of = None  # (a plan that is refused leaves none)
+        starts = self._need(q_start, "q_start", torch.int32, (self.n_seqs + 1,))
         key = (N, Hq, max_new)
         sizes = self._sizes.get(key)
         if sizes is None:
@@ -205,7 +209,6 @@ class PagedCache:
             sizes = self._sizes[key] = (a.value, b.value)
         buf = self._buffer("plan", sizes[0], False)
         self._buffer("attention", sizes[1], True)
-        starts = self._need(q_start, "q_start", torch.int32, (self.n_seqs + 1,))
         self._call("graft_paged_plan", N, Hq, starts, max_new, 1 if tree else 0, buf.data_ptr(), buf.numel())
         self._plan_of = (N, Hq, max_new, bool(tree))
 
