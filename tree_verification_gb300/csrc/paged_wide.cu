@@ -70,7 +70,8 @@ constexpr int BAR_S = BAR_VE + SV;       // [tile] S_t ready in TMEM
 constexpr int BAR_P = BAR_S + 2;         // [tile] P_t written to TMEM (128 arrivals)
 constexpr int BAR_DONE = BAR_P + 2;      // an item's MMAs completed (one phase per item)
 constexpr int BAR_OFREE = BAR_DONE + 1;  // [tile] an item's O_t read out of TMEM (128 arrivals)
-constexpr int N_BARS = BAR_OFREE + 2;
+constexpr int BAR_DRAIN = BAR_OFREE + 2;  // after an abort: everything issued has completed
+constexpr int N_BARS = BAR_DRAIN + 1;
 constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;  // tmem slot, abort flag, odd flags
 constexpr uint32_t SMEM_BYTES = OFF_MISC + 64 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -699,11 +700,13 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
         }
     }
     if (warp == 1 && lane == 0) {
+        // (after an abort several phases of DONE may be pending, which one parity cannot tell apart)
         if (aborted(abort_flag)) {
-            mma_commit(bar(BAR_DONE));
-            ++ndone;
+            mma_commit(bar(BAR_DRAIN));
+            mbar_wait(bar(BAR_DRAIN), 0, kWaitNs);
+        } else if (ndone > 0) {
+            mbar_wait(bar(BAR_DONE), (ndone - 1) & 1, kWaitNs);
         }
-        if (ndone > 0) mbar_wait(bar(BAR_DONE), (ndone - 1) & 1, kWaitNs);
     }
     tc_fence_before();
     __syncthreads();
