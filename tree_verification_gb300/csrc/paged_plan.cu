@@ -251,8 +251,8 @@ __device__ __forceinline__ void plan_wide(const GraftPagedCache& c, int N, int H
         // ---- Three SMs an item or more: all are split by keys into ranges of about one length, one a CTA, so short that
         // they just fit (two blocks at least).  The row blocks may be cut into their single tiles for that: half the
         // partial rows, but a tile alone takes kTileTime of two tiles' time a block; the estimate decides (one
-        // request's 64-node tree at group 4 over 4096 keys: 16.3 us in single tiles, 17.7 in pairs; 300 rows of a
-        // prompt over 6000: 77 and 44).
+        // request's 64-node tree at group 4 over 4096 keys: 15.8 us in single tiles, 16.9 in pairs, over 40000 59 and
+        // 45; 300 rows of a prompt over 6000: 76 and 40).
         const int slots = P / c.Hkv;
         auto block_of = [&](bool single, int e) {
             Wide w = pairs[single ? e >> 1 : e];
@@ -366,8 +366,8 @@ __device__ __forceinline__ void plan_wide(const GraftPagedCache& c, int N, int H
         const int rem = n_items - rounds * P;  // < P
         const Wide* rest = wide + (int64_t)rounds * P;
         // ---- The items past the whole rounds: split over all CTAs where their even share is kMinGain blocks below
-        // the longest (group 16 over 8192 keys: 10 trees, eight items past one round, 204 -> 122 us; 5 trees, 80
-        // items, 103 -> 77; 8 trees, 128 items, 104 whole and 120 split).
+        // the longest (group 16 over 8192 keys: 10 trees, eight items past one round, 201 -> 123 us; 5 trees, 80
+        // items, 102 -> 78; 8 trees, 128 items, 104 whole and 120 split).
         auto blocks_of = [&](int i) { return s_hist[i / c.Hkv]; };  // of item i (ranked)
         const int mine = ranked && tid < rem ? blocks_of(rounds * P + tid) : 0;
         int64_t blocks;
