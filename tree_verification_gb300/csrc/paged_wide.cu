@@ -774,7 +774,7 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const Group& gr, in
 template <int DT>
 __global__ void __launch_bounds__(256, 2)
 join_kernel(const __grid_constant__ AttnArgs a) {
-    // The next kernel may start now: it waits for this one, which waits for the attention's (15.9 -> 15.7 us a call
+    // The next kernel may start now: it waits for this one, which waits for the attention's (15.9 -> 15.8 us a call
     // for one request's tree).
     griddep_launch_dependents();
     // The plan is read ahead of the grid wait: the kernels before this one are the attention's, of which the first
@@ -782,8 +782,16 @@ join_kernel(const __grid_constant__ AttnArgs a) {
     const PlanHead& head = *reinterpret_cast<const PlanHead*>(a.plan);
     const Group* groups = reinterpret_cast<const Group*>(a.plan + a.shape.off_group);
     const int each = 8 * head.tiles, tasks = plan_fits(a, head) ? head.n_groups * each : 0;
+    // (the first task's row block ahead of the wait as well: 15.9 -> 15.7 us, 40000 keys 45.2 -> 44.4)
+    int task = blockIdx.x;
+    Group gr{};
+    if (task < tasks) gr = groups[task / each];
     griddep_wait();
-    for (int task = blockIdx.x; task < tasks; task += gridDim.x) join_rows<DT>(a, groups[task / each], task % each);
+    while (task < tasks) {
+        join_rows<DT>(a, gr, task % each);
+        task += gridDim.x;
+        if (task < tasks) gr = groups[task / each];
+    }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
