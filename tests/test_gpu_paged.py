@@ -462,6 +462,13 @@ def test_append_heads(Hkv, G, page, new):
     run_append(s, G, 128, False)
 
 
+def test_append_of_rows_that_fill_one_wave_three_at_a_time():
+    wave = 5 * torch.cuda.get_device_properties(0).multi_processor_count
+    for N in (2 * wave + 1, 2 * wave + 2, 3 * wave, 3 * wave + 1):
+        new = [N // 3 + 1, 0, 5, N - N // 3 - 6]
+        run_append(Setup([7, 3, 40, 0], new, 1, 64, seed=N % 97), 1, 32, False, pad=2)
+
+
 def test_append_at_far_positions():
     # 64-bit angles: a position past 2^30 times frequencies up to one radian
     s = Setup([40], [6], 1, 16, torch.float16, seed=2)

@@ -8,8 +8,8 @@
 // off by at most |position| / 2^65 turns plus w's own 64-bit rounding, and
 // its upper 32 bits go to sincospi.  No 64-bit floating product a position.
 //
-// Memory bound: every element is read and written once.  A CTA takes one or
-// two rows with all their heads, so a row's cosines are computed once
+// Memory bound: every element is read and written once.  A CTA takes one to
+// three rows with all their heads, so a row's cosines are computed once
 // and serve Hq + Hkv heads; each thread's loads (32 bytes a unit: the two
 // 16-byte chunks whose dims pair up) are issued before the CTA looks up the
 // sequences and pages, so the look-up's dependent reads run behind them; the
@@ -23,7 +23,8 @@ namespace paged {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kTokens = 2;
+constexpr int kTokens = 3;    // rows of a CTA at most
+constexpr int kResident = 5;  // CTAs an SM holds at once
 constexpr int kStep = kThreads / 8;  // heads that the CTA's threads hold at once
 
 struct RopeArgs {
@@ -95,7 +96,7 @@ __device__ __forceinline__ uint32_t turn1(uint32_t a, float2 cs) {
 
 // kAhead: heads that a thread reads at a time, the first ones before the look-up
 template <int DT, int kAhead>
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, kResident)
 rope_append_kernel(const __grid_constant__ RopeArgs a) {
     __shared__ float2 s_cs[kTokens][HD / 2];
     __shared__ int64_t s_dst[kTokens];  // cache row in the pool, -1: not written
@@ -151,7 +152,7 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
     __syncthreads();
     const int page = page_at >= 0 ? a.c.block_table[page_at] : 0;
     for (int x = tid; x < nt * (a.rot / 2); x += kThreads) {
-        const int t = x >= a.rot / 2 ? 1 : 0, p = x - t * (a.rot / 2);
+        const int t = (x >= a.rot / 2) + (x >= a.rot), p = x - t * (a.rot / 2);
         // 2^64 / 2 pi; a frequency of a turn or more per position keeps only its fraction
         const double turns = a.inv_freq[p] * 0.15915494309189533577;
         const uint64_t w = (uint64_t)__double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
@@ -327,9 +328,11 @@ extern "C" int graft_rope_append(const GraftPagedCache* cache, void* K_pool, voi
     a.page_shift = log2_exact(cache->page_rows);
     a.inter = interleaved != 0;
     a.factor = factor;
-    // two rows a CTA share a look-up; few rows go one to a CTA, over more SMs (64 rows: 6.2 against 8.2 us)
-    const int sms = device_sm_count();
-    a.tokens = N <= 4 * sms ? 1 : kTokens;
+    // As few rows a CTA as make one wave of CTAs, up to three; else two, which share a look-up (48 heads, one, two,
+    // three rows: 64 rows 6.2, 8.2 us; 704 rows 7.5, 8.2; 1280 rows 9.1, 9.9 with three; 1600 to 2240 rows, a wave of
+    // three, 11.1 to 13.7, with two 11.8 to 15.0; 2304 rows, past it, 16.5 with three, 14.9 with two).
+    const int64_t wave = (int64_t)kResident * device_sm_count();
+    a.tokens = N <= wave ? 1 : N > 2 * wave && N <= 3 * wave ? 3 : 2;
     const dim3 grid((unsigned)((N + a.tokens - 1) / a.tokens));
     // (a row's heads in one go where three or five a thread do; 4096 rows of 48 heads: 21.4 us, 23.9 with five)
     const bool three = Hq + 2 * cache->Hkv <= 3 * kStep;
