@@ -237,6 +237,35 @@ def test_lengths_change_between_replays_of_one_graph():
         check_attention(s, O, Q, 0.1)
 
 
+def test_a_plan_of_fewer_sequences_right_before_its_attention():
+    """One sequence after another leaves (its pages given back, its row of Q turned into padding) and the captured
+    plan and attention run back to back: what the last plan said of it must not count against the call."""
+    B = 40
+    s = Setup([100 + 5 * b for b in range(B)], [1] * B, 2, 16, seed=15, tables=True)
+    Q = s.randn(B, 8, 128)
+    O = torch.zeros(B, 8, 128, dtype=s.dtype, device=DEV)
+    Qd = Q.to(DEV)
+
+    def step():
+        s.cache.plan(s.q_start, B, 8, 1)
+        s.cache.attend(0, Qd, 0.1, out=O)
+
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    g.replay()
+    assert s.status() == 0
+    for b in range(B - 1):
+        s.cache.free(s.i32([b]))
+        s.lens[b], s.new[b] = 0, 0
+        s.starts = np.concatenate([[0], np.cumsum(s.new)]).astype(np.int32)
+        s.q_start.copy_(s.i32(s.starts))
+        g.replay()
+        assert s.status() == 0
+    check_attention(s, O, Q, 0.1)
+
+
 def test_other_streams():
     s = Setup([300], [3], 2, 16, seed=12)
     Q = s.randn(3, 8, 128)

@@ -397,7 +397,8 @@ few_kernel(const __grid_constant__ AttnArgs a) {
 
         // (Q's reads, and those that check the guess, go ahead of the units': a unit's bytes take the SM's read
         // port for longer than any of them)
-        const int now = guessed ? fetch_pages(0, true) : pages;
+        // (without a status bit as yet: a guess that does not hold may name a sequence whose pages are gone)
+        const int now = guessed ? fetch_pages(0, false) : pages;
         const int32_t again = guessed && has_word ? __ldcg(word) : guess;
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) load(i);
@@ -410,6 +411,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
                 }
                 continue;
             }
+            if (now < 0 && u0 + warp + lane * kWarps < u1) flag_status(a.c.status, GRAFT_STATUS_PAGE);
             if (__any_sync(0xffffffffu, now != pages)) {
                 cp_wait<0>();
                 __syncwarp();
