@@ -237,6 +237,37 @@ def test_lengths_change_between_replays_of_one_graph():
         check_attention(s, O, Q, 0.1)
 
 
+@pytest.mark.parametrize("B,L,Hkv", [(1, 3000, 2), (40, 300, 4)])
+def test_lengths_that_rise_by_one_a_pass(B, L, Hkv):
+    """Decoding: the plan that the attention reads ahead is another one in every pass."""
+    s = Setup([L - 3 * b for b in range(B)], [40] * B, Hkv, 16, seed=16)
+    s.new, s.starts = [1] * B, np.arange(B + 1, dtype=np.int32)
+    s.q_start = s.i32(s.starts)
+    Q = s.randn(B, 4 * Hkv, 128)
+    O = torch.zeros(B, 4 * Hkv, 128, dtype=s.dtype, device=DEV)
+    Qd = Q.to(DEV)
+
+    def step():
+        s.lengths.add_(1)
+        s.cache.plan(s.q_start, B, 4 * Hkv, 1)
+        s.cache.attend(0, Qd, 0.1, out=O)
+
+    step()
+    s.lens = [x + 1 for x in s.lens]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(20):
+        g.replay()
+        s.lens = [x + 1 for x in s.lens]
+        got = O.clone()
+        s.cache.plan(s.q_start, B, 4 * Hkv, 1)
+        torch.cuda.synchronize()
+        s.cache.attend(0, Qd, 0.1, out=O)
+        assert s.status() == 0 and torch.equal(O, got)
+    check_attention(s, O, Q, 0.1)
+
+
 def test_a_plan_of_fewer_sequences_right_before_its_attention():
     """One sequence after another leaves (its pages given back, its row of Q turned into padding) and the captured
     plan and attention run back to back: what the last plan said of it must not count against the call."""
