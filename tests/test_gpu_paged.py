@@ -818,6 +818,23 @@ def test_single_tiles(dtype, tree, odd, Hkv, G, page, new, lens):
     assert torch.equal(again.view(torch.int16), O.view(torch.int16)) and s.status() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_a_cta_takes_pairs_and_single_tiles_in_turn(dtype):
+    """Rounds of two-tile and of one-tile items, the one-tile ones ever shorter: the second tile's warps sit them out."""
+    Hkv = 8
+    each = torch.cuda.get_device_properties(0).multi_processor_count // Hkv
+    new = [40 if k % 2 == 0 else 9 for k in range(8) for _ in range(each)]
+    lens = [max(0, 128 * (5 - k)) + (3 * i) % 80 for k in range(8) for i in range(each)]
+    s = Setup(lens, new, Hkv, 64, dtype, seed=50)
+    Q, O = run_attention(s, 4)
+    check_attention(s, O, Q, 0.09)
+    again = torch.full_like(O, 7.0)
+    for _ in range(20):
+        s.cache.attend(0, Q.to(DEV), 0.09, out=again)
+        assert torch.equal(again, O)
+    assert s.status() == 0
+
+
 @pytest.mark.parametrize("extra", [1, 3])
 def test_a_few_short_items_past_a_whole_round(extra):
     """Every CTA is as busy as the next, and the blocks left over are fewer than the CTAs."""

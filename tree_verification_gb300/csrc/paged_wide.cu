@@ -68,8 +68,10 @@ constexpr int BAR_VF = BAR_KE + SK;      // [SV] V block landed
 constexpr int BAR_VE = BAR_VF + SV;      // [SV] V block consumed by the PV products
 constexpr int BAR_S = BAR_VE + SV;       // [tile] S_t ready in TMEM
 constexpr int BAR_P = BAR_S + 2;         // [tile] P_t written to TMEM (128 arrivals)
-constexpr int BAR_DONE = BAR_P + 2;      // an item's MMAs completed (one phase per item)
-constexpr int BAR_OFREE = BAR_DONE + 1;  // [tile] an item's O_t read out of TMEM (128 arrivals)
+// [tile] an item's MMAs completed: tile 0's one phase per item, tile 1's one phase per item of two tiles.  (Tile 1
+// takes no part in the others and so holds none of them back: a phase for each could pass it by.)
+constexpr int BAR_DONE = BAR_P + 2;
+constexpr int BAR_OFREE = BAR_DONE + 2;  // [tile] an item's O_t read out of TMEM (128 arrivals)
 constexpr int BAR_DRAIN = BAR_OFREE + 2;  // after an abort: everything issued has completed
 constexpr int N_BARS = BAR_DRAIN + 1;
 constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;  // tmem slot, abort flag, odd flags
@@ -445,6 +447,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                     vph = vph_next;
                     pph0 ^= 1u;
                 }
+                if (two) mma_commit(bar(BAR_DONE + 1));
                 mma_commit(bar(BAR_DONE));
                 ++ndone;
                 ++q;
@@ -470,7 +473,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
         const float sl2 = a.scale * 1.4426950408889634f;
         const int rtok = r / G, rg = r - rtok * G;
         bool ok = true;
-        int q = 0, n_two = 0;  // items passed (phase of DONE); those of two tiles
+        int q = 0, n_two = 0;  // items passed; those of two tiles (phase of DONE: tile 0's, tile 1's)
         int g = 0, gv = 0;     // blocks of this tile, blocks of the CTA
         for (int k = 0; ok && k < n_mine; ++k) {
             const Wide* at = item_at(k);
@@ -634,7 +637,8 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                 if (!ok) break;
             }
             // ------------------------------------------------------------ epilogue of the item
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(BAR_DONE), q & 1, kWaitNs) && !aborted(abort_flag));
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(BAR_DONE + t), (t == 0 ? q : n_two) & 1, kWaitNs) &&
+                                             !aborted(abort_flag));
             if (!ok) break;
             tc_fence_after();
             {
