@@ -609,6 +609,11 @@ int graft_paged_attention(const GraftPagedCache* cache, const void* K_pool, cons
                           int max_new, const void* plan, size_t plan_bytes, const void* Q, int64_t q_stride,
                           const uint64_t* mask, float scale, void* O, void* ws, size_t ws_bytes,
                           graft_stream_t stream);
+/* The same with `tuning`, of which wait_ns alone may be set (GraftAttnTuning; it bounds the tensor-core kernel's waits). */
+int graft_paged_attention_ex(const GraftPagedCache* cache, const void* K_pool, const void* V_pool, int N, int Hq,
+                             int max_new, const void* plan, size_t plan_bytes, const void* Q, int64_t q_stride,
+                             const uint64_t* mask, float scale, void* O, const GraftAttnTuning* tuning, void* ws,
+                             size_t ws_bytes, graft_stream_t stream);
 
 /*
  * graft_pages_compact — after a verify step: in every layer, cache row

@@ -86,6 +86,19 @@ def test_attention_arguments():
     assert lib.graft_paged_plan(c, 4, 32, FAKE, 1, 0, FAKE, 64, None) == -3
 
 
+@pytest.mark.parametrize("bad", [dict(tiles=1), dict(min_chunk=256), dict(persist_ctas=-1), dict(split=1), dict(wait_ns=-1),
+                                 dict(reserved=(ctypes.c_int32 * 3)(0, 0, 1))])
+def test_attention_tuning(bad):
+    c, keep = cache()
+    t = gb().GraftAttnTuning()
+    ex = lambda N, t: gb().lib().graft_paged_attention_ex(  # noqa: E731
+        c, FAKE, FAKE, N, 32, 1, FAKE, 1 << 30, FAKE, 4096, None, 0.1, FAKE, t, FAKE, 1 << 40, None)
+    assert ex(0, None) == 0 and ex(0, ctypes.addressof(t)) == 0
+    for k, v in bad.items():
+        setattr(t, k, v)
+    assert ex(4, ctypes.addressof(t)) == -1 and ex(0, ctypes.addressof(t)) == -1
+
+
 def test_append_arguments():
     c, keep = cache()
     assert append(c, rot=24) == -2 and append(c, rot=144) == -2 and append(c, rot=-16) == -2

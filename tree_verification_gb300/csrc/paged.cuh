@@ -125,6 +125,7 @@ struct AttnArgs {
     float scale;
     int N, Hq, G, max_new, page_shift;
     int after_wide;  // the few kernel runs beside the wide one
+    uint64_t wait_ns;  // bound on every pipeline wait of the wide kernel (0.5 s unless tuned)
     PlanShape shape;
     FewWs few;
     float* wide_o;    // [partial row blocks][2][32][128][4] normalised: four dims of the 128 rows side by side

@@ -623,8 +623,24 @@ extern "C" int graft_paged_attention(const GraftPagedCache* cache, const void* K
                                      int Hq, int max_new, const void* plan, size_t plan_bytes, const void* Q,
                                      int64_t q_stride, const uint64_t* mask, float scale, void* O, void* ws,
                                      size_t ws_bytes, graft_stream_t stream) {
+    return graft_paged_attention_ex(cache, K_pool, V_pool, N, Hq, max_new, plan, plan_bytes, Q, q_stride, mask, scale, O,
+                                    nullptr, ws, ws_bytes, stream);
+}
+
+extern "C" int graft_paged_attention_ex(const GraftPagedCache* cache, const void* K_pool, const void* V_pool, int N,
+                                        int Hq, int max_new, const void* plan, size_t plan_bytes, const void* Q,
+                                        int64_t q_stride, const uint64_t* mask, float scale, void* O,
+                                        const GraftAttnTuning* tuning, void* ws, size_t ws_bytes,
+                                        graft_stream_t stream) {
     const int rc = check_attention(cache, N, Hq, max_new);
     if (rc != GRAFT_OK) return rc;
+    if (tuning != nullptr) {
+        if (tuning->tiles != 0 || tuning->min_chunk != 0 || tuning->persist_ctas != 0 || tuning->split != 0 ||
+            tuning->wait_ns < 0)
+            return GRAFT_ERR_INVALID_ARG;
+        for (int r : tuning->reserved)
+            if (r != 0) return GRAFT_ERR_INVALID_ARG;
+    }
     if (mask != nullptr && max_new > GRAFT_MAX_KMAX) return GRAFT_ERR_UNSUPPORTED_SHAPE;
     if (N == 0) return GRAFT_OK;
     if (K_pool == nullptr || V_pool == nullptr || Q == nullptr || O == nullptr) return GRAFT_ERR_INVALID_ARG;
@@ -654,6 +670,7 @@ extern "C" int graft_paged_attention(const GraftPagedCache* cache, const void* K
     a.G = Hq / cache->Hkv;
     a.max_new = max_new;
     a.page_shift = log2_exact(cache->page_rows);
+    a.wait_ns = tuning != nullptr && tuning->wait_ns > 0 ? (uint64_t)tuning->wait_ns : 500000000ull;
     cudaStream_t st = (cudaStream_t)stream;
     if (!a.shape.wide) return few_launch(a, st);
     // Steps of both kinds: the few kernel comes second and does not wait for the first, which has waited for all

@@ -80,6 +80,8 @@ static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr uint32_t TM_S = 0;    // + tile * 128
 constexpr uint32_t TM_O = 256;  // + tile * 128
 constexpr float RESCALE_LOG2 = 8.f;
+// Pipeline waits are bounded by kWaitNs (a.wait_ns in the failure-path tests); the teardown's waits on the loads
+// (kDrainNs) and products (kWaitNs) in flight keep fixed bounds.
 constexpr uint64_t kWaitNs = 500000000ull;
 constexpr uint64_t kDrainNs = 100000000ull;
 
@@ -174,12 +176,14 @@ __device__ __noinline__ void add_odd(const GraftPagedCache& c, const void* V, co
     }
 }
 
-template <int DT>
+// kTestWaits: pipeline waits bounded by a.wait_ns (the failure-path tests); otherwise by a constant.
+template <int DT, bool kTestWaits>
 __global__ void __launch_bounds__(NTHREADS, 1)
 wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a) {
     using E = Elem<DT>;
     constexpr float kLift = DT == GRAFT_FP16 ? 7.f : 0.f;  // see paged_few.cu: small weights keep their bits
     constexpr float kMaxSum = DT == GRAFT_FP16 ? 32768.f : 65536.f;  // of a block weighed by an old maximum
+    const uint64_t wait_ns = kTestWaits ? a.wait_ns : kWaitNs;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -244,7 +248,6 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
     const uint32_t tmem = *tmem_slot;
 
     int k_issued = 0, v_issued = 0, q_issued = 0;
-    int ndone = 0;
     if (warp == 0) {
         // ------------------------------------------------------------ producer: every lane issues its own boxes
         const int page_box = min(a.c.page_rows, BN);  // rows of a box
@@ -332,14 +335,14 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
             bool ok = true;
             if (kc.k >= 0 || next_q) {
                 ok = __all_sync(0xffffffffu,
-                                mbar_wait(bar(BAR_KE + g % SK), (g / SK) & 1, kWaitNs) && !aborted(abort_flag));
+                                mbar_wait(bar(BAR_KE + g % SK), (g / SK) & 1, wait_ns) && !aborted(abort_flag));
                 if (!ok) break;
                 if (next_q) load_q(nx);
                 if (kc.k >= 0) load_k();
             }
             if (vc.k >= 0) {
                 ok = __all_sync(0xffffffffu,
-                                mbar_wait(bar(BAR_VE + g % SV), (g / SV) & 1, kWaitNs) && !aborted(abort_flag));
+                                mbar_wait(bar(BAR_VE + g % SV), (g / SV) & 1, wait_ns) && !aborted(abort_flag));
                 if (!ok) break;
                 load_v();
             }
@@ -367,7 +370,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
             const Pre none{-1, 0u};
             auto test_pre = [&](Pre pre) -> bool { return pre.bar < 0 || mbar_test_now(bar(pre.bar), pre.ph); };
             auto wait_pre = [&](Pre pre, bool ready) -> bool {
-                return ready || mbar_wait(bar(pre.bar), pre.ph, kWaitNs);
+                return ready || mbar_wait(bar(pre.bar), pre.ph, wait_ns);
             };
             auto group_S = [&](int t, bool last, Pre nxt) -> bool {
                 bool ready = false;
@@ -403,8 +406,8 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
             // one item's products; a copy each for one and two tiles, so that the loop decides nothing
             auto run_item = [&](auto two_tiles, int nblk) {
                 constexpr bool two = decltype(two_tiles)::value;
-                ok = mbar_wait(bar(BAR_Q), q & 1, kWaitNs) && !aborted(abort_flag) &&
-                     mbar_wait(bar(BAR_KF + kst), kph, kWaitNs);
+                ok = mbar_wait(bar(BAR_Q), q & 1, wait_ns) && !aborted(abort_flag) &&
+                     mbar_wait(bar(BAR_KF + kst), kph, wait_ns);
                 if (!ok) return;
                 tc_fence_after();
                 Pre vf{BAR_VF + vst, (uint32_t)vph};
@@ -412,9 +415,9 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                 if (two) vf_ready = group_S(1, true, vf);
                 for (int j = 0; j < nblk && ok; ++j) {
                     const bool more = j + 1 < nblk;
-                    ok = wait_pre(vf, vf_ready) && mbar_wait(bar(BAR_P), pph0, kWaitNs);
+                    ok = wait_pre(vf, vf_ready) && mbar_wait(bar(BAR_P), pph0, wait_ns);
                     // the item's first PV overwrites O_t: the previous item's epilogue must have read it
-                    if (ok && j == 0 && q > 0) ok = mbar_wait(bar(BAR_OFREE), (q - 1) & 1, kWaitNs);
+                    if (ok && j == 0 && q > 0) ok = mbar_wait(bar(BAR_OFREE), (q - 1) & 1, wait_ns);
                     if (!ok) break;
                     tc_fence_after();
                     const Pre kf{BAR_KF + kst, (uint32_t)kph};
@@ -435,7 +438,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                     vf_ready = !two && more ? p1_ready : false;
                     if (two) {
                         ok = wait_pre(p1, p1_ready);
-                        if (ok && j == 0 && q1 > 0) ok = mbar_wait(bar(BAR_OFREE + 1), (q1 - 1) & 1, kWaitNs);
+                        if (ok && j == 0 && q1 > 0) ok = mbar_wait(bar(BAR_OFREE + 1), (q1 - 1) & 1, wait_ns);
                         if (!ok) break;
                         tc_fence_after();
                         group_PV(1, true, j == 0, none);
@@ -449,7 +452,6 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                 }
                 if (two) mma_commit(bar(BAR_DONE + 1));
                 mma_commit(bar(BAR_DONE));
-                ++ndone;
                 ++q;
                 q1 += two;
             };
@@ -513,7 +515,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
             {
                 for (int j = 0; j < nblk; ++j) {
                     ok = __all_sync(0xffffffffu,
-                                    mbar_wait(bar(BAR_S + t), g & 1, kWaitNs) && !aborted(abort_flag));
+                                    mbar_wait(bar(BAR_S + t), g & 1, wait_ns) && !aborted(abort_flag));
                     if (!ok) break;
                     ++g;
                     tc_fence_after();
@@ -542,7 +544,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                         // (their pages may hold anything) and infinite or NaN elements that masked rows would
                         // multiply by zero.
                         const int vb = gv + j;
-                        ok = __all_sync(0xffffffffu, mbar_wait(bar(BAR_VF + vb % SV), (vb / SV) & 1, kWaitNs));
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar(BAR_VF + vb % SV), (vb / SV) & 1, wait_ns));
                         if (!ok) break;
                         uint8_t* v0 = gbase + OFF_V + (vb % SV) * BLK_BYTES;
                         bool odd = false;
@@ -637,7 +639,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                 if (!ok) break;
             }
             // ------------------------------------------------------------ epilogue of the item
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(BAR_DONE + t), (t == 0 ? q : n_two) & 1, kWaitNs) &&
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(BAR_DONE + t), (t == 0 ? q : n_two) & 1, wait_ns) &&
                                              !aborted(abort_flag));
             if (!ok) break;
             tc_fence_after();
@@ -692,29 +694,33 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
         if (!ok && !aborted(abort_flag)) raise_abort(abort_flag, a.c.status);
     }
     // ---------------------------------------------------------------- teardown
-    if (warp == 0 && lane == 0 && aborted(abort_flag)) {
-        if (q_issued > 0) mbar_wait(bar(BAR_Q), (q_issued - 1) & 1, kDrainNs);
-        for (int st = 0; st < SK; ++st) {
-            const int n = (k_issued - st + SK - 1) / SK;
-            if (n > 0) mbar_wait(bar(BAR_KF + st), (n - 1) & 1, kDrainNs);
-        }
-        for (int st = 0; st < SV; ++st) {
-            const int n = (v_issued - st + SV - 1) / SV;
-            if (n > 0) mbar_wait(bar(BAR_VF + st), (n - 1) & 1, kDrainNs);
-        }
-    }
-    if (warp == 1 && lane == 0) {
-        // (after an abort several phases of DONE may be pending, which one parity cannot tell apart)
-        if (aborted(abort_flag)) {
-            mma_commit(bar(BAR_DRAIN));
-            mbar_wait(bar(BAR_DRAIN), 0, kWaitNs);
-        } else if (ndone > 0) {
-            mbar_wait(bar(BAR_DONE), (ndone - 1) & 1, kWaitNs);
-        }
-    }
+    // (the products are complete when their last item is: the epilogue waited for it)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // All warps are through, so the flag is final.  (The producer may end with loads in flight that a warp which
+    // gives up later never waits for: looked at before the barrier, the flag could still be down, and the CTA would
+    // leave with its loads outstanding.)
+    if (aborted(abort_flag)) {
+        if (warp == 0 && lane == 0) {
+            if (q_issued > 0) mbar_wait(bar(BAR_Q), (q_issued - 1) & 1, kDrainNs);
+            for (int st = 0; st < SK; ++st) {
+                const int n = (k_issued - st + SK - 1) / SK;
+                if (n > 0) mbar_wait(bar(BAR_KF + st), (n - 1) & 1, kDrainNs);
+            }
+            for (int st = 0; st < SV; ++st) {
+                const int n = (v_issued - st + SV - 1) / SV;
+                if (n > 0) mbar_wait(bar(BAR_VF + st), (n - 1) & 1, kDrainNs);
+            }
+        }
+        if (warp == 1 && lane == 0) {
+            // (a commit and a barrier of their own: several phases of DONE may be pending, which one parity cannot
+            // tell apart)
+            mma_commit(bar(BAR_DRAIN));
+            mbar_wait(bar(BAR_DRAIN), 0, kWaitNs);
+        }
+        __syncthreads();
+    }
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
@@ -824,16 +830,17 @@ bool encode(CUtensorMap* m, int dtype, int rank, const void* ptr, const cuuint64
 
 template <int DT>
 int launch(const AttnArgs& a, const Maps& m, cudaStream_t st) {
-    static bool attr_set[64] = {};
+    static bool attr_set[64][2] = {};
     int dev = 0;
     if (!cuda_ok(cudaGetDevice(&dev))) return GRAFT_ERR_CUDA;
-    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        if (!cuda_ok(cudaFuncSetAttribute(wide_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)SMEM_BYTES)))
+    const bool test_waits = a.wait_ns != kWaitNs;
+    const auto kernel = test_waits ? wide_kernel<DT, true> : wide_kernel<DT, false>;
+    if (dev < 0 || dev >= 64 || !attr_set[dev][test_waits]) {
+        if (!cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)))
             return GRAFT_ERR_CUDA;
-        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+        if (dev >= 0 && dev < 64) attr_set[dev][test_waits] = true;
     }
-    launch_pdl(wide_kernel<DT>, dim3(a.shape.sms), dim3(NTHREADS), SMEM_BYTES, st, m, a);
+    launch_pdl(kernel, dim3(a.shape.sms), dim3(NTHREADS), SMEM_BYTES, st, m, a);
     count_launches(1);
     return launch_status();
 }

@@ -212,9 +212,10 @@ class PagedCache:
         self._call("graft_paged_plan", N, Hq, starts, max_new, 1 if tree else 0, buf.data_ptr(), buf.numel())
         self._plan_of = (N, Hq, max_new, bool(tree))
 
-    def attend(self, layer: int, Q, scale: float, mask=None, out=None):
+    def attend(self, layer: int, Q, scale: float, mask=None, out=None, tuning=None):
         """graft_paged_attention of the planned step: Q [N][Hq][128] (rows may be strided), mask [N] int64 (the
-        ancestor bits) for a tree plan; returns O [N][Hq][128]."""
+        ancestor bits) for a tree plan; returns O [N][Hq][128].  ``tuning`` (a GraftAttnTuning or a dict of its
+        fields, of which wait_ns alone may be set) selects graft_paged_attention_ex."""
         if self._plan_of is None:
             raise ValueError("attend() needs a plan() of the step")
         N, Hq, max_new, tree = self._plan_of
@@ -227,8 +228,13 @@ class PagedCache:
         op = self._need(out, "out", self.dtype, (N, Hq, gb.HEAD_DIM))
         mp = None if mask is None else self._need(mask, "mask", torch.int64, (N,))
         plan, ws = self._buffers["plan"], self._buffers["attention"]
-        self._call("graft_paged_attention", self._kp[layer], self._vp[layer], N, Hq, max_new, plan.data_ptr(),
-                   plan.numel(), qp, qs, mp, float(scale), op, ws.data_ptr(), ws.numel())
+        if tuning is None:
+            self._call("graft_paged_attention", self._kp[layer], self._vp[layer], N, Hq, max_new, plan.data_ptr(),
+                       plan.numel(), qp, qs, mp, float(scale), op, ws.data_ptr(), ws.numel())
+        else:
+            tuning = gb._tuning(tuning)
+            self._call("graft_paged_attention_ex", self._kp[layer], self._vp[layer], N, Hq, max_new, plan.data_ptr(),
+                       plan.numel(), qp, qs, mp, float(scale), op, ctypes.addressof(tuning), ws.data_ptr(), ws.numel())
         return out
 
     def compact(self, path, acc_len, lengths_out=None):
