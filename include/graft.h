@@ -59,7 +59,7 @@ typedef struct CUstream_st* graft_stream_t;
 #define GRAFT_STATUS_TREE 8           /* a kept draft node's parent was not kept (cannot happen for finite logits) */
 #define GRAFT_STATUS_TIMEOUT 16       /* a bounded wait inside a kernel expired; that CTA's output is incomplete */
 #define GRAFT_STATUS_WORKSPACE 32     /* a workspace's arrival counter was found not zeroed (graft_build_tree, graft_tree_attention, graft_paged_attention) */
-#define GRAFT_STATUS_PAGE 64          /* a page number outside the pool, or a page that no sequence holds, was read; it was skipped (read as zeros) */
+#define GRAFT_STATUS_PAGE 64          /* a page number outside the pool, or a page that no sequence holds, was read, or rows were due in a page that the sequence does not hold alone; it was skipped (read as zeros, not written) */
 #define GRAFT_STATUS_PLAN 128         /* a plan that was not made for the call's arguments; nothing was computed */
 #define GRAFT_STATUS_SEQUENCE 256     /* a sequence index out of range, named twice, or not empty where it has to be; it was skipped */
 
@@ -508,6 +508,9 @@ int graft_update_M_noalloc(int32_t* M_succ, int32_t* M_cnt, int V, int W, const 
  *   status       device word for GRAFT_STATUS_* bits, or NULL
  * Pools are 16-byte aligned.  A sequence's rows past its length, and the
  * pages that no sequence holds, may hold anything, NaN included.
+ * Where held and page_refs are both given, append and compaction write only
+ * to pages that the sequence holds (entries below held[b]) and no other does:
+ * a sequence that reserve refused never writes into a page it shares.
  */
 typedef struct GraftPagedCache {
     int32_t dtype, Hkv, head_dim, page_rows, num_pages, n_seqs, max_pages, n_layers;
@@ -558,7 +561,9 @@ int graft_rope_inv_freq(int rot_dim, double base, int scaling, double stretch, d
  * inv_freq may be NULL).  Hq = 0 (Q NULL) appends alone; Q_out may be Q.
  * lengths are not advanced.  A row whose cache row lies outside the block
  * table, or whose sequence starts before row 0, sets GRAFT_STATUS_LENGTH,
- * one outside the pool GRAFT_STATUS_PAGE; its K and V are not written.
+ * one outside the pool, or in a page that is not the sequence's alone (where
+ * the cache has held and page_refs), GRAFT_STATUS_PAGE; its K and V are not
+ * written.
  */
 int graft_rope_append(const GraftPagedCache* cache, void* K_pool, void* V_pool, int N, int Hq,
                       const int32_t* q_start, const int32_t* pos, const double* inv_freq, int rot_dim,
@@ -622,7 +627,9 @@ int graft_paged_attention_ex(const GraftPagedCache* cache, const void* K_pool, c
  * are made in place), and lengths_out[b] = lengths[b] + acc_len[b].
  * lengths_out may be lengths.  A path that does not rise within [0, Kmax)
  * sets GRAFT_STATUS_TREE, rows outside the block table GRAFT_STATUS_LENGTH or
- * the pool GRAFT_STATUS_PAGE; that sequence keeps its rows and its length.
+ * the pool, or in pages that are not the sequence's alone (where the cache has
+ * held and page_refs), GRAFT_STATUS_PAGE; that sequence keeps its rows and its
+ * length.
  */
 int graft_pages_compact(const GraftPagedCache* cache, int Kmax, const int32_t* path, const int32_t* acc_len,
                         int32_t* lengths_out, graft_stream_t stream);

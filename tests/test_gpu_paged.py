@@ -766,6 +766,46 @@ def test_bad_page_calls_are_flagged_and_skipped():
     assert min(s.cache.page_refs.tolist()) == 0
 
 
+def rows_changed(now, before):
+    """(page, row) of a layer's pool whose bits changed."""
+    return sorted(map(tuple, (now.view(torch.int16) != before.view(torch.int16)).any(-1).any(-1).nonzero().tolist()))
+
+
+def test_rows_go_only_to_pages_that_a_sequence_holds_alone():
+    """One page short: of two sequences that share their last page the first gets a copy, the second has the old one to
+    itself; a third shares and a fourth lacks pages (its table names others' behind those it holds)."""
+    new = [8] * 5
+    s, P = bigger([20, 0, 20, 0, 32], new, 2, seed=60)
+    c, b = s.cache, gb()
+    c.free(s.i32([1, 3]))
+    c.fork(s.i32([0, 2]), s.i32([1, 3]))
+    s.t[4, 2] = int(s.t[0, 0])
+    c.held[4] = 2
+    c.page_refs[c.page_refs == 0] = 1
+    shared01 = int(s.t[0, 1])
+    # one free page for the first sequence's copy
+    spare = [p for p in range(s.P) if not (s.t == p).any()][0]
+    c.page_refs[spare] = 0
+    c.reserve(s.i32([8, 8, 8, 8, 8, 0]))
+    assert s.status() == b.STATUS_CACHE_OVERFLOW
+    assert int(s.t[0, 1]) == spare and int(c.page_refs[shared01]) == 1
+    starts = s.i32([0, 8, 16, 24, 32, 40, 40])
+    K, V = s.randn(40, 2, 128).to(DEV), s.randn(40, 2, 128).to(DEV)
+    K0 = s.K.clone()
+    c.append(0, None, K, V, starts)
+    assert s.status() == b.STATUS_PAGE
+    want = sorted([(spare, 4 + i) for i in range(8)] + [(shared01, 4 + i) for i in range(8)])
+    assert rows_changed(s.K[0], K0[0]) == want
+    for q, page in ((0, spare), (1, shared01)):
+        assert torch.equal(s.K[0, page, 4:12], K[8 * q:8 * q + 8]) and torch.equal(s.V[0, page, 4:12], V[8 * q:8 * q + 8])
+    K0 = s.K.clone()
+    path = s.i32(np.tile([0, 3, 5, -1], (6, 1)))
+    c.compact(path, s.i32([3, 3, 3, 3, 3, 0]))
+    assert s.status() == b.STATUS_PAGE
+    assert c.lengths.tolist() == [23, 23, 20, 20, 32, 0]
+    assert rows_changed(s.K[0], K0[0]) == sorted([(p, r) for p in (spare, shared01) for r in (5, 6)])
+
+
 # ------------------------------------------------------------------ schedules
 @pytest.mark.parametrize("Hkv,G,page,new,lens", [
     (2, 8, 16, [200, 1, 1, 1], [5, 900, 300, 0]),            # both kinds: the few rows run beside the wide ones

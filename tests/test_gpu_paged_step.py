@@ -172,6 +172,40 @@ def test_sampling_and_fp16():
     assert w.cache.lengths.tolist() == [a + b for a, b in zip([37, 48, 0], w.step.acc["acc_len"].tolist())]
 
 
+def test_copy_on_write_survives_a_refused_reserve():
+    """Two sequences share a partly filled page and no page is free: neither may write into it, and both stay as they
+    are; once there are pages, the next step goes on as if that one had not been."""
+    b = gb()
+    w = World(7)
+    c, st = w.cache, w.step
+    c.free(i32([2]))
+    c.fork(i32([0]), i32([2]))
+    taken = c.page_refs == 0
+    c.page_refs[taken] = 1  # another owner's
+    K0, V0 = w.K.clone(), w.V.clone()
+    before = [t.clone() for t in (c.block_table, c.held, c.page_refs, c.lengths)]
+    inp = w.inputs()
+    st.run(M_succ=w.M[0], M_cnt=w.M[1], **inp)
+    torch.cuda.synchronize()
+    assert int(st.status.item()) == b.STATUS_CACHE_OVERFLOW | b.STATUS_PAGE
+    assert c.lengths.tolist() == [37, 48, 37]
+    for t, x in zip((c.block_table, c.held, c.page_refs, c.lengths), before):
+        assert torch.equal(t, x)
+    assert torch.equal(w.K, K0) and torch.equal(w.V, V0)  # (no sequence had room of its own)
+    st.status.zero_()
+    c.page_refs[taken] = 0
+    st.run(M_succ=w.M[0], M_cnt=w.M[1], **inp)
+    torch.cuda.synchronize()
+    assert int(st.status.item()) == 0
+    acc = st.acc["acc_len"].tolist()
+    assert c.lengths.tolist() == [37 + acc[0], 48 + acc[1], 37 + acc[2]] and min(acc) >= 1
+    for s, n in enumerate((37, 48, 37)):
+        for r in range(n):
+            old, new = int(before[0][s, r // PAGE]), int(c.block_table[s, r // PAGE])
+            assert torch.equal(w.K[:, new, r % PAGE], K0[:, old, r % PAGE])
+            assert torch.equal(w.V[:, new, r % PAGE], V0[:, old, r % PAGE])
+
+
 def test_refusals():
     from tree_verification_gb300.paged import PagedCache
     from tree_verification_gb300.paged_step import PagedVerifyStep

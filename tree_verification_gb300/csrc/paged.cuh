@@ -22,6 +22,10 @@ inline int log2_exact(int x) {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Copy on write holds for every writer: where the cache says who holds its pages, a sequence's rows are written only
+// to pages among its own (entry k of its block-table row, k < held) that no other sequence holds.
+__device__ __forceinline__ bool guarded(const GraftPagedCache& c) { return c.held != nullptr && c.page_refs != nullptr; }
+
 // ---------------------------------------------------------------- the attention plan
 // A work item of the attention is one entry (a block of query rows of one sequence) and one KV head,
 // against a range of keys.  The plan is one buffer:

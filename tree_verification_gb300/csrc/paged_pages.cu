@@ -30,6 +30,8 @@ __device__ __forceinline__ int find_move(const GraftPagedCache& c, int Kmax, int
     const int32_t* row = c.block_table + (int64_t)b * c.max_pages;
     const int ps = row[from >> page_shift], pd = row[to >> page_shift];
     if (ps < 0 || ps >= c.num_pages || pd < 0 || pd >= c.num_pages) return GRAFT_STATUS_PAGE;
+    if (guarded(c) && ((from >> page_shift) >= c.held[b] || c.page_refs[ps] != 1 || c.page_refs[pd] != 1))
+        return GRAFT_STATUS_PAGE;
     *src = ((int64_t)ps << page_shift) + (from & (c.page_rows - 1));
     *dst = ((int64_t)pd << page_shift) + (to & (c.page_rows - 1));
     return 0;

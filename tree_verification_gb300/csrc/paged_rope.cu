@@ -14,6 +14,7 @@
 // 16-byte chunks whose dims pair up) are issued before the CTA looks up the
 // sequences and pages, so the look-up's dependent reads run behind them; the
 // page's number is read while the cosines are computed.
+#include <climits>
 #include <cmath>
 
 #include "paged.cuh"
@@ -49,6 +50,7 @@ struct Place {
     int b;      // sequence, -1: the row is no sequence's
     int first;  // its first new row
     int L;      // rows before them
+    int held;   // pages that it holds (all, where the cache does not say)
 };
 
 // The sequence of a row, by a warp: 32 probes at a time until 32 sequences are left, whose starts, ends and
@@ -64,18 +66,20 @@ __device__ __forceinline__ Place find_seq(const RopeArgs& a, int row) {
         lo += hit * step;
         len = min(step, len - hit * step);
     }
-    int first = 0, end = 0, L = 0;
+    int first = 0, end = 0, L = 0, held = INT_MAX;
     const bool have = lane < len;
     if (have) {
         first = a.q_start[lo + lane];
         end = a.q_start[lo + lane + 1];
         L = a.c.lengths[lo + lane];
+        if (guarded(a.c)) held = a.c.held[lo + lane];
     }
     const unsigned m = __ballot_sync(0xffffffffu, have && first <= row);
     const int hit = m == 0 ? 0 : 31 - __clz(m);
     Place p;
     p.first = __shfl_sync(0xffffffffu, first, hit);
     p.L = __shfl_sync(0xffffffffu, L, hit);
+    p.held = __shfl_sync(0xffffffffu, held, hit);
     p.b = m != 0 && row < __shfl_sync(0xffffffffu, end, hit) ? lo + hit : -1;
     return p;
 }
@@ -144,6 +148,8 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
             if (p.b >= 0) {
                 if (p.L < 0 || p.first < 0 || (r >> a.page_shift) >= a.c.max_pages)
                     flag_status(a.c.status, GRAFT_STATUS_LENGTH);
+                else if ((r >> a.page_shift) >= p.held)
+                    flag_status(a.c.status, GRAFT_STATUS_PAGE);
                 else
                     page_at = p.b * a.c.max_pages + (int)(r >> a.page_shift);
             }
@@ -151,7 +157,11 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
     }
     __syncthreads();
     const int page = page_at >= 0 ? a.c.block_table[page_at] : 0;
-    for (int x = tid; x < nt * (a.rot / 2); x += kThreads) {
+    const bool in_pool = page >= 0 && page < a.c.num_pages;
+    // (a third dependent read, beside the cosines)
+    const int refs = guarded(a.c) && page_at >= 0 && in_pool ? a.c.page_refs[page] : 1;
+    // (the warps that look nothing up come first: a step of 32 layers over one request 721 -> 715 us, held pages checked)
+    for (int x = tid ^ (kThreads / 2); x < nt * (a.rot / 2); x += kThreads) {
         const int t = (x >= a.rot / 2) + (x >= a.rot), p = x - t * (a.rot / 2);
         // 2^64 / 2 pi; a frequency of a turn or more per position keeps only its fraction
         const double turns = a.inv_freq[p] * 0.15915494309189533577;
@@ -162,9 +172,9 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
         s_cs[t][p] = make_float2(c * a.factor, s * a.factor);
     }
     if (warp < nt && lane == 0) {
-        const bool in_pool = page >= 0 && page < a.c.num_pages;
-        if (page_at >= 0 && !in_pool) flag_status(a.c.status, GRAFT_STATUS_PAGE);
-        s_dst[warp] = page_at >= 0 && in_pool ? ((int64_t)page << a.page_shift) + (r & (a.c.page_rows - 1)) : -1;
+        const bool ours = in_pool && refs == 1;
+        if (page_at >= 0 && !ours) flag_status(a.c.status, GRAFT_STATUS_PAGE);
+        s_dst[warp] = page_at >= 0 && ours ? ((int64_t)page << a.page_shift) + (r & (a.c.page_rows - 1)) : -1;
     }
     __syncthreads();
     for (int t = 0; t < nt; ++t) {

@@ -38,7 +38,8 @@ class PagedCache:
     """Paged cache over per-layer pools ``K``, ``V`` ([num_pages][page_rows][Hkv][128] each, bf16 or fp16).
 
     block_table [n_seqs][max_pages], lengths [n_seqs] int32; held [n_seqs] and page_refs [num_pages] int32 are
-    needed by reserve, fork and free alone.  ``status`` collects the GRAFT_STATUS_* bits of every call.
+    needed by reserve, fork and free alone; with them append and compact write only to pages that a sequence holds
+    alone.  ``status`` collects the GRAFT_STATUS_* bits of every call.
     """
 
     def __init__(self, K: Sequence[torch.Tensor], V: Sequence[torch.Tensor], block_table: torch.Tensor,

@@ -8,7 +8,10 @@ the accepted rows stay where compaction puts them.  On one CUDA stream:
     ->  per layer: append (rotary positions by depth, K and V into pages), attend (tree mask)
     ->  graft_accept_compact without layers (acceptance alone)  ->  compact  ->  M update
 
-Sequences fork and leave between steps with the cache's own calls.  Every
+Sequences fork and leave between steps with the cache's own calls.  A
+sequence for which there were not pages enough (GRAFT_STATUS_CACHE_OVERFLOW)
+keeps its rows and its length where its accepted rows do not fit the pages
+that it holds alone: what ``acc`` says of it did not reach the cache.  Every
 buffer is fixed, so a step can be captured once in a CUDA graph and replayed;
 run it once before capturing (the handle's buffers grow then).
 """
