@@ -506,6 +506,11 @@ int graft_update_M_noalloc(int32_t* M_succ, int32_t* M_cnt, int V, int W, const 
  *   K_layers, V_layers  device arrays of n_layers device pointers to pools
  *                [num_pages][page_rows][Hkv][128] (reserve, compact)
  *   status       device word for GRAFT_STATUS_* bits, or NULL
+ *   active       [n_seqs] bytes, or NULL (all are): a sequence with 0 here
+ *                takes no part in a call of append, plan (and so attention),
+ *                compact or reserve, whatever q_start, new_rows or acc_len
+ *                say of it: its rows, pages, length and rows of Q_out and O
+ *                stay as they were, and no status speaks of it
  * Pools are 16-byte aligned.  A sequence's rows past its length, and the
  * pages that no sequence holds, may hold anything, NaN included.
  * Where held and page_refs are both given, append and compaction write only
@@ -521,6 +526,7 @@ typedef struct GraftPagedCache {
     void* const* K_layers;
     void* const* V_layers;
     int32_t* status;
+    const uint8_t* active;
 } GraftPagedCache;
 
 /*

@@ -806,6 +806,61 @@ def test_rows_go_only_to_pages_that_a_sequence_holds_alone():
     assert rows_changed(s.K[0], K0[0]) == sorted([(p, r) for p in (spare, shared01) for r in (5, 6)])
 
 
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("new,G", [([3, 2, 4, 1], 4), ([40, 64, 30, 64], 8), ([64, 64, 2, 1], 4)])
+def test_sequences_that_take_no_part(tree, new, G):
+    lens = [100, 33, 0, 70]
+    s, P = bigger(lens, new, 4, seed=61)
+    c = s.cache
+    s.lengths.copy_(s.i32(lens + [0]))
+    on = torch.tensor([True, False, True, False, True], device=DEV)
+    s.lengths[3] = -5  # (what a call would flag)
+    state = [t.clone() for t in (s.t, c.held, c.page_refs)]
+    c.reserve(s.i32([0, 500, 0, 10**6, 0]), active=on)
+    assert s.status() == 0
+    for t, x in zip((s.t, c.held, c.page_refs), state):
+        assert torch.equal(t, x)
+    N, H = sum(new), s.Hkv
+    starts = s.i32(np.concatenate([[0], np.cumsum(new), [N]]))
+    Q, K, V = s.randn(N, H * G, 128).to(DEV), s.randn(N, H, 128).to(DEV), s.randn(N, H, 128).to(DEV)
+    mask = tree_masks(s.rng, new) if tree else None
+    md = torch.from_numpy(mask.view(np.int64)).to(DEV) if tree else None
+    out, O = torch.full_like(Q, 7.0), torch.full_like(Q, 7.0)
+    K0, V0 = s.K.clone(), s.V.clone()
+    c.append(0, Q, K, V, starts, out=out, active=on)
+    c.plan(starts, N, H * G, max(new), tree=tree, active=on)
+    c.attend(0, out, 0.09, mask=md, out=O)
+    assert s.status() == 0
+    at = np.concatenate([[0], np.cumsum(new)])
+    s.K0, s.V0 = s.K.cpu(), s.V.cpu()
+    s.lens, s.starts = lens, at.astype(np.int32)
+    s.table = s.t.cpu().numpy()
+    want = []
+    for b in range(4):
+        rows = slice(at[b], at[b + 1])
+        if b in (1, 3):
+            assert bool((out[rows] == 7).all()) and bool((O[rows] == 7).all())
+        else:
+            assert torch.equal(out[rows], Q[rows])
+            want += [(int(s.t[b, r // 16]), r % 16) for r in range(lens[b], lens[b] + new[b])]
+    assert rows_changed(s.K[0], K0[0]) == rows_changed(s.V[0], V0[0]) == sorted(want)
+    ref, size = opg.attention(np64(Q), np64(s.K0[0]), np64(s.V0[0]), s.table, lens, at, 0.09, mask, absolute=True)
+    for b in (0, 2):
+        rows = slice(at[b], at[b + 1])
+        tol = 2.0 ** -8 * (2 * np.abs(ref[rows]) + size[rows]) + 2.0 ** -12 * size[rows] + 1e-6
+        assert (np.abs(np64(O[rows]) - ref[rows]) <= tol).all()
+    for in_place in (False, True):
+        K0 = s.K.clone()
+        got = c.compact(s.i32(np.tile([0, 2, -1], (5, 1))), s.i32([2, 2, 2, 99, 0]), active=on,
+                        lengths_out=None if in_place else torch.zeros_like(s.lengths))
+        assert s.status() == 0 and got.tolist() == [102, 33, 2, -5, 0]
+        assert set(rows_changed(s.K[0], K0[0])) <= {(int(s.t[b, (lens[b] + 1) // 16]), (lens[b] + 1) % 16) for b in (0, 2)}
+    with pytest.raises(ValueError):
+        c.plan(starts, N, H * G, max(new), tree=tree, active=on[:4])
+    with pytest.raises(ValueError):
+        c.reserve(s.i32([0] * 5), active=on.int())
+
+
 # ------------------------------------------------------------------ schedules
 @pytest.mark.parametrize("Hkv,G,page,new,lens", [
     (2, 8, 16, [200, 1, 1, 1], [5, 900, 300, 0]),            # both kinds: the few rows run beside the wide ones

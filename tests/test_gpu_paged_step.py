@@ -172,6 +172,77 @@ def test_sampling_and_fp16():
     assert w.cache.lengths.tolist() == [a + b for a, b in zip([37, 48, 0], w.step.acc["acc_len"].tolist())]
 
 
+@pytest.mark.parametrize("m_policy", ["tree", "both"])
+@pytest.mark.parametrize("captured", [False, True])
+def test_idle_slots(m_policy, captured):
+    """A slot is freed and sits two steps out with senseless inputs; then a fork takes it."""
+    w = World(11, m_policy=m_policy)
+    c, st = w.cache, w.step
+    c.free(i32([1]))  # the middle one
+    st.active[1] = False
+    names = ("draft_logits", "root_tok", "target_logits")
+    held = w.inputs()
+    rows = slice(KMAX, 2 * KMAX)
+
+    def spoil(inp):
+        inp["draft_logits"][1] *= 1e6
+        inp["target_logits"][1] = float("nan")
+        for n in "QKV":
+            for x in inp[n]:
+                x[rows] = float("nan")
+
+    def step(inp):
+        for n in names:
+            held[n].copy_(inp[n])
+        for n in "QKV":
+            for x, y in zip(held[n], inp[n]):
+                x.copy_(y)
+        if graph is None:
+            st.run(M_succ=w.M[0], M_cnt=w.M[1], **held)
+        else:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert int(st.status.item()) == 0
+
+    graph = None
+    if captured:
+        lens, tables = c.lengths.clone(), [t.clone() for t in (c.block_table, c.held, c.page_refs)]
+        M = [t.clone() for t in w.M]
+        spoil(held)
+        graph = st.capture(M_succ=w.M[0], M_cnt=w.M[1], **held)  # (its step is undone)
+        for t, x in zip((c.lengths, c.block_table, c.held, c.page_refs, *w.M), (lens, *tables, *M)):
+            t.copy_(x)
+    refs = int(c.page_refs.sum())
+    for k in range(2):
+        inp = w.inputs()
+        spoil(inp)
+        lens, O = c.lengths.tolist(), st.O.clone()
+        s0, c0 = w.M[0].cpu().numpy(), w.M[1].cpu().numpy()
+        step(inp)
+        acc = st.acc["acc_len"].tolist()
+        assert acc[1] == 0 and acc[0] >= 1 and acc[2] >= 1
+        assert c.lengths.tolist() == [lens[0] + acc[0], 0, lens[2] + acc[2]]
+        assert int(c.held[1]) == 0 and bool((c.block_table[1] == -1).all())
+        assert int(c.page_refs.sum()) == int(c.held.sum()) and int(c.page_refs.max()) == 1
+        assert torch.equal(st.O[1], O[1]) and not torch.equal(st.O[0], O[0])
+        for b in (0, 2):  # the others, as ever
+            t = {n: st.tree[n][b].tolist() for n in ("tok", "parent", "depth")}
+            _, n, p, out_tok, bonus = oacc.accept(inp["target_logits"][b].cpu().numpy(), t["tok"], t["parent"], t["depth"])
+            assert acc[b] == n and st.acc["out_tok"][b, :n].tolist() == out_tok
+        if m_policy == "tree":
+            on = [0, 2]
+            s1, c1 = oupd.update_M(s0, c0, st.tree["tok"].cpu().numpy()[on].reshape(-1),
+                                   st.acc["argmax"].cpu().numpy()[on].reshape(-1))
+            assert np.array_equal(w.M[0].cpu().numpy(), s1) and np.array_equal(w.M[1].cpu().numpy(), c1)
+    c.fork(i32([0]), i32([1]))
+    st.active[1] = True
+    n = int(c.lengths[0])
+    step(w.inputs())
+    acc = st.acc["acc_len"].tolist()
+    assert min(acc) >= 1 and c.lengths.tolist()[:2] == [n + acc[0], n + acc[1]]
+    assert int(c.held[1]) == -(-(n + KMAX) // PAGE)
+
+
 def test_copy_on_write_survives_a_refused_reserve():
     """Two sequences share a partly filled page and no page is free: neither may write into it, and both stay as they
     are; once there are pages, the next step goes on as if that one had not been."""
@@ -214,6 +285,10 @@ def test_refusals():
         PagedVerifyStep(w.cfg, w.cache, 7)
     with pytest.raises(ValueError):
         PagedVerifyStep(w.cfg, w.cache, 8, m_policy="none")
+    inp = w.inputs()
+    for bad in (inp["root_tok"].long(), inp["root_tok"][:1]):
+        with pytest.raises(ValueError):
+            w.step.run(M_succ=w.M[0], M_cnt=w.M[1], **dict(inp, root_tok=bad))
     bare = PagedCache(list(w.K), list(w.V), w.cache.block_table, w.cache.lengths)
     with pytest.raises(ValueError):
         PagedVerifyStep(w.cfg, bare, 8)

@@ -71,7 +71,7 @@ class GraftPagedCache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "Hkv", "head_dim", "page_rows", "num_pages", "n_seqs",
                                               "max_pages", "n_layers")] + \
                [(n, ctypes.c_void_p) for n in ("block_table", "lengths", "held", "page_refs", "K_layers", "V_layers",
-                                               "status")]
+                                               "status", "active")]
 
 
 class GraftError(RuntimeError):

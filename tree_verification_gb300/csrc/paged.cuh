@@ -26,6 +26,9 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // to pages among its own (entry k of its block-table row, k < held) that no other sequence holds.
 __device__ __forceinline__ bool guarded(const GraftPagedCache& c) { return c.held != nullptr && c.page_refs != nullptr; }
 
+// Does sequence b take part in the call?
+__device__ __forceinline__ bool takes_part(const GraftPagedCache& c, int b) { return c.active == nullptr || c.active[b] != 0; }
+
 // ---------------------------------------------------------------- the attention plan
 // A work item of the attention is one entry (a block of query rows of one sequence) and one KV head,
 // against a range of keys.  The plan is one buffer:

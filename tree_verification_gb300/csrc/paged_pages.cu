@@ -50,14 +50,16 @@ compact_rows_kernel(const __grid_constant__ GraftPagedCache c, int Kmax, const i
         p = path[(int64_t)b * Kmax + t];
         if (t > 0) before = path[(int64_t)b * Kmax + t - 1];
     }
-    const int n = acc_len[b], L = c.lengths[b];
+    const int L = c.lengths[b], given = acc_len[b];
+    const bool idle = !takes_part(c, b);
+    const int n = idle ? 0 : given;
     auto pool_of = [&](int l, int x) -> uint4* {
         return l < c.n_layers && x < 2 * per ? static_cast<uint4*>((x < per ? c.K_layers : c.V_layers)[l]) : nullptr;
     };
     const int G = gridDim.x;
     uint4* pool0 = pool_of(blockIdx.x, t);
     uint4* pool1 = pool_of(blockIdx.x + G, t);
-    int bad = (n < 0 || n > Kmax) ? GRAFT_STATUS_TREE : L < 0 ? GRAFT_STATUS_LENGTH : 0;
+    int bad = (n < 0 || n > Kmax) ? GRAFT_STATUS_TREE : L < 0 && !idle ? GRAFT_STATUS_LENGTH : 0;
     if (!bad && t < n) bad = find_move(c, Kmax, p, before, L, b, t, page_shift, &s_src[t], &s_dst[t]);
     if (bad && blockIdx.x == 0) flag_status(c.status, bad);
     const int stop = __syncthreads_or(bad);
@@ -99,7 +101,7 @@ compact_lengths_kernel(const __grid_constant__ GraftPagedCache c, int Kmax, cons
                        const int32_t* __restrict__ acc_len, int page_shift) {
     griddep_enter();
     const int b = blockIdx.x, t = threadIdx.x;
-    const int n = acc_len[b], L = c.lengths[b];
+    const int L = c.lengths[b], n = takes_part(c, b) ? acc_len[b] : 0;
     int64_t src, dst;
     bool bad = n < 0 || n > Kmax || L < 0;
     if (!bad && t < n) {
@@ -252,7 +254,7 @@ reserve_kernel(const __grid_constant__ GraftPagedCache c, const int32_t* __restr
         const int b = b0 + tid;
         int need = 0, bad = 0;
         const bool mine = b < c.n_seqs;
-        const int rows = mine ? new_rows[b] : 0, held = mine ? c.held[b] : 0;
+        const int rows = mine && takes_part(c, b) ? new_rows[b] : 0, held = mine ? c.held[b] : 0;
         const int64_t L = mine ? c.lengths[b] : 0;
         if (rows != 0) {
             const int64_t pages = (L + rows + c.page_rows - 1) >> page_shift;
@@ -302,7 +304,7 @@ reserve_kernel(const __grid_constant__ GraftPagedCache c, const int32_t* __restr
     __syncthreads();
     for (int b = tid; b < c.n_seqs; b += kPlanThreads) {
         Tail tail{0, 0, 0, 0};
-        const int rows = new_rows[b];
+        const int rows = takes_part(c, b) ? new_rows[b] : 0;
         if (rows > 0 && s_need[b] >= 0) {
             const int64_t L = c.lengths[b];
             const int held = c.held[b], pages = (int)((L + rows + c.page_rows - 1) >> page_shift);

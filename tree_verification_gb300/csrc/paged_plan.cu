@@ -474,7 +474,7 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
     // Every block checks all sequences, the first one sets the status.
     auto read_seq = [&](int b, int& q0, int& n, int& L) {
         q0 = n = L = 0;
-        if (b >= c.n_seqs) return;
+        if (b >= c.n_seqs || !takes_part(c, b)) return;
         const int64_t from = q_start[b], to = q_start[b + 1], len = c.lengths[b];
         const int64_t rows = to - from;
         if (from < 0 || rows < 0 || to > N || rows > max_new || len < 0 ||

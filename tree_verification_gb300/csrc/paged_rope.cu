@@ -73,6 +73,7 @@ __device__ __forceinline__ Place find_seq(const RopeArgs& a, int row) {
         end = a.q_start[lo + lane + 1];
         L = a.c.lengths[lo + lane];
         if (guarded(a.c)) held = a.c.held[lo + lane];
+        if (!takes_part(a.c, lo + lane)) end = first;
     }
     const unsigned m = __ballot_sync(0xffffffffu, have && first <= row);
     const int hit = m == 0 ? 0 : 31 - __clz(m);

@@ -12,6 +12,9 @@ enqueue one library call each on the current stream of the pools' device:
     cache.compact(path, acc_len)            accepted tree rows kept
     cache.fork(src, dst), cache.free(seqs)  sequences that share pages; pages given back
 
+reserve, append, plan and compact take ``active`` ([n_seqs] bool on the device): sequences that are False there take no
+part, so a batch keeps its shape (and a captured step its graph) while sequences come and go.
+
 The buffers a handle allocates (plan, workspaces) grow when a call needs
 more and are kept as long as the handle lives, so captured graphs stay
 valid; a call that would have to grow one while a graph is being captured is
@@ -88,6 +91,7 @@ class PagedCache:
                                          ptr(self.status))
         self._c = ctypes.addressof(self.struct)
         self._lib = gb.lib()
+        self._parts = self._parts_at = None  # the last call's ``active`` and its address
         self._plan_of = None    # (N, Hq, max_new, tree) of the last plan
         self._sizes = {}        # (N, Hq, max_new) -> bytes of plan and workspace
         self._buffers = {}      # name -> buffer in use
@@ -110,6 +114,15 @@ class PagedCache:
             make = torch.zeros if zero else torch.empty
             t = self._buffers[name] = make(nbytes, dtype=torch.uint8, device=self.device)
         return t
+
+    def _part(self, active) -> None:
+        """Sets which sequences take part in the call that follows (None: all)."""
+        at = None
+        if active is not None:
+            at = active.data_ptr() if active is self._parts else self._need(active, "active", torch.bool, (self.n_seqs,))
+        if at != self._parts_at:
+            self.struct.active = self._parts_at = at
+        self._parts = active
 
     def _call(self, name: str, *args) -> None:
         stream = _raw_stream(self._index)
@@ -163,7 +176,7 @@ class PagedCache:
 
     # ------------------------------------------------------------------ calls
     def append(self, layer: int, Q, K, V, q_start, inv_freq=None, interleaved: bool = False, positions=None,
-               factor: float = 1.0, out=None):
+               factor: float = 1.0, out=None, active=None):
         """graft_rope_append: rotates Q and K ([N][H][128], rows may be strided), writes K and V to their pages.
 
         Returns the rotated Q (``out``, which may be Q itself).  Q may be None.  Without inv_freq nothing is rotated."""
@@ -189,11 +202,13 @@ class PagedCache:
         if inv_freq is not None:
             rot = 2 * inv_freq.numel()
             fp = self._need(inv_freq, "inv_freq", torch.float64, (rot // 2,))
+        if active is not None or self._parts is not None:
+            self._part(active)
         self._call("graft_rope_append", self._kp[layer], self._vp[layer], N, Hq, starts, pos, fp, rot,
                    1 if interleaved else 0, float(factor), qp, qs, kp, ks, vp, vs, op, os)
         return out
 
-    def plan(self, q_start, N: int, Hq: int, max_new: int, tree: bool = False) -> None:
+    def plan(self, q_start, N: int, Hq: int, max_new: int, tree: bool = False, active=None) -> None:
         """graft_paged_plan for a step of N rows; serves every attend() until the next plan()."""
         self._plan_of = None  # (a plan that is refused leaves none)
         starts = self._need(q_start, "q_start", torch.int32, (self.n_seqs + 1,))
@@ -210,6 +225,8 @@ class PagedCache:
             sizes = self._sizes[key] = (a.value, b.value)
         buf = self._buffer("plan", sizes[0], False)
         self._buffer("attention", sizes[1], True)
+        if active is not None or self._parts is not None:
+            self._part(active)
         self._call("graft_paged_plan", N, Hq, starts, max_new, 1 if tree else 0, buf.data_ptr(), buf.numel())
         self._plan_of = (N, Hq, max_new, bool(tree))
 
@@ -238,7 +255,7 @@ class PagedCache:
                        plan.numel(), qp, qs, mp, float(scale), op, ctypes.addressof(tuning), ws.data_ptr(), ws.numel())
         return out
 
-    def compact(self, path, acc_len, lengths_out=None):
+    def compact(self, path, acc_len, lengths_out=None, active=None):
         """graft_pages_compact: path [n_seqs][Kmax], acc_len [n_seqs]; lengths advance in place unless
         ``lengths_out`` receives them."""
         if not isinstance(path, torch.Tensor) or path.dim() != 2:
@@ -249,6 +266,8 @@ class PagedCache:
         if lengths_out is None:
             lengths_out = self.lengths
         lp = self._need(lengths_out, "lengths_out", torch.int32, (self.n_seqs,))
+        if active is not None or self._parts is not None:
+            self._part(active)
         self._call("graft_pages_compact", Kmax, pp, ap, lp)
         return lengths_out
 
@@ -256,7 +275,7 @@ class PagedCache:
         if self.held is None or self.page_refs is None:
             raise ValueError("reserve, fork and free need held and page_refs")
 
-    def reserve(self, new_rows) -> None:
+    def reserve(self, new_rows, active=None) -> None:
         """graft_pages_reserve: pages for new_rows [n_seqs] more rows of every sequence."""
         self._tables()
         np = self._need(new_rows, "new_rows", torch.int32, (self.n_seqs,))
@@ -266,6 +285,8 @@ class PagedCache:
             gb._check(self._lib.graft_pages_reserve_workspace_size(self._c, ctypes.byref(n)),
                       "graft_pages_reserve_workspace_size")
             ws = self._buffer("reserve", n.value, False)
+        if active is not None or self._parts is not None:
+            self._part(active)
         self._call("graft_pages_reserve", np, ws.data_ptr(), ws.numel())
 
     def fork(self, src, dst) -> None:

@@ -8,12 +8,21 @@ the accepted rows stay where compaction puts them.  On one CUDA stream:
     ->  per layer: append (rotary positions by depth, K and V into pages), attend (tree mask)
     ->  graft_accept_compact without layers (acceptance alone)  ->  compact  ->  M update
 
-Sequences fork and leave between steps with the cache's own calls.  A
-sequence for which there were not pages enough (GRAFT_STATUS_CACHE_OVERFLOW)
+Sequences fork and leave between steps with the cache's own calls; ``active``
+([n_seqs] bool on the device, all True at first) says which the next steps
+verify.  An idle slot (a sequence that left, or one whose prompt is still
+being appended in chunks) keeps its pages, rows and length and adds nothing to
+M; its acc_len is 0, and what else the step leaves of it means nothing (its
+rows of O are left alone).  Its inputs may be anything, except that its root
+token has to be one and its drafter logits finite (its target logits too,
+where the step samples).
+
+A sequence for which there were not pages enough (GRAFT_STATUS_CACHE_OVERFLOW)
 keeps its rows and its length where its accepted rows do not fit the pages
-that it holds alone: what ``acc`` says of it did not reach the cache.  Every
-buffer is fixed, so a step can be captured once in a CUDA graph and replayed;
-run it once before capturing (the handle's buffers grow then).
+that it holds alone: what ``acc`` says of it did not reach the cache.
+
+Every buffer is fixed, so a step can be captured once in a CUDA graph and
+replayed; run it once before capturing (the handle's buffers grow then).
 """
 from __future__ import annotations
 
@@ -63,9 +72,12 @@ class PagedVerifyStep:
         self.ws_smp = torch.empty(max(1, gb.graft_sample_tokens_workspace_size(B, K, cfg.V)), **u8)
         self.q_start = (torch.arange(B + 1, **i32) * K).contiguous()
         self.rows = torch.full((B,), K, **i32)
+        self.active = torch.ones(B, dtype=torch.bool, device=dev)
+        self._src = torch.empty(B, K, **i32)  # tree tokens for M, -1 (no pair) in idle slots
+        self._none = torch.full((), gb.EMPTY_TOKEN, **i32)
         self._no_layers = torch.empty(0, dtype=torch.int64, device=dev)
-        self._lengths = torch.empty(B, **i32)  # the acceptance's copy: compaction advances the cache's own
-        self.O = torch.empty(B, K, Hq, gb.HEAD_DIM, dtype=cache.dtype, device=dev)
+        self._lengths = torch.empty(B, **i32)  # the acceptance's copy (0 in idle slots): compaction advances the cache's own
+        self.O = torch.zeros(B, K, Hq, gb.HEAD_DIM, dtype=cache.dtype, device=dev)
         self.Qr = torch.empty_like(self.O)
         self.scale = 1.0 / math.sqrt(gb.HEAD_DIM)
         self.graph: Optional[torch.cuda.CUDAGraph] = None
@@ -82,21 +94,22 @@ class PagedVerifyStep:
         c, B, Kmax = self.cache, self.B, self.cfg.Kmax
         ready = inputs_ready if inputs_ready is not None else (lambda _: None)
         ready("tree")
-        c.reserve(self.rows)
+        on = self.active
+        c.reserve(self.rows, active=on)
         gb.graft_build_tree(self.cfg, draft_logits, root_tok, M_succ, c.lengths, out=self.tree, status=self.status,
                             ws=self.ws_tree)
-        c.plan(self.q_start, B * Kmax, self.Hq, Kmax, tree=True)
+        c.plan(self.q_start, B * Kmax, self.Hq, Kmax, tree=True, active=on)
         pos, mask = self.tree["pos"].view(-1), self.tree["mask"].view(-1)
         q, o = self.Qr.view(B * Kmax, self.Hq, gb.HEAD_DIM), self.O.view(B * Kmax, self.Hq, gb.HEAD_DIM)
         for layer in range(self.n_layers):
             ready(layer)
             c.append(layer, Q[layer], K[layer], V[layer], self.q_start, inv_freq=self.inv_freq,
-                     interleaved=self.interleaved, positions=pos, factor=self.factor, out=q)
+                     interleaved=self.interleaved, positions=pos, factor=self.factor, out=q, active=on)
             c.attend(layer, q, self.scale, mask=mask, out=o)
             if attended is not None:
                 attended(layer, self.O)
         ready("accept")
-        self._lengths.copy_(c.lengths)
+        torch.mul(c.lengths, on, out=self._lengths)
         tables = [self._no_layers] * 4
         args = (self.tree["tok"], self.tree["parent"], self.tree["depth"], *tables, 0, c.Hkv,
                 c.max_pages * c.page_rows, self._lengths)
@@ -107,10 +120,12 @@ class PagedVerifyStep:
                                     argmax=self.acc["argmax"], V=self.cfg.V)
         else:
             gb.graft_accept_compact(target_logits, *args, out=self.acc, status=self.status, ws=self.ws_acc)
-        c.compact(self.acc["path"], self.acc["acc_len"])
+        self.acc["acc_len"].mul_(on)
+        c.compact(self.acc["path"], self.acc["acc_len"], active=on)
         if self.m_policy in ("tree", "both"):
-            gb.graft_update_M(M_succ, M_cnt, self.tree["tok"].view(-1), self.acc["argmax"].view(-1),
-                              status=self.status, ws=self.ws_upd)
+            torch.where(on[:, None], self.tree["tok"], self._none, out=self._src)
+            gb.graft_update_M(M_succ, M_cnt, self._src.view(-1), self.acc["argmax"].view(-1), status=self.status,
+                              ws=self.ws_upd)
         if self.m_policy in ("emitted", "both"):
             gb.graft_update_M_emitted(M_succ, M_cnt, self.tree["tok"], self.acc["out_tok"], self.acc["acc_len"],
                                       status=self.status, ws=self.ws_emit)
