@@ -456,6 +456,21 @@ def test_host_refusals_of_the_handle():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("which", ["K", "V"])
+@pytest.mark.parametrize("offset", [1, 4])
+def test_pools_that_are_not_aligned_are_refused(which, offset):
+    """Layers carved out of one buffer at an odd place (nothing is launched on them)."""
+    from tree_verification_gb300.paged import PagedCache
+    shape, n = (4, 16, 2, 128), 4 * 16 * 2 * 128
+    flat = torch.zeros(2 * n + 16, dtype=torch.bfloat16, device=DEV)
+    even = [flat[:n].view(shape), flat[n:2 * n].view(shape)]
+    odd = [even[0], flat[n + offset:2 * n + offset].view(shape)]
+    table, lengths = torch.zeros(1, 4, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    PagedCache(even, even, table, lengths)
+    with pytest.raises(ValueError, match=which):
+        PagedCache(odd if which == "K" else even, odd if which == "V" else even, table, lengths)
+
+
 def test_a_refused_plan_leaves_none():
     s = Setup([70, 10], [2, 2], 2, 16, seed=25)
     Q = s.randn(4, 8, 128).to(DEV)

@@ -60,6 +60,8 @@ class PagedCache:
         for name, pools in (("K", K), ("V", V)):
             for i, t in enumerate(pools):
                 gb._need(t, f"{name}[{i}]", self.dtype, (P, R, H, d))
+                if t.data_ptr() % 16:  # (compact and reserve take the pools from device arrays, which no call can check)
+                    raise ValueError(f"{name}[{i}] must be 16-byte aligned")
         self.device = K[0].device
         gb._need(block_table, "block_table", torch.int32)
         if block_table.dim() != 2:
