@@ -203,6 +203,49 @@ def test_what_a_row_does_not_see_has_no_effect(dtype, tree, new, G):
     check_attention(s, O, Q, 0.09, mask)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("j", [0, 127, 300, 899])
+def test_one_infinity_in_a_long_chunk(dtype, j):
+    s = Setup([70, 5], [900, 40], 1, 64, dtype, seed=17)
+    r = 70 + j
+    s.V0[0, int(s.table[0, r // 64]), r % 64, 0, 3:9] = float("inf")
+    s.V0[0, int(s.table[0, 969 // 64]), 969 % 64, 0, 8] = float("-inf")
+    s.V.copy_(s.V0)
+    Q, O = run_attention(s, 4)
+    check_attention(s, O, Q, 0.09)
+
+
+def test_one_infinity_in_a_long_chunk_takes_no_longer():
+    """The elements taken out of the products are looked for in the blocks that were cleaned, not in the whole chunk."""
+    from tree_verification_gb300.paged import PagedCache
+    n, page = 12000, 64
+    pages = -(-n // page)
+    K, V = (torch.randn(pages, page, 1, 128, device=DEV).bfloat16() for _ in range(2))
+    table = torch.randperm(pages, device=DEV).int().view(1, -1)
+    c = PagedCache([K], [V], table, torch.zeros(1, dtype=torch.int32, device=DEV))
+    starts = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    Q = torch.randn(n, 4, 128, device=DEV).bfloat16()
+    c.plan(starts, n, 4, n)
+
+    def best():
+        got = 1e9
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            O = c.attend(0, Q, 0.09)
+            b.record()
+            torch.cuda.synchronize()
+            got = min(got, a.elapsed_time(b))
+        return got, O
+
+    plain, O = best()
+    V[int(table[0, (n - 2) // page]), (n - 2) % page, 0, 5] = float("inf")
+    odd, O2 = best()
+    assert int(c.status.item()) == 0
+    assert torch.equal(O2[:n - 2], O[:n - 2]) and bool(torch.isinf(O2[n - 2:, :, 5]).all())
+    assert odd < 2 * plain + 0.5
+
+
 def test_strided_queries_and_layers():
     s = Setup([70, 0, 130], [4, 1, 2], 2, 32, layers=3, seed=9)
     N, Hq = 7, 8

@@ -682,10 +682,13 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                 }
                 if (row_ok && !direct)
                     a.wide_lse[pblk * 128 + r] = l_sum == 0.f ? -INFINITY : m_used + log2f(l_sum) - kLift;
-                if (*odd_word() == (uint32_t)k + 1 && row_ok)
+                if (*odd_word() == (uint32_t)k + 1 && row_ok) {
+                    // (from the first block that tile 0 cleaned: what lies before is in the products as it is)
+                    const int edge0 = (a.mask != nullptr ? w.L : min(w.L + w.tok0 + 1, w.keys)) / BN;
                     add_odd<DT>(a.c, a.V, a.c.block_table + (int64_t)w.b * a.c.max_pages, a.page_shift, kvh,
-                                max(w.blk0 * BN, w.L), min((w.blk0 + w.nblk) * BN, w.keys), limit, w.L, anc,
-                                direct ? orow : nullptr, direct ? nullptr : part);
+                                max(max(w.blk0, edge0) * BN, w.L), min((w.blk0 + w.nblk) * BN, w.keys), limit, w.L,
+                                anc, direct ? orow : nullptr, direct ? nullptr : part);
+                }
             }
             gv += nblk;
             ++q;
