@@ -311,6 +311,35 @@ def test_lengths_that_rise_by_one_a_pass(B, L, Hkv):
     check_attention(s, O, Q, 0.1)
 
 
+def test_wide_plans_change_between_replays_of_one_graph():
+    """What is split by keys, into how many ranges and where its partial rows lie is another plan's each time; short
+    sequences run beside."""
+    s = Setup([4000, 700, 900], [64, 40, 2], 2, 32, seed=18)
+    N = 106
+    Q = s.randn(N, 8, 128)
+    O = torch.zeros(N, 8, 128, dtype=s.dtype, device=DEV)
+    Qd = Q.to(DEV)
+
+    def step():
+        s.cache.plan(s.q_start, N, 8, 64)
+        for _ in range(2):  # (two layers: the second call's kernels follow the first's directly)
+            s.cache.attend(0, Qd, 0.1, out=O)
+
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    cases = [([4000, 700, 900], [0, 64, 104, 106]), ([130, 700, 900], [0, 64, 104, 106]), ([3000, 0, 902], [0, 2, 42, 42]),
+             ([4064, 740, 800], [0, 0, 0, 64]), ([0, 0, 0], [0, 33, 64, 106]), ([2222, 600, 840], [0, 3, 40, 102])]
+    for lens, starts in cases + cases[::-1]:
+        s.lens, s.starts = lens, np.array(starts, np.int32)
+        s.lengths.copy_(s.i32(lens))
+        s.q_start.copy_(s.i32(starts))
+        g.replay()
+        assert s.status() == 0
+        check_attention(s, O, Q, 0.1)
+
+
 def test_a_plan_of_fewer_sequences_right_before_its_attention():
     """One sequence after another leaves (its pages given back, its row of Q turned into padding) and the captured
     plan and attention run back to back: what the last plan said of it must not count against the call."""

@@ -3,6 +3,8 @@
 
 #include <cuda_fp16.h>
 
+#include <cstddef>
+
 #include "common.cuh"
 
 namespace graft {
@@ -85,6 +87,8 @@ struct Start {
     int64_t item_first;                // step 0: the item's first unit among all
     int64_t total;                     // step 0: all units
 };
+
+constexpr int kHeadBytes = offsetof(PlanHead, reserved);  // of the head's fields
 
 struct PlanShape {
     int max_few;   // bound on the few entries

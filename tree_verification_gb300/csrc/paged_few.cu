@@ -318,7 +318,8 @@ few_kernel(const __grid_constant__ AttnArgs a) {
     }
     if (!a.after_wide) griddep_wait();
     griddep_launch_dependents();
-    // Beside the wide kernel the wait comes last, so that this kernel's end is that of both.
+    // Beside the wide kernel (two row tiles) the wait comes last, so that this kernel's end is that of both; all that
+    // it reads comes from L2, past lines that an earlier kernel left in the SM's L1.
     auto leave = [&]() {
         if (a.after_wide) griddep_wait();
     };
@@ -381,7 +382,8 @@ few_kernel(const __grid_constant__ AttnArgs a) {
                     limit[t][h] = 0;
                 } else if (a.mask != nullptr) {
                     limit[t][h] = e.L;
-                    anc[t][h] = a.mask[e.q0 + tok];
+                    const uint64_t* m = a.mask + e.q0 + tok;
+                    anc[t][h] = RT > 1 ? __ldcg(reinterpret_cast<const unsigned long long*>(m)) : *m;
                 } else {
                     limit[t][h] = e.L + tok + 1;
                 }
@@ -628,7 +630,14 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             s_at.item_first += s_at.e.units;
             if (++s_at.head == a.c.Hkv) {
                 s_at.head = 0;
-                s_at.e = entries[++s_at.entry];
+                const Entry* next = entries + ++s_at.entry;
+                if (RT > 1) {
+                    const int4 lo = __ldcg(reinterpret_cast<const int4*>(next));
+                    const int4 hi = __ldcg(reinterpret_cast<const int4*>(next) + 1);
+                    s_at.e = Entry{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                } else {
+                    s_at.e = *next;
+                }
             }
         }
         __syncthreads();
