@@ -1029,6 +1029,34 @@ def test_a_few_short_items_past_a_whole_round(extra):
     assert torch.equal(again, O) and s.status() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("Hkv,G,new,lens", [
+    (1, 64, [4200, 30, 0, 9], [500, 40, 7, 0]),   # more row blocks than the plan ranks: placed by buckets, nothing split
+    (8, 16, [2500, 1, 60, 2], [77, 900, 0, 128]),  # eight whole rounds and more: no partial rows, no join
+])
+def test_long_chunks_of_many_rounds(dtype, Hkv, G, new, lens):
+    s = Setup(lens, new, Hkv, 64, dtype, seed=70)
+    N, Hq = int(s.starts[-1]), Hkv * G
+    blocks = -(-new[0] // (2 * (128 // G)))
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert blocks > 1024 or blocks * Hkv >= 8 * sms
+    Q = torch.randn(N, Hq, 128, generator=torch.Generator(DEV).manual_seed(1), device=DEV).to(dtype)
+    O = torch.full((N + 3, Hq, 128), 7.0, dtype=dtype, device=DEV)
+    s.cache.plan(s.q_start, N, Hq, max(new))
+    s.cache.attend(0, Q, 0.09, out=O[:N])
+    assert s.status() == 0 and bool((O[N:] == 7).all())
+    # sampled rows, each as a sequence of its own of one new row
+    at = [(b, i) for b, n in enumerate(new) for i in {0, n // 2, n - 1, *s.rng.integers(0, max(n, 1), 12).tolist()} if 0 <= i < n]
+    rows = [int(s.starts[b]) + i for b, i in at]
+    ref, size = opg.attention(np64(Q[rows]), np64(s.K0[0]), np64(s.V0[0]), [s.table[b] for b, _ in at],
+                              [lens[b] + i for b, i in at], np.arange(len(at) + 1), 0.09, absolute=True)
+    tol = HALF[dtype] * (2 * np.abs(ref) + size) + 2.0 ** -12 * size + 1e-6
+    assert (np.abs(np64(O[rows]) - ref) <= tol).all()
+    again = torch.full_like(O, 7.0)
+    s.cache.attend(0, Q, 0.09, out=again[:N])
+    assert torch.equal(again, O) and s.status() == 0
+
+
 def test_more_sequences_than_a_block_has_threads():
     rng = np.random.default_rng(8)
     n = 1100
