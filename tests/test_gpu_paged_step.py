@@ -243,6 +243,23 @@ def test_idle_slots(m_policy, captured):
     assert int(c.held[1]) == -(-(n + KMAX) // PAGE)
 
 
+def test_a_step_runs_on_the_caches_device(monkeypatch):
+    """Whatever device is current: the calls that take their stream from the current device are made under the cache's.
+    (One GPU here: the test sees to it that the step asks for it.)"""
+    w = World(12)
+    asked, inside = [], []
+
+    class Device(torch.cuda.device):
+        def __init__(self, d):
+            asked.append(d)
+            super().__init__(d)
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    w.step.run(M_succ=w.M[0], M_cnt=w.M[1], inputs_ready=lambda x: inside.append(list(asked)), **w.inputs())
+    torch.cuda.synchronize()
+    assert len(inside) == 2 + LAYERS and all(x and x[0] == w.cache.device for x in inside)
+
+
 def test_copy_on_write_survives_a_refused_reserve():
     """Two sequences share a partly filled page and no page is free: neither may write into it, and both stay as they
     are; once there are pages, the next step goes on as if that one had not been."""

@@ -65,11 +65,12 @@ class PagedVerifyStep:
                         out_tok=torch.empty(B, K, **i32), bonus=torch.empty(B, **i32))
         self.status = cache.status  # one word for the step's calls and the cache's
         u8 = dict(dtype=torch.uint8, device=dev)
-        self.ws_tree = torch.zeros(max(1, gb.graft_build_tree_workspace_size(cfg, B)), **u8)
-        self.ws_acc = torch.empty(max(1, gb.graft_accept_compact_workspace_size(B, K, cfg.V)), **u8)
-        self.ws_upd = torch.empty(max(1, gb.graft_update_M_workspace_size(B * K)), **u8)
-        self.ws_emit = torch.empty(max(1, gb.graft_update_M_emitted_workspace_size(B, K)), **u8)
-        self.ws_smp = torch.empty(max(1, gb.graft_sample_tokens_workspace_size(B, K, cfg.V)), **u8)
+        with torch.cuda.device(dev):  # (sizes that go by the device)
+            self.ws_tree = torch.zeros(max(1, gb.graft_build_tree_workspace_size(cfg, B)), **u8)
+            self.ws_acc = torch.empty(max(1, gb.graft_accept_compact_workspace_size(B, K, cfg.V)), **u8)
+            self.ws_upd = torch.empty(max(1, gb.graft_update_M_workspace_size(B * K)), **u8)
+            self.ws_emit = torch.empty(max(1, gb.graft_update_M_emitted_workspace_size(B, K)), **u8)
+            self.ws_smp = torch.empty(max(1, gb.graft_sample_tokens_workspace_size(B, K, cfg.V)), **u8)
         self.q_start = (torch.arange(B + 1, **i32) * K).contiguous()
         self.rows = torch.full((B,), K, **i32)
         self.active = torch.ones(B, dtype=torch.bool, device=dev)
@@ -85,12 +86,16 @@ class PagedVerifyStep:
     def run(self, draft_logits, root_tok, M_succ, M_cnt, Q: Sequence[torch.Tensor], K: Sequence[torch.Tensor],
             V: Sequence[torch.Tensor], target_logits, attended: Optional[Callable[[int, torch.Tensor], None]] = None,
             inputs_ready: Optional[Callable[[object], None]] = None) -> None:
-        """Enqueue one step on the current stream (asynchronous).
+        """Enqueue one step on the current stream of the cache's device (asynchronous).
 
         Q, K, V: per layer, [B * Kmax][heads][128] rows before rotation (they may be columns of one matrix).
         ``attended`` is called with (layer, O) after each layer's attention is enqueued (O is overwritten by the
         next layer); ``inputs_ready`` as in VerifyStep.run ("tree", each layer's index, "accept").
         """
+        with torch.cuda.device(self.device):  # (the calls that are not the handle's go by the current device)
+            self._run(draft_logits, root_tok, M_succ, M_cnt, Q, K, V, target_logits, attended, inputs_ready)
+
+    def _run(self, draft_logits, root_tok, M_succ, M_cnt, Q, K, V, target_logits, attended, inputs_ready) -> None:
         c, B, Kmax = self.cache, self.B, self.cfg.Kmax
         ready = inputs_ready if inputs_ready is not None else (lambda _: None)
         ready("tree")
@@ -135,14 +140,15 @@ class PagedVerifyStep:
 
         The step runs once outside the capture first, on the cache and M as they are: restore them afterwards if
         that step is not wanted."""
-        g = torch.cuda.CUDAGraph()
-        s = torch.cuda.Stream(device=self.device)
-        s.wait_stream(torch.cuda.current_stream())
-        with torch.cuda.stream(s):
-            self.run(*args, **kw)
-        torch.cuda.current_stream().wait_stream(s)
-        torch.cuda.synchronize(self.device)
-        with torch.cuda.graph(g):
-            self.run(*args, **kw)
+        with torch.cuda.device(self.device):
+            g = torch.cuda.CUDAGraph()
+            s = torch.cuda.Stream(device=self.device)
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                self.run(*args, **kw)
+            torch.cuda.current_stream().wait_stream(s)
+            torch.cuda.synchronize(self.device)
+            with torch.cuda.graph(g):
+                self.run(*args, **kw)
         self.graph = g
         return g
