@@ -591,19 +591,6 @@ attn_tc_kernel(const __grid_constant__ Maps maps, AttnArgs a) {
         }
     }
     // ---------------------------------------------------------------- teardown
-    if (warp == 0 && lane == 0 && aborted(abort_flag)) {
-        // loads still in flight write into this CTA's shared memory: the producer waits for the
-        // last armed phase of every stage it used (and the Q load) before the CTA may exit
-        mbar_wait(bar(BAR_Q), 0, kDrainNs);
-        for (int st = 0; st < SK; ++st) {
-            const int n = (k_issued - st + SK - 1) / SK;
-            if (n > 0) mbar_wait(bar(BAR_KF + st), (n - 1) & 1, kDrainNs);
-        }
-        for (int st = 0; st < SV; ++st) {
-            const int n = (v_issued - st + SV - 1) / SV;
-            if (n > 0) mbar_wait(bar(BAR_VF + st), (n - 1) & 1, kDrainNs);
-        }
-    }
     if (warp == 1 && lane == 0) {
         // every issued MMA has completed before TMEM is released
         mbar_wait(bar(BAR_DONE), 0, kTeardownNs);
@@ -611,6 +598,24 @@ attn_tc_kernel(const __grid_constant__ Maps maps, AttnArgs a) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // All warps are through, so the flag is final (looked at before the barrier it could still be down where the
+    // producer had ended before another warp gave up).
+    if (aborted(abort_flag)) {
+        if (warp == 0 && lane == 0) {
+            // loads still in flight write into this CTA's shared memory: the producer waits for the
+            // last armed phase of every stage it used (and the Q load) before the CTA may exit
+            mbar_wait(bar(BAR_Q), 0, kDrainNs);
+            for (int st = 0; st < SK; ++st) {
+                const int n = (k_issued - st + SK - 1) / SK;
+                if (n > 0) mbar_wait(bar(BAR_KF + st), (n - 1) & 1, kDrainNs);
+            }
+            for (int st = 0; st < SV; ++st) {
+                const int n = (v_issued - st + SV - 1) / SV;
+                if (n > 0) mbar_wait(bar(BAR_VF + st), (n - 1) & 1, kDrainNs);
+            }
+        }
+        __syncthreads();
+    }
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 

@@ -546,22 +546,6 @@ attn_tc_kernel(const __grid_constant__ Maps maps, AttnArgs a) {
         }
     }
     // ---------------------------------------------------------------- teardown
-    if (lane == 0 && (warp == 0 || warp == 3) && aborted(abort_flag)) {
-        // loads still in flight write into this CTA's shared memory: each producer waits for
-        // the last armed phase of every stage it used (and the Q load) before the CTA may exit
-        if (warp == 0) {
-            mbar_wait(bar(BAR_Q), 0, kDrainNs);
-            for (int st = 0; st < SK; ++st) {
-                const int n = (k_issued - st + SK - 1) / SK;
-                if (n > 0) mbar_wait(bar(BAR_KF + st), (n - 1) & 1, kDrainNs);
-            }
-        } else {
-            for (int st = 0; st < SV; ++st) {
-                const int n = (v_issued - st + SV - 1) / SV;
-                if (n > 0) mbar_wait(bar(BAR_VF + st), (n - 1) & 1, kDrainNs);
-            }
-        }
-    }
     if (warp == 2 && lane == 0) {
         // every issued MMA has completed before TMEM is released
         mbar_wait(bar(BAR_DONE), 0, kTeardownNs);
@@ -569,6 +553,26 @@ attn_tc_kernel(const __grid_constant__ Maps maps, AttnArgs a) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // All warps are through, so the flag is final (looked at before the barrier it could still be down where a producer
+    // had ended before another warp gave up).
+    if (aborted(abort_flag)) {
+        // loads still in flight write into this CTA's shared memory: each producer waits for
+        // the last armed phase of every stage it used (and the Q load) before the CTA may exit
+        if (lane == 0 && warp == 0) {
+            mbar_wait(bar(BAR_Q), 0, kDrainNs);
+            for (int st = 0; st < SK; ++st) {
+                const int n = (k_issued - st + SK - 1) / SK;
+                if (n > 0) mbar_wait(bar(BAR_KF + st), (n - 1) & 1, kDrainNs);
+            }
+        }
+        if (lane == 0 && warp == 3) {
+            for (int st = 0; st < SV; ++st) {
+                const int n = (v_issued - st + SV - 1) / SV;
+                if (n > 0) mbar_wait(bar(BAR_VF + st), (n - 1) & 1, kDrainNs);
+            }
+        }
+        __syncthreads();
+    }
     if (warp == 2) tmem_dealloc(tmem, 512);
 }
 

@@ -639,31 +639,34 @@ attn_tcp_kernel(const __grid_constant__ Maps maps, AttnArgs a) {
         if (!ok && !aborted(abort_flag)) raise_abort(abort_flag, a.status);
     }
     // ---------------------------------------------------------------- teardown
-    if (warp == 0 && lane == 0 && aborted(abort_flag)) {
-        // loads still in flight write into this CTA's shared memory: wait for the last armed
-        // phase of every stage (and the last Q load) before the CTA may exit
-        if (q_issued > 0) mbar_wait(bar(BAR_Q), (q_issued - 1) & 1, kDrainNs);
-        for (int st = 0; st < SK; ++st) {
-            const int n = (k_issued - st + SK - 1) / SK;
-            if (n > 0) mbar_wait(bar(BAR_KF + st), (n - 1) & 1, kDrainNs);
-        }
-        for (int st = 0; st < SV; ++st) {
-            const int n = (v_issued - st + SV - 1) / SV;
-            if (n > 0) mbar_wait(bar(BAR_VF + st), (n - 1) & 1, kDrainNs);
-        }
-    }
-    if (warp == 1 && lane == 0) {
-        // every issued MMA has completed before TMEM is released: on an abort the MMAs issued
-        // since the last item's DONE get a commit of their own
-        if (aborted(abort_flag)) {
-            mma_commit(bar(BAR_DONE));
-            ++ndone;
-        }
-        if (ndone > 0) mbar_wait(bar(BAR_DONE), (ndone - 1) & 1, kTeardownNs);
-    }
+    if (warp == 1 && lane == 0 && ndone > 0) mbar_wait(bar(BAR_DONE), (ndone - 1) & 1, kTeardownNs);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // All warps are through, so the flag is final (looked at before the barrier it could still be down where the
+    // producer had ended before another warp gave up).
+    if (aborted(abort_flag)) {
+        if (warp == 0 && lane == 0) {
+            // loads still in flight write into this CTA's shared memory: wait for the last armed
+            // phase of every stage (and the last Q load) before the CTA may exit
+            if (q_issued > 0) mbar_wait(bar(BAR_Q), (q_issued - 1) & 1, kDrainNs);
+            for (int st = 0; st < SK; ++st) {
+                const int n = (k_issued - st + SK - 1) / SK;
+                if (n > 0) mbar_wait(bar(BAR_KF + st), (n - 1) & 1, kDrainNs);
+            }
+            for (int st = 0; st < SV; ++st) {
+                const int n = (v_issued - st + SV - 1) / SV;
+                if (n > 0) mbar_wait(bar(BAR_VF + st), (n - 1) & 1, kDrainNs);
+            }
+        }
+        if (warp == 1 && lane == 0) {
+            // every issued MMA has completed before TMEM is released: those issued since the last item's DONE (which
+            // is past: two pending phases could not be told apart) get a commit of their own
+            mma_commit(bar(BAR_DONE));
+            mbar_wait(bar(BAR_DONE), ndone & 1, kTeardownNs);
+        }
+        __syncthreads();
+    }
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
