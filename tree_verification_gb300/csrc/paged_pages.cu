@@ -229,9 +229,12 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
 // so that "shared" means the same to every sequence of the call.  Latency
 // bound: what depends on nothing is read at once (a thread's sequence and its
 // share of the first tile), and the pages found first stay in shared memory.
+// The search is linear in the pages held below the free ones: one page each
+// for 64 sequences of a pool nine tenths full takes 4.3 us with 4096 pages,
+// 7.1 with 16384, 17.7 with 65536.
 constexpr int kTile = kPlanThreads * 4;
 constexpr int kFreshInSmem = 2048;
-__global__ void __launch_bounds__(kPlanThreads)
+__global__ void __launch_bounds__(kPlanThreads, 1)
 reserve_kernel(const __grid_constant__ GraftPagedCache c, const int32_t* __restrict__ new_rows, ReserveWs w,
                int page_shift) {
     __shared__ int s_warp[32];
