@@ -942,6 +942,15 @@ def test_sequences_that_take_no_part(tree, new, G):
                         lengths_out=None if in_place else torch.zeros_like(s.lengths))
         assert s.status() == 0 and got.tolist() == [102, 33, 2, -5, 0]
         assert set(rows_changed(s.K[0], K0[0])) <= {(int(s.t[b, (lens[b] + 1) // 16]), (lens[b] + 1) % 16) for b in (0, 2)}
+    # calls of two masks and of none in turn: each goes by its own
+    masks = [on, torch.tensor([False, True, True, False, True], device=DEV), None]
+    s.lengths.copy_(s.i32(lens + [0]))
+    for m in masks * 2:
+        out.fill_(7.0)
+        c.append(0, Q, K, V, starts, out=out, active=m)
+        for b in range(4):
+            assert bool((out[at[b]:at[b + 1]] == 7).all()) == (m is not None and not bool(m[b]))
+    s.status()
     with pytest.raises(ValueError):
         c.plan(starts, N, H * G, max(new), tree=tree, active=on[:4])
     with pytest.raises(ValueError):

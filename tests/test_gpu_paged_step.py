@@ -243,6 +243,19 @@ def test_idle_slots(m_policy, captured):
     assert int(c.held[1]) == -(-(n + KMAX) // PAGE)
 
 
+def test_all_slots_idle():
+    w = World(13)
+    c, st = w.cache, w.step
+    inp = w.inputs()
+    st.active.zero_()
+    state = [t.clone() for t in (c.block_table, c.held, c.page_refs, c.lengths, w.K, w.V, *w.M)]
+    st.run(M_succ=w.M[0], M_cnt=w.M[1], **inp)
+    torch.cuda.synchronize()
+    assert int(st.status.item()) == 0 and st.acc["acc_len"].tolist() == [0] * B
+    for t, x in zip((c.block_table, c.held, c.page_refs, c.lengths, w.K, w.V, *w.M), state):
+        assert torch.equal(t, x)
+
+
 def test_a_step_runs_on_the_caches_device(monkeypatch):
     """Whatever device is current: the calls that take their stream from the current device are made under the cache's.
     (One GPU here: the test sees to it that the step asks for it.)"""

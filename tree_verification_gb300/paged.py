@@ -34,6 +34,8 @@ from . import binding as gb
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
+_Reference = type(ctypes.byref(ctypes.c_int()))
+
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
@@ -93,7 +95,7 @@ class PagedCache:
                                          ptr(self.status))
         self._c = ctypes.addressof(self.struct)
         self._lib = gb.lib()
-        self._parts = self._parts_at = None  # the last call's ``active`` and its address
+        self._structs = {}      # address of an ``active`` tensor -> the struct with it
         self._plan_of = None    # (N, Hq, max_new, tree) of the last plan
         self._sizes = {}        # (N, Hq, max_new) -> bytes of plan and workspace
         self._buffers = {}      # name -> buffer in use
@@ -117,22 +119,30 @@ class PagedCache:
             t = self._buffers[name] = make(nbytes, dtype=torch.uint8, device=self.device)
         return t
 
-    def _part(self, active) -> None:
-        """Sets which sequences take part in the call that follows (None: all)."""
-        at = None
-        if active is not None:
-            at = active.data_ptr() if active is self._parts else self._need(active, "active", torch.bool, (self.n_seqs,))
-        if at != self._parts_at:
-            self.struct.active = self._parts_at = at
-        self._parts = active
+    def _with(self, active):
+        """The cache's struct with ``active`` in it (None: without), as the calls take it.  (A struct each, never changed:
+        calls of other host threads may be reading theirs.)  What it returned may be given to it again: a step with many
+        layers asks once."""
+        if active is None:
+            return self._c
+        if type(active) is _Reference:
+            return active
+        at = self._need(active, "active", torch.bool, (self.n_seqs,))
+        c = self._structs.get(at)
+        if c is None:
+            c = gb.GraftPagedCache.from_buffer_copy(self.struct)
+            c.active = at
+            if len(self._structs) < 256:
+                self._structs[at] = c
+        return ctypes.byref(c)
 
-    def _call(self, name: str, *args) -> None:
+    def _call(self, name: str, c, *args) -> None:
         stream = _raw_stream(self._index)
         if _current_device() == self._index:
-            rc = getattr(self._lib, name)(self._c, *args, stream)
+            rc = getattr(self._lib, name)(c, *args, stream)
         else:
             with torch.cuda.device(self._index):
-                rc = getattr(self._lib, name)(self._c, *args, stream)
+                rc = getattr(self._lib, name)(c, *args, stream)
         if rc:
             gb._check(rc, name)
 
@@ -204,9 +214,7 @@ class PagedCache:
         if inv_freq is not None:
             rot = 2 * inv_freq.numel()
             fp = self._need(inv_freq, "inv_freq", torch.float64, (rot // 2,))
-        if active is not None or self._parts is not None:
-            self._part(active)
-        self._call("graft_rope_append", self._kp[layer], self._vp[layer], N, Hq, starts, pos, fp, rot,
+        self._call("graft_rope_append", self._with(active), self._kp[layer], self._vp[layer], N, Hq, starts, pos, fp, rot,
                    1 if interleaved else 0, float(factor), qp, qs, kp, ks, vp, vs, op, os)
         return out
 
@@ -227,9 +235,8 @@ class PagedCache:
             sizes = self._sizes[key] = (a.value, b.value)
         buf = self._buffer("plan", sizes[0], False)
         self._buffer("attention", sizes[1], True)
-        if active is not None or self._parts is not None:
-            self._part(active)
-        self._call("graft_paged_plan", N, Hq, starts, max_new, 1 if tree else 0, buf.data_ptr(), buf.numel())
+        self._call("graft_paged_plan", self._with(active), N, Hq, starts, max_new, 1 if tree else 0, buf.data_ptr(),
+                   buf.numel())
         self._plan_of = (N, Hq, max_new, bool(tree))
 
     def attend(self, layer: int, Q, scale: float, mask=None, out=None, tuning=None):
@@ -249,12 +256,13 @@ class PagedCache:
         mp = None if mask is None else self._need(mask, "mask", torch.int64, (N,))
         plan, ws = self._buffers["plan"], self._buffers["attention"]
         if tuning is None:
-            self._call("graft_paged_attention", self._kp[layer], self._vp[layer], N, Hq, max_new, plan.data_ptr(),
-                       plan.numel(), qp, qs, mp, float(scale), op, ws.data_ptr(), ws.numel())
+            self._call("graft_paged_attention", self._c, self._kp[layer], self._vp[layer], N, Hq, max_new,
+                       plan.data_ptr(), plan.numel(), qp, qs, mp, float(scale), op, ws.data_ptr(), ws.numel())
         else:
             tuning = gb._tuning(tuning)
-            self._call("graft_paged_attention_ex", self._kp[layer], self._vp[layer], N, Hq, max_new, plan.data_ptr(),
-                       plan.numel(), qp, qs, mp, float(scale), op, ctypes.addressof(tuning), ws.data_ptr(), ws.numel())
+            self._call("graft_paged_attention_ex", self._c, self._kp[layer], self._vp[layer], N, Hq, max_new,
+                       plan.data_ptr(), plan.numel(), qp, qs, mp, float(scale), op, ctypes.addressof(tuning),
+                       ws.data_ptr(), ws.numel())
         return out
 
     def compact(self, path, acc_len, lengths_out=None, active=None):
@@ -268,9 +276,7 @@ class PagedCache:
         if lengths_out is None:
             lengths_out = self.lengths
         lp = self._need(lengths_out, "lengths_out", torch.int32, (self.n_seqs,))
-        if active is not None or self._parts is not None:
-            self._part(active)
-        self._call("graft_pages_compact", Kmax, pp, ap, lp)
+        self._call("graft_pages_compact", self._with(active), Kmax, pp, ap, lp)
         return lengths_out
 
     def _tables(self) -> None:
@@ -287,9 +293,7 @@ class PagedCache:
             gb._check(self._lib.graft_pages_reserve_workspace_size(self._c, ctypes.byref(n)),
                       "graft_pages_reserve_workspace_size")
             ws = self._buffer("reserve", n.value, False)
-        if active is not None or self._parts is not None:
-            self._part(active)
-        self._call("graft_pages_reserve", np, ws.data_ptr(), ws.numel())
+        self._call("graft_pages_reserve", self._with(active), np, ws.data_ptr(), ws.numel())
 
     def fork(self, src, dst) -> None:
         """graft_pages_fork: sequence dst[i] shares the pages of src[i] ([n] int32 each)."""
@@ -297,10 +301,10 @@ class PagedCache:
         n = src.numel()
         sp = self._need(src, "src", torch.int32, (n,))
         dp = self._need(dst, "dst", torch.int32, (n,))
-        self._call("graft_pages_fork", n, sp, dp)
+        self._call("graft_pages_fork", self._c, n, sp, dp)
 
     def free(self, seqs) -> None:
         """graft_pages_free: gives back the pages of sequences seqs [n] int32."""
         self._tables()
         n = seqs.numel()
-        self._call("graft_pages_free", n, self._need(seqs, "seqs", torch.int32, (n,)))
+        self._call("graft_pages_free", self._c, n, self._need(seqs, "seqs", torch.int32, (n,)))

@@ -99,17 +99,17 @@ class PagedVerifyStep:
         c, B, Kmax = self.cache, self.B, self.cfg.Kmax
         ready = inputs_ready if inputs_ready is not None else (lambda _: None)
         ready("tree")
-        on = self.active
-        c.reserve(self.rows, active=on)
+        on, part = self.active, c._with(self.active)
+        c.reserve(self.rows, active=part)
         gb.graft_build_tree(self.cfg, draft_logits, root_tok, M_succ, c.lengths, out=self.tree, status=self.status,
                             ws=self.ws_tree)
-        c.plan(self.q_start, B * Kmax, self.Hq, Kmax, tree=True, active=on)
+        c.plan(self.q_start, B * Kmax, self.Hq, Kmax, tree=True, active=part)
         pos, mask = self.tree["pos"].view(-1), self.tree["mask"].view(-1)
         q, o = self.Qr.view(B * Kmax, self.Hq, gb.HEAD_DIM), self.O.view(B * Kmax, self.Hq, gb.HEAD_DIM)
         for layer in range(self.n_layers):
             ready(layer)
             c.append(layer, Q[layer], K[layer], V[layer], self.q_start, inv_freq=self.inv_freq,
-                     interleaved=self.interleaved, positions=pos, factor=self.factor, out=q, active=on)
+                     interleaved=self.interleaved, positions=pos, factor=self.factor, out=q, active=part)
             c.attend(layer, q, self.scale, mask=mask, out=o)
             if attended is not None:
                 attended(layer, self.O)
@@ -126,7 +126,7 @@ class PagedVerifyStep:
         else:
             gb.graft_accept_compact(target_logits, *args, out=self.acc, status=self.status, ws=self.ws_acc)
         self.acc["acc_len"].mul_(on)
-        c.compact(self.acc["path"], self.acc["acc_len"], active=on)
+        c.compact(self.acc["path"], self.acc["acc_len"], active=part)
         if self.m_policy in ("tree", "both"):
             torch.where(on[:, None], self.tree["tok"], self._none, out=self._src)
             gb.graft_update_M(M_succ, M_cnt, self._src.view(-1), self.acc["argmax"].view(-1), status=self.status,
