@@ -243,6 +243,14 @@ def test_idle_slots(m_policy, captured):
     assert int(c.held[1]) == -(-(n + KMAX) // PAGE)
 
 
+def test_root_tokens_are_checked():
+    w = World(14)
+    inp = w.inputs()
+    for bad in (inp["root_tok"].long(), inp["root_tok"][:1]):
+        with pytest.raises(ValueError):
+            w.step.run(M_succ=w.M[0], M_cnt=w.M[1], **dict(inp, root_tok=bad))
+
+
 def test_all_slots_idle():
     w = World(13)
     c, st = w.cache, w.step
@@ -315,10 +323,6 @@ def test_refusals():
         PagedVerifyStep(w.cfg, w.cache, 7)
     with pytest.raises(ValueError):
         PagedVerifyStep(w.cfg, w.cache, 8, m_policy="none")
-    inp = w.inputs()
-    for bad in (inp["root_tok"].long(), inp["root_tok"][:1]):
-        with pytest.raises(ValueError):
-            w.step.run(M_succ=w.M[0], M_cnt=w.M[1], **dict(inp, root_tok=bad))
     bare = PagedCache(list(w.K), list(w.V), w.cache.block_table, w.cache.lengths)
     with pytest.raises(ValueError):
         PagedVerifyStep(w.cfg, bare, 8)
