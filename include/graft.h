@@ -561,9 +561,9 @@ int graft_rope_inv_freq(int rot_dim, double base, int scaling, double stretch, d
  * a = position * inv_freq[p] ([rot_dim / 2] f64, device):
  *   (x, y) -> factor * (x cos a - y sin a, x sin a + y cos a)
  * with (x, y) dims (p, p + rot_dim / 2), or (2p, 2p + 1) if interleaved; the
- * other dims are copied.  Angles are reduced exactly (64-bit fractions of a
- * turn), so far positions lose nothing; the rotation runs in 32 bits and is
- * rounded once.  rot_dim is a multiple of 16, 0 .. 128 (0: no rotation,
+ * other dims are copied.  Whole turns of an angle are dropped exactly (64-bit
+ * fractions of a turn; 2^-23 turns off at most at position 2^31 and frequency
+ * 1); the rotation runs in 32 bits and is rounded once.  rot_dim is a multiple of 16, 0 .. 128 (0: no rotation,
  * inv_freq may be NULL).  Hq = 0 (Q NULL) appends alone; Q_out may be Q.
  * lengths are not advanced.  A row whose cache row lies outside the block
  * table, or whose sequence starts before row 0, sets GRAFT_STATUS_LENGTH,
@@ -603,10 +603,14 @@ int graft_paged_plan(const GraftPagedCache* cache, int N, int Hq, const int32_t*
  *         where bit j of mask[row] is set (graft_build_tree's tree_mask for
  *         equal chunks of Kmax nodes)
  * O = softmax over the visible rows of scale * q.k, applied to V; query head
- * h reads KV head h / (Hq / Hkv), Hq / Hkv <= 64.  Scores and sums in 32 bits.  A row
- * that sees nothing gives zeros.  What a row does not see has no effect on
- * it, whatever it holds (NaN and infinities included).  Rows of O outside
- * every sequence are left as they were.
+ * h reads KV head h / (Hq / Hkv), Hq / Hkv <= 64.  Scores, sums and O in 32
+ * bits; the weights are rounded to the cache's type for the product with V,
+ * and summed as rounded.  A row that sees nothing gives zeros.  What a row
+ * does not see has no effect on it, whatever it holds (NaN and infinities
+ * included).  An infinite element of V that a row does see makes its output
+ * infinite, or NaN where the element's score lies so far below the row's
+ * largest (2^-126) that its weight vanishes.  Rows of O outside every sequence
+ * are left as they were.
  * plan: of the same cache sizes, N, Hq, max_new and tree (else
  * GRAFT_STATUS_PLAN); the lengths are the plan's.  ws:
  * graft_paged_attention_workspace_size bytes, ZERO-FILLED once by its owner
@@ -647,7 +651,8 @@ int graft_pages_compact(const GraftPagedCache* cache, int Kmax, const int32_t* p
  * are taken from the free pages (page_refs 0), the lowest first, in the order
  * of the sequences; a page there that is shared (page_refs > 1 when the call
  * starts) is replaced by a new one, and its rows below lengths[b] are copied
- * in every layer (copy on write).  If the free pages run out, that
+ * in every layer (copy on write; for each of its holders that reserves, the
+ * last one too, so that k of them need k free pages).  If the free pages run out, that
  * sequence and those after it that need pages set
  * GRAFT_STATUS_CACHE_OVERFLOW and are left as they were; so is, with
  * GRAFT_STATUS_LENGTH, one that would outgrow its block-table row or holds

@@ -5,8 +5,10 @@
 // Far positions: a's whole turns are dropped exactly.  w / 2 pi is held as a
 // 64-bit fraction of a turn, W = round(w / 2 pi * 2^64); position * W modulo
 // 2^64 is then the fraction of the turn itself (whole turns overflow away),
-// off by at most |position| / 2^65 turns plus w's own 64-bit rounding, and
-// its upper 32 bits go to sincospi.  No 64-bit floating product a position.
+// off by at most |position| (2^-65 + 2^-52 w / 2 pi) turns, the second term
+// the rounding of w / 2 pi: 2^-23 turns at position 2^31, as good as a 64-bit
+// product.  Its upper 32 bits go to sincospi.  No 64-bit floating product a
+// position.
 //
 // Memory bound: every element is read and written once.  A CTA takes one to
 // three rows with all their heads, so a row's cosines are computed once
