@@ -886,7 +886,7 @@ def test_rows_go_only_to_pages_that_a_sequence_holds_alone():
     for q, page in ((0, spare), (1, shared01)):
         assert torch.equal(s.K[0, page, 4:12], K[8 * q:8 * q + 8]) and torch.equal(s.V[0, page, 4:12], V[8 * q:8 * q + 8])
     K0 = s.K.clone()
-    path = s.i32(np.tile([0, 3, 5, -1], (6, 1)))
+    path = s.i32(np.tile([0, 3, 5, -1, -1, -1], (6, 1)))
     c.compact(path, s.i32([3, 3, 3, 3, 3, 0]))
     assert s.status() == b.STATUS_PAGE
     assert c.lengths.tolist() == [23, 23, 20, 20, 32, 0]
