@@ -578,6 +578,21 @@ int graft_rope_append(const GraftPagedCache* cache, void* K_pool, void* V_pool, 
                       graft_stream_t stream);
 
 /*
+ * graft_norm_rope_append — graft_rope_append for models that norm queries and
+ * keys head by head before they rotate them: every Q head (and K head) becomes
+ *   x_d <- w_d x_d / sqrt(mean_d x_d^2 + eps),  d < 128,
+ * then the rotation as above; 32 bits throughout, rounded once, behind the
+ * rotation.  q_weight, k_weight [128] f32 (device, one for all heads), either
+ * NULL: those heads are not normed (both NULL: graft_rope_append).  eps > 0 and finite.
+ * The squares are summed in 32 bits: elements stay below 2^60.
+ */
+int graft_norm_rope_append(const GraftPagedCache* cache, void* K_pool, void* V_pool, int N, int Hq,
+                           const int32_t* q_start, const int32_t* pos, const double* inv_freq, int rot_dim,
+                           int interleaved, float factor, const float* q_weight, const float* k_weight, float eps,
+                           const void* Q, int64_t q_stride, const void* K, int64_t k_stride, const void* V,
+                           int64_t v_stride, void* Q_out, int64_t qo_stride, graft_stream_t stream);
+
+/*
  * graft_paged_plan — splits a step's attention over the GPU, on the device,
  * from lengths and q_start as they are when it runs.  One plan serves every
  * layer's graft_paged_attention of the step.

@@ -5,14 +5,24 @@ target forward over the prefix cache, and the accepted nodes' rows join it.
 Here the cache lies in pages (pool [P][R][H][d], a row of page numbers a
 sequence); everything is written out in float64 from the definitions:
 
+    head norm   x -> w x / sqrt(mean x^2 + eps)
     rotary      (x, y) -> f (x cos a - y sin a, x sin a + y cos a),  a = position * w
-    attention   o = sum_j softmax_j(scale q . k_j) v_j over the rows a new row sees
+    attention   o = sum_j softmax_j(scale q . k_j) v_j over the rows a new row sees; with a window, those of the
+                last positions and the first tokens
     compaction  row L + t <- row L + path[t]
     pages       reference counts; the lowest free pages first; copy on write
 """
 from __future__ import annotations
 
 import numpy as np
+
+
+def head_norm(x: np.ndarray, weight, eps: float) -> np.ndarray:
+    """x [N][H][d]: every head divided by its root mean square, times weight [d] (None: x itself)."""
+    x = x.astype(np.float64)
+    if weight is None:
+        return x
+    return x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * np.asarray(weight, np.float64)
 
 
 def rope(x: np.ndarray, pos, inv_freq, interleaved: bool, factor: float) -> np.ndarray:
@@ -35,9 +45,12 @@ def rows(pool: np.ndarray, table_row, n: int) -> np.ndarray:
     return np.stack([pool[table_row[r // R], r % R] for r in range(n)]) if n else pool[0, :0]
 
 
-def attention(Q, K, V, table, lengths, q_start, scale: float, mask=None, absolute: bool = False):
+def attention(Q, K, V, table, lengths, q_start, scale: float, mask=None, absolute: bool = False, window=None,
+              first: int = 0):
     """Q [N][Hq][d], K, V pools.  Returns float64 [N][Hq][d], NaN in rows outside every sequence; with
-    ``absolute``, also the same weights applied to |V| (the scale of the sums, for error bounds)."""
+    ``absolute``, also the same weights applied to |V| (the scale of the sums, for error bounds).  With ``window``
+    a row sees what it saw without only at the last ``window`` positions, its own among them, and the ``first``
+    tokens'; in a tree the set bits of a row's mask, from the lowest, are positions L, L + 1, ..., the last its own."""
     N, Hq, d = Q.shape
     group = Hq // K.shape[2]
     out = np.full((N, Hq, d), np.nan)
@@ -46,8 +59,11 @@ def attention(Q, K, V, table, lengths, q_start, scale: float, mask=None, absolut
         lo, hi, L = int(q_start[b]), int(q_start[b + 1]), int(lengths[b])
         if hi == lo:
             continue
-        k = rows(K, table[b], L + hi - lo).astype(np.float64)
-        v = rows(V, table[b], L + hi - lo).astype(np.float64)
+        line = table[b]
+        if window is not None:  # (pages that no row sees may be gone)
+            line = [p if 0 <= p < len(K) else 0 for p in table[b]]
+        k = rows(K, line, L + hi - lo).astype(np.float64)
+        v = rows(V, line, L + hi - lo).astype(np.float64)
         n = hi - lo
         seen = np.ones((n, L + n), bool)
         for i in range(n):
@@ -56,6 +72,12 @@ def attention(Q, K, V, table, lengths, q_start, scale: float, mask=None, absolut
             else:
                 bits = int(mask[lo + i]) & (2**64 - 1)
                 seen[i, L:] = [bool(bits >> j & 1) for j in range(n)]
+            if window is not None:
+                at = np.arange(L + n)
+                if mask is not None:
+                    at[L:] = L + np.cumsum(seen[i, L:]) - 1
+                own = max(L, at[seen[i]].max(initial=L))
+                seen[i] &= (at > own - window) | (at < first)
         some = seen.any(1)
         for h in range(Hq):
             # (what a row does not see takes no part: its products may be NaN)

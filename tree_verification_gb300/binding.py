@@ -117,6 +117,8 @@ _SIGNATURES = {
                             ctypes.c_double, _P, _P],
     "graft_rope_append": [_P, _P, _P, _I, _I, _P, _P, _P, _I, _I, ctypes.c_float, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
                           _P],
+    "graft_norm_rope_append": [_P, _P, _P, _I, _I, _P, _P, _P, _I, _I, ctypes.c_float, _P, _P, ctypes.c_float, _P, _I64,
+                               _P, _I64, _P, _I64, _P, _I64, _P],
     "graft_paged_plan_size": [_P, _I, _I, _I, ctypes.POINTER(_SZ)],
     "graft_paged_plan": [_P, _I, _I, _P, _I, _I, _P, _SZ, _P],
     "graft_paged_attention_workspace_size": [_P, _I, _I, _I, ctypes.POINTER(_SZ)],

@@ -16,8 +16,16 @@
 // 16-byte chunks whose dims pair up) are issued before the CTA looks up the
 // sequences and pages, so the look-up's dependent reads run behind them; the
 // page's number is read while the cosines are computed.
+//
+// With norms (graft_norm_rope_append) a head's row is scaled first,
+//   x_d <- w_d x_d / sqrt(mean x^2 + eps):
+// the eight threads of a head hold its 128 elements already, so the sum of
+// their squares is 16 products and three shuffles a thread, and the scaled
+// elements go to the rotation in 32 bits: rounded once, and no byte more is
+// read or written than without the norms.
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -46,6 +54,8 @@ struct RopeArgs {
     int tokens;  // rows of a CTA
     bool inter;
     float factor;
+    const float* norm_w[2];  // weights of Q's and K's norms, null: not normed
+    float eps;
 };
 
 struct Place {
@@ -101,13 +111,51 @@ __device__ __forceinline__ uint32_t turn1(uint32_t a, float2 cs) {
     return E::down(x.x * cs.x - x.y * cs.y, x.x * cs.y + x.y * cs.x);
 }
 
+// A thread's 16 elements of a head scaled by its norm: r w_d x_d.  The head's eight threads are neighbours.
+template <int DT>
+__device__ __forceinline__ void norm_head(const uint4& x0, const uint4& x1, const float* w, float eps, float* f) {
+    using E = Elem<DT>;
+    const uint32_t* w0 = &x0.x;
+    const uint32_t* w1 = &x1.x;
+    float ss = 0.f;
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+        const float2 v = E::up(z < 4 ? w0[z] : w1[z - 4]);
+        f[2 * z] = v.x;
+        f[2 * z + 1] = v.y;
+        ss += v.x * v.x;
+        ss += v.y * v.y;
+    }
+    const unsigned mask = 0xffu << (threadIdx.x & 24);
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) ss += __shfl_xor_sync(mask, ss, d);
+    const float r = rsqrtf(ss * (1.f / HD) + eps);
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+        const float4 g = reinterpret_cast<const float4*>(w)[z];
+        f[4 * z] *= r * g.x;
+        f[4 * z + 1] *= r * g.y;
+        f[4 * z + 2] *= r * g.z;
+        f[4 * z + 3] *= r * g.w;
+    }
+}
+__device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) {
+    const float a = x * c - y * s;
+    y = x * s + y * c;
+    x = a;
+}
+
 // kAhead: heads that a thread reads at a time, the first ones before the look-up
-template <int DT, int kAhead>
+template <int DT, int kAhead, bool kNorm>
 __global__ void __launch_bounds__(kThreads, kResident)
 rope_append_kernel(const __grid_constant__ RopeArgs a) {
     __shared__ float2 s_cs[kTokens][HD / 2];
     __shared__ int64_t s_dst[kTokens];  // cache row in the pool, -1: not written
     __shared__ int s_live[kTokens], s_pos[kTokens];
+    // the norms' weights as the eight threads of a head take them: 16 each, four words apart so that a warp's reads
+    // meet no bank twice
+    constexpr int kWeightStep = 20;
+    __shared__ __align__(16) float s_w[kNorm ? 2 : 1][kNorm ? 8 * kWeightStep : 4];
     griddep_enter();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int t0 = blockIdx.x * a.tokens;
@@ -137,6 +185,15 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
         }
     };
     fetch(0, h_first);
+    if constexpr (kNorm) {
+        static_assert(kThreads == HD, "a weight a thread");
+        const int j = tid >> 4, e = tid & 15;
+        const bool half = j < rot_units && !a.inter;  // (as c0 and c1 of the head's j-th thread)
+        const int chunk = e < 8 ? (half ? j : 2 * j) : (half ? j + rot_units : 2 * j + 1);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (a.norm_w[k] != nullptr) s_w[k][j * kWeightStep + e] = a.norm_w[k][chunk * 8 + (e & 7)];
+    }
     // one warp a row; what the cosines need first, the page behind them
     int page_at = -1;  // entry of the block table
     int64_t r = 0;
@@ -202,7 +259,28 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
                 const int h = h0 + x * kStep;
                 if (h >= heads) continue;
                 uint4 x0 = buf[x][0], x1 = buf[x][1];
-                if (rotates && h < turned) {
+                const bool normed = kNorm && h < turned && a.norm_w[h < a.Hq ? 0 : 1] != nullptr;
+                if (normed) {
+                    using E = Elem<DT>;
+                    float f[16];
+                    norm_head<DT>(x0, x1, &s_w[kNorm && h >= a.Hq][kNorm ? i * kWeightStep : 0], a.eps, f);
+                    if (rotates && a.inter) {
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            turn_pair(f[4 * z], f[4 * z + 1], cs[z].x, cs[z].y);
+                            turn_pair(f[4 * z + 2], f[4 * z + 3], cs[z].z, cs[z].w);
+                        }
+                    } else if (rotates) {
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            turn_pair(f[2 * z], f[8 + 2 * z], cs[z].x, cs[z].y);
+                            turn_pair(f[2 * z + 1], f[9 + 2 * z], cs[z].z, cs[z].w);
+                        }
+                    }
+                    x0 = make_uint4(E::down(f[0], f[1]), E::down(f[2], f[3]), E::down(f[4], f[5]), E::down(f[6], f[7]));
+                    x1 = make_uint4(E::down(f[8], f[9]), E::down(f[10], f[11]), E::down(f[12], f[13]),
+                                    E::down(f[14], f[15]));
+                } else if (rotates && h < turned) {
                     uint32_t* w0 = &x0.x;
                     uint32_t* w1 = &x1.x;
                     if (a.inter) {
@@ -303,8 +381,21 @@ extern "C" int graft_rope_append(const GraftPagedCache* cache, void* K_pool, voi
                                  int interleaved, float factor, const void* Q, int64_t q_stride, const void* K,
                                  int64_t k_stride, const void* V, int64_t v_stride, void* Q_out, int64_t qo_stride,
                                  graft_stream_t stream) {
+    return graft_norm_rope_append(cache, K_pool, V_pool, N, Hq, q_start, pos, inv_freq, rot_dim, interleaved, factor,
+                                  nullptr, nullptr, 0.f, Q, q_stride, K, k_stride, V, v_stride, Q_out, qo_stride, stream);
+}
+
+extern "C" int graft_norm_rope_append(const GraftPagedCache* cache, void* K_pool, void* V_pool, int N, int Hq,
+                                      const int32_t* q_start, const int32_t* pos, const double* inv_freq, int rot_dim,
+                                      int interleaved, float factor, const float* q_weight, const float* k_weight,
+                                      float eps, const void* Q, int64_t q_stride, const void* K, int64_t k_stride,
+                                      const void* V, int64_t v_stride, void* Q_out, int64_t qo_stride,
+                                      graft_stream_t stream) {
     const int rc = check_cache(cache);
     if (rc != GRAFT_OK) return rc;
+    const bool norm = q_weight != nullptr || k_weight != nullptr;
+    if (norm && !(eps > 0.f && std::isfinite(eps))) return GRAFT_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(q_weight) | reinterpret_cast<uintptr_t>(k_weight)) & 3) return GRAFT_ERR_INVALID_ARG;
     if (N < 0 || Hq < 0) return GRAFT_ERR_INVALID_ARG;
     if (Hq > 8192) return GRAFT_ERR_UNSUPPORTED_SHAPE;
     if (rot_dim < 0 || rot_dim > HD || rot_dim % 16 != 0) return GRAFT_ERR_UNSUPPORTED_SHAPE;
@@ -341,6 +432,9 @@ extern "C" int graft_rope_append(const GraftPagedCache* cache, void* K_pool, voi
     a.page_shift = log2_exact(cache->page_rows);
     a.inter = interleaved != 0;
     a.factor = factor;
+    a.norm_w[0] = q_weight;
+    a.norm_w[1] = k_weight;
+    a.eps = eps;
     // As few rows a CTA as make one wave of CTAs, up to three; else two, which share a look-up (48 heads, one, two,
     // three rows: 64 rows 6.2, 8.2 us; 704 rows 7.5, 8.2; 1280 rows 9.1, 9.9 with three; 1600 to 2240 rows, a wave of
     // three, 11.1 to 13.7, with two 11.8 to 15.0; 2304 rows, past it, 16.5 with three, 14.9 with two).
@@ -349,9 +443,13 @@ extern "C" int graft_rope_append(const GraftPagedCache* cache, void* K_pool, voi
     const dim3 grid((unsigned)((N + a.tokens - 1) / a.tokens));
     // (a row's heads in one go where three or five a thread do; 4096 rows of 48 heads: 21.4 us, 23.9 with five)
     const bool three = Hq + 2 * cache->Hkv <= 3 * kStep;
-    const auto kernel = cache->dtype == GRAFT_BF16
-                            ? (three ? rope_append_kernel<GRAFT_BF16, 3> : rope_append_kernel<GRAFT_BF16, 5>)
-                            : (three ? rope_append_kernel<GRAFT_FP16, 3> : rope_append_kernel<GRAFT_FP16, 5>);
+    const auto pick = [&](auto dt) {
+        constexpr int D = decltype(dt)::value;
+        return norm ? (three ? rope_append_kernel<D, 3, true> : rope_append_kernel<D, 5, true>)
+                    : (three ? rope_append_kernel<D, 3, false> : rope_append_kernel<D, 5, false>);
+    };
+    const auto kernel = cache->dtype == GRAFT_BF16 ? pick(std::integral_constant<int, GRAFT_BF16>{})
+                                                   : pick(std::integral_constant<int, GRAFT_FP16>{});
     launch_pdl(kernel, grid, dim3(kThreads), 0, (cudaStream_t)stream, a);
     count_launches(1);
     return launch_status();

@@ -188,10 +188,12 @@ class PagedCache:
 
     # ------------------------------------------------------------------ calls
     def append(self, layer: int, Q, K, V, q_start, inv_freq=None, interleaved: bool = False, positions=None,
-               factor: float = 1.0, out=None, active=None):
+               factor: float = 1.0, out=None, active=None, q_norm=None, k_norm=None, eps: float = 1e-6):
         """graft_rope_append: rotates Q and K ([N][H][128], rows may be strided), writes K and V to their pages.
 
-        Returns the rotated Q (``out``, which may be Q itself).  Q may be None.  Without inv_freq nothing is rotated."""
+        Returns the rotated Q (``out``, which may be Q itself).  Q may be None.  Without inv_freq nothing is rotated.
+        ``q_norm`` and ``k_norm`` ([128] float32 weights, either may be None) norm the heads of Q and K first
+        (graft_norm_rope_append)."""
         layer = self._layer(layer)
         if not isinstance(K, torch.Tensor) or K.dim() != 3:
             raise ValueError("K must be [N][Hkv][128]")
@@ -214,8 +216,15 @@ class PagedCache:
         if inv_freq is not None:
             rot = 2 * inv_freq.numel()
             fp = self._need(inv_freq, "inv_freq", torch.float64, (rot // 2,))
-        self._call("graft_rope_append", self._with(active), self._kp[layer], self._vp[layer], N, Hq, starts, pos, fp, rot,
-                   1 if interleaved else 0, float(factor), qp, qs, kp, ks, vp, vs, op, os)
+        head = (self._kp[layer], self._vp[layer], N, Hq, starts, pos, fp, rot, 1 if interleaved else 0, float(factor))
+        if q_norm is None and k_norm is None:
+            self._call("graft_rope_append", self._with(active), *head, qp, qs, kp, ks, vp, vs, op, os)
+        else:
+            d = (gb.HEAD_DIM,)
+            qw = None if q_norm is None else self._need(q_norm, "q_norm", torch.float32, d)
+            kw = None if k_norm is None else self._need(k_norm, "k_norm", torch.float32, d)
+            self._call("graft_norm_rope_append", self._with(active), *head, qw, kw, float(eps), qp, qs, kp, ks, vp, vs,
+                       op, os)
         return out
 
     def plan(self, q_start, N: int, Hq: int, max_new: int, tree: bool = False, active=None) -> None:
