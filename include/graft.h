@@ -61,7 +61,13 @@ typedef struct CUstream_st* graft_stream_t;
 #define GRAFT_STATUS_WORKSPACE 32     /* a workspace's arrival counter was found not zeroed (graft_build_tree, graft_tree_attention, graft_paged_attention) */
 #define GRAFT_STATUS_PAGE 64          /* a page number outside the pool, or a page that no sequence holds, was read, or rows were due in a page that the sequence does not hold alone; it was skipped (read as zeros, not written) */
 #define GRAFT_STATUS_PLAN 128         /* a plan that was not made for the call's arguments; nothing was computed */
+#define GRAFT_STATUS_ROW 512          /* a row number outside the logits; its outputs are those of no row */
 #define GRAFT_STATUS_SEQUENCE 256     /* a sequence index out of range, named twice, or not empty where it has to be; it was skipped */
+
+/* Element types of calls that take more than one. */
+#define GRAFT_BF16 0
+#define GRAFT_FP16 1
+#define GRAFT_F32 2  /* graft_token_logprobs alone */
 
 /* Limits. */
 #define GRAFT_MAX_KMAX 64        /* tree nodes per request (one uint64 ancestor mask) */
@@ -69,6 +75,7 @@ typedef struct CUstream_st* graft_stream_t;
 #define GRAFT_MAX_TOPK 16        /* draft branching k */
 #define GRAFT_MAX_DEPTH 16       /* drafter calls D */
 #define GRAFT_MAX_W 32           /* successors per row of M */
+#define GRAFT_MAX_TOP_LOGPROBS 32 /* alternatives a row of graft_token_logprobs */
 #define GRAFT_HEAD_DIM 128       /* the only head size the attention kernel supports */
 
 /*
@@ -401,6 +408,41 @@ int graft_lm_head_sample(int N, int d_model, int V, const void* H, const void* W
                          int32_t* status, void* ws, size_t ws_bytes, graft_stream_t stream);
 
 /*
+ * graft_token_logprobs — what a server answers beside a token: its log
+ * probability under the target, the entropy of that law, the token's rank and
+ * the most likely alternatives (Graft article, architecture paragraph: the
+ * emitted tokens follow the target's own distribution).
+ *
+ *   logits   n_logit_rows rows of V numbers of type dtype (GRAFT_BF16,
+ *            GRAFT_FP16 or GRAFT_F32), row_stride elements apart (>= V)
+ *   rows [N] i32, or NULL: the row of entry n; -1: none.  NULL: row n.  With
+ *            block > 0 it counts from row (n / block) * block and lies below
+ *            block: graft_accept_compact's path with block = Kmax
+ *   tokens [N] i32: the token of entry n; -1: none
+ * Outputs, for z = x / temperature, p = softmax(z):
+ *   logprob [N] f32   ln p(token); 0 where there is no token or no row
+ *   entropy [N] f32   -sum p ln p (may be NULL); 0 where there is no row
+ *   rank [N] i32      tokens of a larger logit, or the same at a lower id (may
+ *                     be NULL); -1 where there is no token or no row
+ *   top_id, top_logprob [N][top]   the `top` <= GRAFT_MAX_TOP_LOGPROBS largest
+ *                     logits' ids, largest first, lower ids first among equal
+ *                     ones, and their ln p; -1 and 0 where there is no row
+ * Ranks and ids go by the logits as given, exactly.  Logits may be -inf (such
+ * tokens have p = 0); NaN ranks with them.  A row with NaN or +inf, or of -inf
+ * alone, has no law: its logprob, entropy and top_logprob are NaN.  Sums in 32
+ * bits a thread, joined in 64; rounded once.  A token outside [0, V) sets
+ * GRAFT_STATUS_TOKEN_RANGE and counts as none, a row outside the logits (or
+ * the block) GRAFT_STATUS_ROW.  N <= 65535.  Workspace:
+ * graft_token_logprobs_workspace_size (need not be zeroed; depends on the
+ * current device's SM count).
+ */
+int graft_token_logprobs_workspace_size(int N, int V, int top, size_t* bytes);
+int graft_token_logprobs(int N, int V, int64_t n_logit_rows, int dtype, const void* logits, int64_t row_stride,
+                         const int32_t* rows, int block, const int32_t* tokens, float temperature, int top,
+                         float* logprob, float* entropy, int32_t* rank, int32_t* top_id, float* top_logprob,
+                         int32_t* status, void* ws, size_t ws_bytes, graft_stream_t stream);
+
+/*
  * graft_update_M — online update of the adjacency table from verified
  * pairs (Graft article, method paragraph, fourth point: M is updated
  * continuously from the verified tree's logits).
@@ -480,8 +522,6 @@ int graft_update_M_noalloc(int32_t* M_succ, int32_t* M_cnt, int V, int W, const 
  * attends over them under the tree mask (or causally: prompt chunks, single
  * tokens), graft_pages_compact keeps the accepted ones.
  */
-#define GRAFT_BF16 0
-#define GRAFT_FP16 1
 #define GRAFT_MAX_SEQS 4096      /* sequences (rows of the block table) */
 #define GRAFT_MAX_PAGE_ROWS 256  /* page rows: 16, 32, 64, 128 or 256 */
 

@@ -28,12 +28,14 @@ STATUS_WORKSPACE = 32
 STATUS_PAGE = 64
 STATUS_PLAN = 128
 STATUS_SEQUENCE = 256
+STATUS_ROW = 512
 EMPTY_TOKEN = -1
 
 MAX_KMAX = 64
 MAX_CHECKPOINTS = 4
 MAX_SEQS = 4096
 HEAD_DIM = 128
+MAX_TOP_LOGPROBS = 32
 
 
 class GraftConfig(ctypes.Structure):
@@ -107,6 +109,8 @@ _SIGNATURES = {
     "graft_lm_head_sample": [_I, _I, _I, _P, _P, _I, _P, ctypes.c_float, ctypes.c_uint64, _P, _P, _P, _SZ, _P],
     "graft_sample_tokens_workspace_size": [_I, _I, _I, ctypes.POINTER(_SZ)],
     "graft_sample_tokens": [_I, _I, _I, _P, _P, ctypes.c_float, ctypes.c_uint64, _P, _P, _SZ, _P],
+    "graft_token_logprobs_workspace_size": [_I, _I, _I, ctypes.POINTER(_SZ)],
+    "graft_token_logprobs": [_I, _I, _I64, _I, _P, _I64, _P, _I, _P, ctypes.c_float, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
     "graft_lm_head_argmax": [_I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P],
     "graft_update_M_workspace_size": [_I64, ctypes.POINTER(_SZ)],
     "graft_update_M": [_P, _P, _I, _I, _P, _P, _I64, _P, _P, _SZ, _P],
@@ -400,6 +404,56 @@ def graft_sample_tokens(target_logits, tree_pos, temperature: float, seed: int, 
                                      int(seed) & 0xFFFFFFFFFFFFFFFF, _ptr(sampled), _ptr(ws), nws, _stream(stream)),
            "graft_sample_tokens")
     return sampled
+
+
+LOGIT_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def graft_token_logprobs_workspace_size(N: int, V: int, top: int) -> int:
+    n = _SZ()
+    _check(lib().graft_token_logprobs_workspace_size(N, V, top, ctypes.byref(n)), "workspace size")
+    return n.value
+
+
+def graft_token_logprobs(logits, tokens, rows=None, block: int = 0, top: int = 0, temperature: float = 1.0,
+                         out: Optional[dict] = None, status=None, ws=None, stream=None) -> dict:
+    """Log probability, entropy and rank of tokens [N] under rows of logits [R][V] (float32, bfloat16 or float16; rows
+    may be strided), with the ``top`` most likely alternatives: dict(logprob, entropy [N] f32, rank [N] i32, top_id
+    [N][top] i32, top_logprob [N][top] f32).  ``rows`` ([N] int32, -1: none) names the entries' rows; with ``block``
+    they count from the entry's own block of that many (graft_accept_compact's path)."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be [R][V]")
+    if logits.dtype not in LOGIT_TYPES:
+        raise ValueError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    R, V = logits.shape
+    if not logits.is_cuda or (V > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be on a CUDA device, with contiguous rows")
+    stride = V if R <= 1 else logits.stride(0)
+    if stride < V:
+        raise ValueError("the rows of logits must not overlap")
+    dev, N = logits.device, tokens.numel()
+    _need(tokens, "tokens", torch.int32, (N,))
+    if rows is not None:
+        _need(rows, "rows", torch.int32, (N,))
+    if out is None:
+        f32, i32 = dict(dtype=torch.float32, device=dev), dict(dtype=torch.int32, device=dev)
+        out = dict(logprob=torch.empty(N, **f32), entropy=torch.empty(N, **f32), rank=torch.empty(N, **i32),
+                   top_id=torch.empty(N, top, **i32), top_logprob=torch.empty(N, top, **f32))
+    for name, dtype, shape in (("logprob", torch.float32, (N,)), ("entropy", torch.float32, (N,)),
+                               ("rank", torch.int32, (N,)), ("top_id", torch.int32, (N, top)),
+                               ("top_logprob", torch.float32, (N, top))):
+        _need(out[name], name, dtype, shape)
+    for name, t in (("tokens", tokens), ("rows", rows), ("status", status), ("ws", ws), *out.items()):
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, the logits' device")
+    with torch.cuda.device(dev):
+        ws, nws = _ws(graft_token_logprobs_workspace_size(N, V, top), dev, ws)
+        _check(lib().graft_token_logprobs(N, V, R, LOGIT_TYPES[logits.dtype], _ptr(logits), stride, _ptr(rows), block,
+                                          _ptr(tokens), float(temperature), top, _ptr(out["logprob"]),
+                                          _ptr(out["entropy"]), _ptr(out["rank"]), _ptr(out["top_id"]),
+                                          _ptr(out["top_logprob"]), _ptr(status), _ptr(ws), nws, _stream(stream)),
+               "graft_token_logprobs")
+    return out
 
 
 def graft_lm_head_sample(H, W_lm, tree_pos, temperature: float, seed: int, sampled=None, status=None, ws=None,
