@@ -430,7 +430,7 @@ int graft_lm_head_sample(int N, int d_model, int V, const void* H, const void* W
  * Ranks and ids go by the logits as given, exactly.  Logits may be -inf (such
  * tokens have p = 0); NaN ranks with them.  A row with NaN or +inf, or of -inf
  * alone, has no law: its logprob, entropy and top_logprob are NaN.  Sums in 32
- * bits a thread, joined in 64; rounded once.  A token outside [0, V) sets
+ * bits.  A token outside [0, V) sets
  * GRAFT_STATUS_TOKEN_RANGE and counts as none, a row outside the logits (or
  * the block) GRAFT_STATUS_ROW.  N <= 65535.  Workspace:
  * graft_token_logprobs_workspace_size (need not be zeroed; depends on the

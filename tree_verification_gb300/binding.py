@@ -415,6 +415,18 @@ def graft_token_logprobs_workspace_size(N: int, V: int, top: int) -> int:
     return n.value
 
 
+def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape, index: int) -> int:
+    """Checks a dense tensor on CUDA device ``index``; returns its address.  (The usual case comes first: a call checks
+    nine.)"""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on cuda:{index}, the logits' device")
+
+
+_logprob_sizes = {}
+
+
 def graft_token_logprobs(logits, tokens, rows=None, block: int = 0, top: int = 0, temperature: float = 1.0,
                          out: Optional[dict] = None, status=None, ws=None, stream=None) -> dict:
     """Log probability, entropy and rank of tokens [N] under rows of logits [R][V] (float32, bfloat16 or float16; rows
@@ -423,36 +435,57 @@ def graft_token_logprobs(logits, tokens, rows=None, block: int = 0, top: int = 0
     they count from the entry's own block of that many (graft_accept_compact's path)."""
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be [R][V]")
-    if logits.dtype not in LOGIT_TYPES:
+    code = LOGIT_TYPES.get(logits.dtype)
+    if code is None:
         raise ValueError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
     R, V = logits.shape
-    if not logits.is_cuda or (V > 1 and logits.stride(1) != 1):
+    stride, inner = logits.stride()
+    if not logits.is_cuda or (V > 1 and inner != 1):
         raise ValueError("logits must be on a CUDA device, with contiguous rows")
-    stride = V if R <= 1 else logits.stride(0)
+    if R <= 1:
+        stride = V  # (the stride of a single row means nothing)
     if stride < V:
         raise ValueError("the rows of logits must not overlap")
-    dev, N = logits.device, tokens.numel()
-    _need(tokens, "tokens", torch.int32, (N,))
-    if rows is not None:
-        _need(rows, "rows", torch.int32, (N,))
+    index, dev = logits.get_device(), logits.device
+    if not isinstance(tokens, torch.Tensor):
+        raise TypeError("tokens must be a tensor")
+    N = tokens.numel()
+    tp = _dense(tokens, "tokens", torch.int32, (N,), index)
+    rp = None if rows is None else _dense(rows, "rows", torch.int32, (N,), index)
+    sp = None if status is None else _dense(status, "status", torch.int32, status.shape, index)
+    key = (N, V, top, index)
+    nbytes = _logprob_sizes.get(key)
+    if nbytes is None:
+        with torch.cuda.device(index):
+            nbytes = graft_token_logprobs_workspace_size(N, V, top)
+        if len(_logprob_sizes) >= 4096:
+            _logprob_sizes.clear()
+        _logprob_sizes[key] = nbytes
+    f32, i32 = torch.float32, torch.int32
     if out is None:
-        f32, i32 = dict(dtype=torch.float32, device=dev), dict(dtype=torch.int32, device=dev)
-        out = dict(logprob=torch.empty(N, **f32), entropy=torch.empty(N, **f32), rank=torch.empty(N, **i32),
-                   top_id=torch.empty(N, top, **i32), top_logprob=torch.empty(N, top, **f32))
-    for name, dtype, shape in (("logprob", torch.float32, (N,)), ("entropy", torch.float32, (N,)),
-                               ("rank", torch.int32, (N,)), ("top_id", torch.int32, (N, top)),
-                               ("top_logprob", torch.float32, (N, top))):
-        _need(out[name], name, dtype, shape)
-    for name, t in (("tokens", tokens), ("rows", rows), ("status", status), ("ws", ws), *out.items()):
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, the logits' device")
-    with torch.cuda.device(dev):
-        ws, nws = _ws(graft_token_logprobs_workspace_size(N, V, top), dev, ws)
-        _check(lib().graft_token_logprobs(N, V, R, LOGIT_TYPES[logits.dtype], _ptr(logits), stride, _ptr(rows), block,
-                                          _ptr(tokens), float(temperature), top, _ptr(out["logprob"]),
-                                          _ptr(out["entropy"]), _ptr(out["rank"]), _ptr(out["top_id"]),
-                                          _ptr(out["top_logprob"]), _ptr(status), _ptr(ws), nws, _stream(stream)),
-               "graft_token_logprobs")
+        new = torch.empty
+        out = dict(logprob=new(N, dtype=f32, device=dev), entropy=new(N, dtype=f32, device=dev),
+                   rank=new(N, dtype=i32, device=dev), top_id=new((N, top), dtype=i32, device=dev),
+                   top_logprob=new((N, top), dtype=f32, device=dev))
+        op = [t.data_ptr() for t in out.values()]
+    else:
+        op = [_dense(out[name], name, dtype, shape, index)
+              for name, dtype, shape in (("logprob", f32, (N,)), ("entropy", f32, (N,)), ("rank", i32, (N,)),
+                                         ("top_id", i32, (N, top)), ("top_logprob", f32, (N, top)))]
+    if ws is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if ws.numel() < nbytes:
+        raise ValueError("workspace too small")
+    wp = _dense(ws, "ws", torch.uint8, ws.shape, index)
+    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    args = (N, V, R, code, logits.data_ptr(), stride, rp, block, tp, float(temperature), top, *op, sp, wp, ws.numel(), st)
+    if torch._C._cuda_getDevice() == index:
+        rc = lib().graft_token_logprobs(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = lib().graft_token_logprobs(*args)
+    if rc:
+        _check(rc, "graft_token_logprobs")
     return out
 
 

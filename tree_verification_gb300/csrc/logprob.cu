@@ -5,18 +5,20 @@
 //   rank(v) = #{x > x_v} + #{x = x_v at lower ids},  the top k by (x descending, id ascending).
 //
 // HBM bound: every logit of the rows asked for is read once (4 or 2 bytes) and costs about ten instructions.
-// logprob_part_kernel lays the rows' chunks (kVecs x 16 bytes a thread) side by side and gives every CTA an even
-// run of them, so all end together whatever the number of rows; the next chunk's loads are in flight while one is
-// worked on.  A thread keeps its own maximum and sums over its run's part of a row (one pass, no CTA barrier for
-// them); logprob_join_kernel adds up the pieces of each row, in their order, in 64 bits.
+// logprob_part_kernel lays the rows' chunks (kVecs x 16 bytes a thread) side by side and gives every team of threads
+// an even run of them, so all end together whatever the number of rows; the next chunk's loads are in flight while
+// one is worked on.  A thread keeps its own maximum and sums over its run's part of a row (one pass, no barrier for
+// them).  A team is a CTA; where rows are short (kShort), a warp that takes whole rows, without barriers.
+// logprob_join_kernel adds up the pieces of rows that a run's edges cut, in their order.
 //
-// Top alternatives: a CTA holds the best k of its part of the row so far, in one warp's registers.  Until
-// the list is full a chunk's threshold is a value that at least k of the threads' maxima reach; then logits have to
-// pass the k-th best.  What passes goes to a buffer in shared memory and is merged
-// when the buffer fills or the part ends: a sort of 32 by one warp.  Where more pass than the buffer holds (long
-// runs of equal or rising logits) the chunk's best are drawn one by one instead.
+// Top alternatives cost the pass nothing but one store a thread and chunk, the chunk's largest of the thread's
+// logits.  Once a segment (kSeg chunks, or a row's end) a threshold is taken that at least k of the threads' largest
+// reach; the few chunks of the few threads above it are read once more, what passes goes to a buffer in shared memory
+// and one warp sorts it into the best so far.  Where more pass than the buffer holds (long runs of equal or of rising
+// logits), the segment is gone through chunk by chunk instead.
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -27,26 +29,39 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kVecs = 4;       // 16-byte loads a thread and chunk
+constexpr int kVecs = 4;       // 16-byte pieces of a chunk a thread
+constexpr int kStages = 3;     // chunks in shared memory: one worked on, the others on their way
 constexpr int kResident = 3;   // CTAs an SM
-constexpr int kCap = 512;      // candidates held
-constexpr int kMerge = 64;     // candidates that wait for a merge at most
-constexpr int kMaxRows = 1024; // rows of a CTA's run at most
+constexpr int kSeg = 40;       // chunks of a segment
+constexpr int kMaxRows = 160;  // rows of a CTA's runs at most
+constexpr int kShort = 4096;   // logits of a row that a warp takes
+constexpr int kRing = kStages * kVecs * kThreads * 16;
 constexpr float kFloor = -150.f;  // log2 of a weight that is zero in 32 bits
+constexpr float kSlack = 16.f;    // log2 of the largest weight before the sums are moved to a new maximum
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 template <int DT>
 constexpr int kElems = DT == GRAFT_F32 ? 4 : 8;  // of 16 bytes
 
 struct Args {
     const char* logits;
+    const char* logits_end;
     int64_t stride;  // bytes
     const int32_t* rows;
     const int32_t* tokens;
     int64_t R;
     int N, V, block, top, chunks;  // chunks of a row
     int ctas;
-    float c1;           // log2(e) / T
-    double inv_T;
+    float c1;     // log2(e) / T
+    float inv_T;
     float* logprob;
     float* entropy;
     int32_t* rank;
@@ -60,15 +75,25 @@ struct Args {
     uint64_t* keys;     // [N + ctas][top]
 };
 
-// Units of `units` that CTA k of `ctas` takes: [first(k), first(k + 1)).
-__device__ __forceinline__ int64_t first_of(int64_t units, int ctas, int k) {
-    const int64_t each = units / ctas, left = units % ctas;
-    return each * k + (k < left ? k : left);
+// (32-bit where it fits: a 64-bit division takes a hundred instructions)
+__device__ __forceinline__ int64_t quotient(int64_t x, int y) {
+    return ((uint64_t)x >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
-__device__ __forceinline__ int cta_of(int64_t units, int ctas, int64_t u) {
-    const int64_t each = units / ctas, left = units % ctas, big = left * (each + 1);
-    return (int)(u < big ? u / (each + 1) : left + (u - big) / each);
-}
+// How `units` are shared out: part k of `parts` takes [first(k), first(k + 1)).
+struct Shares {
+    int64_t each;
+    int left, parts;
+    __device__ __forceinline__ Shares(int64_t units, int64_t most) {
+        parts = (int)(units < most ? units : most);
+        each = parts > 0 ? quotient(units, parts) : 0;
+        left = (int)(units - each * parts);
+    }
+    __device__ __forceinline__ int64_t first(int k) const { return each * k + (k < left ? k : left); }
+    __device__ __forceinline__ int of(int64_t u) const {
+        const int64_t big = left * (each + 1);
+        return (int)(u < big ? quotient(u, (int)(each + 1)) : left + quotient(u - big, (int)each));
+    }
+};
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -127,370 +152,555 @@ __device__ __forceinline__ float sort_values(float v, int lane) {
     return v;
 }
 
-// Maximum and sums of two parts of a row: t and s of the lower maximum are moved to the higher one.
-__device__ __forceinline__ void add_part(float& m, float& s, float& t, float m2, float s2, float t2, float c1) {
-    if (m2 == -INFINITY) {  // (nothing but -inf there; NaN sums are kept)
-        s += s2;
-        t += t2;
-        return;
+// Maxima, sums and counts (m, s, t, n) of kLanes neighbouring lanes added up: the sums are moved to the largest maximum.
+template <int kLanes>
+__device__ __forceinline__ void add_lanes(float4& v, float c1) {
+    float m = v.x;
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    // (a lane of -inf alone has sums of zero, or NaN)
+    const float d = v.x == -INFINITY ? 0.f : (v.x - m) * c1, f = ex2(d);
+    v.z = f * (v.z + max_nan(d, kFloor) * v.y);
+    v.y *= f;
+    v.x = m;
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1) {
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
+        v.z += __shfl_xor_sync(0xffffffffu, v.z, d);
+        v.w += __shfl_xor_sync(0xffffffffu, v.w, d);
     }
-    if (m == -INFINITY) {
-        s += s2;
-        t += t2;
-        m = m2;
-        return;
-    }
-    const float hi = fmaxf(m, m2), d1 = (m - hi) * c1, d2 = (m2 - hi) * c1;
-    const float f1 = ex2(d1), f2 = ex2(d2);
-    t = f1 * (t + max_nan(d1, kFloor) * s) + f2 * (t2 + max_nan(d2, kFloor) * s2);
-    s = f1 * s + f2 * s2;
-    m = hi;
 }
 
+// A pair of logits in 32 bits.
 template <int DT>
-__device__ __forceinline__ float element(const uint4& w, int e) {
+__device__ __forceinline__ float2 pair(const uint4& w, int i) {
     const uint32_t* p = &w.x;
-    if (DT == GRAFT_F32) return __uint_as_float(p[e]);
-    const uint32_t x = p[e >> 1];
-    if (DT == GRAFT_BF16) return __uint_as_float((e & 1) ? x & 0xffff0000u : x << 16);
-    const unsigned short h = (unsigned short)((e & 1) ? x >> 16 : x);
-    return __half2float(__ushort_as_half(h));
+    if (DT == GRAFT_F32) return make_float2(__uint_as_float(p[2 * i]), __uint_as_float(p[2 * i + 1]));
+    const uint32_t x = p[i];
+    if (DT == GRAFT_BF16) return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+template <int DT>
+__device__ __forceinline__ float load_logit(const char* row, int id) {
+    if (DT == GRAFT_F32) return reinterpret_cast<const float*>(row)[id];
+    const unsigned short h = reinterpret_cast<const unsigned short*>(row)[id];
+    return DT == GRAFT_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+}
+// The largest of 16 bytes of logits (NaN aside).
+template <int DT>
+__device__ __forceinline__ float largest(const uint4& w) {
+    if (DT == GRAFT_F32)
+        return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+    if (DT == GRAFT_BF16) {
+        const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&w.x);
+        const float2 m = __bfloat1622float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
+        return fmaxf(m.x, m.y);
+    }
+    const __half2* p = reinterpret_cast<const __half2*>(&w.x);
+    const float2 m = __half22float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
+    return fmaxf(m.x, m.y);
+}
+// The largest number of the logits' type below x (of -inf: itself).
+template <int DT>
+__device__ __forceinline__ float below(float x) {
+    const uint32_t step = DT == GRAFT_BF16 ? 0x10000u : 1u;
+    const uint32_t b = __float_as_uint(x);
+    if (DT == GRAFT_FP16) {
+        const uint32_t h = __half_as_ushort(__float2half_rn(x));
+        const uint32_t p = h == 0u || h == 0x8000u ? 0x8001u : h >> 15 ? (h == 0xfc00u ? h : h + 1) : h - 1;
+        return __half2float(__ushort_as_half((unsigned short)p));
+    }
+    if (x == 0.f) return __uint_as_float(0x80000000u + step);
+    if (x == -INFINITY) return x;
+    return __uint_as_float(b >> 31 ? b + step : b - step);
+}
+// How many of 16 bytes of logits lie above x, added to n.
+template <int DT>
+__device__ __forceinline__ void count_above(const uint4& w, float x, float2& n) {
+#pragma unroll
+    for (int e = 0; e < kElems<DT> / 2; ++e) {
+        const float2 v = pair<DT>(w, e);
+        float2 y;
+        asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(y.x) : "f"(v.x), "f"(x));
+        asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(y.y) : "f"(v.y), "f"(x));
+        n = __fadd2_rn(n, y);
+    }
 }
 
+// 16 bytes of logits from id on that reach past the row's ends: -inf there.  `have`: they were read; else they reach
+// past the logits' own ends and are read one by one.  (Out of line: rare, and long.)
 template <int DT>
+__device__ __noinline__ uint4 ragged(uint4 v, bool have, const char* row, int id, int V) {
+    uint32_t* w = &v.x;
+#pragma unroll
+    for (int e = 0; e < kElems<DT>; ++e) {
+        const bool in = id + e >= 0 && id + e < V;
+        if (DT == GRAFT_F32) {
+            if (!in) w[e] = 0xff800000u;
+            else if (!have) w[e] = reinterpret_cast<const uint32_t*>(row)[id + e];
+        } else {
+            uint32_t h = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+            if (!in) h = DT == GRAFT_BF16 ? 0xff80u : 0xfc00u;
+            else if (!have) h = reinterpret_cast<const unsigned short*>(row)[id + e];
+            w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | h << 16 : (w[e >> 1] & 0xffff0000u) | h;
+        }
+    }
+    return v;
+}
+// How many of 16 bytes of logits from id on go ahead of token tok, of logit x.
+template <int DT>
+__device__ __noinline__ float count_ahead(uint4 w, int id, int tok, float x) {
+    float n = 0.f;
+#pragma unroll
+    for (int e = 0; e < kElems<DT>; ++e) {
+        const float2 p = pair<DT>(w, e / 2);
+        const float v = (e & 1) ? p.y : p.x;
+        n += v > x || (v == x && id + e >= 0 && id + e < tok) ? 1.f : 0.f;
+    }
+    return n;
+}
+
+// The outputs of entry n, by a warp: its token's logit (ok: it has one), the sums of the weights relative to m, the
+// better tokens' number, a key a lane.
+__device__ __forceinline__ void finish(const Args& a, int n, bool ok, float given, float m, float s, float t, int cnt,
+                                       uint64_t list) {
+    const int lane = threadIdx.x & 31;
+    // a row of -inf alone has no law, nor has one with NaN or +inf: NaN
+    const float ln_s = m == -INFINITY ? NAN : logf(s);
+    auto logp = [&](float x) -> float { return (x - m) * a.inv_T - ln_s; };
+    if (lane == 0) {
+        a.logprob[n] = ok ? logp(given) : 0.f;
+        if (a.entropy != nullptr) a.entropy[n] = ln_s - 0.693147181f * (t / s);
+        if (a.rank != nullptr) a.rank[n] = ok ? cnt : -1;
+    }
+    if (a.top > 0) {
+        int id = key_id(list);
+        float lp = list != 0 ? logp(key_value(list)) : 0.f;
+        const unsigned have = __ballot_sync(0xffffffffu, list != 0);
+        const int known = __popc(have);
+        if (known < a.top) {
+            // Fewer tokens above -inf than places: all of them are listed, the lowest other ids follow.
+            uint64_t used = 0;
+            for (int k = 0; k < known; ++k) {
+                const int x = __shfl_sync(0xffffffffu, id, k);
+                if (x < 64) used |= 1ull << x;
+            }
+            if (lane >= known) {
+                int skip = lane - known;
+                id = 0;
+                while ((used >> id & 1) || skip-- > 0) ++id;
+                lp = isnan(ln_s) ? NAN : -INFINITY;
+            }
+        }
+        if (lane < a.top) {
+            a.top_id[(int64_t)n * a.top + lane] = id;
+            a.top_logprob[(int64_t)n * a.top + lane] = lp;
+        }
+    }
+}
+
+template <int DT, bool kWarpTeam>
 __global__ void __launch_bounds__(kThreads, kResident)
 logprob_part_kernel(const __grid_constant__ Args a) {
     constexpr int E = kElems<DT>;
     constexpr int kBytes = DT == GRAFT_F32 ? 4 : 2;
-    __shared__ int s_entry[kMaxRows], s_row[kMaxRows], s_tok[kMaxRows];
-    __shared__ uint64_t s_cand[kCap];
-    // Candidates of a chunk are counted in one of three places in turn: the one after next is cleared behind a
-    // chunk's barrier, when all have read it and none adds to it as yet.
-    __shared__ int s_n[3], s_scan[kWarps];
-    __shared__ float s_tau, s_red[kWarps][3], s_reach[32];
-    __shared__ int s_cnt[kWarps];
+    constexpr int kTeams = kWarpTeam ? kWarps : 1;       // of a CTA
+    constexpr int kTeam = kThreads / kTeams;             // threads of a team
+    constexpr int kMaxChunks = kWarpTeam ? kShort / (32 * kVecs * 4) + 1 : kSeg;
+    extern __shared__ __align__(16) unsigned char s_ring[];  // [stage][piece][thread] 16 bytes
+    __shared__ int s_entry[kMaxRows], s_tok[kMaxRows];
+    __shared__ const char* s_row[kMaxRows];
+    __shared__ float2 s_xt[kMaxRows];  // the given token's logit, and the largest number below it
+    constexpr int kCap = kWarpTeam ? 1024 : 256;
+    __shared__ unsigned short s_max[kMaxChunks][kThreads];  // a segment's largest, by chunk and thread: upper bf16 bounds
+    __shared__ uint64_t s_cand[kCap];  // candidates
+    __shared__ int s_n[kTeams][2], s_scan[kWarps];
+    __shared__ float s_kth[kTeams];      // the list's last, -inf: it is not full
+    __shared__ float s_reach[32];
+    __shared__ float4 s_red[2][kWarps];  // the warps' sums at a part's end, by its parity
     __shared__ uint64_t s_best[kWarps];
     griddep_enter();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
     // ---- which rows
-    auto row_of = [&](int n) -> int64_t {  // of entry n, -1: none
-        if (a.rows == nullptr) return n;
-        const int64_t r = a.rows[n];
+    auto row_at = [&](int n, int64_t r) -> int64_t {  // of entry n whose row is given as r, -1: none
         if (r < 0) return -1;
         const int64_t at = a.block > 0 ? (int64_t)(n / a.block) * a.block + r : r;
         return (a.block > 0 && r >= a.block) || at >= a.R ? -1 : at;
     };
-    int n_rows = a.N, mine = 0, before = 0, e0 = 0, e1 = 0;
-    if (a.rows != nullptr) {
-        const int each = (a.N + kThreads - 1) / kThreads;
-        e0 = min(tid * each, a.N);
-        e1 = min(e0 + each, a.N);
-        for (int n = e0; n < e1; ++n) {
-            const bool ok = row_of(n) >= 0;
-            mine += ok;
-            if (!ok && cta == 0 && a.rows[n] != -1) flag_status(a.status, GRAFT_STATUS_ROW);
-        }
-        int x = mine;
+    // With `rows`, a thread looks at kLook entries side by side (again for every kThreads x kLook of them); `seen`
+    // entries before it have a row.  each(n, row, rank of the row).
+    constexpr int kLook = 16;
+    int n_rows = a.N;
+    int32_t given[kLook];
+    auto look = [&](int n0) {  // reads the entries; how many before the thread's have rows, and how many do in all
+        const int first = n0 + tid * kLook;
+#pragma unroll
+        for (int x = 0; x < kLook; ++x) given[x] = first + x < a.N ? a.rows[first + x] : -1;
+        int mine = 0;
+#pragma unroll
+        for (int x = 0; x < kLook; ++x) mine += row_at(first + x, given[x]) >= 0;
+        int up = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += y;
+            const int y = __shfl_up_sync(0xffffffffu, up, d);
+            if (lane >= d) up += y;
         }
-        if (lane == 31) s_scan[warp] = x;
         __syncthreads();
-        n_rows = 0;
+        if (lane == 31) s_scan[warp] = up;
+        __syncthreads();
+        int before = up - mine, all = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            if (w == warp) before = n_rows + x - mine;
-            n_rows += s_scan[w];
+            if (w < warp) before += s_scan[w];
+            all += s_scan[w];
         }
-        // entries without a row
-        for (int n = cta; n < a.N; n += gridDim.x) {
-            if (row_of(n) >= 0) continue;
-            if (tid == 0) {
+        return make_int2(before, all);
+    };
+    int2 seen = make_int2(0, 0);
+    if (a.rows != nullptr) {
+        n_rows = 0;
+        for (int n0 = 0; n0 < a.N; n0 += kThreads * kLook) {
+            seen = look(n0);
+            n_rows += seen.y;
+            // entries without a row: every CTA sees to every gridDim-th
+            const int first = n0 + tid * kLook, skip = (int)gridDim.x - 1 - (first + (int)gridDim.x - 1 - cta) % (int)gridDim.x;
+#pragma unroll
+            for (int x = 0; x < kLook; ++x) {
+                const int n = first + x;
+                if (n >= a.N || row_at(n, given[x]) >= 0) continue;
+                if (given[x] != -1 && cta == 0) flag_status(a.status, GRAFT_STATUS_ROW);
+                if (x < skip || (x - skip) % (int)gridDim.x != 0) continue;
                 a.logprob[n] = 0.f;
                 if (a.entropy != nullptr) a.entropy[n] = 0.f;
                 if (a.rank != nullptr) a.rank[n] = -1;
-            }
-            if (tid < a.top) {
-                a.top_id[(int64_t)n * a.top + tid] = -1;
-                a.top_logprob[(int64_t)n * a.top + tid] = 0.f;
+                for (int k = 0; k < a.top; ++k) {
+                    a.top_id[(int64_t)n * a.top + k] = -1;
+                    a.top_logprob[(int64_t)n * a.top + k] = 0.f;
+                }
             }
         }
     }
     if (cta == 0 && tid == 0) *a.n_rows = n_rows;
-    const int64_t units = (int64_t)n_rows * a.chunks;
-    const int ctas = (int)(units < gridDim.x ? units : gridDim.x);
-    if (cta >= ctas) return;
-    const int64_t u0 = first_of(units, ctas, cta), u1 = first_of(units, ctas, cta + 1);
-    const int r0 = (int)(u0 / a.chunks), r1 = (int)((u1 - 1) / a.chunks);
-    auto take = [&](int r, int n) {
+    // The teams' runs: units of a chunk, or of a row where a warp takes it whole.
+    const int per_row = kWarpTeam ? 1 : a.chunks;
+    const Shares shares((int64_t)n_rows * per_row, (int64_t)gridDim.x * kTeams);
+    const int teams = shares.parts, t_first = cta * kTeams;  // the CTA's first team
+    if (t_first >= teams) return;
+    const int64_t cta_u0 = shares.first(t_first), cta_u1 = shares.first(min(t_first + kTeams, teams));
+    const int cta_r0 = (int)quotient(cta_u0, per_row), cta_r1 = (int)quotient(cta_u1 - 1, per_row);
+    auto take = [&](int r, int n, int64_t at) {
         const int tok = a.tokens[n];
-        s_entry[r - r0] = n;
-        s_row[r - r0] = (int)row_of(n);
+        const char* row = a.logits + at * a.stride;
         const bool ok = tok >= 0 && tok < a.V;
-        s_tok[r - r0] = ok ? tok : -1;
+        s_entry[r - cta_r0] = n;
+        s_row[r - cta_r0] = row;
+        s_tok[r - cta_r0] = ok ? tok : -1;
+        const float x = ok ? load_logit<DT>(row, tok) : INFINITY;
+        s_xt[r - cta_r0] = make_float2(x, below<DT>(x));
         if (!ok && tok != -1) flag_status(a.status, GRAFT_STATUS_TOKEN_RANGE);
     };
     if (a.rows == nullptr) {
-        for (int r = r0 + tid; r <= r1; r += kThreads) take(r, r);
+        for (int r = cta_r0 + tid; r <= cta_r1; r += kThreads) take(r, r, r);
     } else {
-        for (int n = e0, r = before; n < e1; ++n)
-            if (row_of(n) >= 0) {
-                if (r >= r0 && r <= r1) take(r, n);
+        for (int n0 = 0, r0 = 0; n0 < a.N; n0 += kThreads * kLook) {
+            if (a.N > kThreads * kLook) seen = look(n0);  // (else they are at hand)
+            int r = r0 + seen.x;
+#pragma unroll
+            for (int x = 0; x < kLook; ++x) {
+                const int n = n0 + tid * kLook + x;
+                const int64_t at = row_at(n, given[x]);
+                if (at < 0) continue;
+                if (r >= cta_r0 && r <= cta_r1) take(r, n, at);
                 ++r;
             }
+            r0 += seen.y;
+        }
     }
-    if (tid < 3) s_n[tid] = 0;
+    if (tid < 2 * kTeams) s_n[tid >> 1][tid & 1] = 0;
     __syncthreads();
+    const int team = kWarpTeam ? warp : 0;
+    if (t_first + team >= teams) return;  // (warps alone from here on)
+    const int ttid = kWarpTeam ? lane : tid;
+    auto sync = [&]() {
+        if (kWarpTeam) __syncwarp();
+        else __syncthreads();
+    };
+    constexpr int kTeamCap = kCap / kTeams;
+    uint64_t* cand = s_cand + team * kTeamCap;
 
     // ---- the run: chunk c of row j of the list
-    int j = 0, c = (int)(u0 - (int64_t)r0 * a.chunks);
-    auto start_of = [&](int j, int& off) -> const char* {  // 16-byte aligned, `off` elements before the row
-        const char* p = a.logits + (int64_t)s_row[j] * a.stride;
-        const uintptr_t x = reinterpret_cast<uintptr_t>(p);
-        off = (int)(x & 15) / kBytes;
-        return reinterpret_cast<const char*>(x & ~(uintptr_t)15);
+    const int64_t u0 = shares.first(t_first + team);
+    int left = (int)(shares.first(t_first + team + 1) - u0) * (kWarpTeam ? a.chunks : 1);  // chunks
+    const int row0 = (int)quotient(u0, per_row);
+    int j = row0 - cta_r0, c = (int)(u0 - (int64_t)row0 * per_row);
+    constexpr int kChunk = kVecs * kTeam * E;  // logits
+    auto offset_of = [&](const char* row) { return (int)(reinterpret_cast<uintptr_t>(row) & 15) / kBytes; };
+    // A row's chunks start at the 16 bytes that its first logit lies in.
+    auto start_of = [&](const char* row) {
+        return reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15);
     };
-    auto fetch = [&](int j, int c, uint4* buf) {
-        int off;
-        const char* p = start_of(j, off);
+    auto inside = [&](int c, int off) { return (c > 0 || off == 0) && (c + 1) * kChunk - off <= a.V; };
+    // (what of other rows lies in a row's first and last 16 bytes may be read, what lies around the logits may not)
+    auto readable = [&](const char* p) { return p >= a.logits && p + 16 <= a.logits_end; };
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(s_ring)) + tid * 16;
+    constexpr uint32_t kStageBytes = kVecs * kThreads * 16;
+    int j_in = j, c_in = c, in = left;
+    uint32_t dst = ring;
+    const char* src = start_of(s_row[j]) + ((int64_t)c * (kVecs * kTeam) + ttid) * 16;
+    auto issue = [&]() {  // the next chunk's copies (a thread's own pieces: it waits for them alone)
+        if (in > 0) {
+            const int off = offset_of(s_row[j_in]);
+            if (inside(c_in, off)) {
 #pragma unroll
-        for (int x = 0; x < kVecs; ++x) {
-            const int g = (c * kVecs + x) * kThreads + tid;
-            const int id = g * E - off;
-            if (id >= 0 && id + E <= a.V) {
-                buf[x] = __ldcs(reinterpret_cast<const uint4*>(p) + g);
+                for (int x = 0; x < kVecs; ++x) cp_async16(dst + x * kThreads * 16, src + x * kTeam * 16);
             } else {
-                uint32_t* w = &buf[x].x;
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const bool in = id + e >= 0 && id + e < a.V;
-                    if (DT == GRAFT_F32) {
-                        w[e] = in ? reinterpret_cast<const uint32_t*>(p)[(int64_t)g * E + e] : 0xff800000u;
-                    } else {
-                        const uint32_t h = in ? reinterpret_cast<const unsigned short*>(p)[(int64_t)g * E + e]
-                                              : (DT == GRAFT_BF16 ? 0xff80u : 0xfc00u);
-                        w[e >> 1] = (e & 1) ? w[e >> 1] | h << 16 : h;
-                    }
-                }
+                const int id = (c_in * kVecs * kTeam + ttid) * E - off;
+#pragma unroll 1
+                for (int x = 0; x < kVecs; ++x)
+                    if (id + x * kTeam * E < a.V && readable(src + x * kTeam * 16))
+                        cp_async16(dst + x * kThreads * 16, src + x * kTeam * 16);
+            }
+            --in;
+            src += kVecs * kTeam * 16;
+            if (++c_in == a.chunks) {
+                c_in = 0;
+                ++j_in;
+                if (in > 0) src = start_of(s_row[j_in]) + ttid * 16;
             }
         }
+        dst = dst + kStageBytes == ring + kStages * kStageBytes ? ring : dst + kStageBytes;
+        cp_commit();
     };
-    auto given = [&](int j) -> float {
-        const int tok = s_tok[j];
-        if (tok < 0) return INFINITY;
-        const char* p = a.logits + (int64_t)s_row[j] * a.stride + (int64_t)tok * kBytes;
-        if (DT == GRAFT_F32) return *reinterpret_cast<const float*>(p);
-        const unsigned short h = *reinterpret_cast<const unsigned short*>(p);
-        return DT == GRAFT_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
-    };
-    uint4 cur[kVecs], nxt[kVecs];
-    fetch(j, c, cur);
-    float xt = given(j), xt_next = xt;
-    float m = -INFINITY, s = 0.f, t = 0.f;
-    int cnt = 0;
-    uint64_t list = 0;  // warp 0: the best so far, one a lane
-    float tau = -INFINITY;  // what later logits have to pass; -inf: fewer than k are listed
-    int waiting = 0;    // candidates in the buffer
-    int turn = 0;
-    for (int64_t u = u0; u < u1; ++u) {
-        int j2 = j, c2 = c + 1;
-        if (c2 == a.chunks) {
-            c2 = 0;
-            ++j2;
-        }
-        if (u + 1 < u1) {
-            fetch(j2, c2, nxt);
-            if (j2 != j) xt_next = given(j2);
-        }
-        int off;
-        start_of(j, off);
-        const int tok = s_tok[j];
-        const int id_first = (c * kVecs * kThreads + tid) * E - off;
-        auto id_of = [&](int x) { return id_first + x * kThreads * E; };
-        // ---- maximum, sums
-        float top = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < kStages - 1; ++x) issue();
+    int stage = 0;
+    float m = -INFINITY;
+    float2 s = make_float2(0.f, 0.f), t = s, cnt = s;
+    float seg_max = -INFINITY;
+    uint64_t list = 0;  // a team's first warp: the best so far, one a lane
+    int parity = 0, turn = 0, c_part = c, c_seg = c;  // the part's and the segment's first chunk
+    while (true) {
+        const int c2 = c + 1 == a.chunks ? 0 : c + 1;
+        const char* row = s_row[j];
+        const int off = offset_of(row), id0 = c * kChunk - off;  // the chunk's first logit
+        auto id_of = [&](int c, int x) { return ((c * kVecs + x) * kTeam + ttid) * E - off; };
+        issue();
+        cp_wait<kStages - 1>();
+        uint4 cur[kVecs];
 #pragma unroll
         for (int x = 0; x < kVecs; ++x)
+            cur[x] = *reinterpret_cast<const uint4*>(s_ring + ((stage * kVecs + x) * kThreads + tid) * 16);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        if (!inside(c, off)) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) top = fmaxf(top, element<DT>(cur[x], e));
-        if (top > m) {
+            for (int x = 0; x < kVecs; ++x) {
+                const int id = id_of(c, x);
+                if (id < 0 || id + E > a.V) cur[x] = ragged<DT>(cur[x], readable(row + (int64_t)id * kBytes), row, id, a.V);
+            }
+        }
+        // ---- maximum, sums
+        float top = largest<DT>(cur[0]);
+#pragma unroll
+        for (int x = 1; x < kVecs; ++x) top = fmaxf(top, largest<DT>(cur[x]));
+        top = fmaxf(top, -INFINITY);  // (of NaN alone: -inf)
+        // The sums are relative to a maximum that moves only when weights would pass 2^kSlack.
+        if (!((top - m) * a.c1 <= kSlack) && top > m) {
             if (m != -INFINITY) {
-                const float d = (m - top) * a.c1, f = ex2(d);
-                t = f * (t + max_nan(d, kFloor) * s);
-                s *= f;
+                const float d = (m - top) * a.c1, f = ex2(d), dd = max_nan(d, kFloor);
+                t.x = f * (t.x + dd * s.x);
+                t.y = f * (t.y + dd * s.y);
+                s.x *= f;
+                s.y *= f;
             }
             m = top;
         }
-        const float base = m == -INFINITY ? 0.f : m;
+        {
+            const float base = m == -INFINITY ? 0.f : -m;
+            const float2 base2 = make_float2(base, base), c12 = make_float2(a.c1, a.c1);
 #pragma unroll
-        for (int x = 0; x < kVecs; ++x)
+            for (int x = 0; x < kVecs; ++x)
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float d = max_nan((element<DT>(cur[x], e) - base) * a.c1, kFloor);
-                const float w = ex2(d);
-                s += w;
-                t += d * w;
-            }
-        // ---- tokens ahead of the given one
-        if (tok >= 0) {
-#pragma unroll
-            for (int x = 0; x < kVecs; ++x) {
-                const int id = id_of(x);
-                if (id > tok) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) cnt += element<DT>(cur[x], e) > xt;
-                } else if (id >= 0 && id + E <= tok) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) cnt += element<DT>(cur[x], e) >= xt;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float v = element<DT>(cur[x], e);
-                        cnt += v > xt || (v == xt && id + e >= 0 && id + e < tok);
-                    }
+                for (int e = 0; e < E / 2; ++e) {
+                    float2 d = __fmul2_rn(__fadd2_rn(pair<DT>(cur[x], e), base2), c12);
+                    d.x = max_nan(d.x, kFloor);
+                    d.y = max_nan(d.y, kFloor);
+                    const float2 w = make_float2(ex2(d.x), ex2(d.y));
+                    s = __fadd2_rn(s, w);
+                    t = __ffma2_rn(d, w, t);
                 }
+        }
+        // ---- tokens ahead of the given one
+        const int tok = s_tok[j];
+        if (tok >= 0 && a.rank != nullptr) {
+            const float2 xt = s_xt[j];
+            const bool ahead = id0 >= 0 && id0 + kChunk <= tok;
+            if (id0 > tok || (ahead && xt.x > -INFINITY)) {
+                const float x1 = ahead ? xt.y : xt.x;  // (equal ones at lower ids count)
+                // (a likely token has few ahead of it: most chunks have none)
+                if (__any_sync(0xffffffffu, top > x1)) {
+#pragma unroll
+                    for (int x = 0; x < kVecs; ++x) count_above<DT>(cur[x], x1, cnt);
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < kVecs; ++x) cnt.x += count_ahead<DT>(cur[x], id_of(c, x), tok, xt.x);
             }
         }
-        // ---- alternatives
-        const bool ends = c + 1 == a.chunks || u + 1 == u1;
         if (a.top > 0) {
-            const bool open = tau == -INFINITY;
-            if (open) {
-                // Reached by at least k threads' maxima: what 8 / 2^i warps reach 2^i ceil(k / 8) times each, for i up
-                // to 3 (short rows leave warps without logits), the largest of these.
-                const float v = sort_values(top, lane);
+            const uint32_t b = __float_as_uint(top);
+            s_max[c - c_seg][tid] = (unsigned short)((b >> 31 ? b : b + 0xffffu) >> 16);
+            seg_max = fmaxf(seg_max, top);
+        }
+        const bool ends = c2 == 0 || left == 1;  // the part's last chunk
+        if (ends) {
+            float4 v = make_float4(m, s.x + s.y, t.x + t.y, cnt.x + cnt.y);
+            add_lanes<32>(v, a.c1);
+            if (lane == 0) s_red[parity][warp] = v;
+            if (a.top == 0) sync();
+        }
+        // ---- alternatives
+        if (a.top > 0 && (ends || c - c_seg == kSeg - 1)) {
+            const float v = sort_values(seg_max, lane);
+            float tau;
+            if (kWarpTeam) {
+                tau = __shfl_sync(0xffffffffu, v, a.top - 1);
+            } else {
+                // Reached by at least k threads' largest: what 8 / 2^i warps reach 2^i ceil(k / 8) times each, for i
+                // up to 3 (short segments leave warps without logits), the largest of these.
                 const int each = (a.top + kWarps - 1) / kWarps;
                 const float q = __shfl_sync(0xffffffffu, v, min((each << (lane & 3)) - 1, 31));
                 if (lane < 4) s_reach[lane * kWarps + warp] = q;
                 __syncthreads();
                 const float r = s_reach[lane];  // of warp lane & 7, 2^(lane / 8) ceil(k / 8) times
-                int above = 0;
+                int ahead = 0;
 #pragma unroll
                 for (int d = 1; d < kWarps; ++d) {
                     const int o = (lane & 24) | ((lane + d) & 7);
                     const float w = __shfl_sync(0xffffffffu, r, o);
-                    above += w > r || (w == r && o < lane);
+                    ahead += w > r || (w == r && o < lane);
                 }
-                tau = above == (kWarps >> (lane >> 3)) - 1 ? r : -INFINITY;
+                tau = ahead == (kWarps >> (lane >> 3)) - 1 ? r : -INFINITY;
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) tau = fmaxf(tau, __shfl_xor_sync(0xffffffffu, tau, d));
             }
-            // (of equal logits the lower id goes first, so a full list's last has to be passed; a chunk's own threshold
-            // to be reached)
-            auto passes = [&](float v) { return open ? v >= tau && v > -INFINITY : v > tau; };
-            if (passes(top)) {
+            // (of equal logits the lower id goes first, so a full list's last has to be passed, the threshold reached)
+            float kth = c_seg == c_part ? -INFINITY : s_kth[team];
+            auto passes = [&](float v) { return v >= tau && v > kth; };
+            // Each thread takes its own chunks, so that a warp's reads go out together.
+            uint64_t hits = 0;
+            if (passes(seg_max)) {
+#pragma unroll 8
+                for (int x = 0; x <= c - c_seg; ++x)
+                    hits |= (uint64_t)passes(__uint_as_float((uint32_t)s_max[x][tid] << 16)) << x;
+            }
+            for (; __any_sync(0xffffffffu, hits != 0); hits &= hits - 1) {
+                if (hits == 0) continue;
+                const int cc = c_seg + __ffsll(hits) - 1;
+                uint4 again[kVecs];
 #pragma unroll
-                for (int x = 0; x < kVecs; ++x)
+                for (int x = 0; x < kVecs; ++x) {
+                    const int id = id_of(cc, x);
+                    again[x] = make_uint4(0, 0, 0, 0);
+                    if (id >= 0 && id + E <= a.V) again[x] = *reinterpret_cast<const uint4*>(row + (int64_t)id * kBytes);
+                    else again[x] = ragged<DT>(again[x], false, row, id, a.V);
+                }
+#pragma unroll
+                for (int x = 0; x < kVecs; ++x) {
+                    if (!passes(largest<DT>(again[x]))) continue;
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
-                        const float v = element<DT>(cur[x], e);
+                        const float2 p = pair<DT>(again[x], e / 2);
+                        const float v = (e & 1) ? p.y : p.x;
                         if (passes(v)) {
-                            const int at = waiting + atomicAdd(&s_n[turn], 1);
-                            if (at < kCap) s_cand[at] = key_of(v, id_of(x) + e);
+                            const int at = atomicAdd(&s_n[team][turn], 1);
+                            if (at < kTeamCap) cand[at] = key_of(v, id_of(cc, x) + e);
                         }
                     }
+                }
             }
-            __syncthreads();
-            int n = waiting + s_n[turn];
-            const int after = turn == 0 ? 2 : turn - 1;  // (the place after next)
-            if (tid == 0) s_n[after] = 0;
-            turn = turn == 2 ? 0 : turn + 1;
-            if (n > kCap) {
-                // The chunk's best that pass, one by one.  (Rare: long runs of equal or rising logits.)
-                n = waiting;
-                uint64_t last = ~0ull;
-                for (int k = 0; k < a.top; ++k) {
-                    uint64_t best = 0;
-#pragma unroll 1
-                    for (int x = 0; x < kVecs; ++x) {
-                        const uint4 w = x == 0 ? cur[0] : x == 1 ? cur[1] : x == 2 ? cur[2] : cur[3];
-#pragma unroll
-                        for (int e = 0; e < E; ++e) {
-                            const float v = element<DT>(w, e);
-                            const uint64_t key = key_of(v, id_of(x) + e);
+            sync();
+            // (the other counter is cleared here: all have read it, and none adds to it before the next barrier)
+            int n = s_n[team][turn];
+            if (kWarpTeam) __syncwarp();
+            if (ttid == 0) s_n[team][turn ^ 1] = 0;
+            turn ^= 1;
+            auto merge = [&](int n) {  // by the team's first warp
+                for (int at = 0; at < n; at += 32)
+                    list = merge_keys(list, sort_keys(at + lane < n ? cand[at + lane] : 0, lane), lane);
+                const uint64_t last = __shfl_sync(0xffffffffu, list, a.top - 1);
+                if (lane == 0) s_kth[team] = last != 0 ? key_value(last) : -INFINITY;
+            };
+            if (n <= kTeamCap) {
+                if (kWarpTeam || warp == 0) merge(n);
+            } else {
+                // More than the buffer holds: chunk by chunk, the best that pass one by one, each chunk against the
+                // list as the last one left it.
+                for (int cc = c_seg; cc <= c; ++cc) {
+                    const int lo = max(cc * kChunk - off, 0), hi = min((cc + 1) * kChunk - off, a.V);
+                    n = 0;
+                    for (uint64_t last = ~0ull; n < a.top; ++n) {
+                        uint64_t best = 0;
+                        for (int id = lo + ttid; id < hi; id += kTeam) {
+                            const float v = load_logit<DT>(row, id);
+                            const uint64_t key = key_of(v, id);
                             if (passes(v) && key < last && key > best) best = key;
                         }
-                    }
 #pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) {
-                        const uint64_t o = __shfl_xor_sync(0xffffffffu, best, d);
-                        best = o > best ? o : best;
-                    }
-                    __syncthreads();
-                    if (lane == 0) s_best[warp] = best;
-                    __syncthreads();
+                        for (int d = 16; d > 0; d >>= 1) {
+                            const uint64_t o = __shfl_xor_sync(0xffffffffu, best, d);
+                            best = o > best ? o : best;
+                        }
+                        if (!kWarpTeam) {
+                            __syncthreads();
+                            if (lane == 0) s_best[warp] = best;
+                            __syncthreads();
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) best = s_best[w] > best ? s_best[w] : best;
-                    if (best == 0) break;
-                    last = best;
-                    if (tid == 0) s_cand[n] = best;
-                    ++n;
+                            for (int w = 0; w < kWarps; ++w) best = s_best[w] > best ? s_best[w] : best;
+                        }
+                        if (best == 0) break;
+                        last = best;
+                        if (ttid == 0) cand[n] = best;
+                    }
+                    sync();
+                    if (kWarpTeam || warp == 0) merge(n);
+                    sync();
+                    kth = s_kth[team];
                 }
-                __syncthreads();
             }
-            if (n >= kMerge || (n > 0 && (open || ends))) {
-                if (warp == 0) {
-                    for (int at = 0; at < n; at += 32)
-                        list = merge_keys(list, sort_keys(at + lane < n ? s_cand[at + lane] : 0, lane), lane);
-                    const uint64_t kth = __shfl_sync(0xffffffffu, list, a.top - 1);
-                    if (lane == 0) s_tau = kth != 0 ? key_value(kth) : -INFINITY;
-                }
-                __syncthreads();
-                tau = s_tau;
-                n = 0;
-            } else if (open) {
-                tau = -INFINITY;  // (nothing above -inf as yet)
-            }
-            waiting = n;
+            seg_max = -INFINITY;
+            c_seg = c + 1;
         }
-        // ---- the part's end
         if (ends) {
-            float m2 = m, s2 = s, t2 = t;
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) {
-                const float mo = __shfl_xor_sync(0xffffffffu, m2, d), so = __shfl_xor_sync(0xffffffffu, s2, d),
-                            to = __shfl_xor_sync(0xffffffffu, t2, d);
-                add_part(m2, s2, t2, mo, so, to, a.c1);
-                cnt += __shfl_xor_sync(0xffffffffu, cnt, d);
-            }
-            __syncthreads();
-            if (lane == 0) {
-                s_red[warp][0] = m2;
-                s_red[warp][1] = s2;
-                s_red[warp][2] = t2;
-                s_cnt[warp] = cnt;
-            }
-            __syncthreads();
-            const int64_t slot = (int64_t)(r0 + j) + cta;
-            if (tid == 0) {
-#pragma unroll
-                for (int w = 1; w < kWarps; ++w) {
-                    add_part(m2, s2, t2, s_red[w][0], s_red[w][1], s_red[w][2], a.c1);
-                    cnt += s_cnt[w];
+            if (kWarpTeam || warp == 0) {
+                float4 v = s_red[parity][kWarpTeam ? warp : lane & 7];
+                if (!kWarpTeam) add_lanes<kWarps>(v, a.c1);
+                if (c_part == 0 && c2 == 0) {  // the whole row
+                    finish(a, s_entry[j], tok >= 0, s_xt[j].x, v.x, v.y, v.z, (int)v.w, list);
+                } else {
+                    const int64_t slot = (int64_t)(cta_r0 + j) + cta;
+                    if (lane == 0) {
+                        a.sums[slot] = make_float4(v.x, v.y, v.z, __int_as_float((int)v.w));
+                        a.entry[slot] = s_entry[j];
+                    }
+                    if (lane < a.top) a.keys[slot * a.top + lane] = list;
                 }
-                a.sums[slot] = make_float4(m2, s2, t2, __int_as_float(cnt));
-                a.entry[slot] = s_entry[j];
+                list = 0;
             }
-            if (tid < a.top) a.keys[slot * a.top + tid] = list;
-            m = -INFINITY;
-            s = t = 0.f;
-            cnt = 0;
-            list = 0;
-            tau = -INFINITY;
+            m = seg_max = -INFINITY;
+            s = t = cnt = make_float2(0.f, 0.f);
+            parity ^= 1;
+            c_part = c_seg = c2;
         }
-        j = j2;
+        if (--left == 0) break;
+        j += c2 == 0;
         c = c2;
-        xt = xt_next;
-#pragma unroll
-        for (int x = 0; x < kVecs; ++x) cur[x] = nxt[x];
     }
 }
 
 constexpr int kJoinWarps = 4;
 
-// Adds up the pieces of each row: a CTA a row.  A warp merges every fourth piece's alternatives, the first one adds the sums.
+// Adds up the pieces of the rows that are cut: a CTA a row.  A warp merges every fourth piece's alternatives, the
+// first one adds the sums.
 template <int DT>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 logprob_join_kernel(const __grid_constant__ Args a) {
@@ -498,12 +708,12 @@ logprob_join_kernel(const __grid_constant__ Args a) {
     __shared__ uint64_t s_keys[kJoinWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n_rows = *a.n_rows;
-    const int64_t units = (int64_t)n_rows * a.chunks;
-    const int ctas = (int)(units < a.ctas ? units : a.ctas);
+    const Shares shares((int64_t)n_rows * a.chunks, a.ctas);
     for (int r = blockIdx.x; r < n_rows; r += gridDim.x) {
-        const int c0 = cta_of(units, ctas, (int64_t)r * a.chunks), c1 = cta_of(units, ctas, (int64_t)(r + 1) * a.chunks - 1);
+        const int c0 = shares.of((int64_t)r * a.chunks), c1 = shares.of((int64_t)(r + 1) * a.chunks - 1);
         const int64_t slot0 = (int64_t)r + c0;
         const int pieces = c1 - c0 + 1;
+        if (pieces == 1) continue;
         uint64_t list = 0;
         if (a.top > 0) {
             for (int p = warp; p < pieces; p += kJoinWarps)
@@ -519,7 +729,7 @@ logprob_join_kernel(const __grid_constant__ Args a) {
         for (int p = lane; p < pieces; p += 32) m = fmaxf(m, a.sums[slot0 + p].x);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        double s = 0, t = 0;  // t in units of ln
+        float s = 0.f, t = 0.f;
         int cnt = 0;
         for (int p = lane; p < pieces; p += 32) {
             const float4 v = a.sums[slot0 + p];
@@ -527,9 +737,9 @@ logprob_join_kernel(const __grid_constant__ Args a) {
             if (v.x == -INFINITY) {
                 s += v.y;  // (0, or NaN)
             } else {
-                const double d = ((double)v.x - m) * a.inv_T, f = exp(d);
+                const float d = (v.x - m) * a.c1, f = ex2(d);
                 s += f * v.y;
-                t += f * (0.69314718055994530942 * v.z + (f > 0 ? d * v.y : 0.0));
+                t += f * (v.z + max_nan(d, kFloor) * v.y);
             }
         }
 #pragma unroll
@@ -538,73 +748,47 @@ logprob_join_kernel(const __grid_constant__ Args a) {
             t += __shfl_xor_sync(0xffffffffu, t, d);
             cnt += __shfl_xor_sync(0xffffffffu, cnt, d);
         }
-        // a row of -inf alone has no law, nor has one with NaN or +inf: NaN
-        const double ln_s = m == -INFINITY ? (double)NAN : log(s);
         const int n = a.entry[slot0];
-        auto logp = [&](float x) -> float {
-            if (isnan(ln_s)) return NAN;
-            return (float)(((double)x - m) * a.inv_T - ln_s);
-        };
-        if (lane == 0) {
-            const int tok = a.tokens[n];
-            const bool ok = tok >= 0 && tok < a.V;
-            float x = 0.f;
-            if (ok) {
-                int64_t row = n;
-                if (a.rows != nullptr) row = (a.block > 0 ? (int64_t)(n / a.block) * a.block : 0) + a.rows[n];
-                const char* p = a.logits + row * a.stride;
-                if (DT == GRAFT_F32) x = reinterpret_cast<const float*>(p)[tok];
-                if (DT == GRAFT_BF16) x = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[tok]);
-                if (DT == GRAFT_FP16) x = __half2float(reinterpret_cast<const __half*>(p)[tok]);
-            }
-            a.logprob[n] = ok ? logp(x) : 0.f;
-            if (a.entropy != nullptr) a.entropy[n] = isnan(ln_s) ? NAN : (float)(ln_s - t / s);
-            if (a.rank != nullptr) a.rank[n] = ok ? cnt : -1;
-        }
-        if (a.top > 0) {
-            int id = key_id(list);
-            float lp = list != 0 ? logp(key_value(list)) : 0.f;
-            const unsigned have = __ballot_sync(0xffffffffu, list != 0);
-            const int known = __popc(have);
-            if (known < a.top) {
-                // Fewer tokens above -inf than places: all of them are listed, the lowest other ids follow.
-                uint64_t used = 0;
-                for (int k = 0; k < known; ++k) {
-                    const int x = __shfl_sync(0xffffffffu, id, k);
-                    if (x < 64) used |= 1ull << x;
-                }
-                if (lane >= known) {
-                    int skip = lane - known;
-                    id = 0;
-                    while ((used >> id & 1) || skip-- > 0) ++id;
-                    lp = isnan(ln_s) ? NAN : -INFINITY;
-                }
-            }
-            if (lane < a.top) {
-                a.top_id[(int64_t)n * a.top + lane] = id;
-                a.top_logprob[(int64_t)n * a.top + lane] = lp;
-            }
-        }
+        int64_t row = n;
+        if (a.rows != nullptr) row = (a.block > 0 ? (int64_t)(n / a.block) * a.block : 0) + a.rows[n];
+        const int tok = a.tokens[n];
+        const bool ok = tok >= 0 && tok < a.V;
+        finish(a, n, ok, ok ? load_logit<DT>(a.logits + row * a.stride, tok) : 0.f, m, s, t, cnt, list);
     }
 }
 
 template <int DT>
 int launch(Args& a, cudaStream_t st) {
-    constexpr int64_t chunk = (int64_t)kThreads * kVecs * kElems<DT>;
+    const bool warps = a.V <= kShort;
+    const int64_t chunk = (int64_t)(warps ? 32 : kThreads) * kVecs * kElems<DT>;
     a.chunks = (int)((a.V + kElems<DT> - 1 + chunk - 1) / chunk);  // (a row may start inside 16 bytes)
-    const int64_t units = (int64_t)a.N * a.chunks;
-    const int grid = (int)(units < a.ctas ? units : a.ctas);
-    a.ctas = grid;
-    launch_pdl(logprob_part_kernel<DT>, dim3(grid), dim3(kThreads), 0, st, a);
-    const int sms = device_sm_count();
-    launch_pdl(logprob_join_kernel<DT>, dim3(a.N < 8 * sms ? a.N : 8 * sms), dim3(kJoinWarps * 32), 0, st, a);
-    count_launches(2);
+    const int64_t units = warps ? ((int64_t)a.N + kWarps - 1) / kWarps : (int64_t)a.N * a.chunks;
+    a.ctas = (int)(units < a.ctas ? units : a.ctas);
+    const auto kernel = warps ? logprob_part_kernel<DT, true> : logprob_part_kernel<DT, false>;
+    static bool attr_set[64][2] = {};
+    int dev = 0;
+    if (!cuda_ok(cudaGetDevice(&dev))) return GRAFT_ERR_CUDA;
+    if (dev < 0 || dev >= 64 || !attr_set[dev][warps]) {
+        if (!cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing)) ||
+            !cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                          cudaSharedmemCarveoutMaxShared)))
+            return GRAFT_ERR_CUDA;
+        if (dev >= 0 && dev < 64) attr_set[dev][warps] = true;
+    }
+    launch_pdl(kernel, dim3(a.ctas), dim3(kThreads), kRing, st, a);
+    count_launches(1);
+    if (!warps) {
+        const int sms = device_sm_count();
+        launch_pdl(logprob_join_kernel<DT>, dim3(a.N < 8 * sms ? a.N : 8 * sms), dim3(kJoinWarps * 32), 0, st, a);
+        count_launches(1);
+    }
     return launch_status();
 }
 
-int most_ctas() {
-    const int sms = device_sm_count();
-    return kResident * (sms > 0 ? sms : 152);
+// CTAs of a call at most: as many as the SMs hold at once; where those would have longer lists of rows than they keep, more.
+int most_ctas(int N) {
+    const int sms = device_sm_count(), most = kResident * (sms > 0 ? sms : 152), least = N / (kMaxRows - 16) + 1;
+    return most > least ? most : least;
 }
 
 void carve(WsCarver& w, int N, int top, int ctas, Args* a) {
@@ -636,7 +820,7 @@ extern "C" int graft_token_logprobs_workspace_size(int N, int V, int top, size_t
     const int rc = check(N, V, top);
     if (rc != GRAFT_OK) return rc;
     WsCarver w(nullptr);
-    carve(w, N, top, most_ctas(), nullptr);
+    carve(w, N, top, most_ctas(N), nullptr);
     *bytes = w.bytes();
     return GRAFT_OK;
 }
@@ -658,7 +842,7 @@ extern "C" int graft_token_logprobs(int N, int V, int64_t n_logit_rows, int dtyp
     if (row_stride < V || row_stride > (1LL << 40) || reinterpret_cast<uintptr_t>(logits) % size != 0)
         return GRAFT_ERR_INVALID_ARG;
     Args a{};
-    a.ctas = most_ctas();
+    a.ctas = most_ctas(N);
     WsCarver sizer(nullptr);
     carve(sizer, N, top, a.ctas, nullptr);
     if (!ws_ok(ws, ws_bytes, sizer.bytes())) return GRAFT_ERR_WORKSPACE;
@@ -666,6 +850,7 @@ extern "C" int graft_token_logprobs(int N, int V, int64_t n_logit_rows, int dtyp
     carve(w, N, top, a.ctas, &a);
     a.logits = static_cast<const char*>(logits);
     a.stride = row_stride * size;
+    a.logits_end = a.logits + (n_logit_rows > 0 ? (n_logit_rows - 1) * a.stride + (int64_t)V * size : 0);
     a.rows = rows;
     a.tokens = tokens;
     a.R = n_logit_rows;
@@ -674,7 +859,7 @@ extern "C" int graft_token_logprobs(int N, int V, int64_t n_logit_rows, int dtyp
     a.block = block;
     a.top = top;
     a.c1 = (float)(1.4426950408889634074 / (double)temperature);
-    a.inv_T = 1.0 / (double)temperature;
+    a.inv_T = (float)(1.0 / (double)temperature);
     a.logprob = logprob;
     a.entropy = entropy;
     a.rank = rank;
