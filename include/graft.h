@@ -686,6 +686,33 @@ int graft_paged_attention_ex(const GraftPagedCache* cache, const void* K_pool, c
                              size_t ws_bytes, graft_stream_t stream);
 
 /*
+ * graft_paged_plan_window, graft_paged_attention_window — the same for layers
+ * with a sliding window, whose rows see the last `window` positions, their
+ * own among them, and the `first` tokens of the sequence: of what a row sees
+ * without a window (graft_paged_attention) the row at position p keeps cache
+ * row r where r > p - window or r < first.  window >= 1, first >= 0.
+ * The i-th new row stands at position lengths[b] + i; in a tree the set bits
+ * of a row's mask, from the lowest on, stand at positions lengths[b],
+ * lengths[b] + 1, ..., and the row at that of the highest (graft_build_tree's
+ * masks: a node's depth; lengths[b] where no bit is set), so that ancestors
+ * drop out of a window shorter than the path.
+ * Keys that no row of a sequence can see are not read: the cost follows the
+ * window, and pages whose rows all lie from `first` on and at or before
+ * lengths[b] - window may be given back, their entries of the block table
+ * being anything.  plan: graft_paged_plan_size bytes; a plan of another
+ * window or `first`, or of none, is refused on the device
+ * (GRAFT_STATUS_PLAN), so layers of several kinds take a plan each.
+ * Workspace and the rest as above (they may share a workspace); tuning may
+ * be NULL.
+ */
+int graft_paged_plan_window(const GraftPagedCache* cache, int N, int Hq, const int32_t* q_start, int max_new, int tree,
+                            int window, int first, void* plan, size_t plan_bytes, graft_stream_t stream);
+int graft_paged_attention_window(const GraftPagedCache* cache, const void* K_pool, const void* V_pool, int N, int Hq,
+                                 int max_new, int window, int first, const void* plan, size_t plan_bytes, const void* Q,
+                                 int64_t q_stride, const uint64_t* mask, float scale, void* O,
+                                 const GraftAttnTuning* tuning, void* ws, size_t ws_bytes, graft_stream_t stream);
+
+/*
  * graft_pages_compact — after a verify step: in every layer, cache row
  * lengths[b] + t receives row lengths[b] + path[b][t], t < acc_len[b]
  * (graft_accept_compact's path and acc_len; path rises strictly, so the moves

@@ -128,6 +128,9 @@ _SIGNATURES = {
     "graft_paged_attention_workspace_size": [_P, _I, _I, _I, ctypes.POINTER(_SZ)],
     "graft_paged_attention": [_P, _P, _P, _I, _I, _I, _P, _SZ, _P, _I64, _P, ctypes.c_float, _P, _P, _SZ, _P],
     "graft_paged_attention_ex": [_P, _P, _P, _I, _I, _I, _P, _SZ, _P, _I64, _P, ctypes.c_float, _P, _P, _P, _SZ, _P],
+    "graft_paged_plan_window": [_P, _I, _I, _P, _I, _I, _I, _I, _P, _SZ, _P],
+    "graft_paged_attention_window": [_P, _P, _P, _I, _I, _I, _I, _I, _P, _SZ, _P, _I64, _P, ctypes.c_float, _P, _P, _P, _SZ,
+                                     _P],
     "graft_pages_compact": [_P, _I, _P, _P, _P, _P],
     "graft_pages_reserve_workspace_size": [_P, ctypes.POINTER(_SZ)],
     "graft_pages_reserve": [_P, _P, _P, _SZ, _P],

@@ -61,7 +61,7 @@ struct Args {
     int N, V, block, top, chunks;  // chunks of a row
     int ctas;
     float c1;     // log2(e) / T
-    float inv_T;
+    double inv_T;
     float* logprob;
     float* entropy;
     int32_t* rank;
@@ -266,11 +266,18 @@ __device__ __forceinline__ void finish(const Args& a, int n, bool ok, float give
                                        uint64_t list) {
     const int lane = threadIdx.x & 31;
     // a row of -inf alone has no law, nor has one with NaN or +inf: NaN
-    const float ln_s = m == -INFINITY ? NAN : logf(s);
-    auto logp = [&](float x) -> float { return (x - m) * a.inv_T - ln_s; };
+    // (the last few operations in 64 bits: logits, maxima and ln s may be larger than what is left)
+    int e;
+    float f = frexpf(s, &e);
+    if (f < 0.70710678f) {  // (near one: of a certain token, s = 1, ln s is 0)
+        f *= 2.f;
+        --e;
+    }
+    const double ln_s = m == -INFINITY ? (double)NAN : e * 0.69314718055994530942 + (double)logf(f);
+    auto logp = [&](float x) -> float { return (float)(((double)x - m) * a.inv_T - ln_s); };
     if (lane == 0) {
         a.logprob[n] = ok ? logp(given) : 0.f;
-        if (a.entropy != nullptr) a.entropy[n] = ln_s - 0.693147181f * (t / s);
+        if (a.entropy != nullptr) a.entropy[n] = (float)(ln_s - 0.69314718055994530942 * (t / s));
         if (a.rank != nullptr) a.rank[n] = ok ? cnt : -1;
     }
     if (a.top > 0) {
@@ -859,7 +866,7 @@ extern "C" int graft_token_logprobs(int N, int V, int64_t n_logit_rows, int dtyp
     a.block = block;
     a.top = top;
     a.c1 = (float)(1.4426950408889634074 / (double)temperature);
-    a.inv_T = (float)(1.0 / (double)temperature);
+    a.inv_T = 1.0 / (double)temperature;
     a.logprob = logprob;
     a.entropy = entropy;
     a.rank = rank;

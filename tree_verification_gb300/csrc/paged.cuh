@@ -45,7 +45,8 @@ struct PlanHead {
     int32_t rounds;      // whole rounds of wide items: every CTA takes one of each
     int32_t n_groups;    // row blocks split by keys
     int32_t tiles;       // tiles of such a row block at most
-    int32_t reserved[15];
+    int32_t window, first;  // of a windowed plan (window 0: none)
+    int32_t reserved[13];
 };
 constexpr int32_t kPlanMagic = 0x47503033;
 
@@ -56,7 +57,7 @@ struct Entry {
     int32_t row0;    // first query row of the block (row = new row x group + head of the group)
     int32_t rows;    // query rows of the block
     int32_t keys;    // keys that any of them may see
-    int32_t units;   // of 16 keys
+    int32_t units;   // of 16 keys (those that a window leaves out aside)
 };
 
 constexpr int kBlockKeys = 128;
@@ -69,7 +70,7 @@ struct Wide {
     int32_t keys;         // keys that any row of the block may see
     int32_t kvh;          // KV head
     int32_t part;         // partial rows of the range, -1: the rows are written to O
-    int32_t pad;
+    int32_t gap;          // blocks that a window leaves out behind the first tokens' (blk0 and nblk do not count them)
 };
 
 // A row block of one KV head whose key ranges are joined: partial rows part0, part0 + step, ...
@@ -87,6 +88,35 @@ struct Start {
     int64_t item_first;                // step 0: the item's first unit among all
     int64_t total;                     // step 0: all units
 };
+
+// ---------------------------------------------------------------- windows
+// A row at position p sees row r <= p where r > p - window or r < first.  The rows between the first tokens and the
+// window of an item's earliest row are seen by none: an item's units of `unit` keys are those of the first tokens and,
+// behind them, those from key `low` on (low: the earliest row's p - window + 1).  Units are numbered without the gap.
+__host__ __device__ __forceinline__ int window_units(int first, int unit) { return first / unit + (first % unit != 0); }
+__device__ __forceinline__ int window_gap(int low, int first, int unit) {
+    if (low <= first) return 0;  // (the first tokens reach the window)
+    const int gap = low / unit - window_units(first, unit);
+    return gap > 0 ? gap : 0;
+}
+// The new rows that a tree's row sees: set bit k of its mask, counted from the lowest, stands at position L + k, the row
+// itself at the last one's.
+__device__ __forceinline__ uint64_t window_mask(uint64_t anc, int window, int first, int L) {
+    const int n = __popcll(anc), drop = n - window;
+    if (drop <= 0) return anc;
+    const int keep = first > L ? first - L : 0;
+    uint64_t seen = anc, bits = anc;
+    for (int k = 0; k < drop; ++k) {
+        const uint64_t low = bits & (0 - bits);
+        if (k >= keep) seen ^= low;
+        bits ^= low;
+    }
+    return seen;
+}
+__device__ __forceinline__ int window_low(uint64_t anc, int window, int L) {  // of a tree's row, before window_mask
+    const int n = __popcll(anc);
+    return L + (n > 0 ? n - 1 : 0) - window + 1;
+}
 
 constexpr int kHeadBytes = offsetof(PlanHead, reserved);  // of the head's fields
 
@@ -136,6 +166,7 @@ struct AttnArgs {
     float scale;
     int N, Hq, G, max_new, page_shift;
     int after_wide;  // the few kernel runs beside the wide one
+    int window, first;  // window 0: none
     uint64_t wait_ns;  // bound on every pipeline wait of the wide kernel (0.5 s unless tuned)
     PlanShape shape;
     FewWs few;
@@ -151,7 +182,7 @@ int few_launch(const AttnArgs& a, cudaStream_t st);
 __device__ __forceinline__ bool plan_fits(const AttnArgs& a, const PlanHead& h) {
     return h.magic == kPlanMagic && h.N == a.N && h.Hq == a.Hq && h.Hkv == a.c.Hkv && h.n_seqs == a.c.n_seqs &&
            h.max_new == a.max_new && h.tree == (a.mask != nullptr) && h.page_rows == a.c.page_rows &&
-           h.max_pages == a.c.max_pages && h.num_pages == a.c.num_pages && h.few_rows == a.shape.few_rows &&
+           h.max_pages == a.c.max_pages && h.num_pages == a.c.num_pages && h.window == a.window && h.first == a.first && h.few_rows == a.shape.few_rows &&
            h.ctas == a.shape.ctas;
 }
 

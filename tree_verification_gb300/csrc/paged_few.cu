@@ -15,6 +15,10 @@
 // tcgen05 tile, and the products take a quarter of the time the bytes do).
 // A page row index costs a lookup per unit; a lane holds one, 32 units ahead.
 //
+// With a window (kWindow, graft_paged_attention_window) an item's units are those
+// of the first tokens and those from the earliest row's window on; units that
+// some row does not see whole are masked like those with new rows in them.
+//
 // Items that a run's edges cut are joined by the CTA that arrives last (a
 // counter an item): it reads the pieces' 32-bit partial rows in their order,
 // so the result does not depend on which CTA that is.
@@ -199,7 +203,7 @@ __device__ __forceinline__ void join_pieces(const AttnArgs& a, const Start& at, 
     }
 }
 
-template <int DT, int RT, int kWarps>
+template <int DT, int RT, int kWarps, bool kWindow>
 __global__ void __launch_bounds__(kWarps * 32, 8 / kWarps)
 few_kernel(const __grid_constant__ AttnArgs a) {
     using E = Elem<DT>;
@@ -229,7 +233,11 @@ few_kernel(const __grid_constant__ AttnArgs a) {
     int pages = -1, pages_at = 0; // pages of this warp's units pages_at .. pages_at + 31, one a lane
     const int32_t* table = a.c.block_table;
     const Entry& e = s_at.e;
+    int gap = 0;  // units that the window leaves out, behind unit `behind`
+    const int behind = kWindow ? window_units(a.first, kUnit) : 0;
+    auto key_of = [&](int u) { return (kWindow && u >= behind ? u + gap : u) * kUnit; };
     auto begin = [&]() {
+        if (kWindow) gap = window_gap(e.L - a.window + 1, a.first, kUnit);
         keys = e.keys;
         L = e.L;
         n_new = e.n;
@@ -243,7 +251,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
         const int u = u0 + warp + (i0 + lane) * kWarps;
         int p = -1;
         if (u < u1) {
-            p = __ldcg(table + ((u * kUnit) >> a.page_shift));
+            p = __ldcg(table + (key_of(u) >> a.page_shift));
             if (p < 0 || p >= a.c.num_pages) {
                 p = -1;
                 if (flag) flag_status(a.c.status, GRAFT_STATUS_PAGE);
@@ -257,7 +265,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
                 pages_at = i;
                 pages = fetch_pages(i, true);
             }
-            const int key0 = (u0 + warp + i * kWarps) * kUnit;
+            const int key0 = key_of(u0 + warp + i * kWarps);
             const int page = __shfl_sync(0xffffffffu, pages, i - pages_at);
             const int64_t row = ((int64_t)max(page, 0) << a.page_shift) + (key0 & (a.c.page_rows - 1));
             const int64_t off = (row * a.c.Hkv + kvh) * HD;
@@ -294,7 +302,9 @@ few_kernel(const __grid_constant__ AttnArgs a) {
     __syncthreads();
     const bool sound = plan_fits(a, s_head) && cta < s_head.few_ctas && e.b >= 0 && e.b < a.c.n_seqs && e.keys > 0 &&
                  e.L >= 0 && e.keys <= (int64_t)a.c.max_pages * a.c.page_rows &&
-                 e.units == (e.keys - 1) / kUnit + 1 && s_at.unit >= 0 && s_at.unit < e.units && s_at.count > 0 &&
+                 e.units == (e.keys - 1) / kUnit + 1 -
+                                (kWindow ? window_gap(e.L - a.window + 1, a.first, kUnit) : 0) &&
+                 s_at.unit >= 0 && s_at.unit < e.units && s_at.count > 0 &&
                  s_at.head >= 0 && s_at.head < a.c.Hkv && e.row0 == 0 && e.rows > 0 && e.rows <= RT * 16 && e.q0 >= 0 &&
                  e.q0 < a.N && (e.rows - 1) / a.G < a.N - e.q0;
     if (sound) {
@@ -307,7 +317,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
         }
         for (int i = 0; i < min(mine, kAhead); ++i) {
-            const int key0 = (u0 + warp + i * kWarps) * kUnit;
+            const int key0 = key_of(u0 + warp + i * kWarps);
             const int page = __shfl_sync(0xffffffffu, pages, i);
             if (page < 0) continue;
             const int64_t row = ((int64_t)page << a.page_shift) + (key0 & (a.c.page_rows - 1));
@@ -360,6 +370,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
         }
         int limit[RT][2];        // keys below it are seen
         uint64_t anc[RT][2];     // new rows seen (tree)
+        int low[kWindow ? RT : 1][2];  // of the rows below the limit, those from `low` on and the first tokens' are seen
 #pragma unroll
         for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -378,14 +389,21 @@ few_kernel(const __grid_constant__ AttnArgs a) {
                     }
                 }
                 anc[t][h] = 0;
+                if (kWindow) low[t][h] = 0;
                 if (!ok) {
                     limit[t][h] = 0;
                 } else if (a.mask != nullptr) {
                     limit[t][h] = e.L;
                     const uint64_t* m = a.mask + e.q0 + tok;
                     anc[t][h] = RT > 1 ? __ldcg(reinterpret_cast<const unsigned long long*>(m)) : *m;
+                    if (kWindow) {
+                        if (e.n < 64) anc[t][h] &= (1ull << e.n) - 1ull;
+                        low[t][h] = window_low(anc[t][h], a.window, e.L);
+                        anc[t][h] = window_mask(anc[t][h], a.window, a.first, e.L);
+                    }
                 } else {
                     limit[t][h] = e.L + tok + 1;
+                    if (kWindow) low[t][h] = e.L + tok + 1 - a.window;
                 }
             }
         float m_run[RT][2], l_run[RT][2], o[RT][16][4];
@@ -432,7 +450,7 @@ few_kernel(const __grid_constant__ AttnArgs a) {
             cp_wait<kStages - 1>();
             __syncwarp();
             const uint32_t tK = ring + (i % kStages) * 2 * kUnitBytes, tV = tK + kUnitBytes;
-            const int key0 = (u0 + warp + i * kWarps) * kUnit;
+            const int key0 = key_of(u0 + warp + i * kWarps);
             float s[RT][2][4];
 #pragma unroll
             for (int t = 0; t < RT; ++t)
@@ -451,9 +469,11 @@ few_kernel(const __grid_constant__ AttnArgs a) {
                     mma16816<DT>(s[t][1], q, b2, b3);
                 }
             }
-            const bool edge = key0 + kUnit > L;  // the unit holds new rows, or ends the keys
+            // the unit holds new rows, or ends the keys; or some row's window starts in it or behind it
+            const bool edge = key0 + kUnit > L ||
+                              (kWindow && key0 < L + n_new - a.window && key0 > a.first - kUnit);
             auto sees = [&](int t, int h, int key) -> bool {
-                if (key < limit[t][h]) return true;
+                if (key < limit[t][h]) return !kWindow || key >= low[t][h] || key < a.first;
                 const int j = key - L;
                 return a.mask != nullptr && j >= 0 && j < n_new && ((anc[t][h] >> j) & 1ull);
             };
@@ -652,27 +672,32 @@ few_kernel(const __grid_constant__ AttnArgs a) {
     leave();
 }
 
-template <int DT, int RT, int W>
+template <int DT, int RT, int W, bool kWindow>
 int launch(const AttnArgs& a, cudaStream_t st) {
     static bool attr_set[64] = {};
     int dev = 0;
     if (!cuda_ok(cudaGetDevice(&dev))) return GRAFT_ERR_CUDA;
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        if (!cuda_ok(cudaFuncSetAttribute(few_kernel<DT, RT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (!cuda_ok(cudaFuncSetAttribute(few_kernel<DT, RT, W, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           smem_bytes(W, RT))))
             return GRAFT_ERR_CUDA;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    launch_pdl(few_kernel<DT, RT, W>, dim3(a.shape.ctas), dim3(W * 32), smem_bytes(W, RT), st, a);
+    launch_pdl(few_kernel<DT, RT, W, kWindow>, dim3(a.shape.ctas), dim3(W * 32), smem_bytes(W, RT), st, a);
     count_launches(1);
     return launch_status();
 }
 
+template <int DT, bool kWindow>
+int launch_rows(const AttnArgs& a, cudaStream_t st) {
+    if (a.shape.few_warps == 4)
+        return a.shape.few_rows == 16 ? launch<DT, 1, 4, kWindow>(a, st) : launch<DT, 2, 4, kWindow>(a, st);
+    return a.shape.few_rows == 16 ? launch<DT, 1, 8, kWindow>(a, st) : launch<DT, 2, 8, kWindow>(a, st);
+}
+
 template <int DT>
 int launch_type(const AttnArgs& a, cudaStream_t st) {
-    if (a.shape.few_warps == 4)
-        return a.shape.few_rows == 16 ? launch<DT, 1, 4>(a, st) : launch<DT, 2, 4>(a, st);
-    return a.shape.few_rows == 16 ? launch<DT, 1, 8>(a, st) : launch<DT, 2, 8>(a, st);
+    return a.window > 0 ? launch_rows<DT, true>(a, st) : launch_rows<DT, false>(a, st);
 }
 
 }  // namespace

@@ -4,6 +4,8 @@
 // lengths: those are on the device.  One CTA turns them into work items once
 // a step, and every layer's attention reads its share from the plan, so no
 // attention CTA searches or sorts.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace graft {
@@ -83,9 +85,9 @@ __device__ __forceinline__ bool is_few(const PlanShape& shape, int rows) {
 
 constexpr int kFewInSmem = 512;
 
-template <class ReadSeq>
-__device__ __forceinline__ void plan_few(const GraftPagedCache& c, int Hq, char* plan, const PlanShape& shape,
-                                         ReadSeq read_seq) {
+template <bool kWindow, class ReadSeq>
+__device__ __forceinline__ void plan_few(const GraftPagedCache& c, int Hq, int window, int first, char* plan,
+                                         const PlanShape& shape, ReadSeq read_seq) {
     __shared__ int64_t s_warp[32];
     __shared__ Entry s_few[kFewInSmem];
     __shared__ int64_t s_prefix[kFewInSmem];
@@ -101,7 +103,8 @@ __device__ __forceinline__ void plan_few(const GraftPagedCache& c, int Hq, char*
         int q0, n, L;
         read_seq(b0 + tid, q0, n, L);
         const bool mine = is_few(shape, n * G);
-        const Entry e{b0 + tid, q0, n, L, 0, n * G, L + n, (L + n + 15) / 16};
+        const int gap = kWindow ? window_gap(L - window + 1, first, 16) : 0;
+        const Entry e{b0 + tid, q0, n, L, 0, n * G, L + n, (L + n + 15) / 16 - gap};
         int64_t total, all;
         const int at = n_few + (int)scan_block<int64_t>(mine, s_warp, &total);
         const int64_t before = units + scan_block<int64_t>(mine ? (int64_t)e.units * c.Hkv : 0, s_warp, &all);
@@ -200,9 +203,9 @@ __device__ __forceinline__ void plan_few(const GraftPagedCache& c, int Hq, char*
     if (tid == 0) reinterpret_cast<PlanHead*>(plan)->few_ctas = ctas;
 }
 
-template <class ReadSeq>
-__device__ __forceinline__ void plan_wide(const GraftPagedCache& c, int N, int Hq, int tree, char* plan,
-                                          const PlanShape& shape, ReadSeq read_seq) {
+template <bool kWindow, class ReadSeq>
+__device__ __forceinline__ void plan_wide(const GraftPagedCache& c, int N, int Hq, int tree, int window, int first,
+                                          char* plan, const PlanShape& shape, ReadSeq read_seq) {
     __shared__ int64_t s_warp[32];
     __shared__ int s_hist[kBuckets], s_first[kPlanThreads], s_max, s_fits[32];
     const int tid = threadIdx.x, G = Hq / c.Hkv;
@@ -212,6 +215,10 @@ __device__ __forceinline__ void plan_wide(const GraftPagedCache& c, int N, int H
     int32_t* where = reinterpret_cast<int32_t*>(plan + shape.off_where);
     Group* groups = reinterpret_cast<Group*>(plan + shape.off_group);
     const int pair = 2 * shape.tile_tokens;
+    auto count_blocks = [&](Wide& w) {  // from its keys and first row
+        w.gap = kWindow ? window_gap(w.L + (tree ? 0 : w.tok0) - window + 1, first, kBlockKeys) : 0;
+        w.nblk = (w.keys + kBlockKeys - 1) / kBlockKeys - w.gap;
+    };
     int n_pairs = 0;
     if (tid == 0) s_max = 1;
     for (int b0 = 0; b0 < c.n_seqs; b0 += kPlanThreads) {
@@ -234,7 +241,7 @@ __device__ __forceinline__ void plan_wide(const GraftPagedCache& c, int N, int H
             w.tok0 = j * pair;
             w.two = n - w.tok0 > shape.tile_tokens;
             w.keys = tree ? L + n : L + min(w.tok0 + pair, n);
-            w.nblk = (w.keys + kBlockKeys - 1) / kBlockKeys;
+            count_blocks(w);
             w.part = -1;
             pairs[at] = w;
             most = max(most, w.nblk);
@@ -262,7 +269,7 @@ __device__ __forceinline__ void plan_wide(const GraftPagedCache& c, int N, int H
             } else if (single) {
                 w.tok0 += t * shape.tile_tokens;
                 w.keys = tree ? w.L + w.n : w.L + min(w.tok0 + shape.tile_tokens, w.n);
-                w.nblk = (w.keys + kBlockKeys - 1) / kBlockKeys;
+                count_blocks(w);
                 w.two = 0;
             }
             return w;
@@ -465,10 +472,10 @@ __device__ __forceinline__ void plan_wide(const GraftPagedCache& c, int N, int H
 }
 
 // Block 0 plans the few entries, block 1 the wide items (a grid of one block has only the one kind).
-template <bool kFew, bool kWide>
+template <bool kFew, bool kWide, bool kWindow>
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int32_t* __restrict__ q_start, int max_new,
-            int tree, char* plan, const __grid_constant__ PlanShape shape) {
+            int tree, int window, int first, char* plan, const __grid_constant__ PlanShape shape) {
     griddep_wait();
     const bool wide_block = kWide && (!kFew || blockIdx.x > 0);
     // Every block checks all sequences, the first one sets the status.
@@ -487,9 +494,9 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
         L = (int)len;
     };
     if constexpr (kWide)
-        if (wide_block) plan_wide(c, N, Hq, tree, plan, shape, read_seq);
+        if (wide_block) plan_wide<kWindow>(c, N, Hq, tree, window, first, plan, shape, read_seq);
     if constexpr (kFew)
-        if (!wide_block) plan_few(c, Hq, plan, shape, read_seq);
+        if (!wide_block) plan_few<kWindow>(c, Hq, window, first, plan, shape, read_seq);
     if (threadIdx.x == 0 && blockIdx.x == 0) {
         PlanHead& h = *reinterpret_cast<PlanHead*>(plan);
         h.magic = kPlanMagic;
@@ -504,6 +511,8 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
         h.num_pages = c.num_pages;
         h.few_rows = shape.few_rows;
         h.ctas = shape.ctas;
+        h.window = window;
+        h.first = first;
     }
     // The attention reads the plan ahead of its grid wait, as a guess that is checked after it.  A CTA's first thread
     // to let it start does so for all, so a barrier comes before: every thread has made its writes, and the guess
@@ -593,19 +602,36 @@ extern "C" int graft_paged_plan_size(const GraftPagedCache* cache, int N, int Hq
     return GRAFT_OK;
 }
 
-extern "C" int graft_paged_plan(const GraftPagedCache* cache, int N, int Hq, const int32_t* q_start, int max_new,
-                                int tree, void* plan, size_t plan_bytes, graft_stream_t stream) {
+// window 0: none
+static int plan_call(const GraftPagedCache* cache, int N, int Hq, const int32_t* q_start, int max_new, int tree, int window,
+                     int first, void* plan, size_t plan_bytes, graft_stream_t stream) {
     const int rc = check_attention(cache, N, Hq, max_new);
     if (rc != GRAFT_OK) return rc;
     if (tree && max_new > GRAFT_MAX_KMAX) return GRAFT_ERR_UNSUPPORTED_SHAPE;
     if (q_start == nullptr) return GRAFT_ERR_INVALID_ARG;
     const PlanShape s = plan_shape(cache, N, Hq, max_new);
     if (!ws_ok(plan, plan_bytes, s.bytes)) return GRAFT_ERR_WORKSPACE;
-    const auto kernel = !s.wide ? plan_kernel<true, false> : s.few ? plan_kernel<true, true> : plan_kernel<false, true>;
+    const auto pick = [&](auto win) {
+        constexpr bool W = decltype(win)::value;
+        return !s.wide ? plan_kernel<true, false, W> : s.few ? plan_kernel<true, true, W> : plan_kernel<false, true, W>;
+    };
+    const auto kernel = window > 0 ? pick(std::true_type{}) : pick(std::false_type{});
     launch_pdl(kernel, dim3(s.few && s.wide ? 2 : 1), dim3(kPlanThreads), 0, (cudaStream_t)stream, *cache, N, Hq,
-               q_start, max_new, tree != 0 ? 1 : 0, static_cast<char*>(plan), s);
+               q_start, max_new, tree != 0 ? 1 : 0, window, first, static_cast<char*>(plan), s);
     count_launches(1);
     return launch_status();
+}
+
+extern "C" int graft_paged_plan(const GraftPagedCache* cache, int N, int Hq, const int32_t* q_start, int max_new,
+                                int tree, void* plan, size_t plan_bytes, graft_stream_t stream) {
+    return plan_call(cache, N, Hq, q_start, max_new, tree, 0, 0, plan, plan_bytes, stream);
+}
+
+extern "C" int graft_paged_plan_window(const GraftPagedCache* cache, int N, int Hq, const int32_t* q_start, int max_new,
+                                       int tree, int window, int first, void* plan, size_t plan_bytes,
+                                       graft_stream_t stream) {
+    if (window < 1 || first < 0) return GRAFT_ERR_INVALID_ARG;
+    return plan_call(cache, N, Hq, q_start, max_new, tree, window, first, plan, plan_bytes, stream);
 }
 
 extern "C" int graft_paged_attention_workspace_size(const GraftPagedCache* cache, int N, int Hq, int max_new,
@@ -627,11 +653,10 @@ extern "C" int graft_paged_attention(const GraftPagedCache* cache, const void* K
                                     nullptr, ws, ws_bytes, stream);
 }
 
-extern "C" int graft_paged_attention_ex(const GraftPagedCache* cache, const void* K_pool, const void* V_pool, int N,
-                                        int Hq, int max_new, const void* plan, size_t plan_bytes, const void* Q,
-                                        int64_t q_stride, const uint64_t* mask, float scale, void* O,
-                                        const GraftAttnTuning* tuning, void* ws, size_t ws_bytes,
-                                        graft_stream_t stream) {
+static int attention_call(const GraftPagedCache* cache, const void* K_pool, const void* V_pool, int N, int Hq, int max_new,
+                          int window, int first, const void* plan, size_t plan_bytes, const void* Q, int64_t q_stride,
+                          const uint64_t* mask, float scale, void* O, const GraftAttnTuning* tuning, void* ws,
+                          size_t ws_bytes, graft_stream_t stream) {
     const int rc = check_attention(cache, N, Hq, max_new);
     if (rc != GRAFT_OK) return rc;
     if (tuning != nullptr) {
@@ -669,6 +694,8 @@ extern "C" int graft_paged_attention_ex(const GraftPagedCache* cache, const void
     a.Hq = Hq;
     a.G = Hq / cache->Hkv;
     a.max_new = max_new;
+    a.window = window;
+    a.first = first;
     a.page_shift = log2_exact(cache->page_rows);
     a.wait_ns = tuning != nullptr && tuning->wait_ns > 0 ? (uint64_t)tuning->wait_ns : 500000000ull;
     cudaStream_t st = (cudaStream_t)stream;
@@ -682,4 +709,23 @@ extern "C" int graft_paged_attention_ex(const GraftPagedCache* cache, const void
     }
     if (rc2 == GRAFT_OK && a.shape.max_groups > 0) rc2 = join_launch(a, st);
     return rc2;
+}
+
+extern "C" int graft_paged_attention_ex(const GraftPagedCache* cache, const void* K_pool, const void* V_pool, int N,
+                                        int Hq, int max_new, const void* plan, size_t plan_bytes, const void* Q,
+                                        int64_t q_stride, const uint64_t* mask, float scale, void* O,
+                                        const GraftAttnTuning* tuning, void* ws, size_t ws_bytes,
+                                        graft_stream_t stream) {
+    return attention_call(cache, K_pool, V_pool, N, Hq, max_new, 0, 0, plan, plan_bytes, Q, q_stride, mask, scale, O,
+                          tuning, ws, ws_bytes, stream);
+}
+
+extern "C" int graft_paged_attention_window(const GraftPagedCache* cache, const void* K_pool, const void* V_pool, int N,
+                                            int Hq, int max_new, int window, int first, const void* plan,
+                                            size_t plan_bytes, const void* Q, int64_t q_stride, const uint64_t* mask,
+                                            float scale, void* O, const GraftAttnTuning* tuning, void* ws,
+                                            size_t ws_bytes, graft_stream_t stream) {
+    if (window < 1 || first < 0) return GRAFT_ERR_INVALID_ARG;
+    return attention_call(cache, K_pool, V_pool, N, Hq, max_new, window, first, plan, plan_bytes, Q, q_stride, mask,
+                          scale, O, tuning, ws, ws_bytes, stream);
 }

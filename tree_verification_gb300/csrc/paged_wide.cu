@@ -25,6 +25,11 @@
 //     new row; the keep-bits of a row's 128 keys are built once a block.
 //   * rows of a tile that hold no query row (G not a power of two) are zero
 //     from the start and never loaded.
+//   * with a window (kWindow, graft_paged_attention_window) an item's blocks are
+//     those of the first tokens and those from its earliest row's window on;
+//     the blocks that some row's window starts in or behind are masked and
+//     cleaned like those with new rows, and a row that has seen nothing as yet
+//     takes a block's maximum anew.
 //   * V elements that are infinite or NaN in blocks with masked keys are
 //     taken out in shared memory (0 * NaN is NaN) and given to the rows that
 //     do see them after the item's rows are written.
@@ -144,16 +149,27 @@ __device__ __forceinline__ void keep_bits(uint32_t* w, int kb, int limit, int L,
     }
 }
 
+// The same with a window: of the keys below the limit, those from `low` on and the first tokens'.
+__device__ __forceinline__ void hide_bits(uint32_t* w, int kb, int first, int low) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int from = max(first - (kb + 32 * x), 0), to = min(low - (kb + 32 * x), 32);
+        if (from >= to) continue;
+        const uint32_t below = to >= 32 ? 0xffffffffu : (1u << to) - 1u;
+        w[x] &= ~(below & ~((1u << from) - 1u));
+    }
+}
+
 // Infinite and NaN elements of V that row r sees among keys [k0, k1): added to the row's 128 dims where they
 // were written (16-bit rows of O, or 32-bit partial rows, four dims every 512 floats).  Rare, so out of line and straight from memory.
-template <int DT>
+template <int DT, bool kWindow>
 __device__ __noinline__ void add_odd(const GraftPagedCache& c, const void* V, const int32_t* table, int page_shift,
-                                     int kvh, int k0, int k1, int limit, int L, uint64_t anc, void* row16,
-                                     float* row32) {
+                                     int kvh, int k0, int k1, int limit, int first, int low, int L, uint64_t anc,
+                                     void* row16, float* row32) {
     using E = Elem<DT>;
     for (int key = k0; key < k1; ++key) {
         const int j = key - L;
-        if (!(key < limit || (j >= 0 && j < 64 && ((anc >> j) & 1ull)))) continue;
+        if (!((key < limit && (!kWindow || key >= low || key < first)) || (j >= 0 && j < 64 && ((anc >> j) & 1ull)))) continue;
         const int page = table[key >> page_shift];
         if (page < 0 || page >= c.num_pages) continue;
         const int64_t at = ((((int64_t)page << page_shift) + (key & (c.page_rows - 1))) * c.Hkv + kvh) * HD;
@@ -177,7 +193,7 @@ __device__ __noinline__ void add_odd(const GraftPagedCache& c, const void* V, co
 }
 
 // kTestWaits: pipeline waits bounded by a.wait_ns (the failure-path tests); otherwise by a constant.
-template <int DT, bool kTestWaits>
+template <int DT, bool kTestWaits, bool kWindow>
 __global__ void __launch_bounds__(NTHREADS, 1)
 wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a) {
     using E = Elem<DT>;
@@ -198,6 +214,9 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.G, T = a.shape.tile_tokens;
+    // an item's block v lies at block v, or v + gap behind the first tokens' blocks
+    const int behind = kWindow ? window_units(a.first, BN) : 0;
+    auto block_at = [&](int v, int gap) { return kWindow && v >= behind ? v + gap : v; };
 
     // Prologue that touches no global memory: it overlaps the previous kernel's tail.
     if (tid == 0) {
@@ -257,13 +276,14 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
             int k, j;      // place in the deal (-1: past the end), block
             int kvh;
             int blk0, nblk, keys, tok, two, b;  // of the item
+            int gap, low;  // (window)
             int row;       // first pool row / 8 of this lane's box of block j (out of bounds: zeros)
         };
         auto lookup = [&](Cur& c) {
             if (c.k < 0 || !issues) return;
-            const int key = (c.blk0 + c.j) * BN + lane * page_box;
+            const int key = block_at(c.blk0 + c.j, c.gap) * BN + lane * page_box;
             int row = 0x7fffffff >> 3;
-            if (key < c.keys) {
+            if (key < c.keys && (!kWindow || key < a.first || key + page_box > c.low)) {
                 const int page = a.c.block_table[(int64_t)c.b * a.c.max_pages + (key >> a.page_shift)];
                 if (page >= 0 && page < a.c.num_pages)
                     row = ((page << a.page_shift) + (key & (a.c.page_rows - 1))) >> 3;
@@ -286,6 +306,10 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
             c.tok = w.q0 + w.tok0;
             c.two = w.two;
             c.b = w.b;
+            if (kWindow) {
+                c.gap = w.gap;
+                c.low = w.L + (a.mask != nullptr ? 0 : w.tok0) - a.window + 1;
+            }
         };
         auto advance = [&](Cur& c) {
             if (c.k < 0) return;
@@ -482,6 +506,8 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
             // The block loop holds only counts; an edge block reads the item and the row's mask again, and so
             // does the epilogue.
             int nblk, edge;
+            int front = 0;          // (window) blocks before it some row does not see whole
+            bool searching = false;  // (window) the row may see its first key in a later block
             bool two;
             {
                 const Wide& w = *at;
@@ -489,16 +515,28 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                 two = w.two != 0;
                 // first block that some row of the tile does not see whole
                 edge = (a.mask != nullptr ? w.L : min(w.L + w.tok0 + t * T + 1, w.keys)) / BN - w.blk0;
+                if (kWindow) {
+                    edge -= w.gap;
+                    const int rows = a.mask != nullptr ? w.n : min(w.tok0 + (two ? 2 * T : T), w.n);
+                    const int low = w.L + rows - a.window;  // of the last row
+                    if (low > 0) front = (low + BN - 1) / BN - w.gap - w.blk0;
+                    searching = rtok < T && w.tok0 + t * T + rtok < w.n;
+                }
             }
-            auto row_of = [&](const Wide& w, int& tok, int& limit, uint64_t& anc) -> bool {
+            // (low, with a window: of the keys below the limit, those from it on and the first tokens' are seen)
+            auto row_of = [&](const Wide& w, int& tok, int& limit, int& low, uint64_t& anc) -> bool {
                 tok = w.tok0 + t * T + rtok;
                 const bool row_ok = rtok < T && tok < w.n;
-                limit = 0;
+                limit = low = 0;
                 anc = 0;
                 if (row_ok) {
                     limit = a.mask != nullptr ? w.L : w.L + tok + 1;
                     if (a.mask != nullptr)
                         anc = a.mask[w.q0 + tok] & (w.n >= 64 ? ~0ull : ((1ull << w.n) - 1ull));
+                    if (kWindow) {
+                        low = max(a.mask != nullptr ? min(window_low(anc, a.window, w.L), w.L) : limit - a.window, 0);
+                        anc = window_mask(anc, a.window, a.first, w.L);
+                    }
                 }
                 return row_ok;
             };
@@ -519,15 +557,17 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                     if (!ok) break;
                     ++g;
                     tc_fence_after();
-                    if (j >= edge) {
+                    if (j >= edge || (kWindow && j < front)) {
                         // Masked scores are written back as -inf, in a pass of their own over S in tensor memory:
                         // the block loop proper carries no masking code (inlined it cost all blocks 4%).
                         const Wide& w = *at;
-                        int tok, limit;
+                        int tok, limit, low;
                         uint64_t anc;
-                        row_of(w, tok, limit, anc);
+                        row_of(w, tok, limit, low, anc);
                         uint32_t keep[4];
-                        keep_bits(keep, (w.blk0 + j) * BN, limit, w.L, anc);
+                        const int kb = block_at(w.blk0 + j, w.gap) * BN;
+                        keep_bits(keep, kb, limit, w.L, anc);
+                        if (kWindow) hide_bits(keep, kb, a.first, low);
 #pragma unroll
                         for (int x = 0; x < BN / 32; ++x) {
                             float s[32];
@@ -539,7 +579,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                         }
                         tmem_wait_st();
                     }
-                    if (t == 0 && j >= edge) {
+                    if (t == 0 && (j >= edge || (kWindow && j < front))) {
                         // Tile 0 cleans the V block before either tile's PV reads it: rows past the last key
                         // (their pages may hold anything) and infinite or NaN elements that masked rows would
                         // multiply by zero.
@@ -549,8 +589,8 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                         uint8_t* v0 = gbase + OFF_V + (vb % SV) * BLK_BYTES;
                         bool odd = false;
                         const Wide& w = *at;
-                        const int kb = (w.blk0 + j) * BN, keys = w.keys;
-                        const int lo = max(w.L - kb, 0), n = BN - lo;
+                        const int kb = block_at(w.blk0 + j, w.gap) * BN, keys = w.keys;
+                        const int lo = kWindow && j < front ? 0 : max(w.L - kb, 0), n = BN - lo;
                         for (int x = r; x < n * 16; x += 128) {
                             const int rr = lo + x / 16, c16 = x % 16;
                             uint4* p = reinterpret_cast<uint4*>(v0 + (rr >> 3) * GROUP_BYTES +
@@ -578,6 +618,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                     bool rescale = false;
                     float2 acc;
                     float packed[BN / 2];
+                    const bool anew = kWindow && j > 0 && __any_sync(0xffffffffu, searching && m_used == -INFINITY);
                     // An item's first block takes its maximum; a later block is weighed against the running
                     // maximum and stands if its row sum stays small; otherwise it is weighed again with its
                     // own maximum (S is still in TMEM).
@@ -586,7 +627,7 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
 #pragma unroll
                         for (int x = 0; x < BN / 32; ++x) tmem_ld32(sbuf + x * 32, s + x * 32);
                         tmem_wait_ld();
-                        const bool full = j == 0 || pass == 1;
+                        const bool full = j == 0 || pass == 1 || anew;
                         if (full) {
                             float m8[8];
 #pragma unroll
@@ -646,9 +687,9 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
             {
                 const Wide w = *at;
                 const int kvh = w.kvh;
-                int tok, limit;
+                int tok, limit, low;
                 uint64_t anc;
-                const bool row_ok = row_of(w, tok, limit, anc);
+                const bool row_ok = row_of(w, tok, limit, low, anc);
                 const float inv = l_sum != 0.f ? 1.f / l_sum : 0.f;
                 const bool direct = w.part < 0;
                 typename E::T* orow =
@@ -685,9 +726,21 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                 if (*odd_word() == (uint32_t)k + 1 && row_ok) {
                     // (from the first block that tile 0 cleaned: what lies before is in the products as it is)
                     const int edge0 = (a.mask != nullptr ? w.L : min(w.L + w.tok0 + 1, w.keys)) / BN;
-                    add_odd<DT>(a.c, a.V, a.c.block_table + (int64_t)w.b * a.c.max_pages, a.page_shift, kvh,
-                                max(max(w.blk0, edge0) * BN, w.L), min((w.blk0 + w.nblk) * BN, w.keys), limit, w.L,
-                                anc, direct ? orow : nullptr, direct ? nullptr : part);
+                    const int32_t* table = a.c.block_table + (int64_t)w.b * a.c.max_pages;
+                    if (!kWindow) {
+                        add_odd<DT, false>(a.c, a.V, table, a.page_shift, kvh, max(max(w.blk0, edge0) * BN, w.L),
+                                           min((w.blk0 + w.nblk) * BN, w.keys), limit, 0, 0, w.L, anc,
+                                           direct ? orow : nullptr, direct ? nullptr : part);
+                    } else {
+                        for (int j = 0; j < w.nblk; ++j) {
+                            const int kb = block_at(w.blk0 + j, w.gap) * BN;
+                            const bool all = j < front;  // (cleaned from its first row on)
+                            if (!all && j < edge0 - w.gap - w.blk0) continue;
+                            add_odd<DT, true>(a.c, a.V, table, a.page_shift, kvh, all ? kb : max(kb, w.L),
+                                              min(kb + BN, w.keys), limit, a.first, low, w.L, anc,
+                                              direct ? orow : nullptr, direct ? nullptr : part);
+                        }
+                    }
                 }
             }
             gv += nblk;
@@ -795,18 +848,19 @@ join_kernel(const __grid_constant__ AttnArgs a) {
     // still lie in the SM's L1, and in one trip: the head's words, and the first task's row block at both places where
     // it can lie (15.9 -> 15.7 us, 40000 keys 45.2 -> 44.4).
     const Group* groups = reinterpret_cast<const Group*>(a.plan + a.shape.off_group);
-    __shared__ int32_t s_words[32];
-    static_assert(kHeadBytes == 64 && sizeof(Group) == 32, "16 + 8 + 8 words");
-    if (threadIdx.x < 32) {
-        const int x = threadIdx.x, g = min((int)blockIdx.x / (x < 24 ? 8 : 16), a.shape.max_groups - 1);
-        s_words[x] = __ldcg(x < 16 ? reinterpret_cast<const int32_t*>(a.plan) + x
-                                   : reinterpret_cast<const int32_t*>(groups + g) + (x & 7));
+    constexpr int kHead = kHeadBytes / 4;
+    __shared__ int32_t s_words[kHead + 16];
+    static_assert(kHeadBytes % 8 == 0 && sizeof(Group) == 32, "the head's words, 8 + 8");
+    if (threadIdx.x < kHead + 16) {
+        const int x = threadIdx.x, g = min((int)blockIdx.x / (x < kHead + 8 ? 8 : 16), a.shape.max_groups - 1);
+        s_words[x] = __ldcg(x < kHead ? reinterpret_cast<const int32_t*>(a.plan) + x
+                                      : reinterpret_cast<const int32_t*>(groups + g) + ((x - kHead) & 7));
     }
     __syncthreads();
     const PlanHead& head = *reinterpret_cast<const PlanHead*>(s_words);
     const int each = 8 * head.tiles, tasks = plan_fits(a, head) ? head.n_groups * each : 0;
     int task = blockIdx.x;
-    Group gr = *reinterpret_cast<const Group*>(s_words + (head.tiles == 1 ? 16 : 24));
+    Group gr = *reinterpret_cast<const Group*>(s_words + (head.tiles == 1 ? kHead : kHead + 8));
     griddep_wait();
     while (task < tasks) {
         join_rows<DT>(a, gr, task % each);
@@ -839,13 +893,13 @@ bool encode(CUtensorMap* m, int dtype, int rank, const void* ptr, const cuuint64
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DT>
+template <int DT, bool kWindow>
 int launch(const AttnArgs& a, const Maps& m, cudaStream_t st) {
     static bool attr_set[64][2] = {};
     int dev = 0;
     if (!cuda_ok(cudaGetDevice(&dev))) return GRAFT_ERR_CUDA;
     const bool test_waits = a.wait_ns != kWaitNs;
-    const auto kernel = test_waits ? wide_kernel<DT, true> : wide_kernel<DT, false>;
+    const auto kernel = test_waits ? wide_kernel<DT, true, kWindow> : wide_kernel<DT, false, kWindow>;
     if (dev < 0 || dev >= 64 || !attr_set[dev][test_waits]) {
         if (!cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES)))
             return GRAFT_ERR_CUDA;
@@ -877,7 +931,8 @@ int wide_launch(const AttnArgs& a, cudaStream_t st) {
         if (!encode(&m.k, a.c.dtype, 5, a.K, dims, strides, box)) return GRAFT_ERR_CUDA;
         if (!encode(&m.v, a.c.dtype, 5, a.V, dims, strides, box)) return GRAFT_ERR_CUDA;
     }
-    return a.c.dtype == GRAFT_BF16 ? launch<GRAFT_BF16>(a, m, st) : launch<GRAFT_FP16>(a, m, st);
+    if (a.window > 0) return a.c.dtype == GRAFT_BF16 ? launch<GRAFT_BF16, true>(a, m, st) : launch<GRAFT_FP16, true>(a, m, st);
+    return a.c.dtype == GRAFT_BF16 ? launch<GRAFT_BF16, false>(a, m, st) : launch<GRAFT_FP16, false>(a, m, st);
 }
 
 int join_launch(const AttnArgs& a, cudaStream_t st) {

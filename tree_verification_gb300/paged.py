@@ -12,6 +12,9 @@ enqueue one library call each on the current stream of the pools' device:
     cache.compact(path, acc_len)            accepted tree rows kept
     cache.fork(src, dst), cache.free(seqs)  sequences that share pages; pages given back
 
+Layers with a sliding window take a plan of their own, plan(..., window=, first=), and attend(..., window=, first=); a
+step's plans stand side by side.
+
 reserve, append, plan and compact take ``active`` ([n_seqs] bool on the device): sequences that are False there take no
 part, so a batch keeps its shape (and a captured step its graph) while sequences come and go.
 
@@ -37,6 +40,18 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _Reference = type(ctypes.byref(ctypes.c_int()))
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+
+def _kind(window: Optional[int], first: int):
+    """What tells the plans of a step apart: (window, first), or None without a window."""
+    if window is None:
+        if first != 0:
+            raise ValueError("first needs a window")
+        return None
+    if not (isinstance(window, int) and isinstance(first, int) and 1 <= window < 2**31 and 0 <= first < 2**31):
+        raise ValueError("window must be at least 1, first at least 0 (32 bits)")
+    return window, first
 
 
 class PagedCache:
@@ -97,8 +112,9 @@ class PagedCache:
         self._lib = gb.lib()
         self._structs = {}      # address of an ``active`` tensor -> the struct with it
         self._plan_of = None    # (N, Hq, max_new, tree) of the last plan
+        self._window_plans = {}  # (window, first) -> the same of the last plan with that window
         self._sizes = {}        # (N, Hq, max_new) -> bytes of plan and workspace
-        self._buffers = {}      # name -> buffer in use
+        self._buffers = {}      # name (a windowed plan's: its window and first) -> buffer in use
         self._kept = []         # buffers outgrown: captured graphs may still use them
         # a cache the kernels cannot take is refused here
         n = ctypes.c_size_t()
@@ -111,7 +127,7 @@ class PagedCache:
             with torch.cuda.device(self._index):
                 capturing = torch.cuda.is_current_stream_capturing()
             if capturing:
-                raise ValueError(f"the {name} buffer must grow: run the call once before capturing it")
+                raise ValueError(f"the {name if isinstance(name, str) else 'plan'} buffer must grow: run the call once before capturing it")
             if t is not None:
                 self._kept.append(t)
                 nbytes = max(nbytes, 2 * t.numel())
@@ -227,9 +243,17 @@ class PagedCache:
                        op, os)
         return out
 
-    def plan(self, q_start, N: int, Hq: int, max_new: int, tree: bool = False, active=None) -> None:
-        """graft_paged_plan for a step of N rows; serves every attend() until the next plan()."""
-        self._plan_of = None  # (a plan that is refused leaves none)
+    def plan(self, q_start, N: int, Hq: int, max_new: int, tree: bool = False, active=None, window: Optional[int] = None,
+             first: int = 0) -> None:
+        """graft_paged_plan for a step of N rows; serves every attend() until the next plan().
+
+        With ``window`` (and ``first``) graft_paged_plan_window, for the attend()s with the same two: a step whose
+        layers are of several kinds makes a plan of each.  (A handle keeps a plan buffer for every kind it has seen.)"""
+        kind = _kind(window, first)
+        if kind is None:  # (a plan that is refused leaves none)
+            self._plan_of = None
+        else:
+            self._window_plans.pop(kind, None)
         starts = self._need(q_start, "q_start", torch.int32, (self.n_seqs + 1,))
         key = (N, Hq, max_new)
         sizes = self._sizes.get(key)
@@ -242,19 +266,30 @@ class PagedCache:
             if len(self._sizes) >= 4096:
                 self._sizes.clear()
             sizes = self._sizes[key] = (a.value, b.value)
-        buf = self._buffer("plan", sizes[0], False)
+        buf = self._buffer("plan" if kind is None else kind, sizes[0], False)
         self._buffer("attention", sizes[1], True)
-        self._call("graft_paged_plan", self._with(active), N, Hq, starts, max_new, 1 if tree else 0, buf.data_ptr(),
-                   buf.numel())
-        self._plan_of = (N, Hq, max_new, bool(tree))
+        if kind is None:
+            self._call("graft_paged_plan", self._with(active), N, Hq, starts, max_new, 1 if tree else 0, buf.data_ptr(),
+                       buf.numel())
+        else:
+            self._call("graft_paged_plan_window", self._with(active), N, Hq, starts, max_new, 1 if tree else 0, *kind,
+                       buf.data_ptr(), buf.numel())
+        if kind is None:
+            self._plan_of = (N, Hq, max_new, bool(tree))
+        else:
+            self._window_plans[kind] = (N, Hq, max_new, bool(tree))
 
-    def attend(self, layer: int, Q, scale: float, mask=None, out=None, tuning=None):
+    def attend(self, layer: int, Q, scale: float, mask=None, out=None, tuning=None, window: Optional[int] = None,
+               first: int = 0):
         """graft_paged_attention of the planned step: Q [N][Hq][128] (rows may be strided), mask [N] int64 (the
         ancestor bits) for a tree plan; returns O [N][Hq][128].  ``tuning`` (a GraftAttnTuning or a dict of its
-        fields, of which wait_ns alone may be set) selects graft_paged_attention_ex."""
-        if self._plan_of is None:
-            raise ValueError("attend() needs a plan() of the step")
-        N, Hq, max_new, tree = self._plan_of
+        fields, of which wait_ns alone may be set) selects graft_paged_attention_ex.  With ``window`` (and ``first``)
+        graft_paged_attention_window: a row sees the last ``window`` positions and the ``first`` tokens alone."""
+        kind = _kind(window, first)
+        plan_of = self._plan_of if kind is None else self._window_plans.get(kind)
+        if plan_of is None:
+            raise ValueError("attend() needs a plan() of the step" + ("" if kind is None else " with this window"))
+        N, Hq, max_new, tree = plan_of
         if tree != (mask is not None):
             raise ValueError("a plan with tree=True takes a mask, one without takes none")
         layer = self._layer(layer)
@@ -263,8 +298,13 @@ class PagedCache:
             out = torch.empty((N, Hq, gb.HEAD_DIM), dtype=self.dtype, device=self.device)
         op = self._need(out, "out", self.dtype, (N, Hq, gb.HEAD_DIM))
         mp = None if mask is None else self._need(mask, "mask", torch.int64, (N,))
-        plan, ws = self._buffers["plan"], self._buffers["attention"]
-        if tuning is None:
+        plan, ws = self._buffers["plan" if kind is None else kind], self._buffers["attention"]
+        if kind is not None:
+            tuning = gb._tuning(tuning)
+            self._call("graft_paged_attention_window", self._c, self._kp[layer], self._vp[layer], N, Hq, max_new, *kind,
+                       plan.data_ptr(), plan.numel(), qp, qs, mp, float(scale), op,
+                       None if tuning is None else ctypes.addressof(tuning), ws.data_ptr(), ws.numel())
+        elif tuning is None:
             self._call("graft_paged_attention", self._c, self._kp[layer], self._vp[layer], N, Hq, max_new,
                        plan.data_ptr(), plan.numel(), qp, qs, mp, float(scale), op, ws.data_ptr(), ws.numel())
         else:
