@@ -61,7 +61,7 @@ struct Args {
     int N, V, block, top, chunks;  // chunks of a row
     int ctas;
     float c1;     // log2(e) / T
-    double inv_T;
+    float inv_T, inv_T_rest;  // 1 / T
     float* logprob;
     float* entropy;
     int32_t* rank;
@@ -266,18 +266,29 @@ __device__ __forceinline__ void finish(const Args& a, int n, bool ok, float give
                                        uint64_t list) {
     const int lane = threadIdx.x & 31;
     // a row of -inf alone has no law, nor has one with NaN or +inf: NaN
-    // (the last few operations in 64 bits: logits, maxima and ln s may be larger than what is left)
+    // The last few operations keep what they round off, as logits, maxima and ln s may be larger than what is left of
+    // them: (x - m) / T in two parts, ln s = e ln 2 + ln f with e 2839 / 4096 exact.
+    constexpr float kLn2 = 2839.f / 4096.f, kLn2Rest = 3.1946184945309e-5f;
     int e;
     float f = frexpf(s, &e);
     if (f < 0.70710678f) {  // (near one: of a certain token, s = 1, ln s is 0)
         f *= 2.f;
         --e;
     }
-    const double ln_s = m == -INFINITY ? (double)NAN : e * 0.69314718055994530942 + (double)logf(f);
-    auto logp = [&](float x) -> float { return (float)(((double)x - m) * a.inv_T - ln_s); };
+    const bool lawful = m > -INFINITY && s < INFINITY;  // (else NaN, below)
+    const float rest = lawful ? e * kLn2Rest + logf(f) : NAN, whole = e * kLn2;
+    const float ln_s = whole + rest;
+    auto logp = [&](float x) -> float {
+        const float d = x - m, q = d * a.inv_T;
+        if (!(fabsf(q) < INFINITY)) return q - rest;
+        const float back = d + m, lost = x - back + (m - (back - d));  // of x - m
+        const float left = fmaf(d, a.inv_T, -q) + d * a.inv_T_rest + lost * a.inv_T;
+        const float sum = q - whole, gone = sum - q;
+        return sum + (((q - (sum - gone)) + (-whole - gone)) + (left - rest));
+    };
     if (lane == 0) {
         a.logprob[n] = ok ? logp(given) : 0.f;
-        if (a.entropy != nullptr) a.entropy[n] = (float)(ln_s - 0.69314718055994530942 * (t / s));
+        if (a.entropy != nullptr) a.entropy[n] = ln_s - 0.693147181f * (t / s);
         if (a.rank != nullptr) a.rank[n] = ok ? cnt : -1;
     }
     if (a.top > 0) {
@@ -296,7 +307,7 @@ __device__ __forceinline__ void finish(const Args& a, int n, bool ok, float give
                 int skip = lane - known;
                 id = 0;
                 while ((used >> id & 1) || skip-- > 0) ++id;
-                lp = isnan(ln_s) ? NAN : -INFINITY;
+                lp = lawful ? -INFINITY : NAN;
             }
         }
         if (lane < a.top) {
@@ -866,7 +877,8 @@ extern "C" int graft_token_logprobs(int N, int V, int64_t n_logit_rows, int dtyp
     a.block = block;
     a.top = top;
     a.c1 = (float)(1.4426950408889634074 / (double)temperature);
-    a.inv_T = 1.0 / (double)temperature;
+    a.inv_T = (float)(1.0 / (double)temperature);
+    a.inv_T_rest = (float)(1.0 / (double)temperature - (double)a.inv_T);
     a.logprob = logprob;
     a.entropy = entropy;
     a.rank = rank;

@@ -196,6 +196,7 @@ struct Elem<GRAFT_BF16> {
     static __device__ __forceinline__ float2 up(uint32_t w) {
         return __bfloat1622float2(*reinterpret_cast<const T2*>(&w));
     }
+    static __device__ __forceinline__ T2 pack(uint32_t w) { return *reinterpret_cast<const T2*>(&w); }
     static __device__ __forceinline__ uint32_t down(float x, float y) {
         const T2 v = __floats2bfloat162_rn(x, y);
         return *reinterpret_cast<const uint32_t*>(&v);
@@ -210,6 +211,7 @@ struct Elem<GRAFT_FP16> {
     using T = __half;
     using T2 = __half2;
     static __device__ __forceinline__ float2 up(uint32_t w) { return __half22float2(*reinterpret_cast<const T2*>(&w)); }
+    static __device__ __forceinline__ T2 pack(uint32_t w) { return *reinterpret_cast<const T2*>(&w); }
     static __device__ __forceinline__ uint32_t down(float x, float y) {
         const T2 v = __floats2half2_rn(x, y);
         return *reinterpret_cast<const uint32_t*>(&v);

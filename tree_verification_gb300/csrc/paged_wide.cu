@@ -568,15 +568,14 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                         const int kb = block_at(w.blk0 + j, w.gap) * BN;
                         keep_bits(keep, kb, limit, w.L, anc);
                         if (kWindow) hide_bits(keep, kb, a.first, low);
+                        float s[BN];
 #pragma unroll
-                        for (int x = 0; x < BN / 32; ++x) {
-                            float s[32];
-                            tmem_ld32(sbuf + x * 32, s);
-                            tmem_wait_ld();
+                        for (int x = 0; x < BN / 32; ++x) tmem_ld32(sbuf + x * 32, s + x * 32);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) s[y] = ((keep[x] >> y) & 1u) ? s[y] : -INFINITY;
-                            tmem_st32(sbuf + x * 32, s);
-                        }
+                        for (int x = 0; x < BN; ++x) s[x] = ((keep[x >> 5] >> (x & 31)) & 1u) ? s[x] : -INFINITY;
+#pragma unroll
+                        for (int x = 0; x < BN / 32; ++x) tmem_st32(sbuf + x * 32, s + x * 32);
                         tmem_wait_st();
                     }
                     if (t == 0 && (j >= edge || (kWindow && j < front))) {
@@ -587,15 +586,29 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                         ok = __all_sync(0xffffffffu, mbar_wait(bar(BAR_VF + vb % SV), (vb / SV) & 1, wait_ns));
                         if (!ok) break;
                         uint8_t* v0 = gbase + OFF_V + (vb % SV) * BLK_BYTES;
-                        bool odd = false;
                         const Wide& w = *at;
                         const int kb = block_at(w.blk0 + j, w.gap) * BN, keys = w.keys;
                         const int lo = kWindow && j < front ? 0 : max(w.L - kb, 0), n = BN - lo;
-                        for (int x = r; x < n * 16; x += 128) {
-                            const int rr = lo + x / 16, c16 = x % 16;
-                            uint4* p = reinterpret_cast<uint4*>(v0 + (rr >> 3) * GROUP_BYTES +
-                                                                (c16 >> 3) * HALF_BYTES + (rr & 7) * 128 +
-                                                                (c16 & 7) * 16);
+                        // (a thread's pieces: every eighth row from its first on, one group apart)
+                        const int r0 = lo + r / 16, c16 = r % 16;
+                        uint8_t* first = v0 + (r0 >> 3) * GROUP_BYTES + (c16 >> 3) * HALF_BYTES + (r0 & 7) * 128 +
+                                         (c16 & 7) * 16;
+                        // Zero times any of them is zero, or there is something to take out.
+                        typename E::T2 zeros = E::pack(0u);
+#pragma unroll 4
+                        for (int x = 0; x < n - r / 16; x += 8) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(first + (x >> 3) * GROUP_BYTES);
+                            zeros = __hfma2(E::pack(v.x), E::pack(0u), zeros);
+                            zeros = __hfma2(E::pack(v.y), E::pack(0u), zeros);
+                            zeros = __hfma2(E::pack(v.z), E::pack(0u), zeros);
+                            zeros = __hfma2(E::pack(v.w), E::pack(0u), zeros);
+                        }
+                        const bool look = kb + BN > keys || E::odd(*reinterpret_cast<const uint32_t*>(&zeros));
+                        bool odd = false;
+#pragma unroll 1
+                        for (int x = 0; look && x < n - r / 16; x += 8) {
+                            const int rr = r0 + x;
+                            uint4* p = reinterpret_cast<uint4*>(first + (x >> 3) * GROUP_BYTES);
                             uint4 v = *p;
                             if (kb + rr >= keys) {
                                 *p = make_uint4(0, 0, 0, 0);
@@ -645,7 +658,8 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                                 const float m_new = fmaxf(mx, m_used);
                                 alpha = (m_used == -INFINITY) ? 1.f : ex2(m_used - m_new);
                                 m_used = m_new;
-                                rescale = true;
+                                // (a row that saw its first key has nothing to move)
+                                rescale = !kWindow || __any_sync(0xffffffffu, alpha != 1.f);
                             }
                         }
                         const float neg_m = kLift - ((m_used == -INFINITY) ? 0.f : m_used);
