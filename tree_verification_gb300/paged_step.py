@@ -8,6 +8,10 @@ the accepted rows stay where compaction puts them.  On one CUDA stream:
     ->  per layer: append (rotary positions by depth, K and V into pages), attend (tree mask)
     ->  graft_accept_compact without layers (acceptance alone)  ->  compact  ->  M update
 
+with queries and keys normed head by head before the rotation (``norms``), windows in some or all layers (``windows``,
+a plan for each kind) and log probabilities of the emitted tokens (``top_logprobs``) where the model and its server
+want them.
+
 Sequences fork and leave between steps with the cache's own calls; ``active``
 ([n_seqs] bool on the device, all True at first) says which the next steps
 verify.  An idle slot (a sequence that left, or one whose prompt is still
@@ -32,19 +36,24 @@ from typing import Callable, Optional, Sequence
 import torch
 
 from . import binding as gb
-from .paged import PagedCache
+from .paged import PagedCache, _kind
+from .step import EmittedLogprobs
 
 
 class PagedVerifyStep:
     """Buffers of one step for all sequences of ``cache`` (its n_seqs is the batch).
 
     inv_freq, interleaved and factor describe the rotary positions (graft_rope_append; inv_freq None: none).
-    m_policy, temperature and seed are VerifyStep's.
+    norms, if given, holds a pair (q_weight, k_weight) per layer, [128] float32 each, either of them or the pair None;
+    eps is the norms'.  windows, if given, holds per layer None (the layer sees everything), a window or a pair
+    (window, first) (graft_paged_attention_window).  m_policy, temperature, seed and top_logprobs are VerifyStep's;
+    in idle slots logprobs are those of no row.
     """
 
     def __init__(self, cfg: gb.GraftConfig, cache: PagedCache, Hq: int, inv_freq: Optional[torch.Tensor] = None,
                  interleaved: bool = False, factor: float = 1.0, m_policy: str = "tree", temperature: float = 0.0,
-                 seed: int = 0):
+                 seed: int = 0, norms: Optional[Sequence] = None, eps: float = 1e-6,
+                 windows: Optional[Sequence] = None, top_logprobs: Optional[int] = None):
         if m_policy not in ("tree", "emitted", "both"):
             raise ValueError("m_policy must be 'tree', 'emitted' or 'both'")
         if Hq % cache.Hkv:
@@ -56,6 +65,20 @@ class PagedVerifyStep:
         self.B = B = cache.n_seqs
         self.device = dev = cache.device
         self.n_layers = len(cache.K)
+        for name, x in (("norms", norms), ("windows", windows)):
+            if x is not None and len(x) != self.n_layers:
+                raise ValueError(f"{name} must hold one entry per layer")
+        # what each layer's append and attend take beside the tensors; every kind of window is planned once a step
+        pairs = [(None, None) if p is None else tuple(p) for p in ([None] * self.n_layers if norms is None else norms)]
+        for q, k in pairs:
+            for t in (q, k):
+                if t is not None:
+                    cache._need(t, "norms", torch.float32, (gb.HEAD_DIM,))
+        self._norms = [dict(q_norm=q, k_norm=k, eps=float(eps)) for q, k in pairs]
+        kinds = [None] * self.n_layers if windows is None else [_kind(*w) if isinstance(w, tuple) else _kind(w, 0)
+                                                                for w in windows]
+        self._windows = [dict() if k is None else dict(window=k[0], first=k[1]) for k in kinds]
+        self._plans = [w for i, w in enumerate(self._windows) if w not in self._windows[:i]]
         K = cfg.Kmax
         i32 = dict(dtype=torch.int32, device=dev)
         self.tree = dict(tok=torch.empty(B, K, **i32), parent=torch.empty(B, K, **i32),
@@ -78,6 +101,9 @@ class PagedVerifyStep:
         self._none = torch.full((), gb.EMPTY_TOKEN, **i32)
         self._no_layers = torch.empty(0, dtype=torch.int64, device=dev)
         self._lengths = torch.empty(B, **i32)  # the acceptance's copy (0 in idle slots): compaction advances the cache's own
+        self._emitted = None if top_logprobs is None else EmittedLogprobs(B, K, cfg.V, top_logprobs, self.temperature, dev)
+        self.logprobs = None if self._emitted is None else self._emitted.out
+        self._path = torch.empty(B, K, **i32)  # the accepted path for logprobs, none in idle slots
         self.O = torch.zeros(B, K, Hq, gb.HEAD_DIM, dtype=cache.dtype, device=dev)
         self.Qr = torch.empty_like(self.O)
         self.scale = 1.0 / math.sqrt(gb.HEAD_DIM)
@@ -103,14 +129,16 @@ class PagedVerifyStep:
         c.reserve(self.rows, active=part)
         gb.graft_build_tree(self.cfg, draft_logits, root_tok, M_succ, c.lengths, out=self.tree, status=self.status,
                             ws=self.ws_tree)
-        c.plan(self.q_start, B * Kmax, self.Hq, Kmax, tree=True, active=part)
+        for w in self._plans:
+            c.plan(self.q_start, B * Kmax, self.Hq, Kmax, tree=True, active=part, **w)
         pos, mask = self.tree["pos"].view(-1), self.tree["mask"].view(-1)
         q, o = self.Qr.view(B * Kmax, self.Hq, gb.HEAD_DIM), self.O.view(B * Kmax, self.Hq, gb.HEAD_DIM)
         for layer in range(self.n_layers):
             ready(layer)
             c.append(layer, Q[layer], K[layer], V[layer], self.q_start, inv_freq=self.inv_freq,
-                     interleaved=self.interleaved, positions=pos, factor=self.factor, out=q, active=part)
-            c.attend(layer, q, self.scale, mask=mask, out=o)
+                     interleaved=self.interleaved, positions=pos, factor=self.factor, out=q, active=part,
+                     **self._norms[layer])
+            c.attend(layer, q, self.scale, mask=mask, out=o, **self._windows[layer])
             if attended is not None:
                 attended(layer, self.O)
         ready("accept")
@@ -125,6 +153,9 @@ class PagedVerifyStep:
                                     argmax=self.acc["argmax"], V=self.cfg.V)
         else:
             gb.graft_accept_compact(target_logits, *args, out=self.acc, status=self.status, ws=self.ws_acc)
+        if self._emitted is not None:
+            torch.where(on[:, None], self.acc["path"], self._none, out=self._path)
+            self._emitted.run(target_logits, self.acc["out_tok"], self._path, self.status)
         self.acc["acc_len"].mul_(on)
         c.compact(self.acc["path"], self.acc["acc_len"], active=part)
         if self.m_policy in ("tree", "both"):

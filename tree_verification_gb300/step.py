@@ -15,6 +15,13 @@ target argmax) pair (graft_update_M); "emitted" adds the bigrams of the
 tokens the step emitted (graft_update_M_emitted), the prompt-evidence policy
 that ``prefill_M`` seeds with the prompt's bigrams; "both" does both.
 
+With ``top_logprobs`` = k (0 for none of the alternatives) the step also gives
+``logprobs``: the log probabilities of its emitted tokens under the target, the
+law's entropy, the tokens' rank and the k most likely alternatives
+(graft_token_logprobs over the accepted path's rows of the target logits), each
+[B][Kmax] (alternatives [B][Kmax][k]) beside ``acc["out_tok"]``; at
+``temperature`` > 0 those of the law that was sampled.
+
 Because every buffer is fixed, a whole step can be captured once in a CUDA
 graph and replayed, which removes the per-layer host launch cost.  The
 caller owns the model-side tensors: drafter and target logits, per-layer
@@ -30,10 +37,33 @@ import torch
 from . import binding as gb
 
 
+class EmittedLogprobs:
+    """Buffers and the call behind a step's ``top_logprobs``: graft_token_logprobs of its emitted tokens."""
+
+    def __init__(self, B: int, Kmax: int, V: int, top: int, temperature: float, device):
+        if isinstance(top, bool) or not isinstance(top, int) or not 0 <= top <= min(gb.MAX_TOP_LOGPROBS, V):
+            raise ValueError(f"top_logprobs must be a whole number from 0 to {min(gb.MAX_TOP_LOGPROBS, V)}")
+        self.shape, self.top, self.temperature = (B, Kmax, V), top, temperature if temperature > 0.0 else 1.0
+        f32, i32 = dict(dtype=torch.float32, device=device), dict(dtype=torch.int32, device=device)
+        self.out = dict(logprob=torch.zeros(B, Kmax, **f32), entropy=torch.zeros(B, Kmax, **f32),
+                        rank=torch.zeros(B, Kmax, **i32), top_id=torch.zeros(B, Kmax, top, **i32),
+                        top_logprob=torch.zeros(B, Kmax, top, **f32))
+        self._flat = {k: v.view(B * Kmax, *v.shape[2:]) for k, v in self.out.items()}
+        with torch.cuda.device(device):  # (a size that goes by the device)
+            self.ws = torch.empty(gb.graft_token_logprobs_workspace_size(B * Kmax, V, top), dtype=torch.uint8,
+                                  device=device)
+
+    def run(self, target_logits, out_tok, path, status) -> None:
+        B, Kmax, V = self.shape
+        gb.graft_token_logprobs(target_logits.view(B * Kmax, V), out_tok.view(-1), rows=path.view(-1), block=Kmax,
+                                top=self.top, temperature=self.temperature, out=self._flat, status=status, ws=self.ws)
+
+
 class VerifyStep:
     def __init__(self, cfg: gb.GraftConfig, B: int, Hq: int, Hkv: int, n_layers: int, Lcap: int, device,
                  Kc: Sequence[torch.Tensor], Vc: Sequence[torch.Tensor], Kt: Sequence[torch.Tensor],
-                 Vt: Sequence[torch.Tensor], m_policy: str = "tree", temperature: float = 0.0, seed: int = 0):
+                 Vt: Sequence[torch.Tensor], m_policy: str = "tree", temperature: float = 0.0, seed: int = 0,
+                 top_logprobs: Optional[int] = None):
         if m_policy not in ("tree", "emitted", "both"):
             raise ValueError("m_policy must be 'tree', 'emitted' or 'both'")
         self.m_policy = m_policy
@@ -58,6 +88,8 @@ class VerifyStep:
         self.ws_upd = torch.empty(max(1, gb.graft_update_M_workspace_size(B * K)), **u8)
         self.ws_emit = torch.empty(max(1, gb.graft_update_M_emitted_workspace_size(B, K)), **u8)
         self.ws_smp = torch.empty(max(1, gb.graft_sample_tokens_workspace_size(B, K, cfg.V)), **u8)
+        self._emitted = None if top_logprobs is None else EmittedLogprobs(B, K, cfg.V, top_logprobs, self.temperature, dev)
+        self.logprobs = None if self._emitted is None else self._emitted.out
         self.O = torch.empty(B, K, Hq, gb.HEAD_DIM, dtype=torch.bfloat16, device=dev)
         self.Kc, self.Vc, self.Kt, self.Vt = list(Kc), list(Vc), list(Kt), list(Vt)
         self.Kc_ptrs = gb.layer_pointers(self.Kc, dev)
@@ -100,6 +132,8 @@ class VerifyStep:
             gb.graft_accept_compact(target_logits, self.tree["tok"], self.tree["parent"], self.tree["depth"],
                                     self.Kc_ptrs, self.Vc_ptrs, self.Kt_ptrs, self.Vt_ptrs, self.n_layers, self.Hkv,
                                     self.Lcap, L, out=self.acc, status=self.status, ws=self.ws_acc)
+        if self._emitted is not None:
+            self._emitted.run(target_logits, self.acc["out_tok"], self.acc["path"], self.status)
         if self.m_policy in ("tree", "both"):
             gb.graft_update_M(M_succ, M_cnt, self.tree["tok"].view(-1), self.acc["argmax"].view(-1),
                               status=self.status, ws=self.ws_upd)
