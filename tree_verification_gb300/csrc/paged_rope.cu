@@ -168,14 +168,18 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
     const int i = tid & 7, h_first = tid >> 3;
     const bool rotates = i < rot_units;
     const int c0 = rotates && !a.inter ? i : 2 * i, c1 = rotates && !a.inter ? i + rot_units : 2 * i + 1;
-    uint4 buf[kAhead][2];
+    // Without norms a thread's heads are read and turned in one row, whoever they belong to.  With norms, which cost
+    // registers and instructions, Q's heads come kQ of a thread's at a time, K's and V's one by one: what is whose is known
+    // once a pass, not a head (5100 rows of 72 heads: 41.4 -> 35.5 us; without norms 45.8 -> 43.4 for 11000 rows of 48, but
+    // 9.8 -> 10.6 for 2048).
+    uint4 buf[kNorm ? 1 : kAhead][2];
     auto fetch = [&](int t, int h0) {
         const int64_t row = t0 + t;
         const uint4* q = a.Q + row * a.qs;
         const uint4* k = a.K + row * a.ks - a.Hq * 16;
         const uint4* v = a.V + row * a.vs - turned * 16;
 #pragma unroll
-        for (int x = 0; x < kAhead; ++x) {
+        for (int x = 0; x < (kNorm ? 1 : kAhead); ++x) {
             const int h = h0 + x * kStep;
             if (h < heads) {
                 const uint4* src = (h < a.Hq ? q : h < turned ? k : v) + h * 16;
@@ -184,7 +188,30 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
             }
         }
     };
-    fetch(0, h_first);
+    constexpr int kQ = kNorm ? kAhead - 1 : 1;
+    uint4 bq[kQ][2], bkv[2];
+    auto fetch_q = [&](int t, int h0) {
+        const uint4* q = a.Q + (int64_t)(t0 + t) * a.qs + h0 * 16;
+#pragma unroll
+        for (int x = 0; x < kQ; ++x)
+            if (h0 + x * kStep < a.Hq) {
+                bq[x][0] = q[x * kStep * 16 + c0];
+                bq[x][1] = q[x * kStep * 16 + c1];
+            }
+    };
+    auto fetch_kv = [&](int t, int h) {  // K's head h, or V's h - Hkv
+        if (h >= 2 * a.c.Hkv) return;
+        const bool v = h >= a.c.Hkv;
+        const uint4* src = v ? a.V + (int64_t)(t0 + t) * a.vs + (h - a.c.Hkv) * 16 : a.K + (int64_t)(t0 + t) * a.ks + h * 16;
+        bkv[0] = src[v ? 2 * i : c0];
+        bkv[1] = src[v ? 2 * i + 1 : c1];
+    };
+    if constexpr (kNorm) {
+        fetch_q(0, h_first);
+        fetch_kv(0, h_first);
+    } else {
+        fetch(0, h_first);
+    }
     if constexpr (kNorm) {
         static_assert(kThreads == HD, "a weight a thread");
         const int j = tid >> 4, e = tid & 15;
@@ -237,53 +264,90 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
         s_dst[warp] = page_at >= 0 && ours ? ((int64_t)page << a.page_shift) + (r & (a.c.page_rows - 1)) : -1;
     }
     __syncthreads();
-    for (int t = 0; t < nt; ++t) {
-        if (!s_live[t]) {
-            if (t + 1 < nt) fetch(t + 1, h_first);
-            continue;
-        }
-        float4 cs[4];
-        if (rotates) {
-            const float4* s = reinterpret_cast<const float4*>(&s_cs[t][i * 8]);
+    if constexpr (!kNorm) {
+        for (int t = 0; t < nt; ++t) {
+            if (!s_live[t]) {
+                if (t + 1 < nt) fetch(t + 1, h_first);
+                continue;
+            }
+            float4 cs[4];
+            if (rotates) {
+                const float4* s = reinterpret_cast<const float4*>(&s_cs[t][i * 8]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) cs[k] = s[k];
-        }
-        const int64_t dst = s_dst[t];
-        uint4* q = a.Q_out + (int64_t)(t0 + t) * a.qos;
-        uint4* k = a.K_pool + (dst * a.c.Hkv - a.Hq) * 16;
-        uint4* v = a.V_pool + (dst * a.c.Hkv - turned) * 16;
-        for (int h0 = h_first; h0 < heads; h0 += kAhead * kStep) {
-            if (h0 > h_first) fetch(t, h0);
+                for (int k = 0; k < 4; ++k) cs[k] = s[k];
+            }
+            const int64_t dst = s_dst[t];
+            uint4* q = a.Q_out + (int64_t)(t0 + t) * a.qos;
+            uint4* k = a.K_pool + (dst * a.c.Hkv - a.Hq) * 16;
+            uint4* v = a.V_pool + (dst * a.c.Hkv - turned) * 16;
+            for (int h0 = h_first; h0 < heads; h0 += kAhead * kStep) {
+                if (h0 > h_first) fetch(t, h0);
 #pragma unroll
-            for (int x = 0; x < kAhead; ++x) {
-                const int h = h0 + x * kStep;
-                if (h >= heads) continue;
-                uint4 x0 = buf[x][0], x1 = buf[x][1];
-                const bool normed = kNorm && h < turned && a.norm_w[h < a.Hq ? 0 : 1] != nullptr;
-                if (normed) {
-                    using E = Elem<DT>;
-                    float f[16];
-                    norm_head<DT>(x0, x1, &s_w[kNorm && h >= a.Hq][kNorm ? i * kWeightStep : 0], a.eps, f);
-                    if (rotates && a.inter) {
+                for (int x = 0; x < kAhead; ++x) {
+                    const int h = h0 + x * kStep;
+                    if (h >= heads) continue;
+                    uint4 x0 = buf[x][0], x1 = buf[x][1];
+                    if (rotates && h < turned) {
+                        uint32_t* w0 = &x0.x;
+                        uint32_t* w1 = &x1.x;
+                        if (a.inter) {
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            turn_pair(f[4 * z], f[4 * z + 1], cs[z].x, cs[z].y);
-                            turn_pair(f[4 * z + 2], f[4 * z + 3], cs[z].z, cs[z].w);
-                        }
-                    } else if (rotates) {
+                            for (int z = 0; z < 2; ++z) {
+                                w0[2 * z] = turn1<DT>(w0[2 * z], make_float2(cs[z].x, cs[z].y));
+                                w0[2 * z + 1] = turn1<DT>(w0[2 * z + 1], make_float2(cs[z].z, cs[z].w));
+                                w1[2 * z] = turn1<DT>(w1[2 * z], make_float2(cs[z + 2].x, cs[z + 2].y));
+                                w1[2 * z + 1] = turn1<DT>(w1[2 * z + 1], make_float2(cs[z + 2].z, cs[z + 2].w));
+                            }
+                        } else {
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            turn_pair(f[2 * z], f[8 + 2 * z], cs[z].x, cs[z].y);
-                            turn_pair(f[2 * z + 1], f[9 + 2 * z], cs[z].z, cs[z].w);
+                            for (int z = 0; z < 4; ++z)
+                                w0[z] = turn2<DT>(w0[z], w1[z], make_float2(cs[z].x, cs[z].y), make_float2(cs[z].z, cs[z].w));
                         }
                     }
-                    x0 = make_uint4(E::down(f[0], f[1]), E::down(f[2], f[3]), E::down(f[4], f[5]), E::down(f[6], f[7]));
-                    x1 = make_uint4(E::down(f[8], f[9]), E::down(f[10], f[11]), E::down(f[12], f[13]),
-                                    E::down(f[14], f[15]));
-                } else if (rotates && h < turned) {
+                    if (h >= a.Hq && dst < 0) continue;
+                    uint4* to = (h < a.Hq ? q : h < turned ? k : v) + h * 16;
+                    to[h < turned ? c0 : 2 * i] = x0;
+                    to[h < turned ? c1 : 2 * i + 1] = x1;
+                }
+            }
+            if (t + 1 < nt) fetch(t + 1, h_first);
+        }
+    } else {
+        for (int t = 0; t < nt; ++t) {
+            if (s_live[t]) {
+                float4 cs[4];
+                if (rotates) {
+                    const float4* s = reinterpret_cast<const float4*>(&s_cs[t][i * 8]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) cs[k] = s[k];
+                }
+                // a head of Q (which 0) or K, in place
+                auto turn = [&](int which, uint4& x0, uint4& x1) {
+                    using E = Elem<DT>;
                     uint32_t* w0 = &x0.x;
                     uint32_t* w1 = &x1.x;
-                    if (a.inter) {
+                    if (kNorm && a.norm_w[which] != nullptr) {
+                        float f[16];
+                        norm_head<DT>(x0, x1, &s_w[kNorm ? which : 0][kNorm ? i * kWeightStep : 0], a.eps, f);
+                        if (rotates && a.inter) {
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                turn_pair(f[4 * z], f[4 * z + 1], cs[z].x, cs[z].y);
+                                turn_pair(f[4 * z + 2], f[4 * z + 3], cs[z].z, cs[z].w);
+                            }
+                        } else if (rotates) {
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                turn_pair(f[2 * z], f[8 + 2 * z], cs[z].x, cs[z].y);
+                                turn_pair(f[2 * z + 1], f[9 + 2 * z], cs[z].z, cs[z].w);
+                            }
+                        }
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            w0[z] = E::down(f[2 * z], f[2 * z + 1]);
+                            w1[z] = E::down(f[8 + 2 * z], f[9 + 2 * z]);
+                        }
+                    } else if (rotates && a.inter) {
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
                             w0[2 * z] = turn1<DT>(w0[2 * z], make_float2(cs[z].x, cs[z].y));
@@ -291,19 +355,39 @@ rope_append_kernel(const __grid_constant__ RopeArgs a) {
                             w1[2 * z] = turn1<DT>(w1[2 * z], make_float2(cs[z + 2].x, cs[z + 2].y));
                             w1[2 * z + 1] = turn1<DT>(w1[2 * z + 1], make_float2(cs[z + 2].z, cs[z + 2].w));
                         }
-                    } else {
+                    } else if (rotates) {
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
                             w0[z] = turn2<DT>(w0[z], w1[z], make_float2(cs[z].x, cs[z].y), make_float2(cs[z].z, cs[z].w));
                     }
+                };
+                uint4* q = a.Q_out + (int64_t)(t0 + t) * a.qos;
+                for (int h0 = h_first; h0 < a.Hq; h0 += kQ * kStep) {
+                    if (h0 > h_first) fetch_q(t, h0);
+#pragma unroll
+                    for (int x = 0; x < kQ; ++x) {
+                        if (h0 + x * kStep >= a.Hq) continue;
+                        turn(0, bq[x][0], bq[x][1]);
+                        q[(h0 + x * kStep) * 16 + c0] = bq[x][0];
+                        q[(h0 + x * kStep) * 16 + c1] = bq[x][1];
+                    }
                 }
-                if (h >= a.Hq && dst < 0) continue;
-                uint4* to = (h < a.Hq ? q : h < turned ? k : v) + h * 16;
-                to[h < turned ? c0 : 2 * i] = x0;
-                to[h < turned ? c1 : 2 * i + 1] = x1;
+                const int64_t dst = s_dst[t];
+                for (int h = h_first; h < 2 * a.c.Hkv; h += kStep) {
+                    if (h > h_first) fetch_kv(t, h);
+                    const bool v = h >= a.c.Hkv;
+                    if (!v) turn(1, bkv[0], bkv[1]);
+                    if (dst < 0) continue;
+                    uint4* to = (v ? a.V_pool - a.c.Hkv * 16 : a.K_pool) + (dst * a.c.Hkv + h) * 16;
+                    to[v ? 2 * i : c0] = bkv[0];
+                    to[v ? 2 * i + 1 : c1] = bkv[1];
+                }
+            }
+            if (t + 1 < nt) {
+                fetch_q(t + 1, h_first);
+                fetch_kv(t + 1, h_first);
             }
         }
-        if (t + 1 < nt) fetch(t + 1, h_first);
     }
 }
 
