@@ -30,8 +30,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kVecs = 4;       // 16-byte pieces of a chunk a thread
-constexpr int kStages = 3;     // chunks in shared memory: one worked on, the others on their way
-constexpr int kResident = 3;   // CTAs an SM
+constexpr int kStages = 4;     // chunks in shared memory: one worked on, the others on their way
+// CTAs an SM: three of 80 registers left spills in the 16-bit kernels and no room for a fourth stage (1024 rows of 151936:
+// fp32 138 us with three, 134 with two; bf16 161 and 120).
+constexpr int kResident = 2;
 constexpr int kSeg = 40;       // chunks of a segment
 constexpr int kMaxRows = 160;  // rows of a CTA's runs at most
 constexpr int kShort = 4096;   // logits of a row that a warp takes
@@ -122,14 +124,6 @@ __device__ __forceinline__ uint64_t exchange(uint64_t k, int lane, int step, boo
     const uint64_t o = __shfl_xor_sync(0xffffffffu, k, step);
     const bool upper = (lane & step) == 0;
     return (upper == down) == (k > o) ? k : o;
-}
-// A warp's 32 keys in falling order.
-__device__ __forceinline__ uint64_t sort_keys(uint64_t k, int lane) {
-#pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-        for (int step = size >> 1; step > 0; step >>= 1) k = exchange(k, lane, step, (lane & size) == 0);
-    return k;
 }
 // The best 32 of two falling lists, in falling order.
 __device__ __forceinline__ uint64_t merge_keys(uint64_t a, uint64_t b, int lane) {
@@ -331,63 +325,62 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     __shared__ float2 s_xt[kMaxRows];  // the given token's logit, and the largest number below it
     constexpr int kCap = kWarpTeam ? 1024 : 256;
     __shared__ unsigned short s_max[kMaxChunks][kThreads];  // a segment's largest, by chunk and thread: upper bf16 bounds
-    __shared__ uint64_t s_cand[kCap];  // candidates
+    __shared__ uint64_t s_cand[kCap + kTeams * 32];  // candidates, and the best so far behind them
+    __shared__ uint64_t s_list[kTeams][32];          // the best so far, best first; 0: none
     __shared__ int s_n[kTeams][2], s_scan[kWarps];
-    __shared__ float s_kth[kTeams];      // the list's last, -inf: it is not full
     __shared__ float s_reach[32];
     __shared__ float4 s_red[2][kWarps];  // the warps' sums at a part's end, by its parity
     __shared__ uint64_t s_best[kWarps];
     griddep_enter();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
     // ---- which rows
-    auto row_at = [&](int n, int64_t r) -> int64_t {  // of entry n whose row is given as r, -1: none
-        if (r < 0) return -1;
-        const int64_t at = a.block > 0 ? (int64_t)(n / a.block) * a.block + r : r;
-        return (a.block > 0 && r >= a.block) || at >= a.R ? -1 : at;
+    // A row number is good if it lies within the logits and, with blocks, within its block.  (Where the logits hold all
+    // of the entries' blocks, as they do in a step, that takes no division.)
+    const bool whole = a.block > 0 && a.R >= ((int64_t)a.N + a.block - 1) / a.block * a.block;
+    auto good = [&](int n, int64_t r) {
+        if (r < 0) return false;
+        if (a.block == 0) return r < a.R;
+        return r < a.block && (whole || (int64_t)(n / a.block) * a.block + r < a.R);
     };
-    // With `rows`, a thread looks at kLook entries side by side (again for every kThreads x kLook of them); `seen`
-    // entries before it have a row.  each(n, row, rank of the row).
-    constexpr int kLook = 16;
+    // With `rows`: kLook entries a lane side by side, kThreads x kLook at a time.  have[x]: the warp's entries that
+    // have a row among the x-th 32.
+    constexpr int kLook = 16, kLot = kThreads * kLook;
     int n_rows = a.N;
     int32_t given[kLook];
-    auto look = [&](int n0) {  // reads the entries; how many before the thread's have rows, and how many do in all
-        const int first = n0 + tid * kLook;
+    unsigned have[kLook];
+    auto entry_of = [&](int n0, int x) { return n0 + (warp * kLook + x) * 32 + lane; };
+    auto look = [&](int n0) {  // how many rows the warps before this one have, and how many there are
 #pragma unroll
-        for (int x = 0; x < kLook; ++x) given[x] = first + x < a.N ? a.rows[first + x] : -1;
+        for (int x = 0; x < kLook; ++x) given[x] = entry_of(n0, x) < a.N ? a.rows[entry_of(n0, x)] : -1;
         int mine = 0;
 #pragma unroll
-        for (int x = 0; x < kLook; ++x) mine += row_at(first + x, given[x]) >= 0;
-        int up = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, up, d);
-            if (lane >= d) up += y;
+        for (int x = 0; x < kLook; ++x) {
+            have[x] = __ballot_sync(0xffffffffu, good(entry_of(n0, x), given[x]));
+            mine += __popc(have[x]);
         }
         __syncthreads();
-        if (lane == 31) s_scan[warp] = up;
+        if (lane == 0) s_scan[warp] = mine;
         __syncthreads();
-        int before = up - mine, all = 0;
+        int2 n = make_int2(0, 0);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += s_scan[w];
-            all += s_scan[w];
+            if (w < warp) n.x += s_scan[w];
+            n.y += s_scan[w];
         }
-        return make_int2(before, all);
+        return n;
     };
     int2 seen = make_int2(0, 0);
     if (a.rows != nullptr) {
         n_rows = 0;
-        for (int n0 = 0; n0 < a.N; n0 += kThreads * kLook) {
+        const int each = (a.N + (int)gridDim.x - 1) / (int)gridDim.x;  // entries without a row: every CTA sees to its share
+        for (int n0 = 0; n0 < a.N; n0 += kLot) {
             seen = look(n0);
             n_rows += seen.y;
-            // entries without a row: every CTA sees to every gridDim-th
-            const int first = n0 + tid * kLook, skip = (int)gridDim.x - 1 - (first + (int)gridDim.x - 1 - cta) % (int)gridDim.x;
 #pragma unroll
             for (int x = 0; x < kLook; ++x) {
-                const int n = first + x;
-                if (n >= a.N || row_at(n, given[x]) >= 0) continue;
-                if (given[x] != -1 && cta == 0) flag_status(a.status, GRAFT_STATUS_ROW);
-                if (x < skip || (x - skip) % (int)gridDim.x != 0) continue;
+                const int n = entry_of(n0, x);
+                if (n >= a.N || (have[x] >> lane & 1) || n < cta * each || n >= (cta + 1) * each) continue;
+                if (given[x] != -1) flag_status(a.status, GRAFT_STATUS_ROW);
                 a.logprob[n] = 0.f;
                 if (a.entropy != nullptr) a.entropy[n] = 0.f;
                 if (a.rank != nullptr) a.rank[n] = -1;
@@ -407,29 +400,21 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     const int64_t cta_u0 = shares.first(t_first), cta_u1 = shares.first(min(t_first + kTeams, teams));
     const int cta_r0 = (int)quotient(cta_u0, per_row), cta_r1 = (int)quotient(cta_u1 - 1, per_row);
     auto take = [&](int r, int n, int64_t at) {
-        const int tok = a.tokens[n];
-        const char* row = a.logits + at * a.stride;
-        const bool ok = tok >= 0 && tok < a.V;
         s_entry[r - cta_r0] = n;
-        s_row[r - cta_r0] = row;
-        s_tok[r - cta_r0] = ok ? tok : -1;
-        const float x = ok ? load_logit<DT>(row, tok) : INFINITY;
-        s_xt[r - cta_r0] = make_float2(x, below<DT>(x));
-        if (!ok && tok != -1) flag_status(a.status, GRAFT_STATUS_TOKEN_RANGE);
+        s_row[r - cta_r0] = a.logits + at * a.stride;
     };
     if (a.rows == nullptr) {
         for (int r = cta_r0 + tid; r <= cta_r1; r += kThreads) take(r, r, r);
     } else {
-        for (int n0 = 0, r0 = 0; n0 < a.N; n0 += kThreads * kLook) {
-            if (a.N > kThreads * kLook) seen = look(n0);  // (else they are at hand)
+        for (int n0 = 0, r0 = 0; n0 < a.N; n0 += kLot) {
+            if (a.N > kLot) seen = look(n0);  // (else they are at hand)
             int r = r0 + seen.x;
 #pragma unroll
             for (int x = 0; x < kLook; ++x) {
-                const int n = n0 + tid * kLook + x;
-                const int64_t at = row_at(n, given[x]);
-                if (at < 0) continue;
-                if (r >= cta_r0 && r <= cta_r1) take(r, n, at);
-                ++r;
+                const int n = entry_of(n0, x), at = r + __popc(have[x] & ((1u << lane) - 1u));
+                if ((have[x] >> lane & 1) && at >= cta_r0 && at <= cta_r1)
+                    take(at, n, a.block > 0 ? (int64_t)(n / a.block) * a.block + given[x] : given[x]);
+                r += __popc(have[x]);
             }
             r0 += seen.y;
         }
@@ -437,18 +422,18 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     if (tid < 2 * kTeams) s_n[tid >> 1][tid & 1] = 0;
     __syncthreads();
     const int team = kWarpTeam ? warp : 0;
-    if (t_first + team >= teams) return;  // (warps alone from here on)
+    const bool idle = t_first + team >= teams;  // (warps of the last CTA)
     const int ttid = kWarpTeam ? lane : tid;
     auto sync = [&]() {
         if (kWarpTeam) __syncwarp();
         else __syncthreads();
     };
     constexpr int kTeamCap = kCap / kTeams;
-    uint64_t* cand = s_cand + team * kTeamCap;
+    uint64_t* cand = s_cand + team * (kTeamCap + 32);
 
     // ---- the run: chunk c of row j of the list
-    const int64_t u0 = shares.first(t_first + team);
-    int left = (int)(shares.first(t_first + team + 1) - u0) * (kWarpTeam ? a.chunks : 1);  // chunks
+    const int64_t u0 = shares.first(t_first + (idle ? 0 : team));
+    int left = idle ? 0 : (int)(shares.first(t_first + team + 1) - u0) * (kWarpTeam ? a.chunks : 1);  // chunks
     const int row0 = (int)quotient(u0, per_row);
     int j = row0 - cta_r0, c = (int)(u0 - (int64_t)row0 * per_row);
     constexpr int kChunk = kVecs * kTeam * E;  // logits
@@ -457,7 +442,8 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     auto start_of = [&](const char* row) {
         return reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15);
     };
-    auto inside = [&](int c, int off) { return (c > 0 || off == 0) && (c + 1) * kChunk - off <= a.V; };
+    // chunks of a row that lie within it: [x, y)
+    auto inside_of = [&](int off) { return make_int2(off != 0, (a.V + off) / kChunk); };
     // (what of other rows lies in a row's first and last 16 bytes may be read, what lies around the logits may not)
     auto readable = [&](const char* p) { return p >= a.logits && p + 16 <= a.logits_end; };
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(s_ring)) + tid * 16;
@@ -465,14 +451,14 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     int j_in = j, c_in = c, in = left;
     uint32_t dst = ring;
     const char* src = start_of(s_row[j]) + ((int64_t)c * (kVecs * kTeam) + ttid) * 16;
+    int2 in_whole = inside_of(offset_of(s_row[j]));
     auto issue = [&]() {  // the next chunk's copies (a thread's own pieces: it waits for them alone)
         if (in > 0) {
-            const int off = offset_of(s_row[j_in]);
-            if (inside(c_in, off)) {
+            if (c_in >= in_whole.x && c_in < in_whole.y) {
 #pragma unroll
                 for (int x = 0; x < kVecs; ++x) cp_async16(dst + x * kThreads * 16, src + x * kTeam * 16);
             } else {
-                const int id = (c_in * kVecs * kTeam + ttid) * E - off;
+                const int id = (c_in * kVecs * kTeam + ttid) * E - offset_of(s_row[j_in]);
 #pragma unroll 1
                 for (int x = 0; x < kVecs; ++x)
                     if (id + x * kTeam * E < a.V && readable(src + x * kTeam * 16))
@@ -483,7 +469,10 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             if (++c_in == a.chunks) {
                 c_in = 0;
                 ++j_in;
-                if (in > 0) src = start_of(s_row[j_in]) + ttid * 16;
+                if (in > 0) {
+                    src = start_of(s_row[j_in]) + ttid * 16;
+                    in_whole = inside_of(offset_of(s_row[j_in]));
+                }
             }
         }
         dst = dst + kStageBytes == ring + kStages * kStageBytes ? ring : dst + kStageBytes;
@@ -491,16 +480,46 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     };
 #pragma unroll
     for (int x = 0; x < kStages - 1; ++x) issue();
+    // the tokens and their logits, while the first chunks are on their way
+    for (int x = tid; x <= cta_r1 - cta_r0; x += kThreads) {
+        const int tok = a.tokens[s_entry[x]];
+        const bool ok = tok >= 0 && tok < a.V;
+        const float v = ok ? load_logit<DT>(s_row[x], tok) : INFINITY;
+        s_tok[x] = ok ? tok : -1;
+        s_xt[x] = make_float2(v, below<DT>(v));
+        if (!ok && tok != -1) flag_status(a.status, GRAFT_STATUS_TOKEN_RANGE);
+    }
+    __syncthreads();
+    if (idle) return;  // (warps alone from here on)
+
+    // ---- the row at hand
+    const char* row = nullptr;
+    int off = 0, tok = -1;
+    int2 in_row = make_int2(0, 0);   // chunks within the row
+    int2 mixed = make_int2(0, -1);   // chunks [x, y] whose better tokens are counted one by one (the given token's own)
+    float2 xt = make_float2(INFINITY, INFINITY);
+    auto begin_row = [&]() {
+        row = s_row[j];
+        off = offset_of(row);
+        in_row = inside_of(off);
+        tok = s_tok[j];
+        if (tok >= 0 && a.rank != nullptr) {
+            xt = s_xt[j];
+            mixed.y = (tok + off) / kChunk;
+            mixed.x = xt.x > -INFINITY ? mixed.y : 0;  // (there is no number below -inf to compare with)
+        } else {
+            xt = make_float2(INFINITY, INFINITY);
+            mixed = make_int2(0, -1);
+        }
+    };
+    begin_row();
     int stage = 0;
     float m = -INFINITY;
     float2 s = make_float2(0.f, 0.f), t = s, cnt = s;
     float seg_max = -INFINITY;
-    uint64_t list = 0;  // a team's first warp: the best so far, one a lane
     int parity = 0, turn = 0, c_part = c, c_seg = c;  // the part's and the segment's first chunk
     while (true) {
         const int c2 = c + 1 == a.chunks ? 0 : c + 1;
-        const char* row = s_row[j];
-        const int off = offset_of(row), id0 = c * kChunk - off;  // the chunk's first logit
         auto id_of = [&](int c, int x) { return ((c * kVecs + x) * kTeam + ttid) * E - off; };
         issue();
         cp_wait<kStages - 1>();
@@ -509,7 +528,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
         for (int x = 0; x < kVecs; ++x)
             cur[x] = *reinterpret_cast<const uint4*>(s_ring + ((stage * kVecs + x) * kThreads + tid) * 16);
         stage = stage + 1 == kStages ? 0 : stage + 1;
-        if (!inside(c, off)) {
+        if (c < in_row.x || c >= in_row.y) {
 #pragma unroll
             for (int x = 0; x < kVecs; ++x) {
                 const int id = id_of(c, x);
@@ -548,21 +567,16 @@ logprob_part_kernel(const __grid_constant__ Args a) {
                 }
         }
         // ---- tokens ahead of the given one
-        const int tok = s_tok[j];
-        if (tok >= 0 && a.rank != nullptr) {
-            const float2 xt = s_xt[j];
-            const bool ahead = id0 >= 0 && id0 + kChunk <= tok;
-            if (id0 > tok || (ahead && xt.x > -INFINITY)) {
-                const float x1 = ahead ? xt.y : xt.x;  // (equal ones at lower ids count)
-                // (a likely token has few ahead of it: most chunks have none)
-                if (__any_sync(0xffffffffu, top > x1)) {
+        if (c < mixed.x || c > mixed.y) {
+            const float x1 = c < mixed.x ? xt.y : xt.x;  // (equal ones at lower ids count)
+            // (a likely token has few ahead of it: most chunks have none)
+            if (__any_sync(0xffffffffu, top > x1)) {
 #pragma unroll
-                    for (int x = 0; x < kVecs; ++x) count_above<DT>(cur[x], x1, cnt);
-                }
-            } else {
-#pragma unroll
-                for (int x = 0; x < kVecs; ++x) cnt.x += count_ahead<DT>(cur[x], id_of(c, x), tok, xt.x);
+                for (int x = 0; x < kVecs; ++x) count_above<DT>(cur[x], x1, cnt);
             }
+        } else {
+#pragma unroll
+            for (int x = 0; x < kVecs; ++x) cnt.x += count_ahead<DT>(cur[x], id_of(c, x), tok, xt.x);
         }
         if (a.top > 0) {
             const uint32_t b = __float_as_uint(top);
@@ -602,7 +616,13 @@ logprob_part_kernel(const __grid_constant__ Args a) {
                 for (int d = 16; d > 0; d >>= 1) tau = fmaxf(tau, __shfl_xor_sync(0xffffffffu, tau, d));
             }
             // (of equal logits the lower id goes first, so a full list's last has to be passed, the threshold reached)
-            float kth = c_seg == c_part ? -INFINITY : s_kth[team];
+            bool listed = c_seg != c_part;  // the list holds what came before
+            float kth = -INFINITY;          // its last, if it is full
+            auto last_listed = [&]() {
+                const uint64_t last = s_list[team][a.top - 1];
+                return last != 0 ? key_value(last) : -INFINITY;
+            };
+            if (listed) kth = last_listed();
             auto passes = [&](float v) { return v >= tau && v > kth; };
             // Each thread takes its own chunks, so that a warp's reads go out together.
             uint64_t hits = 0;
@@ -642,14 +662,30 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             if (kWarpTeam) __syncwarp();
             if (ttid == 0) s_n[team][turn ^ 1] = 0;
             turn ^= 1;
-            auto merge = [&](int n) {  // by the team's first warp
-                for (int at = 0; at < n; at += 32)
-                    list = merge_keys(list, sort_keys(at + lane < n ? cand[at + lane] : 0, lane), lane);
-                const uint64_t last = __shfl_sync(0xffffffffu, list, a.top - 1);
-                if (lane == 0) s_kth[team] = last != 0 ? key_value(last) : -INFINITY;
+            // The best of the list and n candidates, by their ranks among each other (0 is nobody's key: any order).
+            auto merge = [&](int n) {
+                if (listed) {
+                    if (ttid < a.top) cand[n + ttid] = s_list[team][ttid];
+                    n += a.top;
+                    sync();
+                }
+                for (int x = ttid; x < max(n, a.top); x += kTeam) {
+                    const uint64_t mine = x < n ? cand[x] : 0;
+                    int rank = x < n ? 0 : x;
+                    if (x < n) {
+#pragma unroll 4
+                        for (int y = 0; y < n; ++y) {
+                            const uint64_t o = cand[y];
+                            rank += o > mine || (o == mine && y < x);
+                        }
+                    }
+                    if (rank < a.top) s_list[team][rank] = mine;
+                }
+                listed = true;
+                sync();
             };
             if (n <= kTeamCap) {
-                if (kWarpTeam || warp == 0) merge(n);
+                merge(n);
             } else {
                 // More than the buffer holds: chunk by chunk, the best that pass one by one, each chunk against the
                 // list as the last one left it.
@@ -680,9 +716,9 @@ logprob_part_kernel(const __grid_constant__ Args a) {
                         if (ttid == 0) cand[n] = best;
                     }
                     sync();
-                    if (kWarpTeam || warp == 0) merge(n);
+                    merge(n);
+                    kth = last_listed();
                     sync();
-                    kth = s_kth[team];
                 }
             }
             seg_max = -INFINITY;
@@ -692,6 +728,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             if (kWarpTeam || warp == 0) {
                 float4 v = s_red[parity][kWarpTeam ? warp : lane & 7];
                 if (!kWarpTeam) add_lanes<kWarps>(v, a.c1);
+                const uint64_t list = lane < a.top ? s_list[team][lane] : 0;
                 if (c_part == 0 && c2 == 0) {  // the whole row
                     finish(a, s_entry[j], tok >= 0, s_xt[j].x, v.x, v.y, v.z, (int)v.w, list);
                 } else {
@@ -702,7 +739,6 @@ logprob_part_kernel(const __grid_constant__ Args a) {
                     }
                     if (lane < a.top) a.keys[slot * a.top + lane] = list;
                 }
-                list = 0;
             }
             m = seg_max = -INFINITY;
             s = t = cnt = make_float2(0.f, 0.f);
@@ -710,8 +746,11 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             c_part = c_seg = c2;
         }
         if (--left == 0) break;
-        j += c2 == 0;
         c = c2;
+        if (c2 == 0) {
+            ++j;
+            begin_row();
+        }
     }
 }
 
@@ -775,6 +814,12 @@ logprob_join_kernel(const __grid_constant__ Args a) {
     }
 }
 
+// CTAs of a call at most: as many as the SMs hold at once; where those would have longer lists of rows than they keep, more.
+int most_ctas(int N) {
+    const int sms = device_sm_count(), most = kResident * (sms > 0 ? sms : 152), least = N / (kMaxRows - 16) + 1;
+    return most > least ? most : least;
+}
+
 template <int DT>
 int launch(Args& a, cudaStream_t st) {
     const bool warps = a.V <= kShort;
@@ -801,12 +846,6 @@ int launch(Args& a, cudaStream_t st) {
         count_launches(1);
     }
     return launch_status();
-}
-
-// CTAs of a call at most: as many as the SMs hold at once; where those would have longer lists of rows than they keep, more.
-int most_ctas(int N) {
-    const int sms = device_sm_count(), most = kResident * (sms > 0 ? sms : 152), least = N / (kMaxRows - 16) + 1;
-    return most > least ? most : least;
 }
 
 void carve(WsCarver& w, int N, int top, int ctas, Args* a) {
