@@ -5,7 +5,7 @@
 //   rank(v) = #{x > x_v} + #{x = x_v at lower ids},  the top k by (x descending, id ascending).
 //
 // HBM bound: every logit of the rows asked for is read once (4 or 2 bytes) and costs about ten instructions.
-// logprob_part_kernel lays the rows' chunks (kVecs x 16 bytes a thread) side by side and gives every team of threads
+// logprob_part_kernel lays the rows' chunks (32 logits a thread) side by side and gives every team of threads
 // an even run of them, so all end together whatever the number of rows; the next chunk's loads are in flight while
 // one is worked on.  A thread keeps its own maximum and sums over its run's part of a row (one pass, no barrier for
 // them).  A team is a CTA; where rows are short (kShort), a warp that takes whole rows, without barriers.
@@ -29,15 +29,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kVecs = 4;       // 16-byte pieces of a chunk a thread
-constexpr int kStages = 4;     // chunks in shared memory: one worked on, the others on their way
-// CTAs an SM: three of 80 registers left spills in the 16-bit kernels and no room for a fourth stage (1024 rows of 151936:
-// fp32 138 us with three, 134 with two; bf16 161 and 120).
+// CTAs an SM: three of 80 registers left spills in the 16-bit kernels (1024 rows of 151936: fp32 138 us with three, 134 with
+// two; bf16 161 and 120).
 constexpr int kResident = 2;
 constexpr int kSeg = 40;       // chunks of a segment
 constexpr int kMaxRows = 160;  // rows of a CTA's runs at most
 constexpr int kShort = 4096;   // logits of a row that a warp takes
-constexpr int kRing = kStages * kVecs * kThreads * 16;
 constexpr float kFloor = -150.f;  // log2 of a weight that is zero in 32 bits
 constexpr float kSlack = 16.f;    // log2 of the largest weight before the sums are moved to a new maximum
 
@@ -52,6 +49,13 @@ __device__ __forceinline__ void cp_wait() {
 
 template <int DT>
 constexpr int kElems = DT == GRAFT_F32 ? 4 : 8;  // of 16 bytes
+// 16-byte pieces of a chunk a thread, and chunks in shared memory (one worked on, the others on their way): a thread has 32
+// logits of a chunk (1024 rows of 151936: fp32 126 us, with 16 of them 131; bf16 112, with 64 of them 124).
+template <int DT>
+constexpr int kVecsOf = DT == GRAFT_F32 ? 8 : 4;
+template <int DT>
+constexpr int kStagesOf = 16 / kVecsOf<DT>;
+constexpr int kRing = 16 * kThreads * 16;
 
 struct Args {
     const char* logits;
@@ -314,11 +318,11 @@ __device__ __forceinline__ void finish(const Args& a, int n, bool ok, float give
 template <int DT, bool kWarpTeam>
 __global__ void __launch_bounds__(kThreads, kResident)
 logprob_part_kernel(const __grid_constant__ Args a) {
-    constexpr int E = kElems<DT>;
+    constexpr int E = kElems<DT>, kVecs = kVecsOf<DT>, kStages = kStagesOf<DT>;
     constexpr int kBytes = DT == GRAFT_F32 ? 4 : 2;
     constexpr int kTeams = kWarpTeam ? kWarps : 1;       // of a CTA
     constexpr int kTeam = kThreads / kTeams;             // threads of a team
-    constexpr int kMaxChunks = kWarpTeam ? kShort / (32 * kVecs * 4) + 1 : kSeg;
+    constexpr int kMaxChunks = kWarpTeam ? kShort / (32 * kVecs * E) + 1 : kSeg;
     extern __shared__ __align__(16) unsigned char s_ring[];  // [stage][piece][thread] 16 bytes
     __shared__ int s_entry[kMaxRows], s_tok[kMaxRows];
     __shared__ const char* s_row[kMaxRows];
@@ -327,7 +331,8 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     __shared__ unsigned short s_max[kMaxChunks][kThreads];  // a segment's largest, by chunk and thread: upper bf16 bounds
     __shared__ uint64_t s_cand[kCap + kTeams * 32];  // candidates, and the best so far behind them
     __shared__ uint64_t s_list[kTeams][32];          // the best so far, best first; 0: none
-    __shared__ int s_n[kTeams][2], s_scan[kWarps];
+    __shared__ int s_hit[kCap];                      // chunk and thread whose largest reaches the threshold
+    __shared__ int s_n[kTeams][2], s_hits[kTeams][2], s_scan[kWarps];
     __shared__ float s_reach[32];
     __shared__ float4 s_red[2][kWarps];  // the warps' sums at a part's end, by its parity
     __shared__ uint64_t s_best[kWarps];
@@ -419,7 +424,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             r0 += seen.y;
         }
     }
-    if (tid < 2 * kTeams) s_n[tid >> 1][tid & 1] = 0;
+    if (tid < 2 * kTeams) s_n[tid >> 1][tid & 1] = s_hits[tid >> 1][tid & 1] = 0;
     __syncthreads();
     const int team = kWarpTeam ? warp : 0;
     const bool idle = t_first + team >= teams;  // (warps of the last CTA)
@@ -478,17 +483,20 @@ logprob_part_kernel(const __grid_constant__ Args a) {
         dst = dst + kStageBytes == ring + kStages * kStageBytes ? ring : dst + kStageBytes;
         cp_commit();
     };
-#pragma unroll
-    for (int x = 0; x < kStages - 1; ++x) issue();
-    // the tokens and their logits, while the first chunks are on their way
-    for (int x = tid; x <= cta_r1 - cta_r0; x += kThreads) {
-        const int tok = a.tokens[s_entry[x]];
-        const bool ok = tok >= 0 && tok < a.V;
-        const float v = ok ? load_logit<DT>(s_row[x], tok) : INFINITY;
-        s_tok[x] = ok ? tok : -1;
-        s_xt[x] = make_float2(v, below<DT>(v));
-        if (!ok && tok != -1) flag_status(a.status, GRAFT_STATUS_TOKEN_RANGE);
+    // The tokens and their logits: a read each among the first copies (behind all of them they took 6 us).
+    static_assert(kMaxRows <= kThreads, "a row a thread");
+    const bool listed_row = tid <= cta_r1 - cta_r0;
+    const int my_tok = listed_row ? a.tokens[s_entry[tid]] : -1;
+    issue();
+    if (listed_row) {
+        const bool ok = my_tok >= 0 && my_tok < a.V;
+        const float v = ok ? load_logit<DT>(s_row[tid], my_tok) : INFINITY;
+        s_tok[tid] = ok ? my_tok : -1;
+        s_xt[tid] = make_float2(v, below<DT>(v));
+        if (!ok && my_tok != -1) flag_status(a.status, GRAFT_STATUS_TOKEN_RANGE);
     }
+#pragma unroll
+    for (int x = 0; x < kStages - 2; ++x) issue();
     __syncthreads();
     if (idle) return;  // (warps alone from here on)
 
@@ -624,43 +632,39 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             };
             if (listed) kth = last_listed();
             auto passes = [&](float v) { return v >= tau && v > kth; };
-            // Each thread takes its own chunks, so that a warp's reads go out together.
-            uint64_t hits = 0;
             if (passes(seg_max)) {
 #pragma unroll 8
-                for (int x = 0; x <= c - c_seg; ++x)
-                    hits |= (uint64_t)passes(__uint_as_float((uint32_t)s_max[x][tid] << 16)) << x;
-            }
-            for (; __any_sync(0xffffffffu, hits != 0); hits &= hits - 1) {
-                if (hits == 0) continue;
-                const int cc = c_seg + __ffsll(hits) - 1;
-                uint4 again[kVecs];
-#pragma unroll
-                for (int x = 0; x < kVecs; ++x) {
-                    const int id = id_of(cc, x);
-                    again[x] = make_uint4(0, 0, 0, 0);
-                    if (id >= 0 && id + E <= a.V) again[x] = *reinterpret_cast<const uint4*>(row + (int64_t)id * kBytes);
-                    else again[x] = ragged<DT>(again[x], false, row, id, a.V);
+                for (int x = 0; x <= c - c_seg; ++x) {
+                    if (!passes(__uint_as_float((uint32_t)s_max[x][tid] << 16))) continue;
+                    const int at = atomicAdd(&s_hits[team][turn], 1);
+                    if (at < kTeamCap) s_hit[team * kTeamCap + at] = x * kTeam + ttid;
                 }
+            }
+            sync();
+            // A thread reads one piece of one of them again: all at once, as the reads queue behind the copies under way.
+            const int hits = s_hits[team][turn];
+            for (int y = ttid; y < min(hits, kTeamCap) * kVecs; y += kTeam) {
+                const int hit = s_hit[team * kTeamCap + y / kVecs], x = hit / kTeam;
+                const int id = (((c_seg + x) * kVecs + y % kVecs) * kTeam + hit % kTeam) * E - off;
+                uint4 again = make_uint4(0, 0, 0, 0);
+                if (id >= 0 && id + E <= a.V) again = *reinterpret_cast<const uint4*>(row + (int64_t)id * kBytes);
+                else again = ragged<DT>(again, false, row, id, a.V);
+                if (!passes(largest<DT>(again))) continue;
 #pragma unroll
-                for (int x = 0; x < kVecs; ++x) {
-                    if (!passes(largest<DT>(again[x]))) continue;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float2 p = pair<DT>(again[x], e / 2);
-                        const float v = (e & 1) ? p.y : p.x;
-                        if (passes(v)) {
-                            const int at = atomicAdd(&s_n[team][turn], 1);
-                            if (at < kTeamCap) cand[at] = key_of(v, id_of(cc, x) + e);
-                        }
+                for (int e = 0; e < E; ++e) {
+                    const float2 p = pair<DT>(again, e / 2);
+                    const float v = (e & 1) ? p.y : p.x;
+                    if (passes(v)) {
+                        const int at = atomicAdd(&s_n[team][turn], 1);
+                        if (at < kTeamCap) cand[at] = key_of(v, id + e);
                     }
                 }
             }
             sync();
-            // (the other counter is cleared here: all have read it, and none adds to it before the next barrier)
-            int n = s_n[team][turn];
+            // (the other counters are cleared here: all have read them, and none adds to them before the next barrier)
+            int n = hits > kTeamCap ? kTeamCap + 1 : s_n[team][turn];
             if (kWarpTeam) __syncwarp();
-            if (ttid == 0) s_n[team][turn ^ 1] = 0;
+            if (ttid == 0) s_n[team][turn ^ 1] = s_hits[team][turn ^ 1] = 0;
             turn ^= 1;
             // The best of the list and n candidates, by their ranks among each other (0 is nobody's key: any order).
             auto merge = [&](int n) {
@@ -823,7 +827,7 @@ int most_ctas(int N) {
 template <int DT>
 int launch(Args& a, cudaStream_t st) {
     const bool warps = a.V <= kShort;
-    const int64_t chunk = (int64_t)(warps ? 32 : kThreads) * kVecs * kElems<DT>;
+    const int64_t chunk = (int64_t)(warps ? 32 : kThreads) * kVecsOf<DT> * kElems<DT>;
     a.chunks = (int)((a.V + kElems<DT> - 1 + chunk - 1) / chunk);  // (a row may start inside 16 bytes)
     const int64_t units = warps ? ((int64_t)a.N + kWarps - 1) / kWarps : (int64_t)a.N * a.chunks;
     a.ctas = (int)(units < a.ctas ? units : a.ctas);
@@ -863,7 +867,7 @@ void carve(WsCarver& w, int N, int top, int ctas, Args* a) {
 
 int check(int N, int V, int top) {
     if (N < 0 || V < 1 || top < 0 || top > V) return GRAFT_ERR_INVALID_ARG;
-    if (N > 65535 || V > (1 << 30) || top > GRAFT_MAX_TOP_LOGPROBS) return GRAFT_ERR_UNSUPPORTED_SHAPE;
+    if (N > 65535 || V > (1 << 24) || top > GRAFT_MAX_TOP_LOGPROBS) return GRAFT_ERR_UNSUPPORTED_SHAPE;
     return GRAFT_OK;
 }
 
