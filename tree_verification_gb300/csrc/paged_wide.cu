@@ -197,7 +197,11 @@ template <int DT, bool kTestWaits, bool kWindow>
 __global__ void __launch_bounds__(NTHREADS, 1)
 wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a) {
     using E = Elem<DT>;
-    constexpr float kLift = DT == GRAFT_FP16 ? 7.f : 0.f;  // see paged_few.cu: small weights keep their bits
+    // See paged_few.cu: small weights keep their bits.  Over 2^14 keys at most (a window), a lift of 2^3 keeps their sum to
+    // 2^14 x 2^-28 of the largest weight, an eighth of half a step, and leaves 2^12 for maxima that rise: few blocks are
+    // weighed twice (heads of scores 3 apart, chunks over 1024 keys: 137 -> 125 us).
+    constexpr float kLiftMost = DT == GRAFT_FP16 ? 7.f : 0.f;
+    const float kLift = kWindow && DT == GRAFT_FP16 && a.window <= 8192 && a.first <= 8192 ? 3.f : kLiftMost;
     constexpr float kMaxSum = DT == GRAFT_FP16 ? 32768.f : 65536.f;  // of a block weighed by an old maximum
     const uint64_t wait_ns = kTestWaits ? a.wait_ns : kWaitNs;
     extern __shared__ uint8_t smem_raw[];
