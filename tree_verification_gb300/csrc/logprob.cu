@@ -36,7 +36,9 @@ constexpr int kSeg = 40;       // chunks of a segment
 constexpr int kMaxRows = 160;  // rows of a CTA's runs at most
 constexpr int kShort = 4096;   // logits of a row that a warp takes
 constexpr float kFloor = -150.f;  // log2 of a weight that is zero in 32 bits
-constexpr float kSlack = 16.f;    // log2 of the largest weight before the sums are moved to a new maximum
+// log2 of the largest weight before the sums are moved to a new maximum.  (ln s and t / s cancel where a token is all but
+// certain: at 16 an entropy near 0 was off by 11 x 2^-24.)
+constexpr float kSlack = 2.f;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
