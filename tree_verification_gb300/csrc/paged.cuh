@@ -92,7 +92,8 @@ struct Start {
 // ---------------------------------------------------------------- windows
 // A row at position p sees row r <= p where r > p - window or r < first.  The rows between the first tokens and the
 // window of an item's earliest row are seen by none: an item's units of `unit` keys are those of the first tokens and,
-// behind them, those from key `low` on (low: the earliest row's p - window + 1).  Units are numbered without the gap.
+// behind them, those from key `low` on (low: the earliest row's p - window + 1).  Units are numbered without the gap, so
+// that the schedules and the ranges that they cut need not know of it.
 __host__ __device__ __forceinline__ int window_units(int first, int unit) { return first / unit + (first % unit != 0); }
 __device__ __forceinline__ int window_gap(int low, int first, int unit) {
     if (low <= first) return 0;  // (the first tokens reach the window)

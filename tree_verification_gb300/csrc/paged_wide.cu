@@ -29,7 +29,9 @@
 //     those of the first tokens and those from its earliest row's window on;
 //     the blocks that some row's window starts in or behind are masked and
 //     cleaned like those with new rows, and a row that has seen nothing as yet
-//     takes a block's maximum anew.
+//     takes a block's maximum anew.  (16 trees at group 16 over 4096 keys 138
+//     us; 4100 prompt rows over 1024, where 4 of an item's 10.5 blocks are
+//     masked, 112.)
 //   * V elements that are infinite or NaN in blocks with masked keys are
 //     taken out in shared memory (0 * NaN is NaN) and given to the rows that
 //     do see them after the item's rows are written.
