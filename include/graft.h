@@ -419,6 +419,7 @@ int graft_lm_head_sample(int N, int d_model, int V, const void* H, const void* W
  *            block > 0 it counts from row (n / block) * block and lies below
  *            block: graft_accept_compact's path with block = Kmax
  *   tokens [N] i32: the token of entry n; -1: none
+ *   temperature > 0, finite and not subnormal
  * Outputs, for z = x / temperature, p = softmax(z):
  *   logprob [N] f32   ln p(token); 0 where there is no token or no row
  *   entropy [N] f32   -sum p ln p (may be NULL); 0 where there is no row

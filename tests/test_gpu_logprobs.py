@@ -236,6 +236,26 @@ def test_a_pool_of_logits_past_32_bit_offsets():
     assert got["top_id"].tolist() == [[V - 7, 3, 0]] * 2 and got["rank"].tolist() == [0, 1]
 
 
+def test_temperatures_at_their_ends():
+    x = logits(3, 300, torch.float32, 10)
+    x[1, 7] = x[1].max()  # (two tokens share the largest: half each however cold it is)
+    best = x.argmax(1).numpy()
+    got, _ = run(x, best, top=2, T=1.2e-38)
+    ref = [0.0 if (x[i] == x[i].max()).sum() == 1 else -np.log((x[i] == x[i].max()).sum().item()) for i in range(3)]
+    np.testing.assert_allclose(got["logprob"].cpu().numpy(), ref, atol=1e-6)
+    got, _ = run(x, best, top=2, T=3e38)
+    np.testing.assert_allclose(got["logprob"].cpu().numpy(), -np.log(300), rtol=1e-6)
+    np.testing.assert_allclose(got["entropy"].cpu().numpy(), np.log(300), rtol=1e-6)
+
+
+def test_numbers_below_the_normal_ones():
+    for dtype, step in ((torch.float32, 2.0 ** -149), (torch.bfloat16, 2.0 ** -133), (torch.float16, 2.0 ** -24)):
+        x = (torch.arange(-200, 201) * step).to(dtype).flip(0)[None].repeat(2, 1)
+        toks = [200, 30]  # zero, and one of the larger ones
+        got, _ = run(x, toks, top=5)
+        check(x, toks, got, top=5)
+
+
 def test_captured_and_on_another_stream():
     x = logits(3, 40000, torch.float32, 8).to(DEV)
     toks = i32([1, 2, 3])

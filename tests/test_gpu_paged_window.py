@@ -330,6 +330,25 @@ def test_idle_sequences_and_bad_lengths():
         assert (np.abs(np64(O[lo:hi]) - ref[lo:hi]) <= tol).all()
 
 
+@pytest.mark.parametrize("tree,Hkv,G,page,new,lens", [
+    (True, 8, 4, 16, [64], [1000]), (False, 2, 16, 64, [64] * 3, [700, 300, 129]),
+    (False, 2, 8, 128, [200, 1, 1, 1], [5, 900, 300, 0])])
+def test_a_bounded_wait_runs_out_and_the_device_stays_usable(tree, Hkv, G, page, new, lens):
+    # (a wait bound of 2 ns on valid inputs: every load stays in bounds and completes)
+    s = Setup(lens, new, Hkv, page, seed=len(new) + G)
+    mask = tree_masks(s.rng, new) if tree else None
+    md = torch.from_numpy(mask.view(np.int64)).to(DEV) if tree else None
+    N = int(s.starts[-1])
+    Q = s.randn(N, Hkv * G, 128).to(DEV)
+    for _ in range(2):
+        s.cache.plan(s.q_start, N, Hkv * G, max(new), tree=tree, window=300, first=4)
+        s.cache.attend(0, Q, 0.09, mask=md, tuning=dict(wait_ns=2), window=300, first=4)
+        torch.cuda.synchronize()
+        assert s.status() == gb().STATUS_TIMEOUT
+        s.cache._buffers["attention"].zero_()
+        run(s, G, 300, 4, mask=mask, out_of=False)
+
+
 def test_another_stream_and_strided_queries():
     s = Setup([900, 30], [5, 64], 2, 32, seed=16)
     base = s.randn(69, 12, 128)

@@ -19,9 +19,9 @@ def call(N=4, V=100, R=4, dtype=2, logits=FAKE, stride=100, rows=None, block=0, 
 def test_arguments():
     assert call(N=0) == 0
     assert call(N=-1) == -1 and call(V=0, top=0) == -1 and call(top=-1) == -1 and call(V=1, top=2, stride=1) == -1
-    assert call(N=65536, R=65536) == -2 and call(top=33) == -2 and call(V=(1 << 30) + 1, stride=1 << 31) == -2
+    assert call(N=65536, R=65536) == -2 and call(top=33) == -2 and call(V=(1 << 24) + 1, stride=1 << 25) == -2
     assert call(dtype=3) == -1 and call(dtype=-1) == -1
-    for T in (0.0, -1.0, math.nan, math.inf):
+    for T in (0.0, -1.0, math.nan, math.inf, 1e-39, -1e-39):
         assert call(T=T) == -1
     assert call(logits=None) == -1 and call(tokens=None) == -1 and call(lp=None) == -1
     assert call(ids=None) == -1 and call(lps=None) == -1

@@ -897,7 +897,7 @@ extern "C" int graft_token_logprobs(int N, int V, int64_t n_logit_rows, int dtyp
     const int rc = check(N, V, top);
     if (rc != GRAFT_OK) return rc;
     if (dtype != GRAFT_BF16 && dtype != GRAFT_FP16 && dtype != GRAFT_F32) return GRAFT_ERR_INVALID_ARG;
-    if (!(temperature > 0.f) || !std::isfinite(temperature) || block < 0 || n_logit_rows < 0) return GRAFT_ERR_INVALID_ARG;
+    if (!(temperature > 0.f) || !std::isnormal(temperature) || block < 0 || n_logit_rows < 0) return GRAFT_ERR_INVALID_ARG;
     if (n_logit_rows >= (1LL << 31)) return GRAFT_ERR_UNSUPPORTED_SHAPE;
     if (N == 0) return GRAFT_OK;
     if (logits == nullptr || tokens == nullptr || logprob == nullptr) return GRAFT_ERR_INVALID_ARG;
