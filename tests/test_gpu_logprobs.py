@@ -281,6 +281,24 @@ def test_captured_and_on_another_stream():
         assert torch.equal(out[k], other[k])
 
 
+def test_buffers_belong_to_the_given_stream(monkeypatch):
+    # (scratch of the current stream could be handed to its next kernels before the call on the other one has run)
+    x, st, made = logits(3, 40000, torch.float32, 12).to(DEV), torch.cuda.Stream(), []
+    toks, empty = i32([4, 5, 6]), torch.empty
+    st.wait_stream(torch.cuda.current_stream())
+
+    def spy(*args, **kw):
+        made.append(torch.cuda.current_stream())
+        return empty(*args, **kw)
+
+    monkeypatch.setattr(torch, "empty", spy)
+    got = gb().graft_token_logprobs(x, toks, top=5, stream=st)
+    monkeypatch.undo()
+    assert made and all(s == st for s in made)
+    st.synchronize()
+    check(x.cpu(), [4, 5, 6], got, top=5)
+
+
 def test_calls_of_other_shapes_share_a_workspace():
     ws = torch.empty(gb().graft_token_logprobs_workspace_size(300, 5000, 32), dtype=torch.uint8, device=DEV)
     for N, V, top in ((300, 5000, 32), (1, 90000, 2), (20, 70, 0), (2, 8191, 5)):

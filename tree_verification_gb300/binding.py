@@ -430,6 +430,15 @@ def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape, index: int) ->
 _logprob_sizes = {}
 
 
+def _logprob_buffers(N: int, top: int, dev, out: Optional[dict], nbytes: int, ws):
+    new, f32, i32 = torch.empty, torch.float32, torch.int32
+    if out is None:
+        out = dict(logprob=new(N, dtype=f32, device=dev), entropy=new(N, dtype=f32, device=dev),
+                   rank=new(N, dtype=i32, device=dev), top_id=new((N, top), dtype=i32, device=dev),
+                   top_logprob=new((N, top), dtype=f32, device=dev))
+    return out, new(nbytes, dtype=torch.uint8, device=dev) if ws is None else ws
+
+
 def graft_token_logprobs(logits, tokens, rows=None, block: int = 0, top: int = 0, temperature: float = 1.0,
                          out: Optional[dict] = None, status=None, ws=None, stream=None) -> dict:
     """Log probability, entropy and rank of tokens [N] under rows of logits [R][V] (float32, bfloat16 or float16; rows
@@ -464,19 +473,18 @@ def graft_token_logprobs(logits, tokens, rows=None, block: int = 0, top: int = 0
         if len(_logprob_sizes) >= 4096:
             _logprob_sizes.clear()
         _logprob_sizes[key] = nbytes
-    f32, i32 = torch.float32, torch.int32
-    if out is None:
-        new = torch.empty
-        out = dict(logprob=new(N, dtype=f32, device=dev), entropy=new(N, dtype=f32, device=dev),
-                   rank=new(N, dtype=i32, device=dev), top_id=new((N, top), dtype=i32, device=dev),
-                   top_logprob=new((N, top), dtype=f32, device=dev))
+    f32, i32, own = torch.float32, torch.int32, out is None
+    if stream is not None and (out is None or ws is None):
+        with torch.cuda.stream(stream):  # (memory of the stream that writes it: it may be given back before the call has run)
+            out, ws = _logprob_buffers(N, top, dev, out, nbytes, ws)
+    elif out is None or ws is None:
+        out, ws = _logprob_buffers(N, top, dev, out, nbytes, ws)
+    if own:
         op = [t.data_ptr() for t in out.values()]
     else:
         op = [_dense(out[name], name, dtype, shape, index)
               for name, dtype, shape in (("logprob", f32, (N,)), ("entropy", f32, (N,)), ("rank", i32, (N,)),
                                          ("top_id", i32, (N, top)), ("top_logprob", f32, (N, top)))]
-    if ws is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     if ws.numel() < nbytes:
         raise ValueError("workspace too small")
     wp = _dense(ws, "ws", torch.uint8, ws.shape, index)
