@@ -431,9 +431,8 @@ int graft_lm_head_sample(int N, int d_model, int V, const void* H, const void* W
  * Ranks and ids go by the logits as given, exactly.  Logits may be -inf (such
  * tokens have p = 0); NaN ranks with them.  A row with NaN or +inf, or of -inf
  * alone, has no law: its logprob, entropy and top_logprob are NaN.  Sums in 32
- * bits.  A token outside [0, V) sets
- * GRAFT_STATUS_TOKEN_RANGE and counts as none, a row outside the logits (or
- * the block) GRAFT_STATUS_ROW.  N <= 65535, V <= 2^24.  Workspace:
+ * bits.  A token outside [0, V) sets GRAFT_STATUS_TOKEN_RANGE and counts as
+ * none, a row outside the logits (or the block) GRAFT_STATUS_ROW.  N <= 65535, V <= 2^24.  Workspace:
  * graft_token_logprobs_workspace_size (need not be zeroed; depends on the
  * current device's SM count).
  */
@@ -701,9 +700,10 @@ int graft_paged_attention_ex(const GraftPagedCache* cache, const void* K_pool, c
  * window, and pages whose rows all lie from `first` on and at or before
  * lengths[b] - window may be given back, their entries of the block table
  * set to -1: these calls never read them, graft_pages_free flags them and
- * passes them over, graft_pages_fork refuses a sequence that has them.  plan: graft_paged_plan_size bytes; a plan of another
- * window or `first`, or of none, is refused on the device
- * (GRAFT_STATUS_PLAN), so layers of several kinds take a plan each.
+ * passes them over, graft_pages_fork refuses a sequence that has them.
+ * plan: graft_paged_plan_size bytes; a plan of another window or `first`, or
+ * of none, is refused on the device (GRAFT_STATUS_PLAN), so layers of several
+ * kinds take a plan each.
  * Workspace and the rest as above (they may share a workspace); tuning may
  * be NULL.
  */

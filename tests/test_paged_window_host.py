@@ -41,3 +41,16 @@ def test_arguments():
     t.tiles = 1
     assert attend(c, tuning=ctypes.addressof(t)) == -1
     assert attend(c, N=0) == 0 and attend(c, N=0, window=2**31 - 1, first=2**31 - 1) == 0
+
+
+@pytest.mark.parametrize("window,first", [(True, 0), (0, 0), (-1, 0), (2**31, 0), (1.0, 0), (5, -1), (5, 2**31), (5, True),
+                                          (None, 1)])
+def test_the_handle_refuses(window, first):
+    from tree_verification_gb300.paged import _kind
+    with pytest.raises(ValueError):
+        _kind(window, first)
+
+
+def test_the_handle_takes():
+    from tree_verification_gb300.paged import _kind
+    assert _kind(None, 0) is None and _kind(1, 0) == (1, 0) and _kind(2**31 - 1, 2**31 - 1) == (2**31 - 1, 2**31 - 1)

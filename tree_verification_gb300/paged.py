@@ -42,14 +42,14 @@ _Reference = type(ctypes.byref(ctypes.c_int()))
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
-
 def _kind(window: Optional[int], first: int):
     """What tells the plans of a step apart: (window, first), or None without a window."""
     if window is None:
         if first != 0:
             raise ValueError("first needs a window")
         return None
-    if not (isinstance(window, int) and isinstance(first, int) and 1 <= window < 2**31 and 0 <= first < 2**31):
+    whole = isinstance(window, int) and isinstance(first, int) and not isinstance(window, bool) and not isinstance(first, bool)
+    if not (whole and 1 <= window < 2**31 and 0 <= first < 2**31):
         raise ValueError("window must be at least 1, first at least 0 (32 bits)")
     return window, first
 
