@@ -249,6 +249,17 @@ __device__ __noinline__ uint4 ragged(uint4 v, bool have, const char* row, int id
     }
     return v;
 }
+// How many of 16 bytes of logits from their e0-th on equal x.
+template <int DT>
+__device__ __noinline__ float count_equal(uint4 w, int e0, float x) {
+    float n = 0.f;
+#pragma unroll
+    for (int e = 0; e < kElems<DT>; ++e) {
+        const float2 p = pair<DT>(w, e / 2);
+        n += e >= e0 && ((e & 1) ? p.y : p.x) == x ? 1.f : 0.f;
+    }
+    return n;
+}
 // How many of 16 bytes of logits from id on go ahead of token tok, of logit x.
 template <int DT>
 __device__ __noinline__ float count_ahead(uint4 w, int id, int tok, float x) {
@@ -508,7 +519,8 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     const char* row = nullptr;
     int off = 0, tok = -1;
     int2 in_row = make_int2(0, 0);   // chunks within the row
-    int2 mixed = make_int2(0, -1);   // chunks [x, y] whose better tokens are counted one by one (the given token's own)
+    int tok_chunk = -1;              // the given token's
+    int one_by_one = -1;             // up to this chunk better tokens are counted one by one
     float2 xt = make_float2(INFINITY, INFINITY);
     auto begin_row = [&]() {
         row = s_row[j];
@@ -517,11 +529,11 @@ logprob_part_kernel(const __grid_constant__ Args a) {
         tok = s_tok[j];
         if (tok >= 0 && a.rank != nullptr) {
             xt = s_xt[j];
-            mixed.y = (tok + off) / kChunk;
-            mixed.x = xt.x > -INFINITY ? mixed.y : 0;  // (there is no number below -inf to compare with)
+            tok_chunk = (tok + off) / kChunk;
+            one_by_one = xt.x > -INFINITY ? -1 : tok_chunk;  // (there is no number below -inf to compare with)
         } else {
             xt = make_float2(INFINITY, INFINITY);
-            mixed = make_int2(0, -1);
+            tok_chunk = one_by_one = -1;
         }
     };
     begin_row();
@@ -579,12 +591,18 @@ logprob_part_kernel(const __grid_constant__ Args a) {
                 }
         }
         // ---- tokens ahead of the given one
-        if (c < mixed.x || c > mixed.y) {
-            const float x1 = c < mixed.x ? xt.y : xt.x;  // (equal ones at lower ids count)
-            // (a likely token has few ahead of it: most chunks have none)
-            if (__any_sync(0xffffffffu, top > x1)) {
+        if (c > one_by_one) {
+            // A piece that starts ahead of the token counts equal ones too; of the token's own, those from the token on
+            // are taken off again.  (A likely token has few ahead of it: most chunks have none.)
+            if (__any_sync(0xffffffffu, top > (c <= tok_chunk ? xt.y : xt.x))) {
 #pragma unroll
-                for (int x = 0; x < kVecs; ++x) count_above<DT>(cur[x], x1, cnt);
+                for (int x = 0; x < kVecs; ++x) count_above<DT>(cur[x], id_of(c, x) < tok ? xt.y : xt.x, cnt);
+                if (c == tok_chunk) {
+#pragma unroll
+                    for (int x = 0; x < kVecs; ++x)
+                        if (id_of(c, x) < tok && tok < id_of(c, x) + E)
+                            cnt.x -= count_equal<DT>(cur[x], tok - id_of(c, x), xt.x);
+                }
             }
         } else {
 #pragma unroll
@@ -832,7 +850,9 @@ template <int DT>
 int launch(Args& a, cudaStream_t st) {
     const bool warps = a.V <= kShort;
     const int64_t chunk = (int64_t)(warps ? 32 : kThreads) * kVecsOf<DT> * kElems<DT>;
-    a.chunks = (int)((a.V + kElems<DT> - 1 + chunk - 1) / chunk);  // (a row may start inside 16 bytes)
+    // (a row may start inside 16 bytes)
+    const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && (a.R <= 1 || a.stride % 16 == 0);
+    a.chunks = (int)((a.V + (aligned ? 0 : kElems<DT> - 1) + chunk - 1) / chunk);
     const int64_t units = warps ? ((int64_t)a.N + kWarps - 1) / kWarps : (int64_t)a.N * a.chunks;
     a.ctas = (int)(units < a.ctas ? units : a.ctas);
     const auto kernel = warps ? logprob_part_kernel<DT, true> : logprob_part_kernel<DT, false>;
