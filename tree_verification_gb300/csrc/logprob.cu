@@ -188,19 +188,43 @@ __device__ __forceinline__ float load_logit(const char* row, int id) {
     const unsigned short h = reinterpret_cast<const unsigned short*>(row)[id];
     return DT == GRAFT_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
 }
-// The largest of 16 bytes of logits (NaN aside).
+// Two 16-bit logits in a word.
 template <int DT>
-__device__ __forceinline__ float largest(const uint4& w) {
-    if (DT == GRAFT_F32)
-        return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
-    if (DT == GRAFT_BF16) {
-        const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&w.x);
-        const float2 m = __bfloat1622float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
-        return fmaxf(m.x, m.y);
+struct Two {
+    using T = __nv_bfloat162;
+    static __device__ __forceinline__ T both(float x) { return __floats2bfloat162_rn(x, x); }
+    static __device__ __forceinline__ float2 up(T x) { return __bfloat1622float2(x); }
+};
+template <>
+struct Two<GRAFT_FP16> {
+    using T = __half2;
+    static __device__ __forceinline__ T both(float x) { return __floats2half2_rn(x, x); }
+    static __device__ __forceinline__ float2 up(T x) { return __half22float2(x); }
+};
+// The largest of kVecs x 16 bytes of logits (NaN aside).
+template <int DT, int kVecs>
+__device__ __forceinline__ float largest(const uint4* w) {
+    if constexpr (DT == GRAFT_F32) {
+        float m[kVecs];
+#pragma unroll
+        for (int x = 0; x < kVecs; ++x)
+            m[x] = fmaxf(fmaxf(__uint_as_float(w[x].x), __uint_as_float(w[x].y)),
+                         fmaxf(__uint_as_float(w[x].z), __uint_as_float(w[x].w)));
+#pragma unroll
+        for (int x = 1; x < kVecs; ++x) m[0] = fmaxf(m[0], m[x]);
+        return m[0];
+    } else {
+        typename Two<DT>::T m[kVecs];
+#pragma unroll
+        for (int x = 0; x < kVecs; ++x) {
+            const auto* p = reinterpret_cast<const typename Two<DT>::T*>(&w[x].x);
+            m[x] = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+        }
+#pragma unroll
+        for (int x = 1; x < kVecs; ++x) m[0] = __hmax2(m[0], m[x]);
+        const float2 f = Two<DT>::up(m[0]);
+        return fmaxf(f.x, f.y);
     }
-    const __half2* p = reinterpret_cast<const __half2*>(&w.x);
-    const float2 m = __half22float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
-    return fmaxf(m.x, m.y);
 }
 // The largest number of the logits' type below x (of -inf: itself).
 template <int DT>
@@ -216,11 +240,11 @@ __device__ __forceinline__ float below(float x) {
     if (x == -INFINITY) return x;
     return __uint_as_float(b >> 31 ? b + step : b - step);
 }
-// How many of 16 bytes of logits lie above x, added to n.
+// How many of 16 bytes of logits lie above x, added to n: two counts, of 16-bit logits in 16 bits (exact up to 2^8).
 template <int DT>
 __device__ __forceinline__ void count_above(const uint4& w, float x, float2& n) {
 #pragma unroll
-    for (int e = 0; e < kElems<DT> / 2; ++e) {
+    for (int e = 0; e < 2; ++e) {
         const float2 v = pair<DT>(w, e);
         float2 y;
         asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(y.x) : "f"(v.x), "f"(x));
@@ -228,7 +252,13 @@ __device__ __forceinline__ void count_above(const uint4& w, float x, float2& n) 
         n = __fadd2_rn(n, y);
     }
 }
-
+template <int DT>
+__device__ __forceinline__ void count_above(const uint4& w, float x, typename Two<DT>::T& n) {
+    const auto* p = reinterpret_cast<const typename Two<DT>::T*>(&w.x);
+    const auto y = Two<DT>::both(x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) n = __hadd2(n, __hgt2(p[e], y));
+}
 // 16 bytes of logits from id on that reach past the row's ends: -inf there.  `have`: they were read; else they reach
 // past the logits' own ends and are read one by one.  (Out of line: rare, and long.)
 template <int DT>
@@ -560,10 +590,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             }
         }
         // ---- maximum, sums
-        float top = largest<DT>(cur[0]);
-#pragma unroll
-        for (int x = 1; x < kVecs; ++x) top = fmaxf(top, largest<DT>(cur[x]));
-        top = fmaxf(top, -INFINITY);  // (of NaN alone: -inf)
+        const float top = fmaxf(largest<DT, kVecs>(cur), -INFINITY);  // (of NaN alone: -inf)
         // The sums are relative to a maximum that moves only when weights would pass 2^kSlack.
         if (!((top - m) * a.c1 <= kSlack) && top > m) {
             if (m != -INFINITY) {
@@ -595,8 +622,15 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             // A piece that starts ahead of the token counts equal ones too; of the token's own, those from the token on
             // are taken off again.  (A likely token has few ahead of it: most chunks have none.)
             if (__any_sync(0xffffffffu, top > (c <= tok_chunk ? xt.y : xt.x))) {
+                if constexpr (DT == GRAFT_F32) {
 #pragma unroll
-                for (int x = 0; x < kVecs; ++x) count_above<DT>(cur[x], id_of(c, x) < tok ? xt.y : xt.x, cnt);
+                    for (int x = 0; x < kVecs; ++x) count_above<DT>(cur[x], id_of(c, x) < tok ? xt.y : xt.x, cnt);
+                } else {
+                    auto n = Two<DT>::both(0.f);
+#pragma unroll
+                    for (int x = 0; x < kVecs; ++x) count_above<DT>(cur[x], id_of(c, x) < tok ? xt.y : xt.x, n);
+                    cnt = __fadd2_rn(cnt, Two<DT>::up(n));
+                }
                 if (c == tok_chunk) {
 #pragma unroll
                     for (int x = 0; x < kVecs; ++x)
@@ -671,7 +705,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
                 uint4 again = make_uint4(0, 0, 0, 0);
                 if (id >= 0 && id + E <= a.V) again = *reinterpret_cast<const uint4*>(row + (int64_t)id * kBytes);
                 else again = ragged<DT>(again, false, row, id, a.V);
-                if (!passes(largest<DT>(again))) continue;
+                if (!passes(largest<DT, 1>(&again))) continue;
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const float2 p = pair<DT>(again, e / 2);
