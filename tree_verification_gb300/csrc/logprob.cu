@@ -371,6 +371,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(16) unsigned char s_ring[];  // [stage][piece][thread] 16 bytes
     __shared__ int s_entry[kMaxRows], s_tok[kMaxRows];
     __shared__ const char* s_row[kMaxRows];
+    __shared__ int s_may[kMaxRows];  // which of its pieces may be read
     __shared__ float2 s_xt[kMaxRows];  // the given token's logit, and the largest number below it
     constexpr int kCap = kWarpTeam ? 1024 : 256;
     __shared__ unsigned short s_max[kMaxChunks][kThreads];  // a segment's largest, by chunk and thread: upper bf16 bounds
@@ -471,6 +472,22 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     }
     if (tid < 2 * kTeams) s_n[tid >> 1][tid & 1] = s_hits[tid >> 1][tid & 1] = 0;
     __syncthreads();
+    auto offset_of = [&](const char* row) { return (int)(reinterpret_cast<uintptr_t>(row) & 15) / kBytes; };
+    // A row's chunks start at the 16 bytes that its first logit lies in.
+    auto start_of = [&](const char* row) {
+        return reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15);
+    };
+    static_assert(kMaxRows <= kThreads, "a row a thread");
+    const bool listed_row = tid <= cta_r1 - cta_r0;
+    if (listed_row) {
+        // What of other rows lies in a row's first and last 16 bytes may be read, what lies around the logits may not: the
+        // first piece of the first row, the last one of the last.  (Bit 0: not the first; above it: how many from there.)
+        const char* row = s_row[tid];
+        const int first = start_of(row) < a.logits, pieces = (offset_of(row) + a.V + E - 1) / E;
+        const int64_t there = (a.logits_end - start_of(row)) / 16;
+        s_may[tid] = max((there < pieces ? (int)there : pieces) - first, 0) << 1 | first;
+    }
+    __syncthreads();
     const int team = kWarpTeam ? warp : 0;
     const bool idle = t_first + team >= teams;  // (warps of the last CTA)
     const int ttid = kWarpTeam ? lane : tid;
@@ -487,32 +504,31 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     const int row0 = (int)quotient(u0, per_row);
     int j = row0 - cta_r0, c = (int)(u0 - (int64_t)row0 * per_row);
     constexpr int kChunk = kVecs * kTeam * E;  // logits
-    auto offset_of = [&](const char* row) { return (int)(reinterpret_cast<uintptr_t>(row) & 15) / kBytes; };
-    // A row's chunks start at the 16 bytes that its first logit lies in.
-    auto start_of = [&](const char* row) {
-        return reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15);
-    };
     // chunks of a row that lie within it: [x, y)
     auto inside_of = [&](int off) { return make_int2(off != 0, (a.V + off) / kChunk); };
-    // (what of other rows lies in a row's first and last 16 bytes may be read, what lies around the logits may not)
     auto readable = [&](const char* p) { return p >= a.logits && p + 16 <= a.logits_end; };
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(s_ring)) + tid * 16;
     constexpr uint32_t kStageBytes = kVecs * kThreads * 16;
     int j_in = j, c_in = c, in = left;
     uint32_t dst = ring;
     const char* src = start_of(s_row[j]) + ((int64_t)c * (kVecs * kTeam) + ttid) * 16;
-    int2 in_whole = inside_of(offset_of(s_row[j]));
+    int2 in_may, in_whole;  // of the row: pieces of 16 bytes, x and [x, x + y) of them; chunks wholly among them, [x, y)
+    auto begin_in = [&](int j) {
+        const int may = s_may[j];
+        in_may = make_int2(may & 1, may >> 1);
+        in_whole = make_int2(in_may.x, (in_may.x + in_may.y) / (kVecs * kTeam));
+    };
+    begin_in(j);
     auto issue = [&]() {  // the next chunk's copies (a thread's own pieces: it waits for them alone)
         if (in > 0) {
             if (c_in >= in_whole.x && c_in < in_whole.y) {
 #pragma unroll
                 for (int x = 0; x < kVecs; ++x) cp_async16(dst + x * kThreads * 16, src + x * kTeam * 16);
             } else {
-                const int id = (c_in * kVecs * kTeam + ttid) * E - offset_of(s_row[j_in]);
-#pragma unroll 1
+                const unsigned piece = (unsigned)(c_in * kVecs * kTeam + ttid) - in_may.x;
+#pragma unroll
                 for (int x = 0; x < kVecs; ++x)
-                    if (id + x * kTeam * E < a.V && readable(src + x * kTeam * 16))
-                        cp_async16(dst + x * kThreads * 16, src + x * kTeam * 16);
+                    if (piece + x * kTeam < (unsigned)in_may.y) cp_async16(dst + x * kThreads * 16, src + x * kTeam * 16);
             }
             --in;
             src += kVecs * kTeam * 16;
@@ -521,7 +537,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
                 ++j_in;
                 if (in > 0) {
                     src = start_of(s_row[j_in]) + ttid * 16;
-                    in_whole = inside_of(offset_of(s_row[j_in]));
+                    begin_in(j_in);
                 }
             }
         }
@@ -529,8 +545,6 @@ logprob_part_kernel(const __grid_constant__ Args a) {
         cp_commit();
     };
     // The tokens and their logits: a read each among the first copies (behind all of them they took 6 us).
-    static_assert(kMaxRows <= kThreads, "a row a thread");
-    const bool listed_row = tid <= cta_r1 - cta_r0;
     const int my_tok = listed_row ? a.tokens[s_entry[tid]] : -1;
     issue();
     if (listed_row) {
@@ -586,7 +600,12 @@ logprob_part_kernel(const __grid_constant__ Args a) {
 #pragma unroll
             for (int x = 0; x < kVecs; ++x) {
                 const int id = id_of(c, x);
-                if (id < 0 || id + E > a.V) cur[x] = ragged<DT>(cur[x], readable(row + (int64_t)id * kBytes), row, id, a.V);
+                if (id >= a.V) {
+                    constexpr uint32_t kNone = DT == GRAFT_F32 ? 0xff800000u : DT == GRAFT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+                    cur[x] = make_uint4(kNone, kNone, kNone, kNone);
+                } else if (id < 0 || id + E > a.V) {
+                    cur[x] = ragged<DT>(cur[x], readable(row + (int64_t)id * kBytes), row, id, a.V);
+                }
             }
         }
         // ---- maximum, sums
