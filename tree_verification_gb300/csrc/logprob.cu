@@ -35,7 +35,7 @@ constexpr int kWarps = kThreads / 32;
 // two; bf16 161 and 120).
 constexpr int kResident = 2;
 constexpr int kSeg = 40;       // chunks of a segment
-constexpr int kMaxRows = 160;  // rows of a CTA's runs at most
+constexpr int kMaxRows = 128;  // rows of a CTA's runs at most
 constexpr int kShort = 4096;   // logits of a row that a warp takes
 constexpr float kFloor = -150.f;  // log2 of a weight that is zero in 32 bits
 // log2 of the largest weight before the sums are moved to a new maximum.  (ln s and t / s cancel where a token is all but
@@ -385,19 +385,14 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     __shared__ int s_may[kMaxRows];  // which of its pieces may be read
     __shared__ float2 s_xt[kMaxRows];  // the given token's logit, and the largest number below it
     constexpr int kCap = kWarpTeam ? 1024 : 256;
-    // With alternatives a segment's largest, by chunk and thread: upper bf16 bounds.  Without, the sums of the rows'
-    // parts, by row and warp (of a row alone where warps are teams).
+    __shared__ unsigned short s_max[kMaxChunks][kThreads];  // a segment's largest, by chunk and thread: upper bf16 bounds
     constexpr int kParts = kWarpTeam ? 1 : kWarps;
-    __shared__ __align__(16) unsigned char s_pool[kMaxChunks * kThreads * 2];
-    static_assert(sizeof(s_pool) >= kMaxRows * kParts * sizeof(float4), "");
-    auto s_max = reinterpret_cast<unsigned short(*)[kThreads]>(s_pool);
-    auto s_part = reinterpret_cast<float4(*)[kParts]>(s_pool);
+    __shared__ float4 s_part[kMaxRows][kParts];  // the sums of the rows' parts, by warp
     __shared__ uint64_t s_cand[kCap + kTeams * 32];  // candidates, and the best so far behind them
     __shared__ uint64_t s_list[kTeams][32];          // the best so far, best first; 0: none
     __shared__ int s_hit[kCap];                      // chunk and thread whose largest reaches the threshold
     __shared__ int s_n[kTeams][2], s_hits[kTeams][2], s_scan[kWarps];
     __shared__ float s_reach[32];
-    __shared__ float4 s_red[2][kWarps];  // the warps' sums at a part's end, by its parity
     __shared__ uint64_t s_best[kWarps];
     griddep_enter();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
@@ -603,7 +598,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     float m = -INFINITY;
     float2 s = make_float2(0.f, 0.f), t = s, cnt = s;
     float seg_max = -INFINITY;
-    int parity = 0, turn = 0, c_part = c, c_seg = c;  // the part's and the segment's first chunk
+    int turn = 0, c_part = c, c_seg = c;  // the part's and the segment's first chunk
     while (true) {
         const int c2 = c + 1 == a.chunks ? 0 : c + 1;
         auto id_of = [&](int c, int x) { return ((c * kVecs + x) * kTeam + ttid) * E - off; };
@@ -688,7 +683,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
         if (ends) {
             float4 v = make_float4(m, s.x + s.y, t.x + t.y, cnt.x + cnt.y);
             add_lanes<32>(v, a.c1);
-            if (lane == 0) (a.top > 0 ? s_red[parity][warp] : s_part[j][kWarpTeam ? 0 : warp]) = v;
+            if (lane == 0) s_part[j][kWarpTeam ? 0 : warp] = v;
         }
         // ---- alternatives
         if (a.top > 0 && (ends || c - c_seg == kSeg - 1)) {
@@ -821,24 +816,10 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             c_seg = c + 1;
         }
         if (ends) {
-            if (a.top > 0 && (kWarpTeam || warp == 0)) {
-                float4 v = s_red[parity][kWarpTeam ? warp : lane & 7];
-                if (!kWarpTeam) add_lanes<kWarps>(v, a.c1);
-                const uint64_t list = lane < a.top ? s_list[team][lane] : 0;
-                if (c_part == 0 && c2 == 0) {  // the whole row
-                    finish(a, s_entry[j], tok >= 0, s_xt[j].x, v.x, v.y, v.z, (int)v.w, list);
-                } else {
-                    const int64_t slot = (int64_t)(cta_r0 + j) + cta;
-                    if (lane == 0) {
-                        a.sums[slot] = make_float4(v.x, v.y, v.z, __int_as_float((int)v.w));
-                        a.entry[slot] = s_entry[j];
-                    }
-                    if (lane < a.top) a.keys[slot * a.top + lane] = list;
-                }
-            }
+            if ((kWarpTeam || warp == 0) && lane < a.top)
+                a.keys[((int64_t)(cta_r0 + j) + cta) * a.top + lane] = s_list[team][lane];
             m = seg_max = -INFINITY;
             s = t = cnt = make_float2(0.f, 0.f);
-            parity ^= 1;
             c_part = c_seg = c2;
         }
         c = c2;
@@ -848,10 +829,26 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             begin_row();
         }
     }
-    if (a.top > 0) return;
-    // Without alternatives the rows end here, all at once, a row a thread.  (One after another in the run, by a warp that the
-    // others waited for: 1999 rows of 32003 in bf16 50.6 us, 47.6 here.)
+    // The rows end here, side by side.  (One by one in the run, by a warp that the others waited for, code that is out of
+    // the caches by then took 4000 to 7000 cycles a row: NNN)
     sync();
+    auto is_whole = [&](int x) { return (x > j0 || c0 == 0) && (x < j || c == 0); };
+    if (a.top > 0) {
+#pragma unroll 1
+        for (int x = j0 + (kWarpTeam ? 0 : warp); x <= j; x += kParts) {
+            float4 v = s_part[x][kWarpTeam ? 0 : lane & 7];
+            if (!kWarpTeam) add_lanes<kWarps>(v, a.c1);
+            const int64_t slot = (int64_t)(cta_r0 + x) + cta;
+            if (is_whole(x)) {
+                const uint64_t list = lane < a.top ? a.keys[slot * a.top + lane] : 0;
+                finish(a, s_entry[x], s_tok[x] >= 0, s_xt[x].x, v.x, v.y, v.z, (int)v.w, list);
+            } else if (lane == 0) {
+                a.sums[slot] = make_float4(v.x, v.y, v.z, __int_as_float((int)v.w));
+                a.entry[slot] = s_entry[x];
+            }
+        }
+        return;
+    }
     for (int x = j0 + ttid; x <= j; x += kTeam) {
         float4 v = s_part[x][0];
 #pragma unroll
@@ -866,7 +863,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             v.z += f * (o.z + max_nan(d, kFloor) * o.y);
             v.w += o.w;
         }
-        if ((x > j0 || c0 == 0) && (x < j || c == 0)) {  // the whole row
+        if (is_whole(x)) {
             answer(a, Law(v.x, v.y), s_entry[x], s_tok[x] >= 0, s_xt[x].x, v.y, v.z, (int)v.w);
         } else {
             const int64_t slot = (int64_t)(cta_r0 + x) + cta;
