@@ -5,7 +5,7 @@
 //   rank(v) = #{x > x_v} + #{x = x_v at lower ids},  the top k by (x descending, id ascending).
 //
 // Every logit of the rows asked for is read once (4 or 2 bytes) and costs about ten instructions: HBM bounds fp32, the
-// issue of instructions 16-bit logits (1024 rows of 151936: fp32 108 us, 5.8 TB/s; bf16 88 us, 3.5 TB/s).
+// issue of instructions 16-bit logits (1024 rows of 151936: fp32 110 us, 5.7 TB/s; bf16 69 us, 4.5 TB/s).
 // logprob_part_kernel lays the rows' chunks (32 logits a thread) side by side and gives every team of threads an even run
 // of them, so all end together whatever the number of rows; the next chunks come through a ring in shared memory
 // (cp.async, each thread its own pieces: no barrier) while one is worked on.  A thread keeps its own maximum and sums
@@ -15,7 +15,7 @@
 // Top alternatives cost the pass one store a thread and chunk, a bound of the chunk's largest of the thread's logits.
 // Once a segment (kSeg chunks, or a row's end) a threshold is taken that at least k of the threads' largest reach; the
 // pieces above it (some 50) are read once more, all threads at once; what passes goes to a buffer in shared memory and
-// finds its place by counting (20 alternatives of the rows above: 126 us; 209 with candidates pushed and merged a chunk
+// finds its place by counting (20 alternatives of the rows above: 125 us; 209 with candidates pushed and merged a chunk
 // at a time).  Where more pass than the buffer holds (long runs of equal or of rising logits), the segment is gone
 // through chunk by chunk instead.
 #include <climits>
@@ -53,10 +53,11 @@ __device__ __forceinline__ void cp_wait() {
 
 template <int DT>
 constexpr int kElems = DT == GRAFT_F32 ? 4 : 8;  // of 16 bytes
-// 16-byte pieces of a chunk a thread, and chunks in shared memory (one worked on, the others on their way): a thread has 32
-// logits of a chunk (1024 rows of 151936: fp32 126 us, with 16 of them 131; bf16 112, with 64 of them 124).
+// 16-byte pieces of a chunk a thread, and chunks in shared memory (one worked on, the others on their way).  1024 rows of
+// 151936 with 20 alternatives, eight pieces and four: fp32 126 and 131 us, bf16 98 and 100; 1999 rows of 32768 in bf16 39
+// and 43 (of 8192, half a chunk, 19 and 15.5).
 template <int DT>
-constexpr int kVecsOf = DT == GRAFT_F32 ? 8 : 4;
+constexpr int kVecsOf = 8;
 template <int DT>
 constexpr int kStagesOf = 16 / kVecsOf<DT>;
 constexpr int kRing = 16 * kThreads * 16;
@@ -638,7 +639,8 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             const float base = m == -INFINITY ? 0.f : -m;
             const float2 base2 = make_float2(base, base), c12 = make_float2(a.c1, a.c1);
 #pragma unroll
-            for (int x = 0; x < kVecs; ++x)
+            for (int x = 0; x < kVecs; ++x) {
+                if (x == kVecs / 2 && (c * kVecs + x) * kTeam * E - off >= a.V) break;  // (the row ends in the first half)
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e) {
                     float2 d = __fmul2_rn(__fadd2_rn(pair<DT>(cur[x], e), base2), c12);
@@ -648,6 +650,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
                     s = __fadd2_rn(s, w);
                     t = __ffma2_rn(d, w, t);
                 }
+            }
         }
         // ---- tokens ahead of the given one
         if (c > one_by_one) {
@@ -829,8 +832,8 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             begin_row();
         }
     }
-    // The rows end here, side by side.  (One by one in the run, by a warp that the others waited for, code that is out of
-    // the caches by then took 4000 to 7000 cycles a row: NNN)
+    // The rows end here, side by side.  (One by one in the run, by a warp that the others waited for, that took 4000 to 7000
+    // cycles a row: 1999 rows of 32003 in bf16 51 us, 45.5 here.)
     sync();
     auto is_whole = [&](int x) { return (x > j0 || c0 == 0) && (x < j || c == 0); };
     if (a.top > 0) {
