@@ -82,7 +82,7 @@ struct Args {
     // workspace
     int32_t* n_rows;    // rows that are asked for
     float4* sums;       // [N + ctas] of a piece: m, s, t, bits of the count of better tokens
-    int32_t* entry;     // [N + ctas]
+    int2* entry;        // [N + ctas]: the entry (its complement where it has no token), bits of its token's logit
     uint64_t* keys;     // [N + ctas][top]
 };
 
@@ -835,6 +835,9 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     // The rows end here, side by side.  (One by one in the run, by a warp that the others waited for, that took 4000 to 7000
     // cycles a row: 1999 rows of 32003 in bf16 51 us, 45.5 here.)
     sync();
+    auto given_of = [&](int x) {
+        return make_int2(s_tok[x] >= 0 ? s_entry[x] : ~s_entry[x], __float_as_int(s_xt[x].x));
+    };
     auto is_whole = [&](int x) { return (x > j0 || c0 == 0) && (x < j || c == 0); };
     if (a.top > 0) {
 #pragma unroll 1
@@ -847,7 +850,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
                 finish(a, s_entry[x], s_tok[x] >= 0, s_xt[x].x, v.x, v.y, v.z, (int)v.w, list);
             } else if (lane == 0) {
                 a.sums[slot] = make_float4(v.x, v.y, v.z, __int_as_float((int)v.w));
-                a.entry[slot] = s_entry[x];
+                a.entry[slot] = given_of(x);
             }
         }
         return;
@@ -871,7 +874,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
         } else {
             const int64_t slot = (int64_t)(cta_r0 + x) + cta;
             a.sums[slot] = make_float4(v.x, v.y, v.z, __int_as_float((int)v.w));
-            a.entry[slot] = s_entry[x];
+            a.entry[slot] = given_of(x);
         }
     }
 }
@@ -893,6 +896,7 @@ logprob_join_kernel(const __grid_constant__ Args a) {
         const int64_t slot0 = (int64_t)r + c0;
         const int pieces = c1 - c0 + 1;
         if (pieces == 1) continue;
+        const int2 e = a.entry[slot0];
         uint64_t list = 0;
         if (a.top > 0) {
             for (int p = warp; p < pieces; p += kJoinWarps)
@@ -927,12 +931,7 @@ logprob_join_kernel(const __grid_constant__ Args a) {
             t += __shfl_xor_sync(0xffffffffu, t, d);
             cnt += __shfl_xor_sync(0xffffffffu, cnt, d);
         }
-        const int n = a.entry[slot0];
-        int64_t row = n;
-        if (a.rows != nullptr) row = (a.block > 0 ? (int64_t)(n / a.block) * a.block : 0) + a.rows[n];
-        const int tok = a.tokens[n];
-        const bool ok = tok >= 0 && tok < a.V;
-        finish(a, n, ok, ok ? load_logit<DT>(a.logits + row * a.stride, tok) : 0.f, m, s, t, cnt, list);
+        finish(a, e.x < 0 ? ~e.x : e.x, e.x >= 0, __int_as_float(e.y), m, s, t, cnt, list);
     }
 }
 
@@ -975,7 +974,7 @@ int launch(Args& a, cudaStream_t st) {
 void carve(WsCarver& w, int N, int top, int ctas, Args* a) {
     int32_t* n = w.take<int32_t>(1);
     float4* sums = w.take<float4>((size_t)N + ctas);
-    int32_t* entry = w.take<int32_t>((size_t)N + ctas);
+    int2* entry = w.take<int2>((size_t)N + ctas);
     uint64_t* keys = w.take<uint64_t>(((size_t)N + ctas) * top);
     if (a != nullptr) {
         a->n_rows = n;
