@@ -281,6 +281,20 @@ def test_captured_and_on_another_stream():
         assert torch.equal(out[k], other[k])
 
 
+@pytest.mark.parametrize("top", [0, 3])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V,offset", [(4001, 0), (4001, 5), (20011, 3), (20016, 0)])
+def test_tokens_anywhere_in_a_piece_among_equals(V, offset, dtype, top):
+    # three values and -inf: ranks go by the ids of equal logits, from any place in 16 bytes and beside a chunk's ends
+    rng = np.random.default_rng(V + offset)
+    at = [e + d for e in (0, 64, 1024, 2048, 8192, 16384, V) for d in range(-17, 18) if 0 <= e + d < V]
+    toks = np.array(at)
+    x = torch.from_numpy(rng.choice([-2.0, 0.0, 1.5, -np.inf], (len(toks), V))).to(dtype)
+    got, status = run(x, toks, top=top, offset=offset)
+    check(x, toks, got, top=top)
+    assert status == 0
+
+
 def test_buffers_belong_to_the_given_stream(monkeypatch):
     # (scratch of the current stream could be handed to its next kernels before the call on the other one has run)
     x, st, made = logits(3, 40000, torch.float32, 12).to(DEV), torch.cuda.Stream(), []

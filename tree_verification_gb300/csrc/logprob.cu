@@ -5,7 +5,7 @@
 //   rank(v) = #{x > x_v} + #{x = x_v at lower ids},  the top k by (x descending, id ascending).
 //
 // Every logit of the rows asked for is read once (4 or 2 bytes) and costs about ten instructions: HBM bounds fp32, the
-// issue of instructions 16-bit logits (1024 rows of 151936: fp32 110 us, 5.7 TB/s; bf16 69 us, 4.5 TB/s).
+// issue of instructions 16-bit logits (1024 rows of 151936: fp32 108 us, 5.8 TB/s; bf16 67 us, 4.6 TB/s).
 // logprob_part_kernel lays the rows' chunks (32 logits a thread) side by side and gives every team of threads an even run
 // of them, so all end together whatever the number of rows; the next chunks come through a ring in shared memory
 // (cp.async, each thread its own pieces: no barrier) while one is worked on.  A thread keeps its own maximum and sums
@@ -15,7 +15,7 @@
 // Top alternatives cost the pass one store a thread and chunk, a bound of the chunk's largest of the thread's logits.
 // Once a segment (kSeg chunks, or a row's end) a threshold is taken that at least k of the threads' largest reach; the
 // pieces above it (some 50) are read once more, all threads at once; what passes goes to a buffer in shared memory and
-// finds its place by counting (20 alternatives of the rows above: 125 us; 209 with candidates pushed and merged a chunk
+// finds its place by counting (20 alternatives of the rows above: 124 us; 209 with candidates pushed and merged a chunk
 // at a time).  Where more pass than the buffer holds (long runs of equal or of rising logits), the segment is gone
 // through chunk by chunk instead.
 #include <climits>
