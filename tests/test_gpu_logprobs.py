@@ -119,6 +119,26 @@ def test_many_entries_few_rows():
     check(x, toks, got, rows=rows, top=3)
 
 
+@pytest.mark.parametrize("top", [0, 4])
+@pytest.mark.parametrize("V", [300, 4099])
+def test_the_most_entries(V, top):
+    # the longest lists of rows a CTA keeps: 65535 entries that name 61 rows; each as in a call of those rows alone
+    x = logits(61, V, torch.bfloat16, V)
+    toks = np.arange(61) * 4 % V
+    at = np.arange(65535) % 61
+    small, _ = run(x, toks, top=top)
+    check(x, toks, small, top=top)
+    got, status = run(x, toks[at], rows=at, top=top)
+    assert status == 0
+    pick = torch.from_numpy(at).to(DEV)
+    for k in small:
+        if small[k].dtype == torch.int32:
+            assert torch.equal(got[k], small[k][pick])
+        else:  # (a row that a CTA's run cuts is added up in another order: twice a check's tolerance)
+            ref = small[k][pick]
+            assert bool(((got[k] - ref).abs() <= 2 * (2.0 ** -18 * (8 if k == "entropy" else 1) + 2.0 ** -22 * ref.abs())).all())
+
+
 def test_rows_and_tokens_out_of_range():
     b = gb()
     x = logits(4, 300, torch.float32, 4)
