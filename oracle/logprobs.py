@@ -2,9 +2,9 @@
 
 Graft article, architecture paragraph: the emitted tokens follow the target's
 own distribution, p = softmax(logits / T).  In float64 from the definitions:
-log p = z - log sum exp z, H = -sum p log p, rank = tokens of a larger logit
-or of the same at a lower id, alternatives by (logit descending, id ascending)
-with NaN as low as -inf.
+log p = z - log sum exp z, H = -sum p log p, alternatives by (logit
+descending, id ascending) with NaN as low as -inf, rank = a token's place
+among them.
 """
 from __future__ import annotations
 
@@ -24,10 +24,8 @@ def row(x, token: int, top: int, T: float = 1.0):
     else:
         logp, entropy = np.full(len(x), np.nan), np.nan
     order = np.argsort(np.where(np.isnan(x), np.inf, -x), kind="stable")
-    if token >= 0:
-        with np.errstate(invalid="ignore"):
-            rank = int((x > x[token]).sum() + (x[:token] == x[token]).sum())
-    return (logp[token] if token >= 0 else 0.0), entropy, (rank if token >= 0 else -1), order[:top], logp[order[:top]]
+    rank = int(np.flatnonzero(order == token)[0]) if token >= 0 else -1
+    return (logp[token] if token >= 0 else 0.0), entropy, rank, order[:top], logp[order[:top]]
 
 
 def tokens(logits, toks, rows=None, block: int = 0, top: int = 0, T: float = 1.0):

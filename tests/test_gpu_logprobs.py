@@ -358,3 +358,41 @@ def test_refusals_of_the_binding():
     with pytest.raises(gb().GraftError):
         f(x[:3], t)  # more entries than rows
     assert f(x[:0], t[:0])["logprob"].numel() == 0
+
+
+def places(x, toks):
+    """Place of every row's token by (logit descending, id ascending), NaN as low as -inf."""
+    x = np.where(np.isnan(x), -np.inf, x)
+    at = np.arange(x.shape[1])[None]
+    own = np.take_along_axis(x, toks[:, None], 1)
+    return ((x > own) | ((x == own) & (at < toks[:, None]))).sum(1)
+
+
+@pytest.mark.parametrize("top", [0, 6])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V,offset,N", [(37, 0, 40), (4001, 5, 60), (9001, 0, 700), (33000, 3, 4), (151936, 0, 2)])
+def test_ranks_where_logits_are_nan(V, offset, N, dtype, top):
+    # tokens that are NaN themselves, and tokens of -inf, of +inf and of numbers with NaN at lower and at higher ids
+    rng = np.random.default_rng(V)
+    R = min(N, 8)
+    x = np.round(rng.normal(size=(R, V)) * 4) / 4
+    odd = rng.random((R, V))
+    x[odd < 0.3] = np.nan
+    x[(odd >= 0.3) & (odd < 0.6)] = -np.inf
+    x[R // 2:][(odd[R // 2:] >= 0.6) & (odd[R // 2:] < 0.61)] = np.inf
+    x[R - 1] = np.nan
+    rows = np.arange(N) % R
+    toks = rng.integers(0, V, N)
+    for i in range(N):  # a token of every kind, early, late and at the row's ends
+        r = x[rows[i]]
+        pick = np.flatnonzero([np.isnan, np.isneginf, np.isfinite, np.isposinf][(i // R + i) % 4](r))
+        if len(pick):
+            toks[i] = pick[[0, -1, len(pick) // 2][i % 3]]
+    x = torch.from_numpy(x).to(dtype)
+    got, status = run(x, toks, rows=rows, top=top, offset=offset)
+    assert status == 0
+    assert np.array_equal(got["rank"].cpu().numpy(), places(x.double().numpy()[rows], toks))
+    assert bool(torch.isnan(got["logprob"]).all()) and bool(torch.isnan(got["entropy"]).all())
+    for k in range(min(top, V)):  # the alternatives' own ranks are their places
+        again, _ = run(x, got["top_id"][:, k].cpu().numpy(), rows=rows, offset=offset)
+        assert bool((again["rank"] == k).all())

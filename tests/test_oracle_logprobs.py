@@ -52,3 +52,11 @@ def test_rows_and_blocks():
             assert got["rank"][i] == -1 and got["top_id"][i, 0] == -1 and got["entropy"][i] == 0
         else:
             assert got["logprob"][i] == r[0] and got["rank"][i] == r[2] and got["top_id"][i, 0] == r[3][0]
+
+
+def test_ranks_beside_nan():
+    # NaN ranks with -inf: a token's rank is its place among the alternatives
+    for x in ([0.0, np.nan, 1.0, -np.inf], [np.nan] * 4, [-np.inf, np.nan, -np.inf, 2.0], [np.nan, np.inf, -np.inf, np.inf]):
+        ids = olp.row(np.array(x), 0, 4)[3].tolist()
+        assert [olp.row(np.array(x), v, 0)[2] for v in ids] == [0, 1, 2, 3]
+    assert [olp.row(np.array([0.0, np.nan, 1.0, -np.inf]), v, 0)[2] for v in range(4)] == [1, 2, 0, 3]

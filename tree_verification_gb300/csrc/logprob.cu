@@ -291,14 +291,14 @@ __device__ __noinline__ float count_equal(uint4 w, int e0, float x) {
     }
     return n;
 }
-// How many of 16 bytes of logits from id on go ahead of token tok, of logit x.
+// How many of 16 bytes of logits from id on go ahead of token tok, of logit x (NaN as -inf).
 template <int DT>
 __device__ __noinline__ float count_ahead(uint4 w, int id, int tok, float x) {
     float n = 0.f;
 #pragma unroll
     for (int e = 0; e < kElems<DT>; ++e) {
         const float2 p = pair<DT>(w, e / 2);
-        const float v = (e & 1) ? p.y : p.x;
+        const float v = fmaxf((e & 1) ? p.y : p.x, -INFINITY);
         n += v > x || (v == x && id + e >= 0 && id + e < tok) ? 1.f : 0.f;
     }
     return n;
@@ -563,7 +563,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     issue();
     if (listed_row) {
         const bool ok = my_tok >= 0 && my_tok < a.V;
-        const float v = ok ? load_logit<DT>(s_row[tid], my_tok) : INFINITY;
+        const float v = ok ? fmaxf(load_logit<DT>(s_row[tid], my_tok), -INFINITY) : INFINITY;  // (NaN ranks with -inf)
         s_tok[tid] = ok ? my_tok : -1;
         s_xt[tid] = make_float2(v, below<DT>(v));
         if (!ok && my_tok != -1) flag_status(a.status, GRAFT_STATUS_TOKEN_RANGE);
