@@ -396,3 +396,32 @@ def test_ranks_where_logits_are_nan(V, offset, N, dtype, top):
     for k in range(min(top, V)):  # the alternatives' own ranks are their places
         again, _ = run(x, got["top_id"][:, k].cpu().numpy(), rows=rows, offset=offset)
         assert bool((again["rank"] == k).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V,N", [(151936, 2500), (1 << 20, 2500), ((1 << 24) - 24, 1300)])
+def test_sums_of_long_rows_of_equal_logits(V, N, dtype):
+    """Rows whose first 16384 logits are 0 and whose others are all the same number below: a thread adds the same weight
+    again and again, so its roundings go one way.  So many entries name a row that CTAs take it whole.
+
+    ln s is off by: a chunk's 32 equal terms a lane of a pair, whose partial sums round by k / 32 of 2^-24 each (2^-20);
+    the chunks', which keep what they round off (2^-23); 16 sums of lanes, warps and pieces (2^-20); a weight by 2^-22
+    and by its exponent's two roundings (ln 2 x 4 x 2^-23 < 2^-21); log and differences 2^-23: 2^-18 in all.  log p takes
+    a rounding of the result more (2^-24 of it).  The entropy is ln s - ln 2 t / s with |t / s| < 4, t off as s is: 2^-18
+    (1 + 2 x 2.8) < 2^-15."""
+    C, low = 16384, [-0.21484375, -0.65625, -1.375, -1.484375, -2.21875, -2.4375, -2.6875, -2.71875]
+    low = low[:len(low) if V < 1 << 22 else 2]
+    x = torch.zeros(len(low), V, dtype=dtype, device=DEV)
+    for r, v in zip(x, low):
+        r[C:] = v
+    rows, toks = np.arange(N) * len(low) // N, np.where(np.arange(N) % 2, 5, V - 5)
+    got = gb().graft_token_logprobs(x, i32(toks), rows=i32(rows), top=1)
+    z = np.array(low)[rows]
+    s = C + (V - C) * np.exp(z)
+    for name, ref, tol in (("logprob", np.where(np.arange(N) % 2, 0, z) - np.log(s), 2.0 ** -18),
+                           ("entropy", np.log(s) - (V - C) * np.exp(z) * z / s, 2.0 ** -15),
+                           ("top_logprob", -np.log(s), 2.0 ** -18)):
+        err = np.abs(got[name].double().cpu().numpy().reshape(-1) - ref)
+        tol = tol + 2.0 ** -24 * np.abs(ref)
+        assert (err <= tol).all(), f"{name}: {err.max()}, {(err / tol).max()} of the tolerance"
+    assert got["rank"].tolist() == np.where(np.arange(N) % 2, 5, V - 5).tolist() and bool((got["top_id"] == 0).all())

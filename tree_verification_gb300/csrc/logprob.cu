@@ -389,6 +389,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     __shared__ unsigned short s_max[kMaxChunks][kThreads];  // a segment's largest, by chunk and thread: upper bf16 bounds
     constexpr int kParts = kWarpTeam ? 1 : kWarps;
     __shared__ float4 s_part[kMaxRows][kParts];  // the sums of the rows' parts, by warp
+    __shared__ float4 s_total[kThreads];  // a thread's sums over its part's chunks, and what they round off
     __shared__ uint64_t s_cand[kCap + kTeams * 32];  // candidates, and the best so far behind them
     __shared__ uint64_t s_list[kTeams][32];          // the best so far, best first; 0: none
     __shared__ int s_hit[kCap];                      // chunk and thread whose largest reaches the threshold
@@ -597,7 +598,8 @@ logprob_part_kernel(const __grid_constant__ Args a) {
     begin_row();
     int stage = 0;
     float m = -INFINITY;
-    float2 s = make_float2(0.f, 0.f), t = s, cnt = s;
+    float2 cnt = make_float2(0.f, 0.f);
+    s_total[tid] = make_float4(0.f, 0.f, 0.f, 0.f);
     float seg_max = -INFINITY;
     int turn = 0, c_part = c, c_seg = c;  // the part's and the segment's first chunk
     while (true) {
@@ -628,14 +630,15 @@ logprob_part_kernel(const __grid_constant__ Args a) {
         if (!((top - m) * a.c1 <= kSlack) && top > m) {
             if (m != -INFINITY) {
                 const float d = (m - top) * a.c1, f = ex2(d), dd = max_nan(d, kFloor);
-                t.x = f * (t.x + dd * s.x);
-                t.y = f * (t.y + dd * s.y);
-                s.x *= f;
-                s.y *= f;
+                const float4 v = s_total[tid];
+                s_total[tid] = make_float4(f * v.x, f * (v.y + dd * v.x), f * v.z, f * (v.w + dd * v.z));
             }
             m = top;
         }
         {
+            // A chunk's sums by themselves, then added to those of the chunks before, which keep what they round off: over a
+            // long row of alike weights one chain of sums went one way (ln s of 2^20 logits 3e-5 off, of 2^24 3e-4).
+            float2 s = make_float2(0.f, 0.f), t = s;
             const float base = m == -INFINITY ? 0.f : -m;
             const float2 base2 = make_float2(base, base), c12 = make_float2(a.c1, a.c1);
 #pragma unroll
@@ -651,6 +654,12 @@ logprob_part_kernel(const __grid_constant__ Args a) {
                     t = __ffma2_rn(d, w, t);
                 }
             }
+            const float4 v = s_total[tid];
+            const float2 before = make_float2(v.x, v.y);
+            const float2 more = __fadd2_rn(make_float2(s.x + s.y, t.x + t.y), make_float2(-v.z, -v.w));
+            const float2 sum = __fadd2_rn(before, more);
+            const float2 over = make_float2((sum.x - v.x) - more.x, (sum.y - v.y) - more.y);
+            s_total[tid] = make_float4(sum.x, sum.y, over.x, over.y);
         }
         // ---- tokens ahead of the given one
         if (c > one_by_one) {
@@ -684,7 +693,8 @@ logprob_part_kernel(const __grid_constant__ Args a) {
         }
         const bool ends = c2 == 0 || left == 1;  // the part's last chunk
         if (ends) {
-            float4 v = make_float4(m, s.x + s.y, t.x + t.y, cnt.x + cnt.y);
+            const float4 sums = s_total[tid];
+            float4 v = make_float4(m, sums.x - sums.z, sums.y - sums.w, cnt.x + cnt.y);
             add_lanes<32>(v, a.c1);
             if (lane == 0) s_part[j][kWarpTeam ? 0 : warp] = v;
         }
@@ -822,7 +832,8 @@ logprob_part_kernel(const __grid_constant__ Args a) {
             if ((kWarpTeam || warp == 0) && lane < a.top)
                 a.keys[((int64_t)(cta_r0 + j) + cta) * a.top + lane] = s_list[team][lane];
             m = seg_max = -INFINITY;
-            s = t = cnt = make_float2(0.f, 0.f);
+            cnt = make_float2(0.f, 0.f);
+            s_total[tid] = make_float4(0.f, 0.f, 0.f, 0.f);
             c_part = c_seg = c2;
         }
         c = c2;
