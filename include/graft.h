@@ -699,8 +699,8 @@ int graft_paged_attention_ex(const GraftPagedCache* cache, const void* K_pool, c
  * Keys that no row of a sequence can see are not read: the cost follows the
  * window, and pages whose rows all lie from `first` on and at or before
  * lengths[b] - window may be given back, their entries of the block table
- * set to -1: these calls never read them, graft_pages_free flags them and
- * passes them over, graft_pages_fork refuses a sequence that has them.
+ * set to -1: these calls never read them, graft_pages_free passes them over,
+ * graft_pages_fork refuses a sequence that has them (GRAFT_STATUS_PAGE).
  * plan: graft_paged_plan_size bytes; a plan of another window or `first`, or
  * of none, is refused on the device (GRAFT_STATUS_PLAN), so layers of several
  * kinds take a plan each.
@@ -759,8 +759,11 @@ int graft_pages_fork(const GraftPagedCache* cache, int n, const int32_t* src, co
 
 /*
  * graft_pages_free — gives back the pages of sequences seqs[0 .. n-1]:
- * page_refs fall, held and lengths become 0, the block-table rows -1.  A
- * sequence named twice is freed once (GRAFT_STATUS_SEQUENCE).
+ * page_refs fall, held and lengths become 0, the block-table rows -1.
+ * Entries of -1 are pages given back before (behind a window) and passed
+ * over; other numbers outside the pool, and pages without a reference, set
+ * GRAFT_STATUS_PAGE.  A sequence named twice is freed once
+ * (GRAFT_STATUS_SEQUENCE).
  */
 int graft_pages_free(const GraftPagedCache* cache, int n, const int32_t* seqs, graft_stream_t stream);
 

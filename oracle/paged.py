@@ -116,7 +116,8 @@ class Pages:
     def free(self, seqs):
         for b in dict.fromkeys(int(x) for x in seqs):
             for p in self.table[b][:self.held[b]]:
-                self.refs[p] -= 1
+                if p >= 0:  # (else given back before, behind a window)
+                    self.refs[p] -= 1
             self.table[b] = [-1] * len(self.table[b])
             self.held[b] = self.lengths[b] = 0
 

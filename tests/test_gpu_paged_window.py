@@ -386,3 +386,42 @@ def test_refusals():
     with pytest.raises(ValueError):
         c.attend(0, Q, 0.1, window=5)
     assert c.attend(0, Q, 0.1).shape == Q.shape  # the other plan still stands
+
+
+def test_pages_given_back_behind_the_window():
+    """A sequence whose pages behind the window were given back reserves, attends and is freed like any other; a fork of it
+    is refused, and a number that is no page is still flagged."""
+    window, first, b = 50, 4, gb()
+    s = Setup([200, 40, 0], [8, 8, 0], 2, 16, seed=20, wide=4, tables=True)
+    c, refs = s.cache, s.refs.copy()
+    for j in range(s.counts[0]):
+        if j * s.page >= first and (j + 1) * s.page - 1 <= s.lens[0] - window:
+            refs[s.table[0, j]] = 0
+            s.table[0, j] = -1
+    given_back = int((s.table[0, :s.counts[0]] == -1).sum())
+    assert given_back == 8  # pages 1 to 8: rows 16 .. 143, before row 151 - 1
+    s.t.copy_(s.i32(s.table))
+    c.page_refs.copy_(s.i32(refs))
+    c.reserve(s.i32([30, 0, 0]))
+    assert s.status() == 0
+    held = c.held.tolist()
+    assert held == [15, 3, 0] and (np.array(c.page_refs.tolist()) > 0).sum() == 15 - given_back + 3
+    assert s.t[0, 1:9].tolist() == [-1] * 8
+    run(s, 4, window, first, out_of=False)
+    before = [t.tolist() for t in (c.page_refs, c.held, c.lengths, s.t)]
+    c.fork(s.i32([0]), s.i32([2]))
+    assert s.status() == b.STATUS_PAGE
+    assert before == [t.tolist() for t in (c.page_refs, c.held, c.lengths, s.t)]
+    kept = c.page_refs.clone()
+    for p in s.t[0, :15].tolist():
+        if p >= 0:
+            kept[p] = 0
+    c.free(s.i32([0]))
+    assert s.status() == 0
+    assert torch.equal(c.page_refs, kept) and c.held.tolist() == [0, 3, 0] and c.lengths.tolist() == [0, 40, 0]
+    assert bool((s.t[0] == -1).all())
+    for nonsense in (-2, 10**6, -2**31):  # no page, and none given back
+        s.t[1, 0] = nonsense
+        c.held[1] = 1
+        c.free(s.i32([1]))
+        assert s.status() == b.STATUS_PAGE

@@ -100,3 +100,9 @@ def test_compaction_by_hand():
     # rows 2, 3, 4 receive rows 2, 4, 7
     assert k[0, 1, 2] == K[0, 1, 2] and k[0, 1, 3] == K[0, 0, 0] and k[0, 0, 0] == K[0, 0, 3] and n[0] == 5
     assert v[0, 0, 0] == 100 + K[0, 0, 3]
+
+
+def test_a_sequence_whose_pages_behind_a_window_were_given_back_is_freed():
+    P = opg.Pages([[2, -1, -1, 1], [0, 1, -1, -1]], [4, 2], [60, 20], [1, 2, 1], 16)
+    P.free([0])
+    assert P.refs == [1, 1, 0] and P.table[0] == [-1] * 4 and P.held == [0, 2] and P.lengths == [0, 20]

@@ -127,7 +127,9 @@ free_kernel(const __grid_constant__ GraftPagedCache c, int n, const int32_t* __r
     for (int k = threadIdx.x; k < c.max_pages; k += blockDim.x) {
         if (k < held) {
             const int p = row[k];
-            if (p < 0 || p >= c.num_pages) {
+            if (p == -1) {
+                // (given back already, behind a window)
+            } else if (p < 0 || p >= c.num_pages) {
                 flag_status(c.status, GRAFT_STATUS_PAGE);
             } else if (atomicSub(c.page_refs + p, 1) <= 0) {
                 atomicAdd(c.page_refs + p, 1);  // held by nobody: the count stays
