@@ -388,6 +388,32 @@ def test_refusals():
     assert c.attend(0, Q, 0.1).shape == Q.shape  # the other plan still stands
 
 
+def test_a_plan_of_the_next_step_leaves_none_of_the_last():
+    # a kind that is planned again begins a step: plans that the last one attended are not attended in it
+    s = Setup([70, 10], [2, 2], 2, 16, seed=19)
+    c, Q = s.cache, s.randn(4, 8, 128).to(DEV)
+    kinds = [dict(), dict(window=5), dict(window=5, first=2)]
+    plan, attend = (lambda k: c.plan(s.q_start, 4, 8, 2, **k)), (lambda k: c.attend(0, Q, 0.1, **k))
+    for again in kinds:
+        for order in (kinds, kinds[::-1], kinds[1:] + kinds[:1]):  # steps that plan every kind first, in any order
+            for k in order:
+                plan(k)
+            for k in kinds + kinds:
+                attend(k)
+        for k in kinds:  # one that plans them as they come
+            plan(k)
+            attend(k)
+        attend(kinds[0])
+        plan(again)
+        for k in kinds:
+            if k is again:
+                attend(k)
+            else:
+                with pytest.raises(ValueError):
+                    attend(k)
+    assert s.status() == 0
+
+
 def test_pages_given_back_behind_the_window():
     """A sequence whose pages behind the window were given back reserves, attends and is freed like any other; a fork of it
     is refused, and a number that is no page is still flagged."""

@@ -113,6 +113,7 @@ class PagedCache:
         self._structs = {}      # address of an ``active`` tensor -> the struct with it
         self._plan_of = None    # (N, Hq, max_new, tree) of the last plan
         self._window_plans = {}  # (window, first) -> the same of the last plan with that window
+        self._attended = set()   # kinds (None, (window, first)) whose plan has been attended
         self._sizes = {}        # (N, Hq, max_new) -> bytes of plan and workspace
         self._buffers = {}      # name (a windowed plan's: its window and first) -> buffer in use
         self._kept = []         # buffers outgrown: captured graphs may still use them
@@ -245,15 +246,14 @@ class PagedCache:
 
     def plan(self, q_start, N: int, Hq: int, max_new: int, tree: bool = False, active=None, window: Optional[int] = None,
              first: int = 0) -> None:
-        """graft_paged_plan for a step of N rows; serves every attend() until the next plan().
+        """graft_paged_plan for a step of N rows; serves every attend() until the next step's plan().
 
         With ``window`` (and ``first``) graft_paged_plan_window, for the attend()s with the same two: a step whose
-        layers are of several kinds makes a plan of each.  (A handle keeps a plan buffer for every kind it has seen.)"""
+        layers are of several kinds makes a plan of each.  A kind that is planned again begins the next step: plans of
+        other kinds that have been attended are dropped, so that each is planned anew before it is attended.  (A handle
+        keeps a plan buffer for every kind it has seen.)"""
         kind = _kind(window, first)
-        if kind is None:  # (a plan that is refused leaves none)
-            self._plan_of = None
-        else:
-            self._window_plans.pop(kind, None)
+        again = self._drop(kind)  # (a plan that is refused leaves none)
         starts = self._need(q_start, "q_start", torch.int32, (self.n_seqs + 1,))
         key = (N, Hq, max_new)
         sizes = self._sizes.get(key)
@@ -274,10 +274,21 @@ class PagedCache:
         else:
             self._call("graft_paged_plan_window", self._with(active), N, Hq, starts, max_new, 1 if tree else 0, *kind,
                        buf.data_ptr(), buf.numel())
+        if again:
+            for other in list(self._attended):
+                self._drop(other)
         if kind is None:
             self._plan_of = (N, Hq, max_new, bool(tree))
         else:
             self._window_plans[kind] = (N, Hq, max_new, bool(tree))
+
+    def _drop(self, kind) -> bool:
+        """Forgets the plan of a kind; whether there was one."""
+        self._attended.discard(kind)
+        if kind is not None:
+            return self._window_plans.pop(kind, None) is not None
+        there, self._plan_of = self._plan_of is not None, None
+        return there
 
     def attend(self, layer: int, Q, scale: float, mask=None, out=None, tuning=None, window: Optional[int] = None,
                first: int = 0):
@@ -312,6 +323,7 @@ class PagedCache:
             self._call("graft_paged_attention_ex", self._c, self._kp[layer], self._vp[layer], N, Hq, max_new,
                        plan.data_ptr(), plan.numel(), qp, qs, mp, float(scale), op, ctypes.addressof(tuning),
                        ws.data_ptr(), ws.numel())
+        self._attended.add(kind)
         return out
 
     def compact(self, path, acc_len, lengths_out=None, active=None):
