@@ -388,6 +388,54 @@ def test_refusals():
     assert c.attend(0, Q, 0.1).shape == Q.shape  # the other plan still stands
 
 
+@pytest.mark.parametrize("window,first", [(300, 1), (8192, 1), (8193, 1), (300, 9000)])
+@pytest.mark.parametrize("new,lens", [([1, 2], [500, 310]), ([64] * 20, [500] * 20)])
+def test_small_weights_beside_a_large_one(new, lens, window, first):
+    """fp16: a first token that takes all but some thousandths of the weight and holds nothing, and many keys of equal
+    weights of 2^-20.5 of its: what the rows read is those keys' values, so their weights' rounding (half a step, 2^-11)
+    is all that may show, as it is without a window."""
+    s = Setup(lens, new, 8, 16, torch.float16, seed=18)
+    s.K0[:] = torch.where(torch.isnan(s.K0), s.K0, torch.zeros_like(s.K0))
+    for b in range(len(lens)):
+        for r in range(lens[b] + new[b]):
+            s.K0[:, s.table[b, r // 16], r % 16, :, 0] = 0.0 if r == 0 else -20.5 * np.log(2.0)
+            if r == 0:
+                s.V0[:, s.table[b, 0], 0] = 0.0
+    s.V0[:] = s.V0.abs() * 100 + 100 * (s.V0 != 0)
+    s.K.copy_(s.K0)
+    s.V.copy_(s.V0)
+    N = sum(new)
+    Q = torch.zeros(N, 8, 128, dtype=torch.float16)
+    Q[..., 0] = 1.0
+    for kw in (dict(window=window, first=first), dict()):
+        s.cache.plan(s.q_start, N, 8, max(new), **kw)
+        O = s.cache.attend(0, Q.to(DEV), 1.0, **kw)
+        assert s.status() == 0
+        check(s, O, Q, 1.0, kw.get("window", 10**6), kw.get("first", 0))
+
+
+@pytest.mark.parametrize("rise", [0.01, 0.05, 0.06, 0.07, 0.08, 0.125, 0.3, 2.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_scores_that_rise_from_key_to_key(dtype, rise):
+    # every block's largest score lies 128 `rise` (of log2) above the one before: around what fp16 weights by an old
+    # maximum can hold (2^9), and far past it
+    s = Setup([600] * 4, [200] * 4, 2, 16, dtype, seed=21)
+    s.K0[:] = torch.where(torch.isnan(s.K0), s.K0, torch.zeros_like(s.K0))
+    for b in range(4):
+        for r in range(800):
+            x = rise * np.log(2.0) * (r if b % 2 == 0 else 800 - r)
+            high = float(torch.tensor(x).to(dtype))
+            s.K0[:, s.table[b, r // 16], r % 16, :, 0], s.K0[:, s.table[b, r // 16], r % 16, :, 1] = high, x - high
+    s.K.copy_(s.K0)
+    Q = torch.zeros(800, 4, 128, dtype=dtype)
+    Q[..., :2] = 1.0
+    for window, first in ((500, 0), (500, 4), (129, 130)):
+        s.cache.plan(s.q_start, 800, 4, 200, window=window, first=first)
+        O = s.cache.attend(0, Q.to(DEV), 1.0, window=window, first=first)
+        assert s.status() == 0
+        check(s, O, Q, 1.0, window, first)
+
+
 def test_a_plan_of_the_next_step_leaves_none_of_the_last():
     # a kind that is planned again begins a step: plans that the last one attended are not attended in it
     s = Setup([70, 10], [2, 2], 2, 16, seed=19)

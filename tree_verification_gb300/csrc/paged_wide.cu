@@ -199,12 +199,14 @@ template <int DT, bool kTestWaits, bool kWindow>
 __global__ void __launch_bounds__(NTHREADS, 1)
 wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a) {
     using E = Elem<DT>;
-    // See paged_few.cu: small weights keep their bits.  Over 2^14 keys at most (a window), a lift of 2^3 keeps their sum to
-    // 2^14 x 2^-28 of the largest weight, an eighth of half a step, and leaves 2^12 for maxima that rise: few blocks are
-    // weighed twice (heads of scores 3 apart, chunks over 1024 keys: 137 -> 125 us).
-    constexpr float kLiftMost = DT == GRAFT_FP16 ? 7.f : 0.f;
-    const float kLift = kWindow && DT == GRAFT_FP16 && a.window <= 8192 && a.first <= 8192 ? 3.f : kLiftMost;
-    constexpr float kMaxSum = DT == GRAFT_FP16 ? 32768.f : 65536.f;  // of a block weighed by an old maximum
+    // See paged_few.cu: small weights keep their bits.  (Lifted by 2^3 in windows, so that fewer blocks are weighed twice,
+    // weights below 2^-17 of the largest lost bits, which show where the largest is that of a first token whose values are
+    // small.)
+    constexpr float kLift = DT == GRAFT_FP16 ? 7.f : 0.f;
+    // Most that the weights of a block and row may sum to by an old maximum.  In windows, where heads of scores 3 apart
+    // weighed many a block twice, it is what 128 finite weights can: a block is weighed again where one overflows (chunks of
+    // up to 2048 rows over 1024 keys: 131 us, 138 by 2^15, 126 with the lift of 2^3).
+    constexpr float kMaxSum = DT == GRAFT_FP16 ? (kWindow ? BN * 65504.f : 32768.f) : 65536.f;
     const uint64_t wait_ns = kTestWaits ? a.wait_ns : kWaitNs;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
