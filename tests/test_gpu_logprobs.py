@@ -425,3 +425,49 @@ def test_sums_of_long_rows_of_equal_logits(V, N, dtype):
         tol = tol + 2.0 ** -24 * np.abs(ref)
         assert (err <= tol).all(), f"{name}: {err.max()}, {(err / tol).max()} of the tolerance"
     assert got["rank"].tolist() == np.where(np.arange(N) % 2, 5, V - 5).tolist() and bool((got["top_id"] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [3000, 40000])
+def test_all_but_certain_tokens(dtype, V):
+    """Two tokens a row, the less likely one first in the same thread's logits, others -inf.  s = 1 + w with w <= e^-8 is
+    one rounding off (2^-24), a weight by 2^-22 and its exponent's roundings (16 x 2^-23): less than 2^-18 w < 2^-29, and
+    13 times that in the entropy (|z| <= 11.5); the last operations round numbers below 0.005: 2^-23 in all.  (Relative
+    to the first token's maximum ln s and t / s would be as large as 11 and cancel.)"""
+    gaps = np.linspace(8.0, 11.5, 15)
+    x = torch.full((15, V), -float("inf"))
+    step = {3000: 1024 if dtype == torch.float32 else 2048, 40000: 8192 if dtype == torch.float32 else 16384}[V]
+    x[:, 700] = torch.from_numpy(1.0 - gaps).float()
+    x[:, 700 + step] = 1.0
+    x = x.to(dtype)
+    N = 900
+    rows, toks = np.arange(N) * 15 // N, np.where(np.arange(N) % 2, 700, 700 + step)
+    got, status = run(x, toks, rows=rows, top=2)
+    assert status == 0
+    w = np.exp(x[:, 700].double().numpy() - 1.0)[rows]
+    likely = toks != 700
+    ref = dict(logprob=np.where(likely, 0.0, np.log(w)) - np.log1p(w), entropy=np.log1p(w) - w * np.log(w) / (1 + w),
+               top_logprob=np.stack([-np.log1p(w), np.log(w) - np.log1p(w)], 1))
+    for name, want in ref.items():
+        err = np.abs(got[name].double().cpu().numpy() - want)
+        tol = 2.0 ** -23 + 2.0 ** -24 * np.abs(want)
+        assert (err <= tol).all(), f"{name}: {err.max()}, {(err / tol).max()} of the tolerance"
+
+
+@pytest.mark.parametrize("T", [1.0, 0.7, 3.3])
+@pytest.mark.parametrize("high", [1e3, 1e4, 1e5])
+def test_log_probabilities_far_below_the_largest(high, T):
+    """Logits around zero beside one of 1e3 to 1e5: log p = (x - m) / T - ln s is as large as m / T and rounded once, half a
+    step of it (2^-24); what is left of the difference, of the quotient and of 1 / T comes along in a second number (each
+    within 2^-24 of 2^-24 of the whole: 2^-40).  ln s is 0 here."""
+    x = logits(4, 3000, torch.float32, 13)
+    x[:, 9] = torch.tensor([high, high * 1.1, high * 1.37, high * 1.83])
+    toks = [40 + i for i in range(2900)]
+    rows = np.arange(4).repeat(2900)
+    toks = np.array(toks * 4)
+    got, status = run(x, toks, rows=rows, top=9, T=T)
+    assert status == 0
+    T = float(np.float32(T))
+    ref = (x.double().numpy()[rows, toks] - x[:, 9].double().numpy()[rows]) / T
+    err = np.abs(got["logprob"].double().cpu().numpy() - ref)
+    assert (err <= (2.0 ** -24 + 2.0 ** -40) * np.abs(ref)).all(), (err / np.abs(ref)).max() * 2 ** 24
