@@ -624,7 +624,9 @@ int graft_rope_append(const GraftPagedCache* cache, void* K_pool, void* V_pool, 
  * then the rotation as above; 32 bits throughout, rounded once, behind the
  * rotation.  q_weight, k_weight [128] f32 (device, one for all heads), either
  * NULL: those heads are not normed (both NULL: graft_rope_append).  eps > 0 and finite.
- * The squares are summed in 32 bits: elements stay below 2^60.
+ * The squares are summed in 32 bits: elements stay below 2^60 (a head whose
+ * sum of squares passes 32 bits becomes zeros, as it does in 32-bit arithmetic
+ * throughout; infinities and NaN give NaN).
  */
 int graft_norm_rope_append(const GraftPagedCache* cache, void* K_pool, void* V_pool, int N, int Hq,
                            const int32_t* q_start, const int32_t* pos, const double* inv_freq, int rot_dim,
