@@ -39,16 +39,26 @@ __device__ __forceinline__ bool takes_part(const GraftPagedCache& c, int b) { re
 //   row blocks split by keys
 // "Few" entries (paged_few.cu): sequences of at most few_rows query rows (new rows x group).  "Wide" ones
 // (paged_wide.cu): all others, in blocks of two tiles of tile_tokens new rows.
+// The head's fields take 64 bytes: what a kernel reads of it before it starts is one trip of a warp's half (with 72 bytes
+// a tree of one request took 0.3 us a layer more).
 struct PlanHead {
-    int32_t magic, N, Hq, Hkv, n_seqs, max_new, tree, page_rows, max_pages, num_pages, few_rows, ctas;
+    int32_t magic, N;
+    int32_t heads;       // Hq, Hkv
+    int32_t n_seqs, max_new;
+    int32_t rows;        // few_rows, page_rows, tree
+    int32_t max_pages, num_pages, ctas;
     int32_t few_ctas;    // CTAs of the few kernel that have work
     int32_t rounds;      // whole rounds of wide items: every CTA takes one of each
     int32_t n_groups;    // row blocks split by keys
     int32_t tiles;       // tiles of such a row block at most
     int32_t window, first;  // of a windowed plan (window 0: none)
-    int32_t reserved[13];
+    int32_t reserved[17];
 };
-constexpr int32_t kPlanMagic = 0x47503033;
+constexpr int32_t kPlanMagic = 0x47503034;
+__host__ __device__ __forceinline__ int32_t plan_heads(int Hq, int Hkv) { return Hq << 16 | Hkv; }
+__host__ __device__ __forceinline__ int32_t plan_rows(int few_rows, int page_rows, int tree) {
+    return few_rows << 16 | page_rows << 1 | tree;
+}
 
 struct Entry {
     int32_t b;       // sequence
@@ -181,10 +191,10 @@ int few_launch(const AttnArgs& a, cudaStream_t st);
 
 // Is the plan one for these arguments?  (The lengths and row counts in it were checked when it was made.)
 __device__ __forceinline__ bool plan_fits(const AttnArgs& a, const PlanHead& h) {
-    return h.magic == kPlanMagic && h.N == a.N && h.Hq == a.Hq && h.Hkv == a.c.Hkv && h.n_seqs == a.c.n_seqs &&
-           h.max_new == a.max_new && h.tree == (a.mask != nullptr) && h.page_rows == a.c.page_rows &&
-           h.max_pages == a.c.max_pages && h.num_pages == a.c.num_pages && h.window == a.window && h.first == a.first && h.few_rows == a.shape.few_rows &&
-           h.ctas == a.shape.ctas;
+    return h.magic == kPlanMagic && h.N == a.N && h.heads == plan_heads(a.Hq, a.c.Hkv) && h.n_seqs == a.c.n_seqs &&
+           h.max_new == a.max_new && h.rows == plan_rows(a.shape.few_rows, a.c.page_rows, a.mask != nullptr) &&
+           h.max_pages == a.c.max_pages && h.num_pages == a.c.num_pages && h.ctas == a.shape.ctas &&
+           h.window == a.window && h.first == a.first;
 }
 
 // ---------------------------------------------------------------- element types

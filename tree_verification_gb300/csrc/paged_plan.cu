@@ -501,15 +501,12 @@ plan_kernel(const __grid_constant__ GraftPagedCache c, int N, int Hq, const int3
         PlanHead& h = *reinterpret_cast<PlanHead*>(plan);
         h.magic = kPlanMagic;
         h.N = N;
-        h.Hq = Hq;
-        h.Hkv = c.Hkv;
+        h.heads = plan_heads(Hq, c.Hkv);
         h.n_seqs = c.n_seqs;
         h.max_new = max_new;
-        h.tree = tree;
-        h.page_rows = c.page_rows;
+        h.rows = plan_rows(shape.few_rows, c.page_rows, tree);
         h.max_pages = c.max_pages;
         h.num_pages = c.num_pages;
-        h.few_rows = shape.few_rows;
         h.ctas = shape.ctas;
         h.window = window;
         h.first = first;

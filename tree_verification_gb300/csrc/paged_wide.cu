@@ -576,14 +576,15 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                         const int kb = block_at(w.blk0 + j, w.gap) * BN;
                         keep_bits(keep, kb, limit, w.L, anc);
                         if (kWindow) hide_bits(keep, kb, a.first, low);
-                        float s[BN];
 #pragma unroll
-                        for (int x = 0; x < BN / 32; ++x) tmem_ld32(sbuf + x * 32, s + x * 32);
-                        tmem_wait_ld();
+                        for (int x = 0; x < BN / 32; ++x) {
+                            float s[32];
+                            tmem_ld32(sbuf + x * 32, s);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int x = 0; x < BN; ++x) s[x] = ((keep[x >> 5] >> (x & 31)) & 1u) ? s[x] : -INFINITY;
-#pragma unroll
-                        for (int x = 0; x < BN / 32; ++x) tmem_st32(sbuf + x * 32, s + x * 32);
+                            for (int y = 0; y < 32; ++y) s[y] = ((keep[x] >> y) & 1u) ? s[y] : -INFINITY;
+                            tmem_st32(sbuf + x * 32, s);
+                        }
                         tmem_wait_st();
                     }
                     if (t == 0 && (j >= edge || (kWindow && j < front))) {
@@ -601,19 +602,22 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                         const int r0 = lo + r / 16, c16 = r % 16;
                         uint8_t* first = v0 + (r0 >> 3) * GROUP_BYTES + (c16 >> 3) * HALF_BYTES + (r0 & 7) * 128 +
                                          (c16 & 7) * 16;
-                        // Zero times any of them is zero, or there is something to take out.
-                        typename E::T2 zeros = E::pack(0u);
+                        bool look = true;
+                        if constexpr (kWindow) {
+                            // Whole blocks are cleaned, most without need: zero times any of a thread's elements is zero,
+                            // or there is something to take out.  (Chunks over 1024 keys 141 -> 131 us.)
+                            typename E::T2 zeros = E::pack(0u);
 #pragma unroll 4
-                        for (int x = 0; x < n - r / 16; x += 8) {
-                            const uint4 v = *reinterpret_cast<const uint4*>(first + (x >> 3) * GROUP_BYTES);
-                            zeros = __hfma2(E::pack(v.x), E::pack(0u), zeros);
-                            zeros = __hfma2(E::pack(v.y), E::pack(0u), zeros);
-                            zeros = __hfma2(E::pack(v.z), E::pack(0u), zeros);
-                            zeros = __hfma2(E::pack(v.w), E::pack(0u), zeros);
+                            for (int x = 0; x < n - r / 16; x += 8) {
+                                const uint4 v = *reinterpret_cast<const uint4*>(first + (x >> 3) * GROUP_BYTES);
+                                zeros = __hfma2(E::pack(v.x), E::pack(0u), zeros);
+                                zeros = __hfma2(E::pack(v.y), E::pack(0u), zeros);
+                                zeros = __hfma2(E::pack(v.z), E::pack(0u), zeros);
+                                zeros = __hfma2(E::pack(v.w), E::pack(0u), zeros);
+                            }
+                            look = kb + BN > keys || E::odd(*reinterpret_cast<const uint32_t*>(&zeros));
                         }
-                        const bool look = kb + BN > keys || E::odd(*reinterpret_cast<const uint32_t*>(&zeros));
                         bool odd = false;
-#pragma unroll 1
                         for (int x = 0; look && x < n - r / 16; x += 8) {
                             const int rr = r0 + x;
                             uint4* p = reinterpret_cast<uint4*>(first + (x >> 3) * GROUP_BYTES);
@@ -870,19 +874,18 @@ join_kernel(const __grid_constant__ AttnArgs a) {
     // still lie in the SM's L1, and in one trip: the head's words, and the first task's row block at both places where
     // it can lie (15.9 -> 15.7 us, 40000 keys 45.2 -> 44.4).
     const Group* groups = reinterpret_cast<const Group*>(a.plan + a.shape.off_group);
-    constexpr int kHead = kHeadBytes / 4;
-    __shared__ int32_t s_words[kHead + 16];
-    static_assert(kHeadBytes % 8 == 0 && sizeof(Group) == 32, "the head's words, 8 + 8");
-    if (threadIdx.x < kHead + 16) {
-        const int x = threadIdx.x, g = min((int)blockIdx.x / (x < kHead + 8 ? 8 : 16), a.shape.max_groups - 1);
-        s_words[x] = __ldcg(x < kHead ? reinterpret_cast<const int32_t*>(a.plan) + x
-                                      : reinterpret_cast<const int32_t*>(groups + g) + ((x - kHead) & 7));
+    __shared__ int32_t s_words[32];
+    static_assert(kHeadBytes <= 64 && sizeof(Group) == 32, "16 + 8 + 8 words");
+    if (threadIdx.x < 32) {
+        const int x = threadIdx.x, g = min((int)blockIdx.x / (x < 24 ? 8 : 16), a.shape.max_groups - 1);
+        s_words[x] = __ldcg(x < 16 ? reinterpret_cast<const int32_t*>(a.plan) + x
+                                   : reinterpret_cast<const int32_t*>(groups + g) + (x & 7));
     }
     __syncthreads();
     const PlanHead& head = *reinterpret_cast<const PlanHead*>(s_words);
     const int each = 8 * head.tiles, tasks = plan_fits(a, head) ? head.n_groups * each : 0;
     int task = blockIdx.x;
-    Group gr = *reinterpret_cast<const Group*>(s_words + (head.tiles == 1 ? kHead : kHead + 8));
+    Group gr = *reinterpret_cast<const Group*>(s_words + (head.tiles == 1 ? 16 : 24));
     griddep_wait();
     while (task < tasks) {
         join_rows<DT>(a, gr, task % each);
