@@ -5,17 +5,18 @@
 //   rank(v) = #{x > x_v} + #{x = x_v at lower ids},  the top k by (x descending, id ascending).
 //
 // Every logit of the rows asked for is read once (4 or 2 bytes) and costs about ten instructions: HBM bounds fp32, the
-// issue of instructions 16-bit logits (1024 rows of 151936: fp32 108 us, 5.8 TB/s; bf16 67 us, 4.6 TB/s).
-// logprob_part_kernel lays the rows' chunks (32 logits a thread) side by side and gives every team of threads an even run
-// of them, so all end together whatever the number of rows; the next chunks come through a ring in shared memory
-// (cp.async, each thread its own pieces: no barrier) while one is worked on.  A thread keeps its own maximum and sums
-// over its run's part of a row.  A team is a CTA; where rows are short (kShort), a warp that takes whole rows, without
-// barriers.  logprob_join_kernel adds up the pieces of rows that a run's edges cut, in their order.
+// issue of instructions 16-bit logits (1024 rows of 151936: fp32 109 us, 5.7 TB/s; bf16 69 us, 4.5 TB/s).
+// logprob_part_kernel lays the rows' chunks (32 fp32 or 64 16-bit logits a thread) side by side and gives every team of
+// threads an even run of them, so all end together whatever the number of rows; the next chunk comes through a ring in
+// shared memory (cp.async, each thread its own pieces: no barrier) while one is worked on.  A thread keeps its own
+// maximum and sums over its run's part of a row: a chunk's by themselves, then added to the part's in two numbers.  A
+// team is a CTA; where rows are short (kShort), a warp that takes whole rows, without barriers.  logprob_join_kernel
+// adds up the pieces of rows that a run's edges cut, in their order.
 //
 // Top alternatives cost the pass one store a thread and chunk, a bound of the chunk's largest of the thread's logits.
 // Once a segment (kSeg chunks, or a row's end) a threshold is taken that at least k of the threads' largest reach; the
 // pieces above it (some 50) are read once more, all threads at once; what passes goes to a buffer in shared memory and
-// finds its place by counting (20 alternatives of the rows above: 124 us; 209 with candidates pushed and merged a chunk
+// finds its place by counting (20 alternatives of the rows above: 126 us; 209 with candidates pushed and merged a chunk
 // at a time).  Where more pass than the buffer holds (long runs of equal or of rising logits), the segment is gone
 // through chunk by chunk instead.
 #include <climits>
@@ -31,8 +32,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// CTAs an SM: three of 80 registers left spills in the 16-bit kernels (1024 rows of 151936: fp32 138 us with three, 134 with
-// two; bf16 161 and 120).
+// CTAs an SM, of 128 registers.  (Three of 80, tried with chunks half as long, left spills in the 16-bit kernels: 1024 rows
+// of 151936 in fp32 138 us, 134 with two; bf16 161 and 120.)
 constexpr int kResident = 2;
 constexpr int kSeg = 40;       // chunks of a segment
 constexpr int kMaxRows = 128;  // rows of a CTA's runs at most
@@ -53,14 +54,11 @@ __device__ __forceinline__ void cp_wait() {
 
 template <int DT>
 constexpr int kElems = DT == GRAFT_F32 ? 4 : 8;  // of 16 bytes
-// 16-byte pieces of a chunk a thread, and chunks in shared memory (one worked on, the others on their way).  1024 rows of
-// 151936 with 20 alternatives, eight pieces and four: fp32 126 and 131 us, bf16 98 and 100; 1999 rows of 32768 in bf16 39
-// and 43 (of 8192, half a chunk, 19 and 15.5).
-template <int DT>
-constexpr int kVecsOf = 8;
-template <int DT>
-constexpr int kStagesOf = 16 / kVecsOf<DT>;
-constexpr int kRing = 16 * kThreads * 16;
+// 16-byte pieces of a chunk a thread, and chunks in shared memory (one worked on, one on its way).  When it was chosen, 1024
+// rows of 151936 with 20 alternatives, eight pieces and four (and four chunks): fp32 126 and 131 us, bf16 98 and 100; 1999
+// rows of 32768 in bf16 39 and 43 (of 8192, half a chunk, 19 and 15.5).
+constexpr int kVecs = 8, kStages = 2;
+constexpr int kRing = kStages * kVecs * kThreads * 16;
 
 struct Args {
     const char* logits;
@@ -129,17 +127,15 @@ __device__ __forceinline__ float key_value(uint64_t k) {
 }
 __device__ __forceinline__ int key_id(uint64_t k) { return (int)~(uint32_t)k; }
 
-__device__ __forceinline__ uint64_t exchange(uint64_t k, int lane, int step, bool down) {
-    const uint64_t o = __shfl_xor_sync(0xffffffffu, k, step);
-    const bool upper = (lane & step) == 0;
-    return (upper == down) == (k > o) ? k : o;
-}
 // The best 32 of two falling lists, in falling order.
 __device__ __forceinline__ uint64_t merge_keys(uint64_t a, uint64_t b, int lane) {
     const uint64_t r = __shfl_sync(0xffffffffu, b, 31 - lane);
     uint64_t k = a > r ? a : r;
 #pragma unroll
-    for (int step = 16; step > 0; step >>= 1) k = exchange(k, lane, step, true);
+    for (int step = 16; step > 0; step >>= 1) {
+        const uint64_t o = __shfl_xor_sync(0xffffffffu, k, step);
+        k = ((lane & step) == 0) == (k > o) ? k : o;
+    }
     return k;
 }
 // A warp's 32 values in falling order.
@@ -202,27 +198,27 @@ struct Two<GRAFT_FP16> {
     static __device__ __forceinline__ T both(float x) { return __floats2half2_rn(x, x); }
     static __device__ __forceinline__ float2 up(T x) { return __half22float2(x); }
 };
-// The largest of kVecs x 16 bytes of logits (NaN aside).
-template <int DT, int kVecs>
+// The largest of kN x 16 bytes of logits (NaN aside).
+template <int DT, int kN>
 __device__ __forceinline__ float largest(const uint4* w) {
     if constexpr (DT == GRAFT_F32) {
-        float m[kVecs];
+        float m[kN];
 #pragma unroll
-        for (int x = 0; x < kVecs; ++x)
+        for (int x = 0; x < kN; ++x)
             m[x] = fmaxf(fmaxf(__uint_as_float(w[x].x), __uint_as_float(w[x].y)),
                          fmaxf(__uint_as_float(w[x].z), __uint_as_float(w[x].w)));
 #pragma unroll
-        for (int x = 1; x < kVecs; ++x) m[0] = fmaxf(m[0], m[x]);
+        for (int x = 1; x < kN; ++x) m[0] = fmaxf(m[0], m[x]);
         return m[0];
     } else {
-        typename Two<DT>::T m[kVecs];
+        typename Two<DT>::T m[kN];
 #pragma unroll
-        for (int x = 0; x < kVecs; ++x) {
+        for (int x = 0; x < kN; ++x) {
             const auto* p = reinterpret_cast<const typename Two<DT>::T*>(&w[x].x);
             m[x] = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
         }
 #pragma unroll
-        for (int x = 1; x < kVecs; ++x) m[0] = __hmax2(m[0], m[x]);
+        for (int x = 1; x < kN; ++x) m[0] = __hmax2(m[0], m[x]);
         const float2 f = Two<DT>::up(m[0]);
         return fmaxf(f.x, f.y);
     }
@@ -375,7 +371,7 @@ __device__ __forceinline__ void finish(const Args& a, int n, bool ok, float give
 template <int DT, bool kWarpTeam>
 __global__ void __launch_bounds__(kThreads, kResident)
 logprob_part_kernel(const __grid_constant__ Args a) {
-    constexpr int E = kElems<DT>, kVecs = kVecsOf<DT>, kStages = kStagesOf<DT>;
+    constexpr int E = kElems<DT>;
     constexpr int kBytes = DT == GRAFT_F32 ? 4 : 2;
     constexpr int kTeams = kWarpTeam ? kWarps : 1;       // of a CTA
     constexpr int kTeam = kThreads / kTeams;             // threads of a team
@@ -559,6 +555,7 @@ logprob_part_kernel(const __grid_constant__ Args a) {
         dst = dst + kStageBytes == ring + kStages * kStageBytes ? ring : dst + kStageBytes;
         cp_commit();
     };
+    static_assert(kStages == 2, "one chunk ahead");
     // The tokens and their logits: a read each among the first copies (behind all of them they took 6 us).
     const int my_tok = listed_row ? a.tokens[s_entry[tid]] : -1;
     issue();
@@ -569,8 +566,6 @@ logprob_part_kernel(const __grid_constant__ Args a) {
         s_xt[tid] = make_float2(v, below<DT>(v));
         if (!ok && my_tok != -1) flag_status(a.status, GRAFT_STATUS_TOKEN_RANGE);
     }
-#pragma unroll
-    for (int x = 0; x < kStages - 2; ++x) issue();
     __syncthreads();
     if (idle) return;  // (warps alone from here on)
 
@@ -955,7 +950,7 @@ int most_ctas(int N) {
 template <int DT>
 int launch(Args& a, cudaStream_t st) {
     const bool warps = a.V <= kShort;
-    const int64_t chunk = (int64_t)(warps ? 32 : kThreads) * kVecsOf<DT> * kElems<DT>;
+    const int64_t chunk = (int64_t)(warps ? 32 : kThreads) * kVecs * kElems<DT>;
     // (a row may start inside 16 bytes)
     const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && (a.R <= 1 || a.stride % 16 == 0);
     a.chunks = (int)((a.V + (aligned ? 0 : kElems<DT> - 1) + chunk - 1) / chunk);

@@ -19,8 +19,8 @@
 // of the first tokens and those from the earliest row's window on; units that
 // some row does not see whole are masked like those with new rows in them.
 // The bytes are then the window's: one token each of 64 sequences of up to
-// 32768 rows over 4096 takes 167 us a layer (6.1 TB/s), over 1024 of one
-// sequence 7.8 (latency).
+// 32768 rows over 4096 takes 163 us a layer (6.3 TB/s), over 1024 of one
+// sequence 7.7 (latency).
 //
 // Items that a run's edges cut are joined by the CTA that arrives last (a
 // counter an item): it reads the pieces' 32-bit partial rows in their order,

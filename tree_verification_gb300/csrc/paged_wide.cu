@@ -29,9 +29,9 @@
 //     those of the first tokens and those from its earliest row's window on;
 //     the blocks that some row's window starts in or behind are masked and
 //     cleaned like those with new rows, and a row that has seen nothing as yet
-//     takes a block's maximum anew.  (16 trees at group 16 over 4096 keys 138
+//     takes a block's maximum anew.  (16 trees at group 16 over 4096 keys 137
 //     us; 4100 prompt rows over 1024, where 4 of an item's 10.5 blocks are
-//     masked, 112.)
+//     masked, 121.)
 //   * V elements that are infinite or NaN in blocks with masked keys are
 //     taken out in shared memory (0 * NaN is NaN) and given to the rows that
 //     do see them after the item's rows are written.
@@ -554,9 +554,10 @@ wide_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs 
                 continue;
             }
             auto odd_word = [&]() { return odd_item + (two ? (n_two & 1) : 2 + ((q - n_two) & 1)); };
-            // (a row that sees none of the range's first block sees none of the range: new rows see a run of keys
-            // from the front, and a tree's 64 keys lie in one block unless prefix keys come first; so the maximum
-            // of a row that is still -inf after the first block stays so, and its weights are 0)
+            // (Without a window a row that sees none of the range's first block sees none of the range: new rows see a run
+            // of keys from the front, and a tree's 64 keys lie in one block unless prefix keys come first; so the maximum
+            // of a row that is still -inf after the first block stays so, and its weights are 0.  With one a row may see
+            // its first key in a later block: there it takes that block's maximum anew.)
             float m_used = -INFINITY, l_sum = 0.f;
             {
                 for (int j = 0; j < nblk; ++j) {

@@ -20,7 +20,8 @@ With ``top_logprobs`` = k (0 for none of the alternatives) the step also gives
 law's entropy, the tokens' rank and the k most likely alternatives
 (graft_token_logprobs over the accepted path's rows of the target logits), each
 [B][Kmax] (alternatives [B][Kmax][k]) beside ``acc["out_tok"]``; at
-``temperature`` > 0 those of the law that was sampled.
+``temperature`` > 0 those of the law that was sampled.  (As for the acceptance
+itself, B * Kmax is at most 65535.)
 
 Because every buffer is fixed, a whole step can be captured once in a CUDA
 graph and replayed, which removes the per-layer host launch cost.  The
